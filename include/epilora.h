@@ -413,6 +413,149 @@ EPILORA_API int epilora_layer_forward_noalloc(int fmt, int M, int N, int K,
                           void* Y, int ldy,
                           int* status_dev, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention of a decoder layer between its qkv and o projections: a paged
+ * key/value cache, the kernel that appends to it, and the attention that
+ * reads it; and the attention of whole packed prompts without a cache.
+ *
+ * Common to the three calls: `heads` query heads share `kv_heads` key/value
+ * heads in groups of G = heads / kv_heads (query head h reads key/value head
+ * h / G). Activations are bf16; Q, K, V and O are given by a pointer, a
+ * token stride and a head stride in elements (the head_dim elements of a
+ * head are contiguous; strides are multiples of 8, pointers 16-byte
+ * aligned), so the slices of a fused qkv projection's output are used as
+ * they are. No stride may make two elements of a written tensor coincide.
+ * ------------------------------------------------------------------------ */
+typedef enum { EPILORA_KV_BF16 = 0, EPILORA_KV_E4M3 = 1 } epilora_kv_format;
+
+/*
+ * A paged cache of one layer (this struct is host memory, read during the
+ * call; k, v and the scales are device memory). Entry (page p, head g, token
+ * row i of the page, element d) is at
+ *   k[p * k_page_stride + g * k_head_stride + i * k_token_stride + d]
+ * (strides in elements; the byte strides are multiples of 16, k and v
+ * 16-byte aligned), v alike: pages of heads ("[page][head][token][d]") and
+ * pages of tokens ("[page][token][head][d]") are both one choice of strides.
+ * page_size is 16, 32, 64, 128 or 256 tokens, head_dim 64 or 128.
+ * EPILORA_KV_E4M3: codes of one byte, the value is code * k_scale[g] (fp32
+ * per head, device; required then, ignored for bf16).
+ */
+typedef struct {
+  int kv_fmt;
+  int kv_heads;
+  int head_dim;
+  int page_size;
+  int num_pages;
+  int reserved; /* 0 */
+  void* k;
+  void* v;
+  int64_t k_page_stride, k_head_stride, k_token_stride;
+  int64_t v_page_stride, v_head_stride, v_token_stride;
+  const float* k_scale; /* [kv_heads] */
+  const float* v_scale; /* [kv_heads] */
+} epilora_kv_cache;
+
+/*
+ * The sequences of one step (host struct, device arrays). Sequence b owns
+ * the packed new tokens q_start[b] .. q_start[b+1] - 1 (possibly none) and
+ * holds kv_len[b] tokens once they are appended: its new token i stands at
+ * position kv_len[b] - n_new + i. Position j is row j % page_size of page
+ * page_table[b * table_stride + j / page_size]. q_start ascends from 0;
+ * packed rows from q_start[n_seqs] up to n_tokens belong to no sequence
+ * (padding of a captured graph). max_new is the caller's upper bound of the
+ * new tokens of any sequence (n_tokens always is one): it selects kernels,
+ * not results.
+ * Device-detected, EPILORA_ERR_INVALID_ARG in the status word: q_start that
+ * descends or leaves [0, n_tokens], more new tokens than max_new, kv_len
+ * beyond table_pages * page_size, a page index that is read and is outside
+ * [0, num_pages). No access is made out of bounds then; the outputs of the
+ * sequences concerned are unspecified.
+ */
+typedef struct {
+  int n_seqs;
+  int n_tokens;
+  int max_new;
+  int table_pages;  /* columns of page_table in use */
+  int64_t table_stride;
+  const int32_t* q_start;    /* [n_seqs + 1] */
+  const int32_t* kv_len;     /* [n_seqs] */
+  const int32_t* page_table; /* [n_seqs][table_stride] */
+} epilora_kv_batch;
+
+/*
+ * Appends the new tokens' keys and values to the cache, rotating queries and
+ * keys by their position on the way.
+ * For a token at position p, each q and k head row x with c = cos_sin[p][i],
+ * s = cos_sin[p][rot_dim / 2 + i], i in [0, rot_dim / 2), fp32 arithmetic
+ * with one rounding per operation:
+ *   y[a] = fl(fl(x[a] c) - fl(x[b] s)),  y[b] = fl(fl(x[b] c) + fl(x[a] s))
+ *   (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved != 0;
+ * elements from rot_dim on are copied. Qout takes bf16(y). The cache takes
+ * bf16(y) of k and v itself, or E4M3_rn_satfinite(fl(y / k_scale[g])) and
+ * E4M3_rn_satfinite(fl(v / v_scale[g])): bit-exact functions of the inputs.
+ * cos_sin is fp32 [n_pos][rot_dim] (cosines, then sines), rot_dim a multiple
+ * of 16 up to head_dim; cos_sin == NULL rotates nothing (Q, Qout may then be
+ * NULL too). Qout may be Q itself (same strides); otherwise it must not
+ * overlap Q, K or V.
+ * A token of no sequence, at a negative position (more new tokens than
+ * kv_len), or that fails a device check (the above, or a position >= n_pos)
+ * appends nothing; its Qout rows are zero. The new tokens of a batch have to
+ * go to different cache rows. n_tokens == 0 is a no-op. One kernel, a
+ * programmatic dependent of the previous kernel on the stream (it waits for
+ * that kernel before it reads anything).
+ */
+EPILORA_API int epilora_kv_append(const epilora_kv_cache* cache, const epilora_kv_batch* batch, int heads,
+                      const void* Q, int64_t q_token_stride, int64_t q_head_stride,
+                      const void* K, int64_t k_token_stride, int64_t k_head_stride,
+                      const void* V, int64_t v_token_stride, int64_t v_head_stride,
+                      const float* cos_sin, int n_pos, int rot_dim, int interleaved,
+                      void* Qout, int64_t qo_token_stride, int64_t qo_head_stride,
+                      int* status_dev, void* stream);
+
+/*
+ * Bytes of device workspace epilora_paged_attention and
+ * epilora_prompt_attention need (the partial results of sequences that
+ * several thread blocks share). It depends on the device's number of SMs and
+ * on head_dim only, so one workspace serves every layer and step of a model.
+ * Zero-fill it once after allocating it; calls leave it ready for the next
+ * one. Calls that share a workspace must be ordered on one stream. Returns 0
+ * for a head_dim other than 64 or 128.
+ */
+EPILORA_API size_t epilora_attention_workspace_bytes(int head_dim);
+
+/*
+ * Attention of the new tokens over the paged cache (their own keys and
+ * values appended before): for token t of sequence b at position p,
+ *   x_j = scale * q[t,h] . K[b, j, h / G],  j in [0, p]
+ *   O[t,h] = bf16( sum_j exp(x_j - m) V[b, j, h / G] / sum_j exp(x_j - m) )
+ *   lse[t,h] = ln sum_j exp(x_j)   (fp32 [n_tokens][heads], optional)
+ * with scores, statistics and sums in fp32 (the weights exp(x_j - m) are
+ * rounded to the tensor cores' 16-bit operand type: bf16, or fp16 for an
+ * E4M3 cache; an E4M3 cache's queries are scaled by a power of two per row
+ * into fp16). A row that sees nothing (negative position, no sequence) is
+ * zero, its lse -infinity. What a masked position, a page's unused rows or
+ * an unused page hold never reaches a result, NaN and infinities included.
+ * scale is finite.
+ */
+EPILORA_API int epilora_paged_attention(const epilora_kv_cache* cache, const epilora_kv_batch* batch, int heads,
+                      const void* Q, int64_t q_token_stride, int64_t q_head_stride, float scale,
+                      void* O, int64_t o_token_stride, int64_t o_head_stride, float* lse,
+                      void* workspace, size_t workspace_bytes, int* status_dev, void* stream);
+
+/*
+ * Causal attention of whole packed prompts, keys and values straight from
+ * the projection: prompt b is the packed rows q_start[b] .. q_start[b+1] - 1
+ * of Q, K and V; row i of a prompt attends to its rows 0 .. i. Results and
+ * conventions as epilora_paged_attention (q_start as in epilora_kv_batch).
+ */
+EPILORA_API int epilora_prompt_attention(int n_seqs, int n_tokens, const int32_t* q_start,
+                      int heads, int kv_heads, int head_dim,
+                      const void* Q, int64_t q_token_stride, int64_t q_head_stride,
+                      const void* K, int64_t k_token_stride, int64_t k_head_stride,
+                      const void* V, int64_t v_token_stride, int64_t v_head_stride, float scale,
+                      void* O, int64_t o_token_stride, int64_t o_head_stride, float* lse,
+                      void* workspace, size_t workspace_bytes, int* status_dev, void* stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -24,7 +24,27 @@ EPILORA_ERR_WORKSPACE = -5
 FMT_FP8 = 0
 FMT_NVFP4 = 1
 
+KV_BF16 = 0
+KV_E4M3 = 1
+
 _c_int, _vp, _sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+_i64, _f32 = ctypes.c_int64, ctypes.c_float
+
+
+class KvCache(ctypes.Structure):
+    """epilora_kv_cache"""
+    _fields_ = [("kv_fmt", _c_int), ("kv_heads", _c_int), ("head_dim", _c_int), ("page_size", _c_int),
+                ("num_pages", _c_int), ("reserved", _c_int), ("k", _vp), ("v", _vp),
+                ("k_page_stride", _i64), ("k_head_stride", _i64), ("k_token_stride", _i64),
+                ("v_page_stride", _i64), ("v_head_stride", _i64), ("v_token_stride", _i64),
+                ("k_scale", _vp), ("v_scale", _vp)]
+
+
+class KvBatch(ctypes.Structure):
+    """epilora_kv_batch"""
+    _fields_ = [("n_seqs", _c_int), ("n_tokens", _c_int), ("max_new", _c_int), ("table_pages", _c_int),
+                ("table_stride", _i64), ("q_start", _vp), ("kv_len", _vp), ("page_table", _vp)]
+
 
 # name -> (restype, argtypes), in the order of include/epilora.h
 SIGNATURES = {
@@ -50,6 +70,13 @@ SIGNATURES = {
     "epilora_layer_forward_slices": (_c_int, [_c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp, _vp, _vp,
                                               _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_int, _vp,
                                               _sz, _vp, _vp]),
+    "epilora_kv_append": (_c_int, [_vp, _vp, _c_int, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _c_int,
+                                   _c_int, _c_int, _vp, _i64, _i64, _vp, _vp]),
+    "epilora_attention_workspace_bytes": (_sz, [_c_int]),
+    "epilora_paged_attention": (_c_int, [_vp, _vp, _c_int, _vp, _i64, _i64, _f32, _vp, _i64, _i64, _vp, _vp, _sz, _vp,
+                                         _vp]),
+    "epilora_prompt_attention": (_c_int, [_c_int, _c_int, _vp, _c_int, _c_int, _c_int, _vp, _i64, _i64, _vp, _i64,
+                                          _i64, _vp, _i64, _i64, _f32, _vp, _i64, _i64, _vp, _vp, _sz, _vp, _vp]),
 }
 
 _lib = None
@@ -205,3 +232,30 @@ def epilora_layer_forward_noalloc(fmt, M, N, K, X, ldx, Wq, w_scale, w_block_sca
     return load().epilora_layer_forward_noalloc(fmt, M, N, K, _p(X), ldx, _p(Wq), _p(w_scale), _p(w_block_scale),
                                                 _p(w_global_scale), _p(x_global_scale), _p(A), _p(B), L, r,
                                                 _p(idx), _p(mask), _p(Y), ldy, _p(status_dev), _stream(stream))
+
+
+def epilora_kv_append(cache: KvCache, batch: KvBatch, heads, Q, q_strides, K, k_strides, V, v_strides, cos_sin, n_pos,
+                      rot_dim, interleaved, Qout, qo_strides, status_dev=None, stream=None) -> int:
+    """Strides are (token, head) pairs in elements."""
+    return load().epilora_kv_append(ctypes.addressof(cache), ctypes.addressof(batch), heads, _p(Q), *q_strides, _p(K),
+                                    *k_strides, _p(V), *v_strides, _p(cos_sin), n_pos, rot_dim, int(interleaved),
+                                    _p(Qout), *qo_strides, _p(status_dev), _stream(stream))
+
+
+def epilora_attention_workspace_bytes(head_dim) -> int:
+    return load().epilora_attention_workspace_bytes(head_dim)
+
+
+def epilora_paged_attention(cache: KvCache, batch: KvBatch, heads, Q, q_strides, scale, O, o_strides, lse, workspace,
+                            workspace_bytes, status_dev=None, stream=None) -> int:
+    return load().epilora_paged_attention(ctypes.addressof(cache), ctypes.addressof(batch), heads, _p(Q), *q_strides,
+                                          scale, _p(O), *o_strides, _p(lse), _p(workspace), workspace_bytes,
+                                          _p(status_dev), _stream(stream))
+
+
+def epilora_prompt_attention(n_seqs, n_tokens, q_start, heads, kv_heads, head_dim, Q, q_strides, K, k_strides, V,
+                             v_strides, scale, O, o_strides, lse, workspace, workspace_bytes, status_dev=None,
+                             stream=None) -> int:
+    return load().epilora_prompt_attention(n_seqs, n_tokens, _p(q_start), heads, kv_heads, head_dim, _p(Q), *q_strides,
+                                           _p(K), *k_strides, _p(V), *v_strides, scale, _p(O), *o_strides, _p(lse),
+                                           _p(workspace), workspace_bytes, _p(status_dev), _stream(stream))

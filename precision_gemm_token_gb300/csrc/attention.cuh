@@ -1,0 +1,63 @@
+// Shared definitions of the attention operators: the paged key/value cache's
+// append, attention over the cache, attention of packed prompts.
+#pragma once
+#include "common.cuh"
+
+namespace epi {
+
+// bf16 rows [token][head][head_dim], strides in elements
+struct AttnRows {
+  const __nv_bfloat16* p;
+  int64_t ts, hs;
+};
+struct AttnOut {
+  __nv_bfloat16* p;
+  int64_t ts, hs;
+};
+
+struct AppendArgs {
+  epilora_kv_cache cache;
+  epilora_kv_batch batch;
+  int heads;
+  AttnRows q, k, v;
+  AttnOut qo;
+  const float* cos_sin;
+  int n_pos, rot_dim, interleaved;
+  int* status;
+  cudaStream_t stream;
+};
+int launch_kv_append(const AppendArgs& a);
+
+// Attention over the cache (paged != 0) or over packed prompts (k, v rows).
+struct AttnArgs {
+  int paged;
+  epilora_kv_cache cache;   // paged; prompts: head_dim and kv_heads only
+  epilora_kv_batch batch;   // prompts: n_seqs, n_tokens, q_start only
+  int heads;
+  AttnRows q, k, v;
+  AttnOut o;
+  float* lse;
+  float scale;
+  void* workspace;
+  int* status;
+  cudaStream_t stream;
+};
+int launch_attn(const AttnArgs& a);
+size_t attn_workspace_bytes(int head_dim);
+
+// The new tokens of sequence b: packed rows [first, first + n), clamped to
+// the packed array whatever q_start holds; `bad` is set where it had to be.
+struct SeqRows {
+  int first, n;
+};
+__device__ __forceinline__ SeqRows seq_rows(const int32_t* q_start, int b, int n_tokens, bool& bad) {
+  const int s = __ldg(q_start + b), e = __ldg(q_start + b + 1);
+  SeqRows r;
+  r.first = min(max(s, 0), n_tokens);
+  const int end = min(max(e, r.first), n_tokens);
+  r.n = end - r.first;
+  if (r.first != s || end != e || (b == 0 && s != 0)) bad = true;
+  return r;
+}
+
+}  // namespace epi

@@ -129,6 +129,32 @@ int make_tma_2d_swz(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
   return r == CUDA_SUCCESS ? EPILORA_OK : EPILORA_ERR_CUDA;
 }
 
+int make_tma_4d_u8(CUtensorMap* map, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides_bytes)[3],
+                   const uint32_t (&box)[4], int swizzle_span) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (fn == nullptr) return EPILORA_ERR_CUDA;
+  if (!al16(base) || (swizzle_span != 64 && swizzle_span != 128) || box[0] > static_cast<uint32_t>(swizzle_span))
+    return EPILORA_ERR_INVALID_ARG;
+  std::memset(map, 0, sizeof(*map));
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4];
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    if (dims[i] == 0 || box[i] == 0) return EPILORA_ERR_INVALID_ARG;
+    d[i] = dims[i];
+    b[i] = box[i];
+  }
+  for (int i = 0; i < 3; ++i) {
+    if (strides_bytes[i] % 16 != 0) return EPILORA_ERR_INVALID_ARG;
+    st[i] = strides_bytes[i];
+  }
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), d, st, b, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? EPILORA_OK : EPILORA_ERR_CUDA;
+}
+
 int prefer_max_shared(const void* func, int* done_flags) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EPILORA_ERR_CUDA;

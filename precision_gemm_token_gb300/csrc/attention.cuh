@@ -45,13 +45,24 @@ struct AttnArgs {
 int launch_attn(const AttnArgs& a);
 size_t attn_workspace_bytes(int head_dim);
 
+// attn_decode.cu: the sequences whose new tokens n satisfy
+// attn_decode_takes(n, group), and the packed rows of no sequence.
+bool attn_decode_takes(int n, int group);
+int launch_attn_decode(const AttnArgs& a, uint32_t* counters, float* partials);
+size_t attn_decode_counter_bytes();
+size_t attn_decode_partial_bytes(int head_dim);
+
+// Batch metadata may be written by the previous kernel on the stream, so it is
+// read with ordinary loads: the compiler takes read-only loads for invariant
+// and may move them above griddepcontrol.wait.
+
 // The new tokens of sequence b: packed rows [first, first + n), clamped to
 // the packed array whatever q_start holds; `bad` is set where it had to be.
 struct SeqRows {
   int first, n;
 };
 __device__ __forceinline__ SeqRows seq_rows(const int32_t* q_start, int b, int n_tokens, bool& bad) {
-  const int s = __ldg(q_start + b), e = __ldg(q_start + b + 1);
+  const int s = q_start[b], e = q_start[b + 1];
   SeqRows r;
   r.first = min(max(s, 0), n_tokens);
   const int end = min(max(e, r.first), n_tokens);

@@ -1,0 +1,805 @@
+// Attention of a few new tokens over the paged cache: sequences whose new
+// tokens times the heads of a key/value group are at most 16 rows (one decode
+// token with up to 16 heads a group, a few drafted tokens).
+//
+//   O = sum_j exp2(x_j - m) V_j / sum_j exp2(x_j - m),  x = (scale log2 e) q . K_j
+//
+// One pass over the cache with a running maximum m and sum per row. It is
+// bound by reading the cache once: 2 head_dim elements per position and
+// key/value head against 4 head_dim flops per query row, so the 16-row tensor
+// core tile (mma.sync m16n8k16, rows = the group's heads) costs nothing even
+// where 4 or 8 of its rows are used.
+//
+// The cache's positions are cut into tiles of 64; the tiles of all (sequence,
+// head) pairs form one line that is split evenly over the thread blocks (two
+// per SM), so that any mix of lengths loads every SM alike; a pair cut
+// between blocks is joined by the block that finishes last, in the order of
+// the pieces (results do not depend on which block that is).
+// A block is one copying warp and four computing warps. The copying warp
+// brings units of 16 positions (keys and values of one page) into a ring by
+// TMA (boxes of one page's rows, so every layout with contiguous heads costs
+// the same); warp w computes unit 4 t + w of tile t with a maximum, sum and
+// output of its own, so no barrier stands in the loop; the four meet at the
+// end of a pair.
+#include "attention.cuh"
+#include "ptx.cuh"
+
+namespace epi {
+namespace {
+
+constexpr int kDecTile = 64;         // positions per tile
+constexpr int kDecUnit = 16;         // positions per warp and ring slot
+constexpr int kDecWarps = 4;         // computing warps
+constexpr int kDecThreads = 32 * (kDecWarps + 1);
+constexpr int kDecRows = 16;
+constexpr int kDecMaxCtas = 512;     // blocks of a launch (pieces of a join) at most
+constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
+// a row's maximum is raised (and its sums rescaled) only when a score exceeds
+// it by this many powers of two: weights stay below 2^8, exact in fp32 sums
+// and in range for the 16-bit operands
+constexpr float kRaise = 8.0f;
+
+template <int D, bool E4>
+struct DecCfg {
+  static constexpr int kRowBytes = D * (E4 ? 1 : 2);
+  static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;   // inner extent = swizzle span
+  static constexpr int kBoxes = kRowBytes / kBoxBytes;
+  static constexpr int kBox = kDecUnit * kBoxBytes;                     // bytes of one box
+  static constexpr int kHalf = kBoxes * kBox;                           // keys, then values
+  static constexpr int kUnitBytes = 2 * kHalf;
+  // a multiple of the computing warps: a slot always belongs to one warp, which
+  // waits for its fills in order (a warp ahead of a slot's other readers would
+  // take the parity of the fill before last for its own)
+  static constexpr int kSlots = 64 * 1024 / kUnitBytes < 24 ? 64 * 1024 / kUnitBytes : 24;
+  static_assert(kSlots % kDecWarps == 0, "slots are dealt to the warps");
+  static constexpr int kOld = D + 8;                                    // floats per row of the meeting buffer
+  // bytes: the four warps' outputs, or the weights of a join's pieces
+  static constexpr int kMeetOut = kDecWarps * kDecRows * kOld * 4, kMeetJoin = kDecMaxCtas * kDecRows * 4;
+  static constexpr int kMeet = kMeetOut > kMeetJoin ? kMeetOut : kMeetJoin;
+  static constexpr int kSmem = 1024 + kSlots * kUnitBytes + kMeet + 2048;
+};
+
+struct DecParams {
+  CUtensorMap tk, tv;
+  epilora_kv_batch b;
+  AttnRows q;
+  AttnOut o;
+  float* lse;
+  int heads, kv_heads, group;
+  int page_shift, page_size, num_pages;
+  float scale;
+  const float* k_scale;
+  const float* v_scale;
+  uint32_t* counters;   // [gridDim.x], zero between calls
+  float* partials;      // [2 gridDim.x][32 + 16 D]
+  int* status;
+};
+
+// A sequence of this kernel's class.
+struct DecSeq {
+  int first, n, len, base;   // packed rows, tokens in the cache (clamped), position of new token 0
+  int tiles;                 // 0: not of this class
+};
+__device__ __forceinline__ DecSeq dec_seq(const DecParams& p, int b, bool& bad) {
+  DecSeq s;
+  const SeqRows r = seq_rows(p.b.q_start, b, p.b.n_tokens, bad);
+  const int len = p.b.kv_len[b];
+  const int cap = p.b.table_pages << p.page_shift;
+  if (len > cap || len < 0 || r.n > p.b.max_new) bad = true;
+  s.first = r.first;
+  s.n = r.n;
+  s.base = len - r.n;
+  s.len = max(min(len, cap), 0);
+  s.tiles = r.n > 0 && r.n <= kDecRows / p.group ? max((s.len + kDecTile - 1) / kDecTile, 1) : 0;
+  return s;
+}
+
+// Walks the pieces of a thread block's range of the line of tiles. Every warp
+// holds a copy and steps it alike.
+struct DecWalk {
+  uint64_t x, end;     // tiles still to do: [x, end)
+  uint64_t total;
+  int ctas;
+  int b, h;
+  DecSeq s;
+  int t0, t1;          // this piece's tiles of the pair
+  uint64_t pair0;      // line position of the pair's tile 0
+};
+
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ void dec_piece(const DecParams& p, DecWalk& w) {
+  w.t0 = static_cast<int>(w.x - w.pair0);
+  const uint64_t left = w.end - w.x;
+  w.t1 = static_cast<int>(min(static_cast<uint64_t>(w.s.tiles - w.t0), left)) + w.t0;
+}
+
+// false: nothing to do. Called by whole warps.
+__device__ __forceinline__ bool dec_begin(const DecParams& p, DecWalk& w, int lane) {
+  uint64_t mine = 0;
+  bool bad = false;
+  for (int b = lane; b < p.b.n_seqs; b += 32) mine += dec_seq(p, b, bad).tiles;
+  if (bad && blockIdx.x == 0 && threadIdx.x < 32) record_status(p.status, EPILORA_ERR_INVALID_ARG);
+  w.total = warp_sum(mine) * p.kv_heads;
+  if (w.total == 0) return false;
+  w.ctas = static_cast<int>(min(static_cast<uint64_t>(gridDim.x), w.total));
+  if (static_cast<int>(blockIdx.x) >= w.ctas) return false;
+  w.x = blockIdx.x * w.total / w.ctas;
+  w.end = (blockIdx.x + 1) * w.total / w.ctas;
+  // the sequence that holds x
+  uint64_t before = 0;
+  w.b = -1;
+  for (int b0 = 0; b0 < p.b.n_seqs; b0 += 32) {
+    const int b = b0 + lane;
+    const uint64_t c = b < p.b.n_seqs ? static_cast<uint64_t>(dec_seq(p, b, bad).tiles) * p.kv_heads : 0;
+    uint64_t inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > w.x);
+    if (hit != 0) {
+      const int l = __ffs(hit) - 1;
+      w.b = b0 + l;
+      w.pair0 = before + __shfl_sync(0xffffffffu, inc - c, l);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (w.b < 0) return false;
+  w.s = dec_seq(p, w.b, bad);
+  w.h = static_cast<int>((w.x - w.pair0) / w.s.tiles);
+  w.pair0 += static_cast<uint64_t>(w.h) * w.s.tiles;
+  dec_piece(p, w);
+  return true;
+}
+
+__device__ __forceinline__ bool dec_next(const DecParams& p, DecWalk& w) {
+  w.x += w.t1 - w.t0;
+  if (w.x >= w.end) return false;
+  w.pair0 += w.s.tiles;
+  if (++w.h == p.kv_heads) {
+    w.h = 0;
+    bool bad = false;
+    do {   // x < end: a sequence of the class follows
+      if (++w.b >= p.b.n_seqs) return false;
+      w.s = dec_seq(p, w.b, bad);
+    } while (w.s.tiles == 0);
+  }
+  dec_piece(p, w);
+  return true;
+}
+
+__device__ __forceinline__ void meet_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kDecWarps * 32) : "memory"); }
+
+template <bool E4>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (E4)
+    mma_f16_m16n8k16(d, a, b0, b1);
+  else
+    mma_bf16_m16n8k16(d, a, b0, b1);
+}
+
+template <bool E4>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if (E4) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// shared-memory byte of (row, byte) in a box with rows of SPAN bytes, swizzled
+// over the span by the TMA copy
+template <int SPAN>
+__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t byte) {
+  const uint32_t a = row * SPAN + byte;
+  return a ^ (((a >> 7) & (SPAN / 16 - 1)) << 4);
+}
+
+// O += P V over one unit. SEL: only the rows of one token take the result
+// (sel0 / sel1: the thread's rows g and g + 8).
+template <int D, bool E4, bool SEL>
+__device__ __forceinline__ void dec_pv(float (&acc)[D / 8][4], const uint32_t (&pa)[4], const uint8_t* vs, int lane,
+                                       bool sel0, bool sel1) {
+  using C = DecCfg<D, E4>;
+  const int g = lane >> 2, q = lane & 3;
+  auto add = [&](int nt, uint32_t b0, uint32_t b1) {
+    if (SEL) {
+      float t[4] = {acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]};
+      mma16<E4>(t, pa, b0, b1);
+      if (sel0) acc[nt][0] = t[0], acc[nt][1] = t[1];
+      if (sel1) acc[nt][2] = t[2], acc[nt][3] = t[3];
+    } else {
+      mma16<E4>(acc[nt], pa, b0, b1);
+    }
+  };
+  if (!E4) {
+    const uint32_t base = smem_u32(vs);
+    const uint32_t tok = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+    for (int np = 0; np < D / 16; ++np) {
+      const uint32_t d = np * 16 + (lane >> 4) * 8;
+      uint32_t r[4];
+      ldmatrix_x4_t(r, base + (d / 64) * C::kBox + swz<C::kBoxBytes>(tok, (d % 64) * 2));
+      add(2 * np, r[0], r[1]);
+      add(2 * np + 1, r[2], r[3]);
+    }
+  } else {
+    // Thread (g, q) holds the D / 8 elements from g D / 8 on of the tokens
+    // 2q, 2q+1, 2q+8, 2q+9: column g of n-tile nt is element g D / 8 + nt.
+    constexpr int W = D / 32;   // 32-bit words per thread and token
+    uint32_t w[4][W];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint32_t tok = 2 * q + (t & 1) + (t >> 1) * 8;
+      const uint8_t* src = vs + swz<C::kBoxBytes>(tok, g * (D / 8));
+      if (D == 128) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src);
+        w[t][0] = v.x, w[t][1] = v.y, w[t][2 % W] = v.z, w[t][3 % W] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(src);
+        w[t][0] = v.x, w[t][1] = v.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      uint32_t lo[4], hi[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) lo[t] = e4m3x2_to_f16x2(w[t][i]), hi[t] = e4m3x2_to_f16x2(w[t][i] >> 16);
+      add(4 * i + 0, __byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
+      add(4 * i + 1, __byte_perm(lo[0], lo[1], 0x7632), __byte_perm(lo[2], lo[3], 0x7632));
+      add(4 * i + 2, __byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
+      add(4 * i + 3, __byte_perm(hi[0], hi[1], 0x7632), __byte_perm(hi[2], hi[3], 0x7632));
+    }
+  }
+}
+
+// zero the value rows [from, 16) of a unit (whole warp)
+template <int D, bool E4>
+__device__ __forceinline__ void dec_zero_rows(uint8_t* vs, int from, int lane) {
+  using C = DecCfg<D, E4>;
+  constexpr int per_row = C::kRowBytes / 16;
+  const int n = (kDecUnit - from) * per_row;
+  for (int i = lane; i < n; i += 32) {
+    const int row = from + i / per_row, c = i % per_row;
+    const int box = c / (C::kBoxBytes / 16), cc = c % (C::kBoxBytes / 16);
+    *reinterpret_cast<uint4*>(vs + box * C::kBox + row * C::kBoxBytes + cc * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();   // the slot's next TMA copy comes after these stores
+  __syncwarp();
+}
+
+__device__ __forceinline__ bool word_nonfinite(uint32_t v, bool e4) {
+  if (e4) return ((v & 0x7F) == 0x7F) | ((v & 0x7F00) == 0x7F00) | ((v & 0x7F0000) == 0x7F0000) |
+                 ((v & 0x7F000000) == 0x7F000000);
+  return ((v & 0x7F80) == 0x7F80) | ((v & 0x7F800000) == 0x7F800000);
+}
+
+// whether the value rows [from, to) of a unit hold a NaN or an infinity (whole warp)
+template <int D, bool E4>
+__device__ __forceinline__ bool dec_rows_nonfinite(const uint8_t* vs, int from, int to, int lane) {
+  using C = DecCfg<D, E4>;
+  constexpr int per_row = C::kRowBytes / 16;
+  bool nf = false;
+  for (int i = lane; i < (to - from) * per_row; i += 32) {
+    const int row = from + i / per_row, c = i % per_row;
+    const int box = c / (C::kBoxBytes / 16), cc = c % (C::kBoxBytes / 16);
+    const uint4 v = *reinterpret_cast<const uint4*>(vs + box * C::kBox + row * C::kBoxBytes + cc * 16);
+    nf |= word_nonfinite(v.x, E4) | word_nonfinite(v.y, E4) | word_nonfinite(v.z, E4) | word_nonfinite(v.w, E4);
+  }
+  return __any_sync(0xffffffffu, nf);
+}
+
+template <int D, bool E4>
+__global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __grid_constant__ DecParams p) {
+  using C = DecCfg<D, E4>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* meet = reinterpret_cast<float*>(smem + C::kSlots * C::kUnitBytes);
+  float* ml = meet + C::kMeet / 4;                 // [4][16][2] maximum and sum of each warp's rows
+  float* row_m = ml + kDecWarps * kDecRows * 2;    // [16]
+  float* row_l = row_m + kDecRows;                 // [16]
+  uint64_t* full = reinterpret_cast<uint64_t*>(row_l + kDecRows);
+  uint64_t* empty = full + C::kSlots;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kSlots);
+  volatile int* last_flag = abort_flag + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&p.tk);
+    tma_prefetch_desc(&p.tv);
+  }
+  __syncthreads();
+  pdl_wait_primary();
+
+  // packed rows of no sequence are zero
+  {
+    const int used = p.b.n_seqs > 0 ? min(max(p.b.q_start[p.b.n_seqs], 0), p.b.n_tokens) : 0;
+    const int64_t rows = static_cast<int64_t>(p.b.n_tokens - used) * p.heads;
+    constexpr int V = D / 8;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * V;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+      const int64_t r = i / V;
+      const int64_t t = used + r / p.heads;
+      const int h = static_cast<int>(r % p.heads);
+      *reinterpret_cast<uint4*>(p.o.p + t * p.o.ts + h * p.o.hs + (i % V) * 8) = make_uint4(0, 0, 0, 0);
+      if (p.lse != nullptr && i % V == 0) p.lse[t * p.heads + h] = -INFINITY;
+    }
+  }
+
+  DecWalk w;
+  if (!dec_begin(p, w, lane)) return;
+
+  if (warp == kDecWarps) {
+    // ===== copying warp =====
+    fence_proxy_async_global();
+    int slot = 0;
+    uint32_t phase = 0;
+    bool stop = false;
+    do {
+      const int units = (w.s.len + kDecUnit - 1) / kDecUnit;       // units that hold a token
+      const int u0 = w.t0 * (kDecTile / kDecUnit), u1 = w.t1 * (kDecTile / kDecUnit);
+      const int32_t* table = p.b.page_table + w.b * p.b.table_stride;
+      auto page_of = [&](int u) {
+        return u < min(units, u1) ? table[(u * kDecUnit) >> p.page_shift] : 0;
+      };
+      int pages = page_of(u0 + lane);
+      for (int c = u0; c < u1 && !stop; c += 32) {
+        const int now = pages;
+        pages = page_of(c + 32 + lane);
+        if (now < 0 || now >= p.num_pages) record_status(p.status, EPILORA_ERR_INVALID_ARG);
+        const int n = min(32, u1 - c);
+        for (int i = 0; i < n; ++i) {
+          const int u = c + i;
+          const int pg = __shfl_sync(0xffffffffu, now, i);
+          // the whole warp waits, so that it is together again when one lane
+          // issues the copies
+          const bool ok = !*abort_flag && mbar_wait_bounded(&empty[slot], phase ^ 1u, kWaitLimitNs);
+          if (!__all_sync(0xffffffffu, ok)) {
+            stop = true;
+            break;
+          }
+          if (lane == 0) {
+            if (u < units) {
+              uint8_t* dst = smem + slot * C::kUnitBytes;
+              const int row = (u * kDecUnit) & (p.page_size - 1);
+              mbar_arrive_expect_tx(&full[slot], C::kUnitBytes);
+#pragma unroll
+              for (int x = 0; x < C::kBoxes; ++x) {
+                // a page index out of range reads as zeros
+                tma_load_4d(dst + x * C::kBox, &p.tk, &full[slot], x * C::kBoxBytes, row, w.h, pg);
+                tma_load_4d(dst + C::kHalf + x * C::kBox, &p.tv, &full[slot], x * C::kBoxBytes, row, w.h, pg);
+              }
+            } else {
+              mbar_arrive(&full[slot]);
+            }
+          }
+          __syncwarp();
+          if (++slot == C::kSlots) slot = 0, phase ^= 1u;
+        }
+      }
+    } while (!stop && dec_next(p, w));
+    if (stop) {
+      *abort_flag = 1;
+      record_status(p.status, EPILORA_ERR_TIMEOUT);
+    }
+    if (lane == 0) {
+      // no copy in flight at exit (only after a wait that ran out is there
+      // one that no computing warp has waited for): wait for the slots'
+      // latest phases
+      if (*abort_flag) {
+        for (int i = 0; i < C::kSlots; ++i) {
+          const uint32_t ph = i < slot ? phase : phase ^ 1u;
+          (void)mbar_wait_bounded(&full[i], ph, 1000000ull);
+        }
+      }
+    }
+    return;
+  }
+
+  // ===== computing warps =====
+  const int g = lane >> 2, q = lane & 3;
+  const int tid = threadIdx.x;
+  int slot = warp;
+  uint32_t phase = 0;
+  bool dead = false;
+  do {
+    const int n = w.s.n, rows = n * p.group;
+    // the thread's two rows: token i, head, positions it sees
+    const int r0 = g, r1 = g + 8;
+    const int i0 = r0 / p.group, i1 = r1 / p.group;
+    const bool ok0 = r0 < rows, ok1 = r1 < rows;
+    const int see0 = ok0 ? max(min(w.s.base + i0 + 1, w.s.len), 0) : 0;
+    const int see1 = ok1 ? max(min(w.s.base + i1 + 1, w.s.len), 0) : 0;
+    const int see_all = max(min(w.s.base + 1, w.s.len), 0);    // positions every row sees
+    float s_eff = p.scale;
+    if (E4) s_eff *= p.k_scale[w.h];
+    const uint32_t flip = s_eff < 0.0f ? 0x80008000u : 0u;
+    float c0 = s_eff == 0.0f ? 1.0f : fabsf(s_eff) * kLog2e, c1 = c0;
+
+    // Q fragments
+    uint32_t qa[D / 16][4];
+    {
+      const __nv_bfloat16* q0 = p.q.p + (w.s.first + i0) * p.q.ts + (w.h * p.group + r0 % p.group) * p.q.hs;
+      const __nv_bfloat16* q1 = p.q.p + (w.s.first + i1) * p.q.ts + (w.h * p.group + r1 % p.group) * p.q.hs;
+      const bool zero = s_eff == 0.0f;
+      if (!E4) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int d = ks * 16 + 2 * q;
+          qa[ks][0] = ok0 && !zero ? *reinterpret_cast<const uint32_t*>(q0 + d) ^ flip : 0u;
+          qa[ks][1] = ok1 && !zero ? *reinterpret_cast<const uint32_t*>(q1 + d) ^ flip : 0u;
+          qa[ks][2] = ok0 && !zero ? *reinterpret_cast<const uint32_t*>(q0 + d + 8) ^ flip : 0u;
+          qa[ks][3] = ok1 && !zero ? *reinterpret_cast<const uint32_t*>(q1 + d + 8) ^ flip : 0u;
+        }
+      } else {
+        // fp16 queries: bf16's 8 significant bits fit; each row is scaled by
+        // the power of two that puts its largest element near 2^13 (elements
+        // 2^27 below that are still exact, the rest is off by 2^-38 of the
+        // largest), the scores' factor takes it back
+        uint4 raw[2][D / 64][2];
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d = 64 * c + 16 * q + 8 * e;
+            raw[0][c][e] = ok0 && !zero ? *reinterpret_cast<const uint4*>(q0 + d) : make_uint4(0, 0, 0, 0);
+            raw[1][c][e] = ok1 && !zero ? *reinterpret_cast<const uint4*>(q1 + d) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float big = 0.0f;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4 v = raw[r][c][e];
+              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+            }
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          // 2^(13 - exponent), within the normal range; 1 for rows of zeros
+          // or with an infinity
+          const int ex = static_cast<int>((__float_as_uint(big) >> 23) & 0xFF);
+          const int up = big == 0.0f || ex == 0xFF ? 0 : min(13 - (ex - 127), 126);
+          const float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+          (r == 0 ? c0 : c1) *= up == 0 ? 1.0f : __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint4 v = raw[r][c][j >> 1];
+              const uint32_t a = (j & 1) ? v.z : v.x, b = (j & 1) ? v.w : v.y;
+              qa[4 * c + j][r] = pack16<true>(bf16_lo(a) * f, bf16_hi(a) * f) ^ flip;
+              qa[4 * c + j][2 + r] = pack16<true>(bf16_lo(b) * f, bf16_hi(b) * f) ^ flip;
+            }
+        }
+      }
+    }
+
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+
+    for (int t = w.t0; t < w.t1; ++t) {
+      const int at = t * kDecTile + warp * kDecUnit;
+      if (!dead && (*abort_flag || !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs))) {
+        *abort_flag = 1;
+        record_status(p.status, EPILORA_ERR_TIMEOUT);
+        dead = true;
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      if (!dead && at < w.s.len) {
+        uint8_t* ks = smem + slot * C::kUnitBytes;
+        uint8_t* vs = ks + C::kHalf;
+        // rows of the page that hold no token of this sequence
+        if (at + kDecUnit > w.s.len) dec_zero_rows<D, E4>(vs, w.s.len - at, lane);
+        float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        if (!E4) {
+          const uint32_t base = smem_u32(ks);
+          const uint32_t tok = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t d = k * 16 + ((lane >> 3) & 1) * 8;
+            uint32_t r[4];
+            ldmatrix_x4(r, base + (d / 64) * C::kBox + swz<C::kBoxBytes>(tok, (d % 64) * 2));
+            mma16<E4>(s[0], qa[k], r[0], r[1]);
+            mma16<E4>(s[1], qa[k], r[2], r[3]);
+          }
+        } else {
+          // thread (g, q): elements 64 c + 16 q .. + 15 of token g (and g + 8);
+          // step j of a c contracts elements 4 j .. 4 j + 3 of each thread
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const uint4 v = *reinterpret_cast<const uint4*>(ks + swz<C::kBoxBytes>(nt * 8 + g, 64 * c + 16 * q));
+              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma16<E4>(s[nt], qa[4 * c + j], e4m3x2_to_f16x2(x[j]), e4m3x2_to_f16x2(x[j] >> 16));
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          s[nt][0] *= c0, s[nt][1] *= c0;
+          s[nt][2] *= c1, s[nt][3] *= c1;
+        }
+        const bool edge = at + kDecUnit > see_all;
+        if (edge) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int pos = at + nt * 8 + 2 * q + e;
+              if (pos >= see0) s[nt][e] = -INFINITY;
+              if (pos >= see1) s[nt][2 + e] = -INFINITY;
+            }
+        }
+        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+        const bool up0 = x0 > m0 + kRaise, up1 = x1 > m1 + kRaise;
+        if (__any_sync(0xffffffffu, up0 || up1)) {
+          const float f0 = up0 ? exp2_approx(m0 - x0) : 1.0f, f1 = up1 ? exp2_approx(m1 - x1) : 1.0f;
+          if (up0) m0 = x0;
+          if (up1) m1 = x1;
+          l0 *= f0;
+          l1 *= f1;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) acc[i][0] *= f0, acc[i][1] *= f0, acc[i][2] *= f1, acc[i][3] *= f1;
+        }
+        const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          s[nt][0] = exp2_approx(s[nt][0] - b0), s[nt][1] = exp2_approx(s[nt][1] - b0);
+          s[nt][2] = exp2_approx(s[nt][2] - b1), s[nt][3] = exp2_approx(s[nt][3] - b1);
+        }
+        l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
+        l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
+        // the weights as 16-bit operands (each within 2^-9 of itself, 2^-11 in fp16)
+        const uint32_t pa[4] = {pack16<E4>(s[0][0], s[0][1]), pack16<E4>(s[0][2], s[0][3]),
+                                pack16<E4>(s[1][0], s[1][1]), pack16<E4>(s[1][2], s[1][3])};
+        // A zero weight times a NaN or an infinity is NaN: where a position
+        // is hidden from some rows and holds one, each token's rows take
+        // their own product, the later positions zeroed from the last token
+        // to the first.
+        if (edge && n > 1 && dec_rows_nonfinite<D, E4>(vs, max(see_all - at, 0), min(kDecUnit, w.s.len - at), lane)) {
+          for (int i = n - 1; i >= 0; --i) {
+            const int see = max(min(w.s.base + i + 1, w.s.len), 0) - at;
+            if (see < kDecUnit) dec_zero_rows<D, E4>(vs, max(see, 0), lane);
+            dec_pv<D, E4, true>(acc, pa, vs, lane, ok0 && i0 == i, ok1 && i1 == i);
+          }
+        } else {
+          dec_pv<D, E4, false>(acc, pa, vs, lane, true, true);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      slot += kDecWarps;
+      if (slot >= C::kSlots) slot -= C::kSlots, phase ^= 1u;
+    }
+
+    // ===== the four warps meet =====
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (q == 0) {
+      ml[(warp * kDecRows + r0) * 2] = m0, ml[(warp * kDecRows + r0) * 2 + 1] = l0;
+      ml[(warp * kDecRows + r1) * 2] = m1, ml[(warp * kDecRows + r1) * 2 + 1] = l1;
+    }
+    meet_barrier();
+    float f[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = r == 0 ? r0 : r1;
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kDecWarps; ++k) top = fmaxf(top, ml[(k * kDecRows + row) * 2]);
+      const float base = top == -INFINITY ? 0.0f : top;
+      f[r] = exp2_approx((r == 0 ? m0 : m1) - base);
+      if (warp == 0 && q == 0) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kDecWarps; ++k)
+          sum += ml[(k * kDecRows + row) * 2 + 1] * exp2_approx(ml[(k * kDecRows + row) * 2] - base);
+        row_m[row] = top;
+        row_l[row] = sum;
+      }
+    }
+    float* mine = meet + warp * kDecRows * C::kOld;
+#pragma unroll
+    for (int nt = 0; nt < D / 8; ++nt) {
+      // columns 2q and 2q + 1 of n-tile nt
+      const int d0 = E4 ? 2 * q * (D / 8) + nt : nt * 8 + 2 * q;
+      const int d1 = E4 ? d0 + D / 8 : d0 + 1;
+      if (ok0) mine[r0 * C::kOld + d0] = acc[nt][0] * f[0], mine[r0 * C::kOld + d1] = acc[nt][1] * f[0];
+      if (ok1) mine[r1 * C::kOld + d0] = acc[nt][2] * f[1], mine[r1 * C::kOld + d1] = acc[nt][3] * f[1];
+    }
+    meet_barrier();
+
+    const float vscale = E4 ? p.v_scale[w.h] : 1.0f;
+    auto put = [&](int row, int d, float o0, float o1, float m, float l) {
+      const int i = row / p.group, h = w.h * p.group + row % p.group;
+      const int64_t tok = w.s.first + i;
+      const float inv = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);
+      const uint32_t v = l == 0.0f ? 0u : pack16<false>(o0 * inv, o1 * inv);
+      *reinterpret_cast<uint32_t*>(p.o.p + tok * p.o.ts + h * p.o.hs + d) = v;
+      if (p.lse != nullptr && d == 0)
+        p.lse[tok * p.heads + h] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    };
+    const bool whole = w.t0 == 0 && w.t1 == w.s.tiles;
+    constexpr int kPart = 2 * kDecRows + kDecRows * D;   // floats of a partial result: m, l, O
+    // slot of a block's piece: 0 where it starts the block's range, else 1
+    const uint64_t range0 = blockIdx.x * w.total / w.ctas;
+    float* part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (w.x == range0 ? 0 : 1)) * kPart;
+    for (int e = tid; e < rows * (D / 2); e += kDecWarps * 32) {
+      const int row = e / (D / 2), d = 2 * (e % (D / 2));
+      float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < kDecWarps; ++k) {
+        const float2 v = *reinterpret_cast<const float2*>(meet + (k * kDecRows + row) * C::kOld + d);
+        o.x += v.x;
+        o.y += v.y;
+      }
+      if (whole)
+        put(row, d, o.x, o.y, row_m[row], row_l[row]);
+      else
+        *reinterpret_cast<float2*>(part + 2 * kDecRows + row * D + d) = o;
+    }
+    if (!whole) {
+      if (tid < kDecRows) part[tid] = row_m[tid], part[kDecRows + tid] = row_l[tid];
+      // the blocks that hold the pair's first and last tile
+      const int first = static_cast<int>(((w.pair0 + 1) * w.ctas - 1) / w.total);
+      const int last = static_cast<int>(((w.pair0 + w.s.tiles) * w.ctas - 1) / w.total);
+      const int pieces = last - first + 1;
+      __threadfence();
+      meet_barrier();
+      if (tid == 0) {
+        const uint32_t before = atomicAdd(p.counters + first, 1u);
+        const int is_last = before == static_cast<uint32_t>(pieces - 1);
+        if (is_last) p.counters[first] = 0;
+        *last_flag = is_last;
+      }
+      meet_barrier();
+      if (*last_flag) {
+        __threadfence();
+        // the first piece starts its block's range, or follows other pairs in it
+        const bool at_start = first * w.total / w.ctas == w.pair0;
+        auto piece = [&](int k) {
+          const int64_t s = k == 0 ? 2 * static_cast<int64_t>(first) + (at_start ? 0 : 1)
+                                   : 2 * static_cast<int64_t>(first + k);
+          return p.partials + s * kPart;
+        };
+        // weights of the pieces per row: 8 threads a row
+        {
+          const int row = tid >> 3, sub = tid & 7;
+          float top = -INFINITY;
+          for (int k = sub; k < pieces; k += 8) top = fmaxf(top, __ldcg(piece(k) + row));
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float base = top == -INFINITY ? 0.0f : top;
+          for (int k = sub; k < pieces; k += 8) meet[k * kDecRows + row] = exp2_approx(__ldcg(piece(k) + row) - base);
+          if (sub == 0) row_m[row] = top;
+        }
+        meet_barrier();
+        if (tid < kDecRows) {
+          float sum = 0.0f;
+          for (int k = 0; k < pieces; ++k) sum += __ldcg(piece(k) + kDecRows + tid) * meet[k * kDecRows + tid];
+          row_l[tid] = sum;
+        }
+        meet_barrier();
+        for (int e = tid; e < rows * (D / 2); e += kDecWarps * 32) {
+          const int row = e / (D / 2), d = 2 * (e % (D / 2));
+          float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+          for (int k = 0; k < pieces; ++k) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(piece(k) + 2 * kDecRows + row * D + d));
+            const float f2 = meet[k * kDecRows + row];
+            o.x += v.x * f2;
+            o.y += v.y * f2;
+          }
+          put(row, d, o.x, o.y, row_m[row], row_l[row]);
+        }
+      }
+    }
+    meet_barrier();   // the meeting buffer is free again
+  } while (dec_next(p, w));
+}
+
+template <int D, bool E4>
+int launch(const AttnArgs& a, DecParams& p, int grid) {
+  using C = DecCfg<D, E4>;
+  const epilora_kv_cache& c = a.cache;
+  const uint64_t es = E4 ? 1 : 2;
+  const uint64_t dims[4] = {static_cast<uint64_t>(C::kRowBytes), static_cast<uint64_t>(c.page_size),
+                            static_cast<uint64_t>(c.kv_heads), static_cast<uint64_t>(c.num_pages)};
+  const uint32_t box[4] = {static_cast<uint32_t>(C::kBoxBytes), kDecUnit, 1, 1};
+  const uint64_t ks[3] = {c.k_token_stride * es, c.k_head_stride * es, c.k_page_stride * es};
+  const uint64_t vs[3] = {c.v_token_stride * es, c.v_head_stride * es, c.v_page_stride * es};
+  int rc = make_tma_4d_u8(&p.tk, c.k, dims, ks, box, C::kBoxBytes);
+  if (rc == EPILORA_OK) rc = make_tma_4d_u8(&p.tv, c.v, dims, vs, box, C::kBoxBytes);
+  if (rc != EPILORA_OK) return rc;
+  auto kern = attn_decode_kernel<D, E4>;
+  static int attr_done[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EPILORA_ERR_CUDA;
+  if (!attr_done[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+      return EPILORA_ERR_CUDA;
+    attr_done[dev] = 1;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kDecThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? EPILORA_OK : EPILORA_ERR_CUDA;
+}
+
+int dec_ctas() {
+  const int n = 2 * num_sms();
+  return n < kDecMaxCtas ? n : kDecMaxCtas;
+}
+
+}  // namespace
+
+size_t attn_decode_counter_bytes() { return kDecMaxCtas * sizeof(uint32_t); }
+size_t attn_decode_partial_bytes(int head_dim) {
+  return static_cast<size_t>(2 * dec_ctas()) * (2 * kDecRows + kDecRows * head_dim) * sizeof(float);
+}
+bool attn_decode_takes(int n, int group) { return n <= kDecRows / group; }
+
+int launch_attn_decode(const AttnArgs& a, uint32_t* counters, float* partials) {
+  DecParams p{};
+  p.b = a.batch;
+  p.q = a.q;
+  p.o = a.o;
+  p.lse = a.lse;
+  p.heads = a.heads;
+  p.kv_heads = a.cache.kv_heads;
+  p.group = a.heads / a.cache.kv_heads;
+  p.page_shift = __builtin_ctz(a.cache.page_size);
+  p.page_size = a.cache.page_size;
+  p.num_pages = a.cache.num_pages;
+  p.scale = a.scale;
+  p.k_scale = a.cache.k_scale;
+  p.v_scale = a.cache.v_scale;
+  p.counters = counters;
+  p.partials = partials;
+  p.status = a.status;
+  // no more blocks than tiles there can be
+  const int64_t cap = static_cast<int64_t>(a.batch.table_pages) * a.cache.page_size;
+  const int64_t most = a.batch.n_seqs * (a.cache.kv_heads * ((cap + kDecTile - 1) / kDecTile + 1));
+  const int grid = static_cast<int>(most < 1 ? 1 : (most < dec_ctas() ? most : dec_ctas()));
+  const bool e4 = a.cache.kv_fmt == EPILORA_KV_E4M3;
+  if (a.cache.head_dim == 64) return e4 ? launch<64, true>(a, p, grid) : launch<64, false>(a, p, grid);
+  return e4 ? launch<128, true>(a, p, grid) : launch<128, false>(a, p, grid);
+}
+
+}  // namespace epi

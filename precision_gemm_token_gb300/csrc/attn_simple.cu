@@ -27,6 +27,7 @@ __global__ void attn_simple_kernel(const __grid_constant__ SimpleParams sp) {
   if (b < p.batch.n_seqs) {
     const SeqRows s = seq_rows(p.batch.q_start, b, p.batch.n_tokens, bad);
     first = s.first;
+    if (p.paged && s.n <= 16 / (p.heads / p.cache.kv_heads)) return;
     if (p.paged) {
       const int len = __ldg(p.batch.kv_len + b);
       seen = len - s.n + (t - s.first) + 1;
@@ -98,9 +99,7 @@ __global__ void attn_simple_kernel(const __grid_constant__ SimpleParams sp) {
 
 }  // namespace
 
-size_t attn_workspace_bytes(int) { return 256; }
-
-int launch_attn(const AttnArgs& a) {
+int launch_attn_simple(const AttnArgs& a) {
   SimpleParams p{a, a.paged ? __builtin_ctz(a.cache.page_size) : 0};
   const dim3 grid(a.batch.n_tokens, (a.heads + 3) / 4);
   if (a.cache.head_dim == 64)

@@ -178,6 +178,12 @@ int make_tma_2d_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t c
 int make_tma_2d_swz(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols_bytes, uint64_t pitch_bytes,
                     uint32_t box_rows, uint32_t box_cols, int swizzle_span);
 
+// Encodes a 4D tiled TMA descriptor of bytes: dims[0] is the inner extent in
+// bytes, strides_bytes[i] the pitch of dimension i + 1 (multiples of 16),
+// swizzled over `swizzle_span` bytes (64 or 128).
+int make_tma_4d_u8(CUtensorMap* map, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides_bytes)[3],
+                   const uint32_t (&box)[4], int swizzle_span);
+
 // Once per device: prefer the largest shared-memory carveout for a small
 // kernel, so that the SMs it lands on keep room for the GEMM's CTAs beside it.
 int prefer_max_shared(const void* func, int* done_flags);

@@ -35,7 +35,7 @@ struct AppendParams {
 // tokens count like any other.
 __device__ __forceinline__ int find_seq(const int32_t* q_start, int n_seqs, int t, int lane) {
   int n = 0;
-  for (int i = lane; i < n_seqs; i += 32) n += __ldg(q_start + i + 1) <= t;
+  for (int i = lane; i < n_seqs; i += 32) n += q_start[i + 1] <= t;
   return __reduce_add_sync(0xffffffffu, n);
 }
 
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const __grid_constant__
       if (b < p.b.n_seqs) {
         bool bad = false;
         const SeqRows s = seq_rows(p.b.q_start, b, p.b.n_tokens, bad);
-        const int len = __ldg(p.b.kv_len + b);
+        const int len = p.b.kv_len[b];
         pos = len - s.n + (t - s.first);
         const int at = pos >> p.page_shift;
         row_in_page = pos & (p.c.page_size - 1);
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const __grid_constant__
           if (at >= p.b.table_pages || (rot_units > 0 && pos >= p.n_pos)) {
             bad = true;
           } else {
-            const int pg = __ldg(p.b.page_table + b * p.b.table_stride + at);
+            const int pg = p.b.page_table[b * p.b.table_stride + at];
             if (pg < 0 || pg >= p.c.num_pages)
               bad = true;
             else
@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const __grid_constant__
       float c[8], s[8];
 #pragma unroll
       for (int j = 0; j < 8; j += 4) {
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(row + j));
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + j));
+        const float4 cv = *reinterpret_cast<const float4*>(row + j);
+        const float4 sv = *reinterpret_cast<const float4*>(row + half + j);
         c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
         s[j] = sv.x, s[j + 1] = sv.y, s[j + 2] = sv.z, s[j + 3] = sv.w;
       }
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const __grid_constant__
         *reinterpret_cast<uint4*>(o + e1) = v1;
       } else {
         uint8_t* o = static_cast<uint8_t*>(is_k ? p.c.k : p.c.v) + at;
-        const float s = __ldg((is_k ? p.c.k_scale : p.c.v_scale) + h);
+        const float s = (is_k ? p.c.k_scale : p.c.v_scale)[h];
         *reinterpret_cast<uint2*>(o + e0) = codes8(x0, s);
         *reinterpret_cast<uint2*>(o + e1) = codes8(x1, s);
       }

@@ -94,14 +94,19 @@ class Batch:
         return A.paged_attention(q, self.cache, start, length, table, **kw)
 
 
-def out_bound(o, mean_abs, mag):
-    """|O - o| allowed: the output's rounding to bf16 (2^-9 of it), the
-    weights' rounding to bf16 (2^-9 of the weighted mean of |v|), and the fp32
-    scores: each of up to 128 products and sums within 2^-24 of the score's
-    magnitude, 2^-17 of it in all, which moves a weight by as much relative
-    to the others on both sides of the quotient (2^-16), besides 2^-14 for
-    the exponentials and the fp32 sums of up to 2^9 roundings."""
-    return 2.0 ** -9 * np.abs(o) + (2.0 ** -9 + 2.0 ** -16 * mag[..., None] + 2.0 ** -14) * mean_abs + 1e-30
+# unit roundoffs: bf16 has 8 significant bits (1 + 2^-8 lies halfway between
+# the neighbours 1 and 1 + 2^-7), fp16 has 11
+BF16_U, FP16_U = 2.0 ** -8, 2.0 ** -11
+
+
+def out_bound(o, mean_abs, mag, weight_u):
+    """|O - o| allowed: the output's rounding to bf16, the weights' rounding
+    to the tensor cores' operand type (weight_u of the weighted mean of |v|),
+    and the fp32 scores: each of up to 128 products and sums within 2^-24 of
+    the score's magnitude, 2^-17 of it in all, which moves a weight by as much
+    relative to the others on both sides of the quotient (2^-16), besides
+    2^-14 for the exponentials and the fp32 sums of up to 2^9 roundings."""
+    return BF16_U * np.abs(o) + (weight_u + 2.0 ** -16 * mag[..., None] + 2.0 ** -14) * mean_abs + 1e-30
 
 
 def lse_bound(lse, mag):
@@ -110,8 +115,8 @@ def lse_bound(lse, mag):
     return 2.0 ** -17 * mag + 2.0 ** -14 + 2.0 ** -20 * np.abs(np.where(np.isfinite(lse), lse, 0.0))
 
 
-def assert_attention(o_gpu, lse_gpu, o, lse, mean_abs, mag, what=""):
-    got, bound = f64(o_gpu), out_bound(o, mean_abs, mag)
+def assert_attention(o_gpu, lse_gpu, o, lse, mean_abs, mag, what="", fmt="bf16"):
+    got, bound = f64(o_gpu), out_bound(o, mean_abs, mag, FP16_U if fmt == "e4m3" else BF16_U)
     err = np.abs(got - o)
     assert np.isfinite(got).all(), (what, np.argwhere(~np.isfinite(got))[:5])
     assert (err <= bound).all(), (what, np.argwhere(err > bound)[:5], float((err / bound).max()))

@@ -26,7 +26,7 @@ def check(b: Batch, scale=None, what="", **kw):
     o = b.attend(scale=scale, lse=lse, out=out, status=st, **kw)
     assert int(st.item()) == 0
     scale = b.dim ** -0.5 if scale is None else scale
-    assert_attention(o, lse, *b.oracle(scale), what=what)
+    assert_attention(o, lse, *b.oracle(scale), what=what, fmt=b.fmt)
     return o
 
 
@@ -52,6 +52,20 @@ def test_decode_long_split(fmt):
     """One sequence alone on the GPU: split along its length and joined."""
     check(Batch([(1, 9001)], 8, 2, 128, fmt=fmt, seed=3))
     check(Batch([(1, 4099), (1, 3), (1, 0), (1, 2500)], 4, 1, 64, fmt=fmt, page=64, seed=4))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_decode_long_line(fmt, dim):
+    """More positions than SMs by far: every thread block goes round its ring
+    many times, over several sequences and heads; repeated, since the order
+    in which copies land changes from run to run."""
+    seqs = [(1, 4096), (1, 17), (1, 3001), (1, 64)] + [(1, 2500 + 37 * i) for i in range(10)]
+    b = Batch(seqs, 8, 8, dim, fmt=fmt, seed=dim, page=64)
+    first = check(b)
+    ws = A.AttentionWorkspace("cuda")
+    for _ in range(50):
+        assert torch.equal(b.attend(workspace=ws), first)
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
@@ -157,7 +171,7 @@ def test_masked_positions_do_not_reach_earlier_rows(fmt, n, heads, which, bad):
     o = b.attend(status=st)
     assert int(st.item()) == 0
     keep = np.r_[0:n - 1, n:n + 1]
-    assert_attention(o[torch.from_numpy(keep).cuda()], None, *(x[keep] for x in clean))
+    assert_attention(o[torch.from_numpy(keep).cuda()], None, *(x[keep] for x in clean), fmt=fmt)
     assert not torch.isfinite(o[n - 1]).all()    # the row that sees it shows it
 
 

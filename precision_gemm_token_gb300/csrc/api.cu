@@ -133,7 +133,8 @@ int make_tma_4d_u8(CUtensorMap* map, const void* base, const uint64_t (&dims)[4]
                    const uint32_t (&box)[4], int swizzle_span) {
   EncodeTiledFn fn = get_encode_fn();
   if (fn == nullptr) return EPILORA_ERR_CUDA;
-  if (!al16(base) || (swizzle_span != 64 && swizzle_span != 128) || box[0] > static_cast<uint32_t>(swizzle_span))
+  if (!al16(base) || (swizzle_span != 0 && swizzle_span != 64 && swizzle_span != 128) ||
+      (swizzle_span != 0 && box[0] > static_cast<uint32_t>(swizzle_span)))
     return EPILORA_ERR_INVALID_ARG;
   std::memset(map, 0, sizeof(*map));
   cuuint64_t d[4], st[3];
@@ -150,7 +151,10 @@ int make_tma_4d_u8(CUtensorMap* map, const void* base, const uint64_t (&dims)[4]
   }
   const CUresult r =
       fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), d, st, b, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+         CU_TENSOR_MAP_INTERLEAVE_NONE,
+         swizzle_span == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+         : swizzle_span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                              : CU_TENSOR_MAP_SWIZZLE_NONE,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? EPILORA_OK : EPILORA_ERR_CUDA;
 }

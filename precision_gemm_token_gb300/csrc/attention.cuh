@@ -47,10 +47,15 @@ size_t attn_workspace_bytes(int head_dim);
 
 // attn_decode.cu: the sequences whose new tokens n satisfy
 // attn_decode_takes(n, group), and the packed rows of no sequence.
-bool attn_decode_takes(int n, int group);
+__host__ __device__ inline bool attn_decode_takes(int n, int group) { return n <= 16 / group; }
 int launch_attn_decode(const AttnArgs& a, uint32_t* counters, float* partials);
 size_t attn_decode_counter_bytes();
 size_t attn_decode_partial_bytes(int head_dim);
+// attn_tile.cu: the other sequences of a call over the cache; all of a call
+// over packed prompts, and its packed rows of no prompt.
+int launch_attn_tile(const AttnArgs& a, uint32_t* counters, float* partials);
+size_t attn_tile_counter_bytes();
+size_t attn_tile_partial_bytes(int head_dim);
 
 // Batch metadata may be written by the previous kernel on the stream, so it is
 // read with ordinary loads: the compiler takes read-only loads for invariant

@@ -23,6 +23,9 @@ bool heads_ok(int heads, int kv_heads, int head_dim) {
   return kv_heads >= 1 && heads >= 1 && heads % kv_heads == 0 && heads <= 65536 && head_dim >= 1;
 }
 
+// the kernels count a sequence's (token, head) rows in 31 bits
+bool rows_fit(int tokens, int heads) { return static_cast<int64_t>(tokens) * heads < (int64_t{1} << 30); }
+
 int cache_check(const epilora_kv_cache* c, int heads) {
   if (c == nullptr || c->reserved != 0) return EPILORA_ERR_INVALID_ARG;
   if (c->kv_fmt != EPILORA_KV_BF16 && c->kv_fmt != EPILORA_KV_E4M3) return EPILORA_ERR_INVALID_ARG;
@@ -124,6 +127,7 @@ EPILORA_API int epilora_paged_attention(const epilora_kv_cache* cache, const epi
   if (!std::isfinite(scale)) return EPILORA_ERR_INVALID_ARG;
   const int T = batch->n_tokens, D = cache->head_dim;
   if (T == 0) return EPILORA_OK;
+  if (!rows_fit(T, heads)) return EPILORA_ERR_UNSUPPORTED;
   if (!rows_ok(Q, q_token_stride, q_head_stride, T, heads, D) ||
       !rows_ok(O, o_token_stride, o_head_stride, T, heads, D) || !al(lse, 4))
     return EPILORA_ERR_INVALID_ARG;
@@ -154,6 +158,7 @@ EPILORA_API int epilora_prompt_attention(int n_seqs, int n_tokens, const int32_t
     return EPILORA_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return EPILORA_ERR_UNSUPPORTED;
   if (n_tokens == 0) return EPILORA_OK;
+  if (!rows_fit(n_tokens, heads)) return EPILORA_ERR_UNSUPPORTED;
   if (q_start == nullptr || !al(q_start, 4)) return EPILORA_ERR_INVALID_ARG;
   if (!rows_ok(Q, q_token_stride, q_head_stride, n_tokens, heads, head_dim) ||
       !rows_ok(K, k_token_stride, k_head_stride, n_tokens, kv_heads, head_dim) ||

@@ -90,7 +90,7 @@ __device__ __forceinline__ DecSeq dec_seq(const DecParams& p, int b, bool& bad) 
   s.n = r.n;
   s.base = len - r.n;
   s.len = max(min(len, cap), 0);
-  s.tiles = r.n > 0 && r.n <= kDecRows / p.group ? max((s.len + kDecTile - 1) / kDecTile, 1) : 0;
+  s.tiles = r.n > 0 && attn_decode_takes(r.n, p.group) ? max((s.len + kDecTile - 1) / kDecTile, 1) : 0;
   return s;
 }
 
@@ -773,7 +773,6 @@ size_t attn_decode_counter_bytes() { return kDecMaxCtas * sizeof(uint32_t); }
 size_t attn_decode_partial_bytes(int head_dim) {
   return static_cast<size_t>(2 * dec_ctas()) * (2 * kDecRows + kDecRows * head_dim) * sizeof(float);
 }
-bool attn_decode_takes(int n, int group) { return n <= kDecRows / group; }
 
 int launch_attn_decode(const AttnArgs& a, uint32_t* counters, float* partials) {
   DecParams p{};

@@ -1,0 +1,1022 @@
+// Attention of chunks of new tokens over the paged cache, and of whole packed
+// prompts, on the tensor cores (tcgen05).
+//
+//   S = Q K^T,  P = exp2(c S - c m),  O += P V,  l += sum P,  c = scale log2 e
+//
+// The rows of a key/value head are its group's heads of consecutive new
+// tokens (row = token * G + head), cut into tiles of 2 x 128; the keys and
+// values into tiles of 128 positions. Per row tile and position tile the two
+// products are 4 x 128 x 128 x head_dim fused multiply-adds, 2048 cycles of
+// the SM's tensor pipe at head_dim 128, against 2 x 128 x 128 exponentials:
+// the tensor pipe bounds it as long as the softmax of one half runs while the
+// products of the other half do.
+//
+// One thread block per SM, twelve warps:
+//   0-3, 4-7  two softmax groups, one per 128 rows ("stream"): a thread owns a
+//             row, reads its scores from TMEM, keeps the row's maximum and
+//             sum in registers, writes the weights back over the scores
+//             (16-bit, the A operand of the second product) and, where the
+//             maximum rose by more than 2^8, rescales the row of O in TMEM
+//   8         copies key and value tiles into a ring of shared memory by TMA
+//   9         issues the products; S and O of both streams fill the TMEM
+//   10 (11)   bf16: clean the value rows that some row must not see;
+//             E4M3: convert the copied codes to fp16 tiles
+// Where an item has at most 128 rows both streams take the same rows and
+// alternate the position tiles; they meet at the end.
+//
+// The position tiles of all (sequence, head, row tile) items form one line
+// that is split evenly over the blocks, whatever the lengths; an item cut
+// between blocks is joined by the block that finishes last, in the order of
+// the pieces.
+#include "attention.cuh"
+#include "ptx.cuh"
+
+namespace epi {
+namespace {
+
+constexpr int kTileThreads = 384;
+constexpr int kPosTile = 128;      // positions per tile
+constexpr int kRowTile = 128;      // rows per stream
+constexpr int kItemRows = 2 * kRowTile;
+constexpr int kTileMaxCtas = 512;
+constexpr int kGroups = 128;       // entries of the block's table of sequence weights
+constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
+// a row's maximum is raised (and its sums rescaled) only when a score exceeds
+// it by this many powers of two: weights stay below 2^8, in range for the
+// 16-bit operands, and after a few tiles nothing is rescaled any more
+constexpr float kRaise = 8.0f;
+
+template <int D, bool E4>
+struct TileCfg {
+  static constexpr int kTileBytes = kPosTile * D * 2;            // 16-bit key or value tile
+  static constexpr int kBlock = 128 * 128;                       // 128 rows of 64 elements, swizzled
+  static constexpr int kQBytes = 2 * kTileBytes;
+  static constexpr int kStages = E4 ? 3 : 160 * 1024 / kTileBytes;
+  static constexpr int kRawBytes = kPosTile * D;                 // E4M3 codes of a tile
+  static constexpr int kRawStages = E4 ? 4 : 0;
+  static constexpr int kRing = kQBytes, kRaw = kRing + kStages * kTileBytes;
+  static constexpr int kPlan = kRaw + kRawStages * kRawBytes;
+  static constexpr int kBars = kPlan + kGroups * 8;
+  static constexpr int kBytes = kBars + 512;
+  static constexpr int kSmem = 1024 + kBytes;
+};
+
+struct TileParams {
+  CUtensorMap tk, tv;
+  epilora_kv_batch b;
+  epilora_kv_cache c;      // paged
+  AttnRows q, k, v;        // k, v: prompts
+  AttnOut o;
+  float* lse;
+  int paged;
+  int heads, kv_heads, group;
+  int page_shift;
+  int box_rows;            // rows per TMA box
+  float scale;
+  uint32_t* counters;      // [2 gridDim.x], zero between calls
+  float4* partials;        // [2 gridDim.x][(2 + D) * 256 / 4]
+  int* status;
+};
+
+struct TileSeq {
+  int first, n, len, base, rts;   // packed rows, tokens held, position of new token 0, row tiles (0: not of the class)
+};
+__device__ __forceinline__ TileSeq tile_seq(const TileParams& p, int b, bool& bad) {
+  TileSeq s;
+  const SeqRows r = seq_rows(p.b.q_start, b, p.b.n_tokens, bad);
+  s.first = r.first;
+  s.n = r.n;
+  if (p.paged) {
+    const int len = p.b.kv_len[b];
+    const int cap = p.b.table_pages << p.page_shift;
+    s.base = len - r.n;
+    s.len = max(min(len, cap), 0);
+    s.rts = attn_decode_takes(r.n, p.group) ? 0 : (r.n * p.group + kItemRows - 1) / kItemRows;
+  } else {
+    s.base = 0;
+    s.len = r.n;
+    s.rts = (r.n * p.group + kItemRows - 1) / kItemRows;
+  }
+  return s;
+}
+// positions that row `row` of the sequence sees
+__device__ __forceinline__ int row_sees(const TileParams& p, const TileSeq& s, int row) {
+  return max(min(s.base + row / p.group + 1, s.len), 0);
+}
+__device__ __forceinline__ int item_tiles(const TileParams& p, const TileSeq& s, int rt) {
+  const int e = row_sees(p, s, min((rt + 1) * kItemRows, s.n * p.group) - 1);
+  return max((e + kPosTile - 1) / kPosTile, 1);
+}
+
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// position tiles of all row tiles of a sequence, one key/value head (whole warp)
+__device__ __forceinline__ uint64_t seq_weight(const TileParams& p, int b, int lane, bool& bad) {
+  const TileSeq s = tile_seq(p, b, bad);
+  uint64_t w = 0;
+  for (int rt = lane; rt < s.rts; rt += 32) w += item_tiles(p, s, rt);
+  return warp_sum(w);
+}
+
+// Walks the pieces of a thread block's range of the line of tiles. Every warp
+// holds a copy and steps it alike.
+struct TileWalk {
+  uint64_t x, end, total;
+  int ctas;
+  int b, h, rt;
+  TileSeq s;
+  int nt;            // tiles of the item
+  int t0, t1;        // this piece's
+  uint64_t item0;    // line position of the item's tile 0
+};
+
+__device__ __forceinline__ void tile_piece(TileWalk& w) {
+  w.t0 = static_cast<int>(w.x - w.item0);
+  w.t1 = static_cast<int>(min(static_cast<uint64_t>(w.nt - w.t0), w.end - w.x)) + w.t0;
+}
+
+// Called by the whole block; false: nothing to do.
+__device__ __forceinline__ bool tile_begin(const TileParams& p, TileWalk& w, uint64_t* plan, int warp, int lane) {
+  const int per = (p.b.n_seqs + kGroups - 1) / kGroups;     // sequences per table entry
+  const int entries = per == 0 ? 0 : (p.b.n_seqs + per - 1) / per;
+  bool bad = false;
+  for (int e = warp; e < entries; e += kTileThreads / 32) {
+    uint64_t v = 0;
+    for (int b = e * per; b < min((e + 1) * per, p.b.n_seqs); ++b) v += seq_weight(p, b, lane, bad);
+    if (lane == 0) plan[e] = v;
+  }
+  if (bad && blockIdx.x == 0) record_status(p.status, EPILORA_ERR_INVALID_ARG);
+  __syncthreads();
+  uint64_t mine[kGroups / 32], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kGroups / 32; ++i) {
+    const int e = lane * (kGroups / 32) + i;
+    mine[i] = e < entries ? plan[e] * p.kv_heads : 0;
+    sum += mine[i];
+  }
+  const uint64_t inc = warp_scan(sum, lane);
+  w.total = __shfl_sync(0xffffffffu, inc, 31);
+  if (w.total == 0) return false;
+  w.ctas = static_cast<int>(min(static_cast<uint64_t>(gridDim.x), w.total));
+  if (static_cast<int>(blockIdx.x) >= w.ctas) return false;
+  w.x = blockIdx.x * w.total / w.ctas;
+  w.end = (blockIdx.x + 1) * w.total / w.ctas;
+  // the table entry that holds x
+  const uint32_t hit = __ballot_sync(0xffffffffu, inc > w.x);
+  const int l = __ffs(hit) - 1;
+  uint64_t at = inc - sum;
+  int e = lane * (kGroups / 32);
+#pragma unroll
+  for (int i = 0; i < kGroups / 32 - 1; ++i)
+    if (at + mine[i] <= w.x && e == lane * (kGroups / 32) + i) at += mine[i], ++e;
+  at = __shfl_sync(0xffffffffu, at, l);
+  e = __shfl_sync(0xffffffffu, e, l);
+  // the sequence in it
+  uint64_t weight = 0;
+  int b = e * per;
+  for (;; ++b) {
+    if (b >= p.b.n_seqs) return false;   // metadata changed under the call
+    weight = seq_weight(p, b, lane, bad);
+    if (at + weight * p.kv_heads > w.x) break;
+    at += weight * p.kv_heads;
+  }
+  w.b = b;
+  w.s = tile_seq(p, b, bad);
+  w.h = static_cast<int>((w.x - at) / weight);
+  at += w.h * weight;
+  // the row tile
+  for (int r0 = 0;; r0 += 32) {
+    if (r0 >= w.s.rts) return false;
+    const uint64_t c = r0 + lane < w.s.rts ? item_tiles(p, w.s, r0 + lane) : 0;
+    const uint64_t in = warp_scan(c, lane);
+    const uint32_t found = __ballot_sync(0xffffffffu, at + in > w.x);
+    if (found != 0) {
+      const int k = __ffs(found) - 1;
+      w.rt = r0 + k;
+      w.nt = static_cast<int>(__shfl_sync(0xffffffffu, c, k));
+      w.item0 = at + __shfl_sync(0xffffffffu, in - c, k);
+      break;
+    }
+    at += __shfl_sync(0xffffffffu, in, 31);
+  }
+  tile_piece(w);
+  return true;
+}
+
+__device__ __forceinline__ bool tile_next(const TileParams& p, TileWalk& w) {
+  w.x += w.t1 - w.t0;
+  if (w.x >= w.end) return false;
+  w.item0 += w.nt;
+  if (++w.rt == w.s.rts) {
+    w.rt = 0;
+    if (++w.h == p.kv_heads) {
+      w.h = 0;
+      bool bad = false;
+      do {   // x < end: a sequence of the class follows
+        if (++w.b >= p.b.n_seqs) return false;
+        w.s = tile_seq(p, w.b, bad);
+      } while (w.s.rts == 0);
+    }
+  }
+  w.nt = item_tiles(p, w.s, w.rt);
+  tile_piece(w);
+  return true;
+}
+
+// What every role derives from a piece.
+struct Item {
+  int row0, rows;      // rows of the sequence's (token, head) rows
+  bool two;            // two row tiles; else both streams share one
+  int see_all;         // positions every row sees
+  int see_end;         // positions the last row sees
+};
+__device__ __forceinline__ Item item_of(const TileParams& p, const TileWalk& w) {
+  Item i;
+  i.row0 = w.rt * kItemRows;
+  i.rows = min(kItemRows, w.s.n * p.group - i.row0);
+  i.two = i.rows > kRowTile;
+  i.see_all = row_sees(p, w.s, i.row0);
+  i.see_end = row_sees(p, w.s, i.row0 + i.rows - 1);
+  return i;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// the registers of a TMEM load are read from here on
+template <int N>
+__device__ __forceinline__ void loaded(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
+}
+
+__device__ __forceinline__ void bar_group(int s) { asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory"); }
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+
+// whether a 32-bit word of two bf16 holds a NaN or an infinity
+__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t v) {
+  return ((v & 0x7F80u) == 0x7F80u) | ((v & 0x7F800000u) == 0x7F800000u);
+}
+// whether a 32-bit word of four E4M3 codes holds a NaN (they have no infinity)
+__device__ __forceinline__ bool e4m3x4_nan(uint32_t v) {
+  return ((v & 0x7Fu) == 0x7Fu) | ((v & 0x7F00u) == 0x7F00u) | ((v & 0x7F0000u) == 0x7F0000u) |
+         ((v & 0x7F000000u) == 0x7F000000u);
+}
+
+template <int D, bool E4>
+__global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid_constant__ TileParams p) {
+  using C = TileCfg<D, E4>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* plan = reinterpret_cast<uint64_t*>(smem + C::kPlan);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);   // [stages] tile complete
+  uint64_t* empty = full + C::kStages;                             // [stages] tile read
+  uint64_t* raw_full = empty + C::kStages;                         // [raw stages] codes complete
+  uint64_t* raw_empty = raw_full + C::kRawStages;
+  uint64_t* q_full = raw_empty + C::kRawStages;                    // the item's queries are in place
+  uint64_t* s_full = q_full + 1;                                   // [2] scores complete
+  uint64_t* p_full = s_full + 2;                                   // [2] weights written
+  uint64_t* o_full = p_full + 2;                                   // [2] output complete
+  uint64_t* fix_req = o_full + 2;                                  // a value tile is to be cleaned
+  uint64_t* fix_done = fix_req + 1;
+  uint64_t* drain = fix_done + 1;                                  // after an abort: products complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_flag = abort_flag + 1;                        // [2]
+  volatile int* nf_item = last_flag + 2;                           // [8] items (by number) with non-finite hidden values
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], E4 ? 2 : 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::kRawStages; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 2);
+    }
+    mbar_init(q_full, kItemRows);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kRowTile);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(fix_req, 1);
+    mbar_init(fix_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    for (int i = 0; i < 8; ++i) nf_item[i] = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&p.tk);
+    tma_prefetch_desc(&p.tv);
+  }
+  pdl_wait_primary();
+
+  // packed rows of no sequence are zero (the decode kernel's part of a call over the cache)
+  if (!p.paged) {
+    const int used = p.b.n_seqs > 0 ? min(max(p.b.q_start[p.b.n_seqs], 0), p.b.n_tokens) : 0;
+    const int64_t rows = static_cast<int64_t>(p.b.n_tokens - used) * p.heads;
+    constexpr int V = D / 8;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * V;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+      const int64_t r = i / V;
+      const int64_t t = used + r / p.heads;
+      const int h = static_cast<int>(r % p.heads);
+      *reinterpret_cast<uint4*>(p.o.p + t * p.o.ts + h * p.o.hs + (i % V) * 8) = make_uint4(0, 0, 0, 0);
+      if (p.lse != nullptr && i % V == 0) p.lse[t * p.heads + h] = -INFINITY;
+    }
+  }
+
+  TileWalk w;
+  if (!tile_begin(p, w, plan, warp, lane)) return;   // the same answer in every warp
+
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tm_s = tmem, tm_o = tmem + 256;   // S of stream s at tm_s + 128 s, O at tm_o + D s
+
+  // a bounded wait of a whole warp; false once any wait of the block ran out
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = !*abort_flag && mbar_wait_bounded(bar, parity, kWaitLimitNs);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (lane == 0) {
+      *abort_flag = 1;
+      record_status(p.status, EPILORA_ERR_TIMEOUT);
+    }
+    return false;
+  };
+
+  if (warp == 8) {
+    // ===== copies =====
+    fence_proxy_async_global();
+    constexpr int kSt = E4 ? C::kRawStages : C::kStages;
+    constexpr int kBytes = E4 ? C::kRawBytes : C::kTileBytes;
+    constexpr int kRowBytes = E4 ? D : 128;              // inner extent of a box
+    constexpr int kBoxes = E4 ? 1 : D / 64;
+    uint64_t* bar_full = E4 ? raw_full : full;
+    uint64_t* bar_empty = E4 ? raw_empty : empty;
+    uint8_t* ring = smem + (E4 ? C::kRaw : C::kRing);
+    const int nb = kPosTile / p.box_rows;                // boxes per tile along the positions
+    int slot = 0;
+    uint32_t phase = 0;
+    bool stop = false;
+    do {
+      const Item it = item_of(p, w);
+      const int32_t* table = p.paged ? p.b.page_table + w.b * p.b.table_stride : nullptr;
+      auto page_of = [&](int u) {   // page of box u of the sequence
+        return p.paged && u * p.box_rows < it.see_end ? table[(u * p.box_rows) >> p.page_shift] : 0;
+      };
+      int c0 = w.t0 * nb;
+      int ids = page_of(c0 + lane);
+      for (int j = w.t0; j < w.t1 && !stop; ++j) {
+        if (j * nb >= c0 + 32) {
+          c0 += 32;
+          ids = page_of(c0 + lane);
+        }
+        if (p.paged && (ids < 0 || ids >= p.c.num_pages)) record_status(p.status, EPILORA_ERR_INVALID_ARG);
+        const int held = min(max(it.see_end - j * kPosTile, 0), kPosTile);           // rows some row of the item sees
+        const int boxes = p.paged ? (held + p.box_rows - 1) / p.box_rows : (held > 0 ? 1 : 0);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!wait(&bar_empty[slot], phase ^ 1u)) {
+            stop = true;
+            break;
+          }
+          uint8_t* dst = ring + slot * kBytes;
+          if (lane == 0) {
+            if (boxes > 0)
+              mbar_arrive_expect_tx(&bar_full[slot], boxes * p.box_rows * kBoxes * kRowBytes);
+            else
+              mbar_arrive(&bar_full[slot]);
+          }
+          __syncwarp();
+          const CUtensorMap* map = kv ? &p.tv : &p.tk;
+          for (int i = 0; i < boxes; ++i) {
+            const int pg = __shfl_sync(0xffffffffu, ids, j * nb + i - c0);
+            if (lane == 0) {
+              const int pos = j * kPosTile + i * p.box_rows;
+              // a page index out of range, and rows past the packed array, read as zeros
+              const int y = p.paged ? pos & (p.c.page_size - 1) : w.s.first + pos;
+#pragma unroll
+              for (int x = 0; x < kBoxes; ++x)
+                tma_load_4d(dst + x * C::kBlock + i * p.box_rows * kRowBytes, map, &bar_full[slot], x * kRowBytes, y,
+                            w.h, p.paged ? pg : 0);
+            }
+            __syncwarp();
+          }
+          if (++slot == kSt) slot = 0, phase ^= 1u;
+        }
+      }
+    } while (!stop && tile_next(p, w));
+    if (*abort_flag && lane == 0) {
+      // no copy in flight at exit
+      for (int i = 0; i < kSt; ++i)
+        (void)mbar_wait_bounded(&bar_full[i], i < slot ? phase : phase ^ 1u, 1000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ===== products =====
+    constexpr uint32_t kIdQK = idesc_f16(128, 128, !E4, false);
+    constexpr uint32_t kIdPV = idesc_f16(128, D, !E4, true);
+    const uint32_t q_addr = smem_u32(smem), ring = smem_u32(smem + C::kRing);
+    uint32_t pos = 0;               // ring position (keys and values alternating) of the piece's first tile
+    uint32_t item = 0, pn[2] = {0, 0}, fixes = 0;
+    bool ok = true;
+    bool issued = false;
+    do {
+      const Item it = item_of(p, w);
+      const int nt = w.t1 - w.t0;
+      const int steps = it.two ? 2 * nt : nt;
+      auto slot_of = [&](int j, int kv) { return (pos + 2 * j + kv) % C::kStages; };
+      auto par_of = [&](int j, int kv) { return ((pos + 2 * j + kv) / C::kStages) & 1u; };
+      auto qk = [&](int i) {
+        const int s = i & 1, j = it.two ? i >> 1 : i;
+        const uint32_t st = slot_of(j, 0);
+        if (!(it.two && s == 1)) ok = ok && wait(&full[st], par_of(j, 0));
+        if (!ok) return;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t a0 = q_addr + (it.two ? s * C::kTileBytes : 0), b0 = ring + st * C::kTileBytes;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * C::kBlock + (k % 4) * 32;
+            mma_f16_ss(tm_s + s * 128, make_smem_desc(a0 + off, 16, 1024, kSwizzle128B),
+                       make_smem_desc(b0 + off, 16, 1024, kSwizzle128B), kIdQK, k > 0);
+          }
+          tc_commit(&s_full[s]);
+          if (!(it.two && s == 0)) tc_commit(&empty[st]);
+        }
+        issued = true;
+        __syncwarp();
+      };
+      auto pv = [&](int i) {
+        const int s = i & 1, j = it.two ? i >> 1 : i;
+        const uint32_t st = slot_of(j, 1);
+        if (!(it.two && s == 1)) {
+          ok = ok && wait(&full[st], par_of(j, 1));
+          if (ok && !E4 && (w.t0 + j + 1) * kPosTile > it.see_all) {
+            if (lane == 0) mbar_arrive(fix_req);
+            __syncwarp();
+            ok = wait(fix_done, fixes & 1u);
+            ++fixes;
+          }
+        }
+        ok = ok && wait(&p_full[s], pn[s] & 1u);
+        ++pn[s];
+        if (!ok) return;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t b0 = ring + st * C::kTileBytes;
+#pragma unroll
+          for (int k = 0; k < kPosTile / 16; ++k)
+            mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8,
+                       make_smem_desc(b0 + k * 2048, C::kBlock, 1024, kSwizzle128B), kIdPV, i >= 2 || k > 0);   // a stream's first product starts its sum
+          if (!(it.two && s == 0)) tc_commit(&empty[st]);
+          if (i + 2 >= steps) tc_commit(&o_full[s]);
+        }
+        __syncwarp();
+      };
+      ok = ok && wait(q_full, item & 1u);
+      if (ok) qk(0);
+      if (ok && steps > 1) qk(1);
+      for (int i = 0; i < steps && ok; ++i) {
+        pv(i);
+        if (ok && i + 2 < steps) qk(i + 2);
+      }
+      pos += 2 * nt;
+      ++item;
+    } while (ok && tile_next(p, w));
+    if (!ok && issued && lane == 0) {
+      // no product in flight at exit: a commit covers everything issued before it
+      tc_commit(drain);
+      (void)mbar_wait_bounded(drain, 0, 1000000ull);
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    if (!E4) {
+      // ===== cleaning of value tiles =====
+      // A position that a row does not see has weight zero, but zero times a
+      // NaN or an infinity is NaN: rows past the item's last position are
+      // zeroed; non-finite values at positions that only some rows see are
+      // zeroed too and the item noted (its epilogue adds them where they belong).
+      if (warp == 10) {
+        uint32_t pos = 0, fixes = 0;
+        int item = 0;
+        bool ok = true;
+        do {
+          const Item it = item_of(p, w);
+          for (int j = max(w.t0, it.see_all / kPosTile); j < w.t1 && ok; ++j) {
+            ok = wait(fix_req, fixes & 1u);
+            ++fixes;
+            if (!ok) break;
+            uint8_t* v = smem + C::kRing + ((pos + 2 * (j - w.t0) + 1) % C::kStages) * C::kTileBytes;
+            const int from = max(it.see_all - j * kPosTile, 0);
+            const int to = min(max(it.see_end - j * kPosTile, from), kPosTile);
+            bool nf = false;
+            for (int i = from * 8 + lane; i < kPosTile * 8; i += 32) {
+#pragma unroll
+              for (int x = 0; x < D / 64; ++x) {
+                uint4* q = reinterpret_cast<uint4*>(v + x * C::kBlock + i * 16);
+                if ((i >> 3) >= to) {
+                  *q = make_uint4(0, 0, 0, 0);
+                } else {
+                  const uint4 u = *q;
+                  if (bf16x2_nonfinite(u.x) | bf16x2_nonfinite(u.y) | bf16x2_nonfinite(u.z) | bf16x2_nonfinite(u.w)) {
+                    nf = true;
+                    uint32_t e[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
+                      if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0xFFFFu;
+                    }
+                    *q = make_uint4(e[0], e[1], e[2], e[3]);
+                  }
+                }
+              }
+            }
+            if (nf) nf_item[item & 7] = item + 1;
+            fence_proxy_async_smem();
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fix_done);
+          }
+          pos += 2 * (w.t1 - w.t0);
+          ++item;
+        } while (ok && tile_next(p, w));
+      }
+    } else {
+      // ===== E4M3 codes to fp16 tiles =====
+      const int t = (warp - 10) * 32 + lane;
+      uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
+      int item = 0;
+      bool ok = true;
+      do {
+        const Item it = item_of(p, w);
+        for (int j = w.t0; j < w.t1 && ok; ++j) {
+          const int from = max(it.see_all - j * kPosTile, 0);
+          const int to = min(max(it.see_end - j * kPosTile, 0), kPosTile);
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            ok = wait(&raw_full[rslot], rphase) && wait(&empty[slot], phase ^ 1u);
+            if (!ok) break;
+            const uint8_t* src = smem + C::kRaw + rslot * C::kRawBytes;
+            uint8_t* dst = smem + C::kRing + slot * C::kTileBytes;
+            bool nf = false;
+            const bool clean = kv == 1 && from < kPosTile;
+            constexpr int kPer = D / 16;   // 16-code chunks per row
+#pragma unroll 4
+            for (int i = t; i < kPosTile * kPer; i += 64) {
+              uint4 u = *reinterpret_cast<const uint4*>(src + i * 16);
+              const int row = i / kPer, c = i % kPer;
+              if (clean) {
+                if (row >= to) {
+                  u = make_uint4(0, 0, 0, 0);
+                } else if (row >= from && (e4m3x4_nan(u.x) | e4m3x4_nan(u.y) | e4m3x4_nan(u.z) | e4m3x4_nan(u.w))) {
+                  nf = true;
+                  uint32_t e[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int y = 0; y < 32; y += 8)
+                      if ((e[k] & (0x7Fu << y)) == (0x7Fu << y)) e[k] &= ~(0xFFu << y);
+                  u = make_uint4(e[0], e[1], e[2], e[3]);
+                }
+              }
+              uint4 lo, hi;
+              lo.x = e4m3x2_to_f16x2(u.x), lo.y = e4m3x2_to_f16x2(u.x >> 16);
+              lo.z = e4m3x2_to_f16x2(u.y), lo.w = e4m3x2_to_f16x2(u.y >> 16);
+              hi.x = e4m3x2_to_f16x2(u.z), hi.y = e4m3x2_to_f16x2(u.z >> 16);
+              hi.z = e4m3x2_to_f16x2(u.w), hi.w = e4m3x2_to_f16x2(u.w >> 16);
+              // chunks 2c and 2c + 1 of the row's 16-byte chunks, swizzled; the
+              // two halves of a 128-element row store theirs in opposite order,
+              // so that they use different banks
+              uint8_t* row_at = dst + (c / 4) * C::kBlock + row * 128;
+              const int k0 = (c % 4) * 2, sw = row & 7, first = (c / 4) & 1;
+              *reinterpret_cast<uint4*>(row_at + (((k0 + first) ^ sw) * 16)) = first ? hi : lo;
+              *reinterpret_cast<uint4*>(row_at + (((k0 + 1 - first) ^ sw) * 16)) = first ? lo : hi;
+            }
+            if (nf) nf_item[item & 7] = item + 1;
+            fence_proxy_async_smem();
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&full[slot]);
+              mbar_arrive(&raw_empty[rslot]);
+            }
+            if (++slot == C::kStages) slot = 0, phase ^= 1u;
+            if (++rslot == C::kRawStages) rslot = 0, rphase ^= 1u;
+          }
+        }
+        ++item;
+      } while (ok && tile_next(p, w));
+    }
+  } else {
+    // ===== softmax =====
+    const int s = warp >> 2;                       // stream
+    const int r = threadIdx.x & (kRowTile - 1);    // lane of TMEM = row of the stream
+    const uint32_t quad = static_cast<uint32_t>(warp & 3) << 21;   // TMEM lane 32 (warp % 4), in bits 16..
+    const uint32_t ts = tm_s + s * 128 + quad, to = tm_o + s * D + quad;
+    uint32_t sn = 0, on[2] = {0, 0};
+    int item = 0;
+    bool ok = true;
+    float* other = reinterpret_cast<float*>(smem + C::kTileBytes);   // m, l of stream 1 (the unused second Q tile)
+    do {
+      const Item it = item_of(p, w);
+      const int nt = w.t1 - w.t0;
+      const int lrow = it.two ? s * kRowTile + r : r;      // row within the item
+      const bool live = lrow < it.rows;
+      const int grow = it.row0 + (live ? lrow : 0);
+      const int64_t tok = w.s.first + grow / p.group;
+      const int head = w.h * p.group + grow % p.group;
+      const int see = live ? row_sees(p, w.s, grow) : 0;
+      float s_eff = p.scale;
+      if (E4) s_eff *= p.c.k_scale[w.h];
+      float c = s_eff == 0.0f ? 1.0f : fabsf(s_eff) * kLog2e;
+
+      // the row of queries into shared memory (swizzled, K-major)
+      {
+        const __nv_bfloat16* src = p.q.p + tok * p.q.ts + head * p.q.hs;
+        const bool use = live && s_eff != 0.0f;
+        const uint32_t flip = s_eff < 0.0f ? 0x80008000u : 0u;
+        uint4 u[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) u[i] = use ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
+        if (E4) {
+          // fp16 queries: bf16's 8 significant bits fit; the row is scaled by
+          // the power of two that puts its largest element near 2^13
+          // (elements 2^27 below that are still exact, the rest is off by
+          // 2^-38 of the largest), the scores' factor takes it back
+          float big = 0.0f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(bf16_lo(e[k])), fabsf(bf16_hi(e[k]))));
+          }
+          const int ex = static_cast<int>((__float_as_uint(big) >> 23) & 0xFF);
+          const int up = big == 0.0f || ex == 0xFF ? 0 : min(13 - (ex - 127), 126);
+          const float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+          if (up != 0) c *= __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            u[i].x = pack_half(bf16_lo(u[i].x) * f, bf16_hi(u[i].x) * f);
+            u[i].y = pack_half(bf16_lo(u[i].y) * f, bf16_hi(u[i].y) * f);
+            u[i].z = pack_half(bf16_lo(u[i].z) * f, bf16_hi(u[i].z) * f);
+            u[i].w = pack_half(bf16_lo(u[i].w) * f, bf16_hi(u[i].w) * f);
+          }
+        }
+        if (it.two || s == 0) {
+          uint8_t* dst = smem + s * C::kTileBytes + r * 128;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = make_uint4(u[i].x ^ flip, u[i].y ^ flip, u[i].z ^ flip, u[i].w ^ flip);
+            *reinterpret_cast<uint4*>(dst + (i / 8) * C::kBlock + (((i & 7) ^ (r & 7)) * 16)) = v;
+          }
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(q_full);
+      }
+
+      float m = -INFINITY, l = 0.0f;   // m in units of S
+      const int steps = it.two ? nt : (nt + 1 - s) / 2;
+      for (int k = 0; k < steps; ++k) {
+        const int j = w.t0 + (it.two ? k : 2 * k + s);
+        ok = ok && wait(&s_full[s], sn & 1u);
+        ++sn;
+        if (!ok) continue;
+        tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + i * 32, x + i * 32);
+        tmem_ld_wait();
+        loaded(x);
+        const int lim = see - j * kPosTile;     // the row sees columns below
+        if (__any_sync(0xffffffffu, lim < kPosTile)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= lim) x[i] = 0xff800000u;
+        }
+        float top[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
+#pragma unroll
+        for (int i = 8; i < 128; i += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            top[q] = fmaxf(top[q], fmaxf(__uint_as_float(x[i + q]), __uint_as_float(x[i + q + 4])));
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const bool up = (mx - m) * c > kRaise;      // false for -inf - -inf
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = up ? exp2_approx((m - mx) * c) : 1.0f;
+          if (up) m = mx;
+          l *= f;
+          if (k > 0) {
+            // every product into O is complete: the scores' commit came after them
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(to + i * 32, o);
+              tmem_ld_wait();
+              loaded(o);
+#pragma unroll
+              for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+              tmem_st_32x32b_x32(to + i * 32, o);
+            }
+          }
+        }
+        const float mc = m == -INFINITY ? 0.0f : m * c;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float a = exp2_approx(fmaf(__uint_as_float(x[i * 32 + 2 * q]), c, -mc));
+            const float b = exp2_approx(fmaf(__uint_as_float(x[i * 32 + 2 * q + 1]), c, -mc));
+            sum[q & 3] += a + b;
+            // the weights as 16-bit operands (each within 2^-8 of itself, 2^-11 in fp16)
+            pk[q] = E4 ? pack_half(a, b) : pack_bf16(a, b);
+          }
+          // over the scores that have been read
+          tmem_st_32x32b_x16(ts + i * 16, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[s]);
+      }
+
+      // ===== the piece's result =====
+      if (steps > 0) {
+        ok = ok && wait(&o_full[s], on[s] & 1u);
+        ++on[s];
+      }
+      float f0 = 1.0f, f1 = 0.0f;      // factors of the two streams' outputs
+      bool both = false;
+      if (!it.two) {
+        if (s == 1) other[r] = m, other[kRowTile + r] = l;
+        bar_softmax();
+        if (s == 0) {
+          both = nt > 1;
+          if (both) {
+            ok = ok && wait(&o_full[1], on[1] & 1u);
+            ++on[1];
+            const float m1 = other[r], l1 = other[kRowTile + r];
+            const float mm = fmaxf(m, m1);
+            const float base = mm == -INFINITY ? 0.0f : mm;
+            f0 = exp2_approx((m - base) * c);
+            f1 = exp2_approx((m1 - base) * c);
+            l = l * f0 + l1 * f1;
+            m = mm;
+          }
+        }
+      } else if (s == 0) {
+        ++on[1];     // keep count of the other stream's outputs
+      }
+      tc_fence_after();
+      // (after a wait that ran out the rest still runs: its barriers count every warp)
+      if (it.two || s == 0) {
+        const bool whole = w.t0 == 0 && w.t1 == w.nt;
+        const float vscale = E4 ? p.c.v_scale[w.h] : 1.0f;
+        const bool nf = nf_item[item & 7] == item + 1;
+        const uint64_t range0 = blockIdx.x * w.total / w.ctas;
+        constexpr int kPart = (2 + D) * kItemRows / 4;      // float4s of a partial result: m c, l, O [D / 4][256]
+        float4* part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (w.x == range0 ? 0 : 1)) * kPart;
+        const int prow = s * kRowTile + r;
+        auto put = [&](int i, const float* o, float sum) {   // 8 outputs from element i on
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (sum != 0.0f) {
+            const float inv = vscale / sum;
+            v = make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                           pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
+          }
+          *reinterpret_cast<uint4*>(p.o.p + tok * p.o.ts + head * p.o.hs + i) = v;
+        };
+        auto put_lse = [&](float mc, float sum) {
+          if (p.lse != nullptr) p.lse[tok * p.heads + head] = sum == 0.0f ? -INFINITY : (mc + __log2f(sum)) * kLn2;
+        };
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(tm_o + s * D + quad + i, o);
+          tmem_ld_wait();
+          loaded(o);
+          float a[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) a[q] = __uint_as_float(o[q]);
+          if (!it.two && both) {
+            tmem_ld_32x32b_x32(tm_o + D + quad + i, o);
+            tmem_ld_wait();
+            loaded(o);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) a[q] = a[q] * f0 + __uint_as_float(o[q]) * f1;
+          }
+          if (nf) {
+            // the non-finite values that were taken out, where this row sees them
+            const int to_pos = min(see, w.t1 * kPosTile);
+            for (int pos = max(it.see_all, w.t0 * kPosTile); pos < to_pos; ++pos) {
+              if (!p.paged) {
+                const __nv_bfloat16* v = p.v.p + (w.s.first + pos) * p.v.ts + w.h * p.v.hs + i;
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                  const float e = __bfloat162float(v[q]);
+                  if (!(fabsf(e) < INFINITY)) a[q] += e;
+                }
+              } else {
+                const int pg = p.b.page_table[w.b * p.b.table_stride + (pos >> p.page_shift)];
+                if (pg < 0 || pg >= p.c.num_pages) continue;
+                const int64_t at = pg * p.c.v_page_stride + w.h * p.c.v_head_stride +
+                                   (pos & (p.c.page_size - 1)) * p.c.v_token_stride + i;
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                  const float e = E4 ? e4m3_to_f32(static_cast<const uint8_t*>(p.c.v)[at + q])
+                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(p.c.v)[at + q]);
+                  if (!(fabsf(e) < INFINITY)) a[q] += e;
+                }
+              }
+            }
+          }
+          if (whole) {
+            if (live) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 8) put(i + q, a + q, l);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 32; q += 4)
+              part[2 * kItemRows / 4 + (i + q) / 4 * kItemRows + prow] = make_float4(a[q], a[q + 1], a[q + 2], a[q + 3]);
+          }
+        }
+        const float mc = m == -INFINITY ? -INFINITY : m * c;
+        if (whole) {
+          if (live) put_lse(mc, l);
+        } else {
+          float* pf = reinterpret_cast<float*>(part);
+          pf[prow] = mc;
+          pf[kItemRows + prow] = l;
+          // the blocks that hold the item's first and last tile
+          const int first = static_cast<int>(((w.item0 + 1) * w.ctas - 1) / w.total);
+          const int last = static_cast<int>(((w.item0 + w.nt) * w.ctas - 1) / w.total);
+          const int pieces = last - first + 1;
+          __threadfence();
+          bar_group(s);
+          if (r == 0) {
+            const uint32_t before = atomicAdd(p.counters + 2 * first + s, 1u);
+            const int is_last = before == static_cast<uint32_t>(pieces - 1);
+            if (is_last) p.counters[2 * first + s] = 0;
+            last_flag[s] = is_last;
+          }
+          bar_group(s);
+          if (last_flag[s] && live) {
+            __threadfence();
+            // the first piece starts its block's range, or follows other items in it
+            const bool at_start = first * w.total / w.ctas == w.item0;
+            auto piece = [&](int k) {
+              const int64_t n = k == 0 ? 2 * static_cast<int64_t>(first) + (at_start ? 0 : 1)
+                                       : 2 * static_cast<int64_t>(first + k);
+              return p.partials + n * kPart;
+            };
+            float top = -INFINITY;
+            for (int k = 0; k < pieces; ++k) top = fmaxf(top, __ldcg(reinterpret_cast<const float*>(piece(k)) + prow));
+            const float base = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
+            for (int k = 0; k < pieces; ++k) {
+              const float* f = reinterpret_cast<const float*>(piece(k));
+              sum += __ldcg(f + kItemRows + prow) * exp2_approx(__ldcg(f + prow) - base);
+            }
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              float a[32];
+#pragma unroll
+              for (int q = 0; q < 32; ++q) a[q] = 0.0f;
+              for (int k = 0; k < pieces; ++k) {
+                const float4* f = piece(k);
+                const float wk = exp2_approx(__ldcg(reinterpret_cast<const float*>(f) + prow) - base);
+#pragma unroll
+                for (int q = 0; q < 32; q += 4) {
+                  const float4 v = __ldcg(f + 2 * kItemRows / 4 + (i + q) / 4 * kItemRows + prow);
+                  a[q] += v.x * wk, a[q + 1] += v.y * wk, a[q + 2] += v.z * wk, a[q + 3] += v.w * wk;
+                }
+              }
+#pragma unroll
+              for (int q = 0; q < 32; q += 8) put(i + q, a + q, sum);
+            }
+            put_lse(top, sum);
+          }
+        }
+        tc_fence_before();
+      }
+      if (!it.two) bar_softmax();    // both streams' outputs and `other` are free again
+      ++item;
+    } while (tile_next(p, w));
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool E4>
+int launch(const AttnArgs& a, TileParams& p) {
+  using C = TileCfg<D, E4>;
+  const uint64_t es = E4 ? 1 : 2;
+  const uint32_t inner = E4 ? D : 128;
+  int rc;
+  if (a.paged) {
+    const epilora_kv_cache& c = a.cache;
+    const uint64_t dims[4] = {D * es, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.kv_heads),
+                              static_cast<uint64_t>(c.num_pages)};
+    const uint32_t box[4] = {inner, static_cast<uint32_t>(p.box_rows), 1, 1};
+    const uint64_t ks[3] = {c.k_token_stride * es, c.k_head_stride * es, c.k_page_stride * es};
+    const uint64_t vs[3] = {c.v_token_stride * es, c.v_head_stride * es, c.v_page_stride * es};
+    rc = make_tma_4d_u8(&p.tk, c.k, dims, ks, box, E4 ? 0 : 128);
+    if (rc == EPILORA_OK) rc = make_tma_4d_u8(&p.tv, c.v, dims, vs, box, E4 ? 0 : 128);
+  } else {
+    const uint64_t T = static_cast<uint64_t>(a.batch.n_tokens);
+    const uint64_t dims[4] = {D * es, T, static_cast<uint64_t>(a.cache.kv_heads), 1};
+    const uint32_t box[4] = {inner, kPosTile, 1, 1};
+    const uint64_t ks[3] = {a.k.ts * es, a.k.hs * es, a.k.ts * es * T};
+    const uint64_t vs[3] = {a.v.ts * es, a.v.hs * es, a.v.ts * es * T};
+    rc = make_tma_4d_u8(&p.tk, a.k.p, dims, ks, box, 128);
+    if (rc == EPILORA_OK) rc = make_tma_4d_u8(&p.tv, a.v.p, dims, vs, box, 128);
+  }
+  if (rc != EPILORA_OK) return rc;
+  auto kern = attn_tile_kernel<D, E4>;
+  static int attr_done[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EPILORA_ERR_CUDA;
+  if (!attr_done[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+      return EPILORA_ERR_CUDA;
+    attr_done[dev] = 1;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(num_sms() < kTileMaxCtas ? num_sms() : kTileMaxCtas, 1, 1);
+  cfg.blockDim = dim3(kTileThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? EPILORA_OK : EPILORA_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t attn_tile_counter_bytes() { return 2 * kTileMaxCtas * sizeof(uint32_t); }
+size_t attn_tile_partial_bytes(int head_dim) {
+  const int n = num_sms() < kTileMaxCtas ? num_sms() : kTileMaxCtas;
+  return static_cast<size_t>(2 * n) * (2 + head_dim) * kItemRows * sizeof(float);
+}
+
+int launch_attn_tile(const AttnArgs& a, uint32_t* counters, float* partials) {
+  TileParams p{};
+  p.b = a.batch;
+  p.c = a.cache;
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.o = a.o;
+  p.lse = a.lse;
+  p.paged = a.paged;
+  p.heads = a.heads;
+  p.kv_heads = a.cache.kv_heads;
+  p.group = a.heads / a.cache.kv_heads;
+  p.page_shift = a.paged ? __builtin_ctz(a.cache.page_size) : 0;
+  p.box_rows = a.paged && a.cache.page_size < kPosTile ? a.cache.page_size : kPosTile;
+  p.scale = a.scale;
+  p.counters = counters;
+  p.partials = reinterpret_cast<float4*>(partials);
+  p.status = a.status;
+  const bool e4 = a.paged && a.cache.kv_fmt == EPILORA_KV_E4M3;
+  if (a.cache.head_dim == 64) return e4 ? launch<64, true>(a, p) : launch<64, false>(a, p);
+  return e4 ? launch<128, true>(a, p) : launch<128, false>(a, p);
+}
+
+}  // namespace epi

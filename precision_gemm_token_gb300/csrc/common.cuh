@@ -180,7 +180,7 @@ int make_tma_2d_swz(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
 
 // Encodes a 4D tiled TMA descriptor of bytes: dims[0] is the inner extent in
 // bytes, strides_bytes[i] the pitch of dimension i + 1 (multiples of 16),
-// swizzled over `swizzle_span` bytes (64 or 128).
+// swizzled over `swizzle_span` bytes (64 or 128; 0: not at all).
 int make_tma_4d_u8(CUtensorMap* map, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides_bytes)[3],
                    const uint32_t (&box)[4], int swizzle_span);
 

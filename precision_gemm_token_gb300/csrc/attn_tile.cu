@@ -17,7 +17,8 @@
 //             sum in registers, writes the weights back over the scores
 //             (16-bit, the A operand of the second product) and, where the
 //             maximum rose by more than 2^8, rescales the row of O in TMEM
-//   8         copies key and value tiles into a ring of shared memory by TMA
+//   8         walks the block's pieces of work and tells them to the others;
+//             copies key and value tiles into a ring of shared memory by TMA
 //   9         issues the products; S and O of both streams fill the TMEM
 //   10 (11)   bf16: clean the value rows that some row must not see;
 //             E4M3: convert the copied codes to fp16 tiles
@@ -35,6 +36,11 @@ namespace epi {
 namespace {
 
 constexpr int kTileThreads = 384;
+// registers per thread: at launch, of the softmax warps, of the others; the
+// softmax keeps a row of 128 scores in registers (at 168 it spills some 190 KB
+// a tile, more than the L1 left beside the ring holds)
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kTileThreads * kRegsLaunch, "split of the block's registers");
 constexpr int kPosTile = 128;      // positions per tile
 constexpr int kRowTile = 128;      // rows per stream
 constexpr int kItemRows = 2 * kRowTile;
@@ -45,6 +51,9 @@ constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
 // it by this many powers of two: weights stay below 2^8, in range for the
 // 16-bit operands, and after a few tiles nothing is rescaled any more
 constexpr float kRaise = 8.0f;
+
+constexpr int kPieces = 4;         // pieces of work told ahead
+constexpr int kPieceInts = 16;
 
 template <int D, bool E4>
 struct TileCfg {
@@ -57,7 +66,8 @@ struct TileCfg {
   static constexpr int kRing = kQBytes, kRaw = kRing + kStages * kTileBytes;
   static constexpr int kPlan = kRaw + kRawStages * kRawBytes;
   static constexpr int kBars = kPlan + kGroups * 8;
-  static constexpr int kBytes = kBars + 512;
+  static constexpr int kPieceAt = kBars + 384;
+  static constexpr int kBytes = kPieceAt + kPieces * kPieceInts * 4;
   static constexpr int kSmem = 1024 + kBytes;
 };
 
@@ -130,8 +140,7 @@ __device__ __forceinline__ uint64_t seq_weight(const TileParams& p, int b, int l
   return warp_sum(w);
 }
 
-// Walks the pieces of a thread block's range of the line of tiles. Every warp
-// holds a copy and steps it alike.
+// Walks the pieces of a thread block's range of the line of tiles (one warp).
 struct TileWalk {
   uint64_t x, end, total;
   int ctas;
@@ -147,8 +156,8 @@ __device__ __forceinline__ void tile_piece(TileWalk& w) {
   w.t1 = static_cast<int>(min(static_cast<uint64_t>(w.nt - w.t0), w.end - w.x)) + w.t0;
 }
 
-// Called by the whole block; false: nothing to do.
-__device__ __forceinline__ bool tile_begin(const TileParams& p, TileWalk& w, uint64_t* plan, int warp, int lane) {
+// The table of sequence weights, by the whole block.
+__device__ __forceinline__ void tile_plan(const TileParams& p, uint64_t* plan, int warp, int lane) {
   const int per = (p.b.n_seqs + kGroups - 1) / kGroups;     // sequences per table entry
   const int entries = per == 0 ? 0 : (p.b.n_seqs + per - 1) / per;
   bool bad = false;
@@ -159,6 +168,13 @@ __device__ __forceinline__ bool tile_begin(const TileParams& p, TileWalk& w, uin
   }
   if (bad && blockIdx.x == 0) record_status(p.status, EPILORA_ERR_INVALID_ARG);
   __syncthreads();
+}
+
+// One warp; false: nothing to do.
+__device__ __forceinline__ bool tile_begin(const TileParams& p, TileWalk& w, const uint64_t* plan, int lane) {
+  const int per = (p.b.n_seqs + kGroups - 1) / kGroups;
+  const int entries = per == 0 ? 0 : (p.b.n_seqs + per - 1) / per;
+  bool bad = false;
   uint64_t mine[kGroups / 32], sum = 0;
 #pragma unroll
   for (int i = 0; i < kGroups / 32; ++i) {
@@ -235,21 +251,40 @@ __device__ __forceinline__ bool tile_next(const TileParams& p, TileWalk& w) {
   return true;
 }
 
-// What every role derives from a piece.
-struct Item {
-  int row0, rows;      // rows of the sequence's (token, head) rows
-  bool two;            // two row tiles; else both streams share one
+// A piece as the walking warp tells it to the other roles.
+struct Piece {
+  int b, h;            // sequence, key/value head
+  int first, base, len;
+  int row0, rows;      // of the sequence's (token, head) rows
   int see_all;         // positions every row sees
   int see_end;         // positions the last row sees
+  int t0, t1;          // position tiles; t0 == t1: no more work
+  int whole;           // the item's only piece
+  int first_cta, pieces;   // of an item in several pieces: the blocks first_cta, ...
+  int slot, slot0;     // where this piece's, and the first piece's, partial result goes
+  __device__ __forceinline__ bool two() const { return rows > kRowTile; }   // two row tiles; else both streams share one
 };
-__device__ __forceinline__ Item item_of(const TileParams& p, const TileWalk& w) {
-  Item i;
-  i.row0 = w.rt * kItemRows;
-  i.rows = min(kItemRows, w.s.n * p.group - i.row0);
-  i.two = i.rows > kRowTile;
-  i.see_all = row_sees(p, w.s, i.row0);
-  i.see_end = row_sees(p, w.s, i.row0 + i.rows - 1);
-  return i;
+static_assert(sizeof(Piece) == kPieceInts * 4, "one int per field");
+
+__device__ __forceinline__ void piece_of(const TileParams& p, const TileWalk& w, Piece& q) {
+  q.b = w.b;
+  q.h = w.h;
+  q.first = w.s.first;
+  q.base = w.s.base;
+  q.len = w.s.len;
+  q.row0 = w.rt * kItemRows;
+  q.rows = min(kItemRows, w.s.n * p.group - q.row0);
+  q.see_all = row_sees(p, w.s, q.row0);
+  q.see_end = row_sees(p, w.s, q.row0 + q.rows - 1);
+  q.t0 = w.t0;
+  q.t1 = w.t1;
+  q.whole = w.t0 == 0 && w.t1 == w.nt;
+  // the blocks that hold the item's first and last tile
+  q.first_cta = static_cast<int>(((w.item0 + 1) * w.ctas - 1) / w.total);
+  q.pieces = static_cast<int>(((w.item0 + w.nt) * w.ctas - 1) / w.total) - q.first_cta + 1;
+  // a piece that starts its block's range goes to the block's slot 0, the one that ends it to slot 1
+  q.slot = 2 * blockIdx.x + (w.x == blockIdx.x * w.total / w.ctas ? 0 : 1);
+  q.slot0 = 2 * q.first_cta + (q.first_cta * w.total / w.ctas == w.item0 ? 0 : 1);
 }
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
@@ -267,9 +302,6 @@ __device__ __forceinline__ void loaded(uint32_t (&v)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 
-__device__ __forceinline__ void bar_group(int s) { asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory"); }
-__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
-
 // whether a 32-bit word of two bf16 holds a NaN or an infinity
 __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t v) {
   return ((v & 0x7F80u) == 0x7F80u) | ((v & 0x7F800000u) == 0x7F800000u);
@@ -278,6 +310,77 @@ __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t v) {
 __device__ __forceinline__ bool e4m3x4_nan(uint32_t v) {
   return ((v & 0x7Fu) == 0x7Fu) | ((v & 0x7F00u) == 0x7F00u) | ((v & 0x7F0000u) == 0x7F0000u) |
          ((v & 0x7F000000u) == 0x7F000000u);
+}
+
+// One tile of scores to weights; a thread owns a row, m is in units of S, the
+// row sees columns below lim. The weights are taken against the maximum so
+// far while the tile's own is being found, 32 columns at a time; only where it
+// rises by more than kRaise (a row's first tile, then hardly ever) is the row
+// of O rescaled and the tile taken again.
+template <int D, bool E4>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, int lim, bool started, float& m,
+                                             float& l) {
+  uint32_t pk[64];
+  float add;
+  const bool edge = __any_sync(0xffffffffu, lim < kPosTile);
+#pragma unroll 1
+  while (true) {
+    const float mc = m == -INFINITY ? 0.0f : m * c;
+    float top[2] = {-INFINITY, -INFINITY}, sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t x[2][32];
+    tmem_ld_32x32b_x32(ts, x[0]);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t (&v)[32] = x[g & 1];
+      tmem_ld_wait();
+      loaded(v);
+      if (g < 3) tmem_ld_32x32b_x32(ts + (g + 1) * 32, x[(g + 1) & 1]);
+      if (edge) {
+        const int n = lim - 32 * g;
+        const uint32_t seen = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!(seen & (1u << i))) v[i] = 0xff800000u;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        top[0] = fmaxf(top[0], fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+        top[1] = fmaxf(top[1], fmaxf(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])));
+      }
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const float a = exp2_approx(fmaf(__uint_as_float(v[2 * q]), c, -mc));
+        const float b = exp2_approx(fmaf(__uint_as_float(v[2 * q + 1]), c, -mc));
+        sum[q & 3] += a + b;
+        // the weights as 16-bit operands (each within 2^-8 of itself, 2^-11 in fp16)
+        pk[16 * g + q] = E4 ? pack_half(a, b) : pack_bf16(a, b);
+      }
+    }
+    add = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    const float mx = fmaxf(top[0], top[1]);
+    const bool up = (mx - m) * c > kRaise;      // false for -inf - -inf
+    if (!__any_sync(0xffffffffu, up)) break;
+    const float f = up ? exp2_approx((m - mx) * c) : 1.0f;
+    if (up) m = mx;
+    l *= f;
+    if (started) {
+      // every product into O is complete: the scores' commit came after them
+#pragma unroll 1
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t o[16];
+        tmem_ld_32x32b_x16(to + i * 16, o);
+        tmem_ld_wait();
+        loaded(o);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+        tmem_st_32x32b_x16(to + i * 16, o);
+      }
+    }
+  }
+  l += add;
+  // over the scores that have been read
+  tmem_st_32x32b_x32(ts, pk);
+  tmem_st_32x32b_x32(ts + 32, pk + 32);
 }
 
 template <int D, bool E4>
@@ -297,10 +400,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   uint64_t* fix_req = o_full + 2;                                  // a value tile is to be cleaned
   uint64_t* fix_done = fix_req + 1;
   uint64_t* drain = fix_done + 1;                                  // after an abort: products complete
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* piece_full = drain + 1;                                // [pieces] told
+  uint64_t* piece_empty = piece_full + kPieces;                    // [pieces] read by every role
+  uint64_t* group_bar = piece_empty + kPieces;                     // [2] a softmax group meets
+  uint64_t* both_bar = group_bar + 2;                              // both meet
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(both_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* last_flag = abort_flag + 1;                        // [2]
-  volatile int* nf_item = last_flag + 2;                           // [8] items (by number) with non-finite hidden values
+  volatile int* nf_item = last_flag + 2;                           // [8] pieces (by number) with non-finite hidden values
+  volatile int* told = reinterpret_cast<volatile int*>(smem + C::kPieceAt);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -321,6 +429,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     mbar_init(fix_req, 1);
     mbar_init(fix_done, 1);
     mbar_init(drain, 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], E4 ? 11 : 10);     // 8 softmax warps, the products', the cleaning or converting ones
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&group_bar[i], kRowTile);
+    mbar_init(both_bar, kItemRows);
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) nf_item[i] = 0;
     fence_mbarrier_init();
@@ -344,8 +458,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     }
   }
 
-  TileWalk w;
-  if (!tile_begin(p, w, plan, warp, lane)) return;   // the same answer in every warp
+  tile_plan(p, plan, warp, lane);
 
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
@@ -357,9 +470,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_s = tmem, tm_o = tmem + 256;   // S of stream s at tm_s + 128 s, O at tm_o + D s
 
+  uint32_t told_n = 0;
   // a bounded wait of a whole warp; false once any wait of the block ran out
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = !*abort_flag && mbar_wait_bounded(bar, parity, kWaitLimitNs);
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    bool ok = false;
+    for (uint32_t polls = 1; !ok; ++polls) {
+      ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+      if ((polls & 63u) == 0u && (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs)) break;
+    }
     if (__all_sync(0xffffffffu, ok)) return true;
     if (lane == 0) {
       *abort_flag = 1;
@@ -367,7 +487,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     }
     return false;
   };
+  // the next piece, as every role but the walking one gets it; false: no more
+  auto next_piece = [&](Piece& q) {
+    const int e = told_n % kPieces;
+    if (!wait(&piece_full[e], (told_n / kPieces) & 1u)) return false;
+    int* to = reinterpret_cast<int*>(&q);
+#pragma unroll
+    for (int i = 0; i < kPieceInts; ++i) to[i] = told[e * kPieceInts + i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&piece_empty[e]);
+    ++told_n;
+    return q.t1 > q.t0;
+  };
 
+  if (warp >= 8) {
+    setmaxnreg_dec<kRegsOther>();
   if (warp == 8) {
     // ===== copies =====
     fence_proxy_async_global();
@@ -381,16 +515,35 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     const int nb = kPosTile / p.box_rows;                // boxes per tile along the positions
     int slot = 0;
     uint32_t phase = 0;
-    bool stop = false;
-    do {
-      const Item it = item_of(p, w);
-      const int32_t* table = p.paged ? p.b.page_table + w.b * p.b.table_stride : nullptr;
+    TileWalk w;
+    Piece it;
+    bool more = tile_begin(p, w, plan, lane), stop = false;
+    while (!stop) {
+      // tell the piece
+      {
+        const int e = told_n % kPieces;
+        if (more)
+          piece_of(p, w, it);
+        else
+          it.t0 = it.t1 = 0;
+        if (!wait(&piece_empty[e], ((told_n / kPieces) & 1u) ^ 1u)) break;
+        if (lane == 0) {
+          const int* from = reinterpret_cast<const int*>(&it);
+#pragma unroll
+          for (int i = 0; i < kPieceInts; ++i) told[e * kPieceInts + i] = from[i];
+          mbar_arrive(&piece_full[e]);
+        }
+        __syncwarp();
+        ++told_n;
+        if (!more) break;
+      }
+      const int32_t* table = p.paged ? p.b.page_table + it.b * p.b.table_stride : nullptr;
       auto page_of = [&](int u) {   // page of box u of the sequence
         return p.paged && u * p.box_rows < it.see_end ? table[(u * p.box_rows) >> p.page_shift] : 0;
       };
-      int c0 = w.t0 * nb;
+      int c0 = it.t0 * nb;
       int ids = page_of(c0 + lane);
-      for (int j = w.t0; j < w.t1 && !stop; ++j) {
+      for (int j = it.t0; j < it.t1 && !stop; ++j) {
         if (j * nb >= c0 + 32) {
           c0 += 32;
           ids = page_of(c0 + lane);
@@ -418,18 +571,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             if (lane == 0) {
               const int pos = j * kPosTile + i * p.box_rows;
               // a page index out of range, and rows past the packed array, read as zeros
-              const int y = p.paged ? pos & (p.c.page_size - 1) : w.s.first + pos;
+              const int y = p.paged ? pos & (p.c.page_size - 1) : it.first + pos;
 #pragma unroll
               for (int x = 0; x < kBoxes; ++x)
                 tma_load_4d(dst + x * C::kBlock + i * p.box_rows * kRowBytes, map, &bar_full[slot], x * kRowBytes, y,
-                            w.h, p.paged ? pg : 0);
+                            it.h, p.paged ? pg : 0);
             }
             __syncwarp();
           }
           if (++slot == kSt) slot = 0, phase ^= 1u;
         }
       }
-    } while (!stop && tile_next(p, w));
+      more = tile_next(p, w);
+    }
     if (*abort_flag && lane == 0) {
       // no copy in flight at exit
       for (int i = 0; i < kSt; ++i)
@@ -445,70 +599,93 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     uint32_t item = 0, pn[2] = {0, 0}, fixes = 0;
     bool ok = true;
     bool issued = false;
-    do {
-      const Item it = item_of(p, w);
-      const int nt = w.t1 - w.t0;
-      const int steps = it.two ? 2 * nt : nt;
+    Piece it;
+    while (ok && next_piece(it)) {
+      const int nt = it.t1 - it.t0;
+      const bool two = it.two();
+      const int steps = two ? 2 * nt : nt;
       auto slot_of = [&](int j, int kv) { return (pos + 2 * j + kv) % C::kStages; };
       auto par_of = [&](int j, int kv) { return ((pos + 2 * j + kv) / C::kStages) & 1u; };
+      // one lane: scores of step i (of stream i % 2)
       auto qk = [&](int i) {
-        const int s = i & 1, j = it.two ? i >> 1 : i;
+        const int s = i & 1, j = two ? i >> 1 : i;
         const uint32_t st = slot_of(j, 0);
-        if (!(it.two && s == 1)) ok = ok && wait(&full[st], par_of(j, 0));
-        if (!ok) return;
-        if (lane == 0) {
-          tc_fence_after();
-          const uint32_t a0 = q_addr + (it.two ? s * C::kTileBytes : 0), b0 = ring + st * C::kTileBytes;
+        const uint64_t a = make_smem_desc(q_addr + (two ? s * C::kTileBytes : 0), 16, 1024, kSwizzle128B);
+        const uint64_t b = make_smem_desc(ring + st * C::kTileBytes, 16, 1024, kSwizzle128B);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * C::kBlock + (k % 4) * 32;
-            mma_f16_ss(tm_s + s * 128, make_smem_desc(a0 + off, 16, 1024, kSwizzle128B),
-                       make_smem_desc(b0 + off, 16, 1024, kSwizzle128B), kIdQK, k > 0);
-          }
-          tc_commit(&s_full[s]);
-          if (!(it.two && s == 0)) tc_commit(&empty[st]);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k / 4) * C::kBlock + (k % 4) * 32) >> 4;
+          mma_f16_ss(tm_s + s * 128, a + off, b + off, kIdQK, k > 0);
         }
-        issued = true;
-        __syncwarp();
+        tc_commit(&s_full[s]);
+        if (!(two && s == 0)) tc_commit(&empty[st]);
       };
-      auto pv = [&](int i) {
-        const int s = i & 1, j = it.two ? i >> 1 : i;
+      // a step's first use of its key tile
+      auto wait_k = [&](int i) {
+        const int j = two ? i >> 1 : i;
+        if (!(two && (i & 1) == 1)) ok = ok && wait(&full[slot_of(j, 0)], par_of(j, 0));
+      };
+      ok = wait(q_full, item & 1u);
+      wait_k(0);
+      if (ok && elect_one()) {
+        tc_fence_after();
+        qk(0);
+      }
+      __syncwarp();
+      if (steps > 1) {
+        wait_k(1);
+        if (ok && elect_one()) {
+          tc_fence_after();
+          qk(1);
+        }
+        __syncwarp();
+      }
+      issued = true;
+      // with three stages and one row tile the next keys arrive only once this step's values are read
+      const bool early = C::kStages >= 5 || two;
+#pragma unroll 1
+      for (int i = 0; i < steps && ok; ++i) {
+        const int s = i & 1, j = two ? i >> 1 : i;
         const uint32_t st = slot_of(j, 1);
-        if (!(it.two && s == 1)) {
-          ok = ok && wait(&full[st], par_of(j, 1));
-          if (ok && !E4 && (w.t0 + j + 1) * kPosTile > it.see_all) {
+        const bool more = i + 2 < steps;
+        if (!(two && s == 1)) {
+          ok = wait(&full[st], par_of(j, 1));
+          if (ok && !E4 && (it.t0 + j + 1) * kPosTile > it.see_all) {
             if (lane == 0) mbar_arrive(fix_req);
             __syncwarp();
             ok = wait(fix_done, fixes & 1u);
             ++fixes;
           }
         }
+        if (more && early) wait_k(i + 2);
         ok = ok && wait(&p_full[s], pn[s] & 1u);
         ++pn[s];
-        if (!ok) return;
-        if (lane == 0) {
+        if (!ok) break;
+        if (elect_one()) {
           tc_fence_after();
-          const uint32_t b0 = ring + st * C::kTileBytes;
+          const uint64_t b = make_smem_desc(ring + st * C::kTileBytes, C::kBlock, 1024, kSwizzle128B);
 #pragma unroll
           for (int k = 0; k < kPosTile / 16; ++k)
-            mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8,
-                       make_smem_desc(b0 + k * 2048, C::kBlock, 1024, kSwizzle128B), kIdPV, i >= 2 || k > 0);   // a stream's first product starts its sum
-          if (!(it.two && s == 0)) tc_commit(&empty[st]);
-          if (i + 2 >= steps) tc_commit(&o_full[s]);
+            // (a stream's first product starts its sum)
+            mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, i >= 2 || k > 0);
+          if (!(two && s == 0)) tc_commit(&empty[st]);
+          if (!more) tc_commit(&o_full[s]);
+          if (more && early) qk(i + 2);
         }
         __syncwarp();
-      };
-      ok = ok && wait(q_full, item & 1u);
-      if (ok) qk(0);
-      if (ok && steps > 1) qk(1);
-      for (int i = 0; i < steps && ok; ++i) {
-        pv(i);
-        if (ok && i + 2 < steps) qk(i + 2);
+        if (more && !early) {
+          wait_k(i + 2);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            qk(i + 2);
+          }
+          __syncwarp();
+        }
       }
       pos += 2 * nt;
       ++item;
-    } while (ok && tile_next(p, w));
-    if (!ok && issued && lane == 0) {
+    }
+    if (*abort_flag && issued && lane == 0) {
       // no product in flight at exit: a commit covers everything issued before it
       tc_commit(drain);
       (void)mbar_wait_bounded(drain, 0, 1000000ull);
@@ -525,13 +702,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         uint32_t pos = 0, fixes = 0;
         int item = 0;
         bool ok = true;
-        do {
-          const Item it = item_of(p, w);
-          for (int j = max(w.t0, it.see_all / kPosTile); j < w.t1 && ok; ++j) {
+        Piece it;
+        while (ok && next_piece(it)) {
+          for (int j = max(it.t0, it.see_all / kPosTile); j < it.t1 && ok; ++j) {
             ok = wait(fix_req, fixes & 1u);
             ++fixes;
             if (!ok) break;
-            uint8_t* v = smem + C::kRing + ((pos + 2 * (j - w.t0) + 1) % C::kStages) * C::kTileBytes;
+            uint8_t* v = smem + C::kRing + ((pos + 2 * (j - it.t0) + 1) % C::kStages) * C::kTileBytes;
             const int from = max(it.see_all - j * kPosTile, 0);
             const int to = min(max(it.see_end - j * kPosTile, from), kPosTile);
             bool nf = false;
@@ -562,9 +739,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(fix_done);
           }
-          pos += 2 * (w.t1 - w.t0);
+          pos += 2 * (it.t1 - it.t0);
           ++item;
-        } while (ok && tile_next(p, w));
+        }
       }
     } else {
       // ===== E4M3 codes to fp16 tiles =====
@@ -572,9 +749,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
       int item = 0;
       bool ok = true;
-      do {
-        const Item it = item_of(p, w);
-        for (int j = w.t0; j < w.t1 && ok; ++j) {
+      Piece it;
+      while (ok && next_piece(it)) {
+        for (int j = it.t0; j < it.t1 && ok; ++j) {
           const int from = max(it.see_all - j * kPosTile, 0);
           const int to = min(max(it.see_end - j * kPosTile, 0), kPosTile);
           for (int kv = 0; kv < 2 && ok; ++kv) {
@@ -629,29 +806,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
         }
         ++item;
-      } while (ok && tile_next(p, w));
+      }
     }
+  }
   } else {
     // ===== softmax =====
+    setmaxnreg_inc<kRegsSoftmax>();
     const int s = warp >> 2;                       // stream
     const int r = threadIdx.x & (kRowTile - 1);    // lane of TMEM = row of the stream
     const uint32_t quad = static_cast<uint32_t>(warp & 3) << 21;   // TMEM lane 32 (warp % 4), in bits 16..
     const uint32_t ts = tm_s + s * 128 + quad, to = tm_o + s * D + quad;
     uint32_t sn = 0, on[2] = {0, 0};
     int item = 0;
-    bool ok = true;
+    uint32_t group_n = 0, both_n = 0;
+    auto meet_group = [&]() {
+      mbar_arrive(&group_bar[s]);
+      return wait(&group_bar[s], group_n++ & 1u);
+    };
+    auto meet_both = [&]() {
+      mbar_arrive(both_bar);
+      return wait(both_bar, both_n++ & 1u);
+    };
     float* other = reinterpret_cast<float*>(smem + C::kTileBytes);   // m, l of stream 1 (the unused second Q tile)
-    do {
-      const Item it = item_of(p, w);
-      const int nt = w.t1 - w.t0;
-      const int lrow = it.two ? s * kRowTile + r : r;      // row within the item
+    Piece it;
+    // a wait that ran out ends the loop at once: no barrier in it waits for ever
+    while (next_piece(it)) {
+      const int nt = it.t1 - it.t0;
+      const bool two = it.two();
+      const int lrow = two ? s * kRowTile + r : r;      // row within the item
       const bool live = lrow < it.rows;
       const int grow = it.row0 + (live ? lrow : 0);
-      const int64_t tok = w.s.first + grow / p.group;
-      const int head = w.h * p.group + grow % p.group;
-      const int see = live ? row_sees(p, w.s, grow) : 0;
+      const int64_t tok = it.first + grow / p.group;
+      const int head = it.h * p.group + grow % p.group;
+      const int see = live ? max(min(it.base + grow / p.group + 1, it.len), 0) : 0;
       float s_eff = p.scale;
-      if (E4) s_eff *= p.c.k_scale[w.h];
+      if (E4) s_eff *= p.c.k_scale[it.h];
       float c = s_eff == 0.0f ? 1.0f : fabsf(s_eff) * kLog2e;
 
       // the row of queries into shared memory (swizzled, K-major)
@@ -686,7 +875,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             u[i].w = pack_half(bf16_lo(u[i].w) * f, bf16_hi(u[i].w) * f);
           }
         }
-        if (it.two || s == 0) {
+        if (two || s == 0) {
           uint8_t* dst = smem + s * C::kTileBytes + r * 128;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
@@ -699,89 +888,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       }
 
       float m = -INFINITY, l = 0.0f;   // m in units of S
-      const int steps = it.two ? nt : (nt + 1 - s) / 2;
+      const int steps = two ? nt : (nt + 1 - s) / 2;
+      int lim = see - (it.t0 + (two ? 0 : s)) * kPosTile;     // the row sees the tile's columns below lim
+      const int lim_step = two ? kPosTile : 2 * kPosTile;
+      bool started = false;
+#pragma unroll 1
       for (int k = 0; k < steps; ++k) {
-        const int j = w.t0 + (it.two ? k : 2 * k + s);
-        ok = ok && wait(&s_full[s], sn & 1u);
-        ++sn;
-        if (!ok) continue;
+        if (!wait(&s_full[s], sn++ & 1u)) break;
         tc_fence_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + i * 32, x + i * 32);
-        tmem_ld_wait();
-        loaded(x);
-        const int lim = see - j * kPosTile;     // the row sees columns below
-        if (__any_sync(0xffffffffu, lim < kPosTile)) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= lim) x[i] = 0xff800000u;
-        }
-        float top[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
-#pragma unroll
-        for (int i = 8; i < 128; i += 8)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            top[q] = fmaxf(top[q], fmaxf(__uint_as_float(x[i + q]), __uint_as_float(x[i + q + 4])));
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        const bool up = (mx - m) * c > kRaise;      // false for -inf - -inf
-        if (__any_sync(0xffffffffu, up)) {
-          const float f = up ? exp2_approx((m - mx) * c) : 1.0f;
-          if (up) m = mx;
-          l *= f;
-          if (k > 0) {
-            // every product into O is complete: the scores' commit came after them
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(to + i * 32, o);
-              tmem_ld_wait();
-              loaded(o);
-#pragma unroll
-              for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
-              tmem_st_32x32b_x32(to + i * 32, o);
-            }
-          }
-        }
-        const float mc = m == -INFINITY ? 0.0f : m * c;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const float a = exp2_approx(fmaf(__uint_as_float(x[i * 32 + 2 * q]), c, -mc));
-            const float b = exp2_approx(fmaf(__uint_as_float(x[i * 32 + 2 * q + 1]), c, -mc));
-            sum[q & 3] += a + b;
-            // the weights as 16-bit operands (each within 2^-8 of itself, 2^-11 in fp16)
-            pk[q] = E4 ? pack_half(a, b) : pack_bf16(a, b);
-          }
-          // over the scores that have been read
-          tmem_st_32x32b_x16(ts + i * 16, pk);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        softmax_tile<D, E4>(ts, to, c, lim, started, m, l);
+        started = true;
+        lim -= lim_step;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_full[s]);
       }
 
       // ===== the piece's result =====
-      if (steps > 0) {
-        ok = ok && wait(&o_full[s], on[s] & 1u);
-        ++on[s];
-      }
+      if (steps > 0 && !wait(&o_full[s], on[s]++ & 1u)) break;
       float f0 = 1.0f, f1 = 0.0f;      // factors of the two streams' outputs
       bool both = false;
-      if (!it.two) {
+      if (!two) {
         if (s == 1) other[r] = m, other[kRowTile + r] = l;
-        bar_softmax();
+        if (!meet_both()) break;
         if (s == 0) {
           both = nt > 1;
           if (both) {
-            ok = ok && wait(&o_full[1], on[1] & 1u);
-            ++on[1];
+            if (!wait(&o_full[1], on[1]++ & 1u)) break;
             const float m1 = other[r], l1 = other[kRowTile + r];
             const float mm = fmaxf(m, m1);
             const float base = mm == -INFINITY ? 0.0f : mm;
@@ -795,14 +928,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         ++on[1];     // keep count of the other stream's outputs
       }
       tc_fence_after();
-      // (after a wait that ran out the rest still runs: its barriers count every warp)
-      if (it.two || s == 0) {
-        const bool whole = w.t0 == 0 && w.t1 == w.nt;
-        const float vscale = E4 ? p.c.v_scale[w.h] : 1.0f;
+      if (two || s == 0) {
+        const bool whole = it.whole != 0;
+        const float vscale = E4 ? p.c.v_scale[it.h] : 1.0f;
         const bool nf = nf_item[item & 7] == item + 1;
-        const uint64_t range0 = blockIdx.x * w.total / w.ctas;
         constexpr int kPart = (2 + D) * kItemRows / 4;      // float4s of a partial result: m c, l, O [D / 4][256]
-        float4* part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (w.x == range0 ? 0 : 1)) * kPart;
+        float4* part = p.partials + static_cast<int64_t>(it.slot) * kPart;
         const int prow = s * kRowTile + r;
         auto put = [&](int i, const float* o, float sum) {   // 8 outputs from element i on
           uint4 v = make_uint4(0, 0, 0, 0);
@@ -825,7 +956,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           float a[32];
 #pragma unroll
           for (int q = 0; q < 32; ++q) a[q] = __uint_as_float(o[q]);
-          if (!it.two && both) {
+          if (!two && both) {
             tmem_ld_32x32b_x32(tm_o + D + quad + i, o);
             tmem_ld_wait();
             loaded(o);
@@ -834,19 +965,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
           if (nf) {
             // the non-finite values that were taken out, where this row sees them
-            const int to_pos = min(see, w.t1 * kPosTile);
-            for (int pos = max(it.see_all, w.t0 * kPosTile); pos < to_pos; ++pos) {
+            const int to_pos = min(see, it.t1 * kPosTile);
+            for (int pos = max(it.see_all, it.t0 * kPosTile); pos < to_pos; ++pos) {
               if (!p.paged) {
-                const __nv_bfloat16* v = p.v.p + (w.s.first + pos) * p.v.ts + w.h * p.v.hs + i;
+                const __nv_bfloat16* v = p.v.p + (it.first + pos) * p.v.ts + it.h * p.v.hs + i;
 #pragma unroll
                 for (int q = 0; q < 32; ++q) {
                   const float e = __bfloat162float(v[q]);
                   if (!(fabsf(e) < INFINITY)) a[q] += e;
                 }
               } else {
-                const int pg = p.b.page_table[w.b * p.b.table_stride + (pos >> p.page_shift)];
+                const int pg = p.b.page_table[it.b * p.b.table_stride + (pos >> p.page_shift)];
                 if (pg < 0 || pg >= p.c.num_pages) continue;
-                const int64_t at = pg * p.c.v_page_stride + w.h * p.c.v_head_stride +
+                const int64_t at = pg * p.c.v_page_stride + it.h * p.c.v_head_stride +
                                    (pos & (p.c.page_size - 1)) * p.c.v_token_stride + i;
 #pragma unroll
                 for (int q = 0; q < 32; ++q) {
@@ -875,27 +1006,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           float* pf = reinterpret_cast<float*>(part);
           pf[prow] = mc;
           pf[kItemRows + prow] = l;
-          // the blocks that hold the item's first and last tile
-          const int first = static_cast<int>(((w.item0 + 1) * w.ctas - 1) / w.total);
-          const int last = static_cast<int>(((w.item0 + w.nt) * w.ctas - 1) / w.total);
-          const int pieces = last - first + 1;
+          const int first = it.first_cta, pieces = it.pieces;
           __threadfence();
-          bar_group(s);
+          if (!meet_group()) break;
           if (r == 0) {
             const uint32_t before = atomicAdd(p.counters + 2 * first + s, 1u);
             const int is_last = before == static_cast<uint32_t>(pieces - 1);
             if (is_last) p.counters[2 * first + s] = 0;
             last_flag[s] = is_last;
           }
-          bar_group(s);
+          if (!meet_group()) break;
           if (last_flag[s] && live) {
             __threadfence();
-            // the first piece starts its block's range, or follows other items in it
-            const bool at_start = first * w.total / w.ctas == w.item0;
             auto piece = [&](int k) {
-              const int64_t n = k == 0 ? 2 * static_cast<int64_t>(first) + (at_start ? 0 : 1)
-                                       : 2 * static_cast<int64_t>(first + k);
-              return p.partials + n * kPart;
+              return p.partials + static_cast<int64_t>(k == 0 ? it.slot0 : 2 * (first + k)) * kPart;
             };
             float top = -INFINITY;
             for (int k = 0; k < pieces; ++k) top = fmaxf(top, __ldcg(reinterpret_cast<const float*>(piece(k)) + prow));
@@ -927,9 +1051,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         }
         tc_fence_before();
       }
-      if (!it.two) bar_softmax();    // both streams' outputs and `other` are free again
+      if (!two && !meet_both()) break;    // both streams' outputs and `other` are free again
       ++item;
-    } while (tile_next(p, w));
+    }
   }
 
   tc_fence_before();

@@ -20,7 +20,31 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
+// Registers of a warp's threads from here on, executed alike by the four warps
+// of a warpgroup. What one group takes another has to have given back: the sum
+// over the block stays within its registers at launch.
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ bool elect_lane0() { return (threadIdx.x & 31) == 0; }
+
+// True in one lane of a converged warp; the compiler knows that the branch it
+// guards runs in one lane and keeps its operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 
 // ----------------------------------------------------------------------------
 // mbarrier

@@ -592,103 +592,131 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     __syncwarp();
   } else if (warp == 9) {
     // ===== products =====
-    constexpr uint32_t kIdQK = idesc_f16(128, 128, !E4, false);
-    constexpr uint32_t kIdPV = idesc_f16(128, D, !E4, true);
-    const uint32_t q_addr = smem_u32(smem), ring = smem_u32(smem + C::kRing);
-    uint32_t pos = 0;               // ring position (keys and values alternating) of the piece's first tile
-    uint32_t item = 0, pn[2] = {0, 0}, fixes = 0;
-    bool ok = true;
-    bool issued = false;
-    Piece it;
-    while (ok && next_piece(it)) {
-      const int nt = it.t1 - it.t0;
-      const bool two = it.two();
-      const int steps = two ? 2 * nt : nt;
-      auto slot_of = [&](int j, int kv) { return (pos + 2 * j + kv) % C::kStages; };
-      auto par_of = [&](int j, int kv) { return ((pos + 2 * j + kv) / C::kStages) & 1u; };
-      // one lane: scores of step i (of stream i % 2)
-      auto qk = [&](int i) {
-        const int s = i & 1, j = two ? i >> 1 : i;
-        const uint32_t st = slot_of(j, 0);
-        const uint64_t a = make_smem_desc(q_addr + (two ? s * C::kTileBytes : 0), 16, 1024, kSwizzle128B);
-        const uint64_t b = make_smem_desc(ring + st * C::kTileBytes, 16, 1024, kSwizzle128B);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k / 4) * C::kBlock + (k % 4) * 32) >> 4;
-          mma_f16_ss(tm_s + s * 128, a + off, b + off, kIdQK, k > 0);
+    // One lane does it all: between two products there is no time for a
+    // warp's votes (a wait of the whole warp takes some 130 cycles even where
+    // the barrier is ready, two products' worth).
+    if (elect_one()) {
+      constexpr uint32_t kIdQK = idesc_f16(128, 128, !E4, false);
+      constexpr uint32_t kIdPV = idesc_f16(128, D, !E4, true);
+      const uint32_t q_addr = smem_u32(smem), ring = smem_u32(smem + C::kRing);
+      uint32_t slot = 0, phase = 0;   // ring position (keys and values alternating) of the piece's first tile
+      uint32_t item = 0, fixes = 0, p_phase = 0;   // p_phase: bit s for stream s
+      bool ok = true, issued = false;
+      auto wait1 = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t polls = 1;; ++polls) {
+          if (mbar_try_wait(bar, parity)) return true;
+          if ((polls & 63u) == 0u && (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs)) break;
         }
-        tc_commit(&s_full[s]);
-        if (!(two && s == 0)) tc_commit(&empty[st]);
+        *abort_flag = 1;
+        record_status(p.status, EPILORA_ERR_TIMEOUT);
+        return false;
       };
-      // a step's first use of its key tile
-      auto wait_k = [&](int i) {
-        const int j = two ? i >> 1 : i;
-        if (!(two && (i & 1) == 1)) ok = ok && wait(&full[slot_of(j, 0)], par_of(j, 0));
-      };
-      ok = wait(q_full, item & 1u);
-      wait_k(0);
-      if (ok && elect_one()) {
+      while (ok) {
+        // the piece
+        const int e = told_n % kPieces;
+        if (!(ok = wait1(&piece_full[e], (told_n / kPieces) & 1u))) break;
+        Piece it;
+        int* to = reinterpret_cast<int*>(&it);
+#pragma unroll
+        for (int i = 0; i < kPieceInts; ++i) to[i] = told[e * kPieceInts + i];
+        mbar_arrive(&piece_empty[e]);
+        ++told_n;
+        const int nt = it.t1 - it.t0;
+        if (nt <= 0) break;
+        const bool two = it.two();
+        const int steps = two ? 2 * nt : nt;
+        // ring slots and parities: keys and values of the next step's tile
+        struct Ring {
+          uint32_t slot, phase;
+          __device__ __forceinline__ void skip(uint32_t n) {
+            slot += n;
+            if (slot >= C::kStages) slot -= C::kStages, phase ^= 1u;
+          }
+        };
+        Ring kr{slot, phase}, vr{slot, phase};
+        vr.skip(1);
+        // scores of step i (of stream i % 2)
+        auto wait_k = [&](int i) {
+          if (!(two && (i & 1) == 1)) ok = ok && wait1(&full[kr.slot], kr.phase);
+        };
+        auto qk = [&](int i) {
+          const int s = i & 1;
+          const uint64_t a = make_smem_desc(q_addr + (two ? s * C::kTileBytes : 0), 16, 1024, kSwizzle128B);
+          const uint64_t b = make_smem_desc(ring + kr.slot * C::kTileBytes, 16, 1024, kSwizzle128B);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k / 4) * C::kBlock + (k % 4) * 32) >> 4;
+            mma_f16_ss(tm_s + s * 128, a + off, b + off, kIdQK, k > 0);
+          }
+          tc_commit(&s_full[s]);
+          if (!(two && s == 0)) {
+            tc_commit(&empty[kr.slot]);
+            kr.skip(2);
+          }
+        };
+        ok = wait1(q_full, item & 1u);
+        wait_k(0);
+        if (!ok) break;
         tc_fence_after();
         qk(0);
-      }
-      __syncwarp();
-      if (steps > 1) {
-        wait_k(1);
-        if (ok && elect_one()) {
+        issued = true;
+        if (steps > 1) {
+          wait_k(1);
+          if (!ok) break;
           tc_fence_after();
           qk(1);
         }
-        __syncwarp();
-      }
-      issued = true;
-      // with three stages and one row tile the next keys arrive only once this step's values are read
-      const bool early = C::kStages >= 5 || two;
+        // with three stages and one row tile the next keys arrive only once this step's values are read
+        const bool early = C::kStages >= 5 || two;
 #pragma unroll 1
-      for (int i = 0; i < steps && ok; ++i) {
-        const int s = i & 1, j = two ? i >> 1 : i;
-        const uint32_t st = slot_of(j, 1);
-        const bool more = i + 2 < steps;
-        if (!(two && s == 1)) {
-          ok = wait(&full[st], par_of(j, 1));
-          if (ok && !E4 && (it.t0 + j + 1) * kPosTile > it.see_all) {
-            if (lane == 0) mbar_arrive(fix_req);
-            __syncwarp();
-            ok = wait(fix_done, fixes & 1u);
-            ++fixes;
+        for (int i = 0; i < steps; ++i) {
+          const int s = i & 1, j = two ? i >> 1 : i;
+          const bool more = i + 2 < steps;
+          if (!(two && s == 1)) {
+            ok = wait1(&full[vr.slot], vr.phase);
+            if (ok && !E4 && (it.t0 + j + 1) * kPosTile > it.see_all) {
+              mbar_arrive(fix_req);
+              ok = wait1(fix_done, fixes & 1u);
+              ++fixes;
+            }
           }
-        }
-        if (more && early) wait_k(i + 2);
-        ok = ok && wait(&p_full[s], pn[s] & 1u);
-        ++pn[s];
-        if (!ok) break;
-        if (elect_one()) {
+          if (more && early) wait_k(i + 2);
+          ok = ok && wait1(&p_full[s], (p_phase >> s) & 1u);
+          p_phase ^= 1u << s;
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t b = make_smem_desc(ring + st * C::kTileBytes, C::kBlock, 1024, kSwizzle128B);
+          const uint64_t b = make_smem_desc(ring + vr.slot * C::kTileBytes, C::kBlock, 1024, kSwizzle128B);
 #pragma unroll
           for (int k = 0; k < kPosTile / 16; ++k)
             // (a stream's first product starts its sum)
             mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, i >= 2 || k > 0);
-          if (!(two && s == 0)) tc_commit(&empty[st]);
+          if (!(two && s == 0)) {
+            tc_commit(&empty[vr.slot]);
+            vr.skip(2);
+          }
           if (!more) tc_commit(&o_full[s]);
-          if (more && early) qk(i + 2);
-        }
-        __syncwarp();
-        if (more && !early) {
-          wait_k(i + 2);
-          if (ok && elect_one()) {
-            tc_fence_after();
+          if (more) {
+            if (!early) {
+              wait_k(i + 2);
+              if (!ok) break;
+              tc_fence_after();
+            }
             qk(i + 2);
           }
-          __syncwarp();
         }
+        // 2 nt tiles further
+        const uint32_t turned = slot + 2 * static_cast<uint32_t>(nt);
+        slot = turned % C::kStages;
+        phase ^= (turned / C::kStages) & 1u;
+        ++item;
       }
-      pos += 2 * nt;
-      ++item;
-    }
-    if (*abort_flag && issued && lane == 0) {
-      // no product in flight at exit: a commit covers everything issued before it
-      tc_commit(drain);
-      (void)mbar_wait_bounded(drain, 0, 1000000ull);
+      if (!ok && issued) {
+        // no product in flight at exit: a commit covers everything issued before it
+        tc_commit(drain);
+        (void)mbar_wait_bounded(drain, 0, 1000000ull);
+      }
     }
     __syncwarp();
   } else if (warp >= 10) {

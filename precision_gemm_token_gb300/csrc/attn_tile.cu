@@ -45,7 +45,8 @@ constexpr int kPosTile = 128;      // positions per tile
 constexpr int kRowTile = 128;      // rows per stream
 constexpr int kItemRows = 2 * kRowTile;
 constexpr int kTileMaxCtas = 512;
-constexpr int kGroups = 128;       // entries of the block's table of sequence weights
+constexpr int kGroups = 256;       // entries of the block's table of sequence weights
+constexpr int kItemCost = 2;       // cost of an item besides its tiles, in tiles
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
 // a row's maximum is raised (and its sums rescaled) only when a score exceeds
 // it by this many powers of two: weights stay below 2^8, in range for the
@@ -65,14 +66,15 @@ struct TileCfg {
   static constexpr int kRawStages = E4 ? 4 : 0;
   static constexpr int kRing = kQBytes, kRaw = kRing + kStages * kTileBytes;
   static constexpr int kPlan = kRaw + kRawStages * kRawBytes;
-  static constexpr int kBars = kPlan + kGroups * 8;
+  static constexpr int kBars = kPlan + kGroups * 4;
   static constexpr int kPieceAt = kBars + 384;
   static constexpr int kBytes = kPieceAt + kPieces * kPieceInts * 4;
   static constexpr int kSmem = 1024 + kBytes;
 };
 
 struct TileParams {
-  CUtensorMap tk, tv;
+  CUtensorMap tk, tv, tq;
+  int q_tma;               // queries are copied by TMA (see q_boxes_fit)
   epilora_kv_batch b;
   epilora_kv_cache c;      // paged
   AttnRows q, k, v;        // k, v: prompts
@@ -118,51 +120,54 @@ __device__ __forceinline__ int item_tiles(const TileParams& p, const TileSeq& s,
   return max((e + kPosTile - 1) / kPosTile, 1);
 }
 
-__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   return v;
 }
 
-// position tiles of all row tiles of a sequence, one key/value head (whole warp)
-__device__ __forceinline__ uint64_t seq_weight(const TileParams& p, int b, int lane, bool& bad) {
+// The line: every item takes item_tiles units, after kItemCost units that
+// stand for what an item costs besides its tiles (queries, the first tile's
+// maximum, the output); a piece is a run of units of one item.
+// units of all row tiles of a sequence, one key/value head (whole warp)
+__device__ __forceinline__ uint32_t seq_weight(const TileParams& p, int b, int lane, bool& bad) {
   const TileSeq s = tile_seq(p, b, bad);
-  uint64_t w = 0;
-  for (int rt = lane; rt < s.rts; rt += 32) w += item_tiles(p, s, rt);
-  return warp_sum(w);
+  uint32_t w = 0;
+  for (int rt = lane; rt < s.rts; rt += 32) w += kItemCost + item_tiles(p, s, rt);
+  return __reduce_add_sync(0xffffffffu, w);
 }
 
-// Walks the pieces of a thread block's range of the line of tiles (one warp).
+// Walks the pieces of a thread block's range of the line (one warp).
 struct TileWalk {
-  uint64_t x, end, total;
-  int ctas;
+  uint32_t x, end;     // units still to do
+  uint32_t each, more; // units per block: each + 1 for the first `more` blocks, else each
   int b, h, rt;
   TileSeq s;
-  int nt;            // tiles of the item
-  int t0, t1;        // this piece's
-  uint64_t item0;    // line position of the item's tile 0
+  int nt;              // tiles of the item
+  int u0, u1;          // this piece's units of it
+  uint32_t item0;      // line position of the item's first unit
+  __device__ __forceinline__ uint32_t start_of(uint32_t cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ uint32_t owner_of(uint32_t unit) const {
+    const uint32_t low = more * (each + 1);
+    return unit < low ? unit / (each + 1) : more + (unit - low) / each;
+  }
 };
 
 __device__ __forceinline__ void tile_piece(TileWalk& w) {
-  w.t0 = static_cast<int>(w.x - w.item0);
-  w.t1 = static_cast<int>(min(static_cast<uint64_t>(w.nt - w.t0), w.end - w.x)) + w.t0;
+  w.u0 = static_cast<int>(w.x - w.item0);
+  w.u1 = static_cast<int>(min(static_cast<uint32_t>(kItemCost + w.nt - w.u0), w.end - w.x)) + w.u0;
 }
 
 // The table of sequence weights, by the whole block.
-__device__ __forceinline__ void tile_plan(const TileParams& p, uint64_t* plan, int warp, int lane) {
+__device__ __forceinline__ void tile_plan(const TileParams& p, uint32_t* plan, int warp, int lane) {
   const int per = (p.b.n_seqs + kGroups - 1) / kGroups;     // sequences per table entry
   const int entries = per == 0 ? 0 : (p.b.n_seqs + per - 1) / per;
   bool bad = false;
   for (int e = warp; e < entries; e += kTileThreads / 32) {
-    uint64_t v = 0;
+    uint32_t v = 0;
     for (int b = e * per; b < min((e + 1) * per, p.b.n_seqs); ++b) v += seq_weight(p, b, lane, bad);
     if (lane == 0) plan[e] = v;
   }
@@ -171,36 +176,38 @@ __device__ __forceinline__ void tile_plan(const TileParams& p, uint64_t* plan, i
 }
 
 // One warp; false: nothing to do.
-__device__ __forceinline__ bool tile_begin(const TileParams& p, TileWalk& w, const uint64_t* plan, int lane) {
+__device__ __forceinline__ bool tile_begin(const TileParams& p, TileWalk& w, const uint32_t* plan, int lane) {
   const int per = (p.b.n_seqs + kGroups - 1) / kGroups;
   const int entries = per == 0 ? 0 : (p.b.n_seqs + per - 1) / per;
   bool bad = false;
-  uint64_t mine[kGroups / 32], sum = 0;
+  constexpr int kMine = kGroups / 32;
+  uint32_t mine[kMine], sum = 0;
 #pragma unroll
-  for (int i = 0; i < kGroups / 32; ++i) {
-    const int e = lane * (kGroups / 32) + i;
+  for (int i = 0; i < kMine; ++i) {
+    const int e = lane * kMine + i;
     mine[i] = e < entries ? plan[e] * p.kv_heads : 0;
     sum += mine[i];
   }
-  const uint64_t inc = warp_scan(sum, lane);
-  w.total = __shfl_sync(0xffffffffu, inc, 31);
-  if (w.total == 0) return false;
-  w.ctas = static_cast<int>(min(static_cast<uint64_t>(gridDim.x), w.total));
-  if (static_cast<int>(blockIdx.x) >= w.ctas) return false;
-  w.x = blockIdx.x * w.total / w.ctas;
-  w.end = (blockIdx.x + 1) * w.total / w.ctas;
+  const uint32_t inc = warp_scan(sum, lane);
+  const uint32_t total = __shfl_sync(0xffffffffu, inc, 31);
+  const uint32_t ctas = min(gridDim.x, total);
+  if (blockIdx.x >= ctas) return false;
+  w.each = total / ctas;
+  w.more = total - w.each * ctas;
+  w.x = w.start_of(blockIdx.x);
+  w.end = w.start_of(blockIdx.x + 1);
   // the table entry that holds x
   const uint32_t hit = __ballot_sync(0xffffffffu, inc > w.x);
   const int l = __ffs(hit) - 1;
-  uint64_t at = inc - sum;
-  int e = lane * (kGroups / 32);
+  uint32_t at = inc - sum;
+  int e = lane * kMine;
 #pragma unroll
-  for (int i = 0; i < kGroups / 32 - 1; ++i)
-    if (at + mine[i] <= w.x && e == lane * (kGroups / 32) + i) at += mine[i], ++e;
+  for (int i = 0; i < kMine - 1; ++i)
+    if (at + mine[i] <= w.x && e == lane * kMine + i) at += mine[i], ++e;
   at = __shfl_sync(0xffffffffu, at, l);
   e = __shfl_sync(0xffffffffu, e, l);
   // the sequence in it
-  uint64_t weight = 0;
+  uint32_t weight = 0;
   int b = e * per;
   for (;; ++b) {
     if (b >= p.b.n_seqs) return false;   // metadata changed under the call
@@ -215,13 +222,13 @@ __device__ __forceinline__ bool tile_begin(const TileParams& p, TileWalk& w, con
   // the row tile
   for (int r0 = 0;; r0 += 32) {
     if (r0 >= w.s.rts) return false;
-    const uint64_t c = r0 + lane < w.s.rts ? item_tiles(p, w.s, r0 + lane) : 0;
-    const uint64_t in = warp_scan(c, lane);
+    const uint32_t c = r0 + lane < w.s.rts ? kItemCost + item_tiles(p, w.s, r0 + lane) : 0;
+    const uint32_t in = warp_scan(c, lane);
     const uint32_t found = __ballot_sync(0xffffffffu, at + in > w.x);
     if (found != 0) {
       const int k = __ffs(found) - 1;
       w.rt = r0 + k;
-      w.nt = static_cast<int>(__shfl_sync(0xffffffffu, c, k));
+      w.nt = static_cast<int>(__shfl_sync(0xffffffffu, c, k)) - kItemCost;
       w.item0 = at + __shfl_sync(0xffffffffu, in - c, k);
       break;
     }
@@ -232,9 +239,9 @@ __device__ __forceinline__ bool tile_begin(const TileParams& p, TileWalk& w, con
 }
 
 __device__ __forceinline__ bool tile_next(const TileParams& p, TileWalk& w) {
-  w.x += w.t1 - w.t0;
+  w.x += w.u1 - w.u0;
   if (w.x >= w.end) return false;
-  w.item0 += w.nt;
+  w.item0 += kItemCost + w.nt;
   if (++w.rt == w.s.rts) {
     w.rt = 0;
     if (++w.h == p.kv_heads) {
@@ -276,15 +283,16 @@ __device__ __forceinline__ void piece_of(const TileParams& p, const TileWalk& w,
   q.rows = min(kItemRows, w.s.n * p.group - q.row0);
   q.see_all = row_sees(p, w.s, q.row0);
   q.see_end = row_sees(p, w.s, q.row0 + q.rows - 1);
-  q.t0 = w.t0;
-  q.t1 = w.t1;
-  q.whole = w.t0 == 0 && w.t1 == w.nt;
+  q.t0 = max(w.u0 - kItemCost, 0);
+  q.t1 = max(w.u1 - kItemCost, 0);
+  q.whole = q.t0 == 0 && q.t1 == w.nt;
   // the blocks that hold the item's first and last tile
-  q.first_cta = static_cast<int>(((w.item0 + 1) * w.ctas - 1) / w.total);
-  q.pieces = static_cast<int>(((w.item0 + w.nt) * w.ctas - 1) / w.total) - q.first_cta + 1;
+  const uint32_t tile0 = w.item0 + kItemCost;
+  q.first_cta = static_cast<int>(w.owner_of(tile0));
+  q.pieces = static_cast<int>(w.owner_of(tile0 + w.nt - 1)) - q.first_cta + 1;
   // a piece that starts its block's range goes to the block's slot 0, the one that ends it to slot 1
-  q.slot = 2 * blockIdx.x + (w.x == blockIdx.x * w.total / w.ctas ? 0 : 1);
-  q.slot0 = 2 * q.first_cta + (q.first_cta * w.total / w.ctas == w.item0 ? 0 : 1);
+  q.slot = 2 * blockIdx.x + (w.x == w.start_of(blockIdx.x) ? 0 : 1);
+  q.slot0 = 2 * q.first_cta + (w.start_of(q.first_cta) >= w.item0 ? 0 : 1);
 }
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
@@ -315,14 +323,36 @@ __device__ __forceinline__ bool e4m3x4_nan(uint32_t v) {
 // One tile of scores to weights; a thread owns a row, m is in units of S, the
 // row sees columns below lim. The weights are taken against the maximum so
 // far while the tile's own is being found, 32 columns at a time; only where it
-// rises by more than kRaise (a row's first tile, then hardly ever) is the row
-// of O rescaled and the tile taken again.
+// rises by more than kRaise (hardly ever) is the row of O rescaled and the tile
+// taken again.
 template <int D, bool E4>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, int lim, bool started, float& m,
                                              float& l) {
   uint32_t pk[64];
   float add;
   const bool edge = __any_sync(0xffffffffu, lim < kPosTile);
+  auto hide = [&](uint32_t (&v)[32], int g) {
+    const int n = lim - 32 * g;
+    const uint32_t seen = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(seen & (1u << i))) v[i] = 0xff800000u;
+  };
+  if (!started) {
+    // a row's first tile: its maximum first
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int g = 0; g < 4; ++g) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(ts + g * 32, v);
+      tmem_ld_wait();
+      loaded(v);
+      if (edge) hide(v, g);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+    }
+    m = top;
+  }
 #pragma unroll 1
   while (true) {
     const float mc = m == -INFINITY ? 0.0f : m * c;
@@ -335,13 +365,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
       tmem_ld_wait();
       loaded(v);
       if (g < 3) tmem_ld_32x32b_x32(ts + (g + 1) * 32, x[(g + 1) & 1]);
-      if (edge) {
-        const int n = lim - 32 * g;
-        const uint32_t seen = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (!(seen & (1u << i))) v[i] = 0xff800000u;
-      }
+      if (edge) hide(v, g);
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
         top[0] = fmaxf(top[0], fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
@@ -363,7 +387,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
     const float f = up ? exp2_approx((m - mx) * c) : 1.0f;
     if (up) m = mx;
     l *= f;
-    if (started) {
+    if (started) {   // (else the row's first tile: nothing in O yet)
       // every product into O is complete: the scores' commit came after them
 #pragma unroll 1
       for (int i = 0; i < D / 16; ++i) {
@@ -388,13 +412,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   using C = TileCfg<D, E4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* plan = reinterpret_cast<uint64_t*>(smem + C::kPlan);
+  uint32_t* plan = reinterpret_cast<uint32_t*>(smem + C::kPlan);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);   // [stages] tile complete
   uint64_t* empty = full + C::kStages;                             // [stages] tile read
   uint64_t* raw_full = empty + C::kStages;                         // [raw stages] codes complete
   uint64_t* raw_empty = raw_full + C::kRawStages;
-  uint64_t* q_full = raw_empty + C::kRawStages;                    // the item's queries are in place
-  uint64_t* s_full = q_full + 1;                                   // [2] scores complete
+  uint64_t* q_full = raw_empty + C::kRawStages;                    // the piece's queries are in place
+  uint64_t* q_free = q_full + 1;                                   // and have been read
+  uint64_t* s_full = q_free + 1;                                   // [2] scores complete
   uint64_t* p_full = s_full + 2;                                   // [2] weights written
   uint64_t* o_full = p_full + 2;                                   // [2] output complete
   uint64_t* fix_req = o_full + 2;                                  // a value tile is to be cleaned
@@ -420,7 +445,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 2);
     }
-    mbar_init(q_full, kItemRows);
+    mbar_init(q_full, p.q_tma ? 1 : kItemRows);
+    mbar_init(q_free, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], kRowTile);
@@ -431,7 +457,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     mbar_init(drain, 1);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&piece_full[i], 1);
-      mbar_init(&piece_empty[i], E4 ? 11 : 10);     // 8 softmax warps, the products', the cleaning or converting ones
+      mbar_init(&piece_empty[i], 11);   // 8 softmax warps, the products', and the last two
     }
     for (int i = 0; i < 2; ++i) mbar_init(&group_bar[i], kRowTile);
     mbar_init(both_bar, kItemRows);
@@ -440,6 +466,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     fence_mbarrier_init();
     tma_prefetch_desc(&p.tk);
     tma_prefetch_desc(&p.tv);
+    if (p.q_tma) tma_prefetch_desc(&p.tq);
   }
   pdl_wait_primary();
 
@@ -519,13 +546,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     Piece it;
     bool more = tile_begin(p, w, plan, lane), stop = false;
     while (!stop) {
-      // tell the piece
+      // tell the piece (one that holds no tile of its item is left out)
       {
         const int e = told_n % kPieces;
-        if (more)
+        it.t0 = it.t1 = 0;
+        while (more) {
           piece_of(p, w, it);
-        else
-          it.t0 = it.t1 = 0;
+          if (it.t1 > it.t0) break;
+          more = tile_next(p, w);
+        }
         if (!wait(&piece_empty[e], ((told_n / kPieces) & 1u) ^ 1u)) break;
         if (lane == 0) {
           const int* from = reinterpret_cast<const int*>(&it);
@@ -655,6 +684,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             tc_commit(&empty[kr.slot]);
             kr.skip(2);
           }
+          if (i + 1 == steps) tc_commit(q_free);
         };
         ok = wait1(q_full, item & 1u);
         wait_k(0);
@@ -770,6 +800,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           pos += 2 * (it.t1 - it.t0);
           ++item;
         }
+      } else {
+        // ===== copies of queries =====
+        fence_proxy_async_global();
+        uint32_t item = 0;
+        Piece it;
+        while (next_piece(it)) {
+          if (!p.q_tma) continue;
+          // the last piece's products have read its queries
+          if (!wait(q_free, (item & 1u) ^ 1u)) break;
+          if (lane == 0) {
+            const int tiles = it.two() ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, tiles * C::kTileBytes);
+            for (int t = 0; t < tiles; ++t)
+#pragma unroll
+              for (int x = 0; x < D / 64; ++x)
+                tma_load_4d(smem + t * C::kTileBytes + x * C::kBlock, &p.tq, q_full, x * 128, it.h * p.group,
+                            it.first + (it.row0 + t * kRowTile) / p.group, 0);
+          }
+          __syncwarp();
+          ++item;
+        }
+        if (*abort_flag && item > 0) (void)mbar_wait_bounded(q_full, (item - 1) & 1u, 1000000ull);   // no copy in flight at exit
       }
     } else {
       // ===== E4M3 codes to fp16 tiles =====
@@ -855,7 +907,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       mbar_arrive(both_bar);
       return wait(both_bar, both_n++ & 1u);
     };
-    float* other = reinterpret_cast<float*>(smem + C::kTileBytes);   // m, l of stream 1 (the unused second Q tile)
+    float* other = reinterpret_cast<float*>(smem + C::kPlan);   // m, l of stream 1 (the plan has been read)
     Piece it;
     // a wait that ran out ends the loop at once: no barrier in it waits for ever
     while (next_piece(it)) {
@@ -871,8 +923,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       if (E4) s_eff *= p.c.k_scale[it.h];
       float c = s_eff == 0.0f ? 1.0f : fabsf(s_eff) * kLog2e;
 
-      // the row of queries into shared memory (swizzled, K-major)
-      {
+      // the row of queries into shared memory (swizzled, K-major), where no copy does it
+      if (E4 || !p.q_tma) {
         const __nv_bfloat16* src = p.q.p + tok * p.q.ts + head * p.q.hs;
         const bool use = live && s_eff != 0.0f;
         const uint32_t flip = s_eff < 0.0f ? 0x80008000u : 0u;
@@ -1092,6 +1144,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   }
 }
 
+// Whether a tile's 128 rows are a box [tokens][group heads] of the queries, to
+// be used as they are: the group divides the tile, the scale needs no change of
+// sign. (Other queries are loaded by the softmax threads, which then start a
+// piece only when the last one's output is written: 3.5 us later.)
+bool q_boxes_fit(const TileParams& p, const AttnArgs& a) { return kRowTile % p.group == 0 && a.scale > 0.0f; }
+
 template <int D, bool E4>
 int launch(const AttnArgs& a, TileParams& p) {
   using C = TileCfg<D, E4>;
@@ -1115,6 +1173,15 @@ int launch(const AttnArgs& a, TileParams& p) {
     const uint64_t vs[3] = {a.v.ts * es, a.v.hs * es, a.v.ts * es * T};
     rc = make_tma_4d_u8(&p.tk, a.k.p, dims, ks, box, 128);
     if (rc == EPILORA_OK) rc = make_tma_4d_u8(&p.tv, a.v.p, dims, vs, box, 128);
+  }
+  if (rc == EPILORA_OK && !E4 && q_boxes_fit(p, a)) {
+    const uint64_t T = static_cast<uint64_t>(a.batch.n_tokens);
+    const uint64_t dims[4] = {D * 2, static_cast<uint64_t>(a.heads), T, 1};
+    const uint32_t box[4] = {128, static_cast<uint32_t>(p.group), static_cast<uint32_t>(kRowTile / p.group), 1};
+    const uint64_t hs = a.q.hs * es, ts = a.q.ts * es;
+    const uint64_t qs[3] = {hs, ts, ts * T};
+    rc = make_tma_4d_u8(&p.tq, a.q.p, dims, qs, box, 128);
+    p.q_tma = 1;
   }
   if (rc != EPILORA_OK) return rc;
   auto kern = attn_tile_kernel<D, E4>;
@@ -1148,6 +1215,12 @@ size_t attn_tile_partial_bytes(int head_dim) {
 }
 
 int launch_attn_tile(const AttnArgs& a, uint32_t* counters, float* partials) {
+  // the line's units are counted in 32 bits
+  const double longest =
+      a.paged ? static_cast<double>(a.batch.table_pages) * a.cache.page_size : static_cast<double>(a.batch.n_tokens);
+  const double items = static_cast<double>(a.batch.n_tokens) * a.heads / kItemRows +
+                       static_cast<double>(a.batch.n_seqs) * a.cache.kv_heads;
+  if (items * (longest / kPosTile + 1 + kItemCost) >= 4e9) return EPILORA_ERR_UNSUPPORTED;
   TileParams p{};
   p.b = a.batch;
   p.c = a.cache;

@@ -84,6 +84,7 @@ struct TileParams {
   int heads, kv_heads, group;
   int page_shift;
   int box_rows;            // rows per TMA box
+  int o_sectors;           // every output row is 32-byte aligned
   float scale;
   uint32_t* counters;      // [2 gridDim.x], zero between calls
   float4* partials;        // [2 gridDim.x][(2 + D) * 256 / 4]
@@ -321,15 +322,13 @@ __device__ __forceinline__ bool e4m3x4_nan(uint32_t v) {
 }
 
 // One tile of scores to weights; a thread owns a row, m is in units of S, the
-// row sees columns below lim. The weights are taken against the maximum so
-// far while the tile's own is being found, 32 columns at a time; only where it
-// rises by more than kRaise (hardly ever) is the row of O rescaled and the tile
-// taken again.
-template <int D, bool E4>
+// row sees columns below lim. The scores are read from TMEM twice, 32 columns
+// at a time (a row of 128 in registers would spill): for the maximum, then for
+// the weights, which go over the scores already read. `ready` tells the
+// products' warp of each half of the weights.
+template <int D, bool E4, typename Ready>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, int lim, bool started, float& m,
-                                             float& l) {
-  uint32_t pk[64];
-  float add;
+                                             float& l, Ready ready) {
   const bool edge = __any_sync(0xffffffffu, lim < kPosTile);
   auto hide = [&](uint32_t (&v)[32], int g) {
     const int n = lim - 32 * g;
@@ -338,52 +337,26 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
     for (int i = 0; i < 32; ++i)
       if (!(seen & (1u << i))) v[i] = 0xff800000u;
   };
-  if (!started) {
-    // a row's first tile: its maximum first
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int g = 0; g < 4; ++g) {
-      uint32_t v[32];
-      tmem_ld_32x32b_x32(ts + g * 32, v);
-      tmem_ld_wait();
-      loaded(v);
-      if (edge) hide(v, g);
+  uint32_t x[2][32];
+  float top[2] = {-INFINITY, -INFINITY};
+  tmem_ld_32x32b_x32(ts, x[0]);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+  for (int g = 0; g < 4; ++g) {
+    uint32_t (&v)[32] = x[g & 1];
+    tmem_ld_wait();
+    loaded(v);
+    // (the last one starts the second reading)
+    tmem_ld_32x32b_x32(ts + ((g + 1) & 3) * 32, x[(g + 1) & 1]);
+    if (edge) hide(v, g);
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      top[0] = max3(top[0], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+      top[1] = max3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
     }
-    m = top;
   }
-#pragma unroll 1
-  while (true) {
-    const float mc = m == -INFINITY ? 0.0f : m * c;
-    float top[2] = {-INFINITY, -INFINITY}, sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t x[2][32];
-    tmem_ld_32x32b_x32(ts, x[0]);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      uint32_t (&v)[32] = x[g & 1];
-      tmem_ld_wait();
-      loaded(v);
-      if (g < 3) tmem_ld_32x32b_x32(ts + (g + 1) * 32, x[(g + 1) & 1]);
-      if (edge) hide(v, g);
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        top[0] = fmaxf(top[0], fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-        top[1] = fmaxf(top[1], fmaxf(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])));
-      }
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const float a = exp2_approx(fmaf(__uint_as_float(v[2 * q]), c, -mc));
-        const float b = exp2_approx(fmaf(__uint_as_float(v[2 * q + 1]), c, -mc));
-        sum[q & 3] += a + b;
-        // the weights as 16-bit operands (each within 2^-8 of itself, 2^-11 in fp16)
-        pk[16 * g + q] = E4 ? pack_half(a, b) : pack_bf16(a, b);
-      }
-    }
-    add = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    const float mx = fmaxf(top[0], top[1]);
-    const bool up = (mx - m) * c > kRaise;      // false for -inf - -inf
-    if (!__any_sync(0xffffffffu, up)) break;
+  const float mx = fmaxf(top[0], top[1]);
+  const bool up = (mx - m) * c > kRaise;      // false for -inf - -inf
+  if (__any_sync(0xffffffffu, up)) {
     const float f = up ? exp2_approx((m - mx) * c) : 1.0f;
     if (up) m = mx;
     l *= f;
@@ -401,10 +374,33 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
       }
     }
   }
-  l += add;
-  // over the scores that have been read
-  tmem_st_32x32b_x32(ts, pk);
-  tmem_st_32x32b_x32(ts + 32, pk + 32);
+  const float mc = m == -INFINITY ? 0.0f : m * c;
+  const uint64_t cc = f32x2(c, c), mm = f32x2(-mc, -mc);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t (&v)[32] = x[g & 1];
+    tmem_ld_wait();
+    loaded(v);
+    if (g < 3) tmem_ld_32x32b_x32(ts + (g + 1) * 32, x[(g + 1) & 1]);
+    if (edge) hide(v, g);
+    uint32_t pk[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      float a, b;
+      f32x2_parts(fma_f32x2(f32x2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), cc, mm), a, b);
+      a = exp2_approx(a);
+      b = exp2_approx(b);
+      sum[q & 1] = add_f32x2(sum[q & 1], f32x2(a, b));
+      // the weights as 16-bit operands (each within 2^-8 of itself, 2^-11 in fp16)
+      pk[q] = E4 ? pack_half(a, b) : pack_bf16(a, b);
+    }
+    tmem_st_32x32b_x16(ts + g * 16, pk);
+    if (g & 1) ready(g >> 1);
+  }
+  float s0, s1;
+  f32x2_parts(add_f32x2(sum[0], sum[1]), s0, s1);
+  l += s0 + s1;
 }
 
 template <int D, bool E4>
@@ -420,8 +416,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   uint64_t* q_full = raw_empty + C::kRawStages;                    // the piece's queries are in place
   uint64_t* q_free = q_full + 1;                                   // and have been read
   uint64_t* s_full = q_free + 1;                                   // [2] scores complete
-  uint64_t* p_full = s_full + 2;                                   // [2] weights written
-  uint64_t* o_full = p_full + 2;                                   // [2] output complete
+  uint64_t* p_full = s_full + 2;                                   // [2][2] halves of the weights written
+  uint64_t* o_full = p_full + 4;                                   // [2] output complete
   uint64_t* fix_req = o_full + 2;                                  // a value tile is to be cleaned
   uint64_t* fix_done = fix_req + 1;
   uint64_t* drain = fix_done + 1;                                  // after an abort: products complete
@@ -449,7 +445,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     mbar_init(q_free, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kRowTile);
+      mbar_init(&p_full[2 * i], kRowTile);
+      mbar_init(&p_full[2 * i + 1], kRowTile);
       mbar_init(&o_full[i], 1);
     }
     mbar_init(fix_req, 1);
@@ -686,12 +683,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
           if (i + 1 == steps) tc_commit(q_free);
         };
+        // Value tiles that hold positions some row must not see are cleaned
+        // first; asked for as soon as the tile before is under way.
+        auto to_clean = [&](int j) { return !E4 && j < nt && (it.t0 + j + 1) * kPosTile > it.see_all; };
+        auto ask_clean = [&](int j) {
+          if (!to_clean(j)) return;
+          ok = ok && wait1(&full[vr.slot], vr.phase);     // (vr: the next value tile to be used)
+          mbar_arrive(fix_req);
+        };
         ok = wait1(q_full, item & 1u);
         wait_k(0);
         if (!ok) break;
         tc_fence_after();
         qk(0);
         issued = true;
+        ask_clean(0);
         if (steps > 1) {
           wait_k(1);
           if (!ok) break;
@@ -706,22 +712,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           const bool more = i + 2 < steps;
           if (!(two && s == 1)) {
             ok = wait1(&full[vr.slot], vr.phase);
-            if (ok && !E4 && (it.t0 + j + 1) * kPosTile > it.see_all) {
-              mbar_arrive(fix_req);
+            if (ok && to_clean(j)) {
               ok = wait1(fix_done, fixes & 1u);
               ++fixes;
             }
           }
           if (more && early) wait_k(i + 2);
-          ok = ok && wait1(&p_full[s], (p_phase >> s) & 1u);
-          p_phase ^= 1u << s;
-          if (!ok) break;
-          tc_fence_after();
           const uint64_t b = make_smem_desc(ring + vr.slot * C::kTileBytes, C::kBlock, 1024, kSwizzle128B);
 #pragma unroll
-          for (int k = 0; k < kPosTile / 16; ++k)
-            // (a stream's first product starts its sum)
-            mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, i >= 2 || k > 0);
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && wait1(&p_full[2 * s + half], (p_phase >> s) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < kPosTile / 32; ++q) {
+              const int k = half * (kPosTile / 32) + q;
+              // (a stream's first product starts its sum)
+              mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, i >= 2 || k > 0);
+            }
+          }
+          if (!ok) break;
+          p_phase ^= 1u << s;
           if (!(two && s == 0)) {
             tc_commit(&empty[vr.slot]);
             vr.skip(2);
@@ -735,6 +746,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             }
             qk(i + 2);
           }
+          if (!two || s == 1) ask_clean(j + 1);
         }
         // 2 nt tiles further
         const uint32_t turned = slot + 2 * static_cast<uint32_t>(nt);
@@ -770,23 +782,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             const int from = max(it.see_all - j * kPosTile, 0);
             const int to = min(max(it.see_end - j * kPosTile, from), kPosTile);
             bool nf = false;
-            for (int i = from * 8 + lane; i < kPosTile * 8; i += 32) {
+#pragma unroll 1
+            for (int x = 0; x < D / 64; ++x) {
+              uint4* q = reinterpret_cast<uint4*>(v + x * C::kBlock);
+              for (int i = to * 8 + lane; i < kPosTile * 8; i += 32) q[i] = make_uint4(0, 0, 0, 0);
+              for (int i0 = from * 8 + lane; i0 < to * 8; i0 += 128) {
+                uint4 u[4];
+                bool any = false;
 #pragma unroll
-              for (int x = 0; x < D / 64; ++x) {
-                uint4* q = reinterpret_cast<uint4*>(v + x * C::kBlock + i * 16);
-                if ((i >> 3) >= to) {
-                  *q = make_uint4(0, 0, 0, 0);
-                } else {
-                  const uint4 u = *q;
-                  if (bf16x2_nonfinite(u.x) | bf16x2_nonfinite(u.y) | bf16x2_nonfinite(u.z) | bf16x2_nonfinite(u.w)) {
-                    nf = true;
-                    uint32_t e[4] = {u.x, u.y, u.z, u.w};
+                for (int k = 0; k < 4; ++k) u[k] = i0 + 32 * k < to * 8 ? q[i0 + 32 * k] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                      if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
-                      if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0xFFFFu;
+                for (int k = 0; k < 4; ++k)
+                  any |= bf16x2_nonfinite(u[k].x) | bf16x2_nonfinite(u[k].y) | bf16x2_nonfinite(u[k].z) |
+                         bf16x2_nonfinite(u[k].w);
+                if (any) {
+                  nf = true;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    uint32_t e[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                      if ((e[y] & 0x7F80u) == 0x7F80u) e[y] &= 0xFFFF0000u;
+                      if ((e[y] & 0x7F800000u) == 0x7F800000u) e[y] &= 0xFFFFu;
                     }
-                    *q = make_uint4(e[0], e[1], e[2], e[3]);
+                    if (i0 + 32 * k < to * 8) q[i0 + 32 * k] = make_uint4(e[0], e[1], e[2], e[3]);
                   }
                 }
               }
@@ -976,12 +995,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       for (int k = 0; k < steps; ++k) {
         if (!wait(&s_full[s], sn++ & 1u)) break;
         tc_fence_after();
-        softmax_tile<D, E4>(ts, to, c, lim, started, m, l);
+        softmax_tile<D, E4>(ts, to, c, lim, started, m, l, [&](int half) {
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[2 * s + half]);
+        });
         started = true;
         lim -= lim_step;
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&p_full[s]);
       }
 
       // ===== the piece's result =====
@@ -1015,18 +1035,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         constexpr int kPart = (2 + D) * kItemRows / 4;      // float4s of a partial result: m c, l, O [D / 4][256]
         float4* part = p.partials + static_cast<int64_t>(it.slot) * kPart;
         const int prow = s * kRowTile + r;
-        auto put = [&](int i, const float* o, float sum) {   // 8 outputs from element i on
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (sum != 0.0f) {
-            const float inv = vscale / sum;
-            v = make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
-                           pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
+        auto put = [&](int i, const float* o, float inv, bool empty) {   // 32 outputs from element i on
+          uint32_t v[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) v[q] = empty ? 0u : pack_bf16(o[2 * q] * inv, o[2 * q + 1] * inv);
+          __nv_bfloat16* at = p.o.p + tok * p.o.ts + head * p.o.hs + i;
+          if (p.o_sectors) {
+            st_global_v8(at, v);
+            st_global_v8(at + 16, v + 8);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 16; q += 4) *reinterpret_cast<uint4*>(at + 2 * q) = make_uint4(v[q], v[q + 1], v[q + 2], v[q + 3]);
           }
-          *reinterpret_cast<uint4*>(p.o.p + tok * p.o.ts + head * p.o.hs + i) = v;
         };
         auto put_lse = [&](float mc, float sum) {
           if (p.lse != nullptr) p.lse[tok * p.heads + head] = sum == 0.0f ? -INFINITY : (mc + __log2f(sum)) * kLn2;
         };
+        const float inv = vscale / l;      // (l == 0: the row sees nothing)
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
           uint32_t o[32];
@@ -1070,8 +1095,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
           if (whole) {
             if (live) {
-#pragma unroll
-              for (int q = 0; q < 32; q += 8) put(i + q, a + q, l);
+              put(i, a, inv, l == 0.0f);
             }
           } else {
 #pragma unroll
@@ -1109,6 +1133,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
               const float* f = reinterpret_cast<const float*>(piece(k));
               sum += __ldcg(f + kItemRows + prow) * exp2_approx(__ldcg(f + prow) - base);
             }
+            const float inv = vscale / sum;
 #pragma unroll 1
             for (int i = 0; i < D; i += 32) {
               float a[32];
@@ -1123,8 +1148,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                   a[q] += v.x * wk, a[q + 1] += v.y * wk, a[q + 2] += v.z * wk, a[q + 3] += v.w * wk;
                 }
               }
-#pragma unroll
-              for (int q = 0; q < 32; q += 8) put(i + q, a + q, sum);
+              put(i, a, inv, sum == 0.0f);
             }
             put_lse(top, sum);
           }
@@ -1235,6 +1259,8 @@ int launch_attn_tile(const AttnArgs& a, uint32_t* counters, float* partials) {
   p.group = a.heads / a.cache.kv_heads;
   p.page_shift = a.paged ? __builtin_ctz(a.cache.page_size) : 0;
   p.box_rows = a.paged && a.cache.page_size < kPosTile ? a.cache.page_size : kPosTile;
+  p.o_sectors = (reinterpret_cast<uintptr_t>(a.o.p) | static_cast<uintptr_t>(a.o.ts * 2) |
+                 static_cast<uintptr_t>(a.o.hs * 2)) % 32 == 0;
   p.scale = a.scale;
   p.counters = counters;
   p.partials = reinterpret_cast<float4*>(partials);

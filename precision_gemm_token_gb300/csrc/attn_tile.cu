@@ -11,17 +11,18 @@
 // the tensor pipe bounds it as long as the softmax of one half runs while the
 // products of the other half do.
 //
-// One thread block per SM, twelve warps:
+// One thread block per SM, twelve warps (sixteen for an E4M3 cache):
 //   0-3, 4-7  two softmax groups, one per 128 rows ("stream"): a thread owns a
 //             row, reads its scores from TMEM, keeps the row's maximum and
 //             sum in registers, writes the weights back over the scores
 //             (16-bit, the A operand of the second product) and, where the
 //             maximum rose by more than 2^8, rescales the row of O in TMEM
 //   8         walks the block's pieces of work and tells them to the others;
-//             copies key and value tiles into a ring of shared memory by TMA
+//             copies queries, and key and value tiles into a ring of shared
+//             memory, by TMA
 //   9         issues the products; S and O of both streams fill the TMEM
-//   10 (11)   bf16: clean the value rows that some row must not see;
-//             E4M3: convert the copied codes to fp16 tiles
+//   10        bf16: cleans the value rows that some row must not see
+//   12-15     E4M3: convert the copied codes to fp16 tiles
 // Where an item has at most 128 rows both streams take the same rows and
 // alternate the position tiles; they meet at the end.
 //
@@ -35,12 +36,16 @@
 namespace epi {
 namespace {
 
-constexpr int kTileThreads = 384;
-// registers per thread: at launch, of the softmax warps, of the others; the
-// softmax keeps a row of 128 scores in registers (at 168 it spills some 190 KB
-// a tile, more than the L1 left beside the ring holds)
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
-static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kTileThreads * kRegsLaunch, "split of the block's registers");
+// registers per thread of the softmax warps and of the others, within the
+// block's at launch; the softmax keeps 64 scores and 16 packed weights in
+// registers (in the launch's 168 it spills, more than the L1 left beside the
+// ring holds)
+template <bool E4>
+struct TileWarps {
+  static constexpr int kThreads = E4 ? 512 : 384;
+  static constexpr int kLaunch = E4 ? 128 : 168, kSoftmax = E4 ? 192 : 208, kOther = E4 ? 64 : 88;
+  static_assert(256 * kSoftmax + (kThreads - 256) * kOther <= kThreads * kLaunch, "split of the block's registers");
+};
 constexpr int kPosTile = 128;      // positions per tile
 constexpr int kRowTile = 128;      // rows per stream
 constexpr int kItemRows = 2 * kRowTile;
@@ -67,9 +72,12 @@ struct TileCfg {
   static constexpr int kRing = kQBytes, kRaw = kRing + kStages * kTileBytes;
   static constexpr int kPlan = kRaw + kRawStages * kRawBytes;
   static constexpr int kBars = kPlan + kGroups * 4;
-  static constexpr int kPieceAt = kBars + 384;
+  // barriers: three per stage, two per raw stage, 22 more; then 12 words of flags
+  static constexpr int kBarBytes = (3 * kStages + 2 * kRawStages + 22) * 8 + 12 * 4;
+  static constexpr int kPieceAt = kBars + (kBarBytes + 15) / 16 * 16;
   static constexpr int kBytes = kPieceAt + kPieces * kPieceInts * 4;
   static constexpr int kSmem = 1024 + kBytes;
+  static_assert(kSmem <= 232448, "shared memory of a block");
 };
 
 struct TileParams {
@@ -163,11 +171,11 @@ __device__ __forceinline__ void tile_piece(TileWalk& w) {
 }
 
 // The table of sequence weights, by the whole block.
-__device__ __forceinline__ void tile_plan(const TileParams& p, uint32_t* plan, int warp, int lane) {
+__device__ __forceinline__ void tile_plan(const TileParams& p, uint32_t* plan, int warp, int warps, int lane) {
   const int per = (p.b.n_seqs + kGroups - 1) / kGroups;     // sequences per table entry
   const int entries = per == 0 ? 0 : (p.b.n_seqs + per - 1) / per;
   bool bad = false;
-  for (int e = warp; e < entries; e += kTileThreads / 32) {
+  for (int e = warp; e < entries; e += warps) {
     uint32_t v = 0;
     for (int b = e * per; b < min((e + 1) * per, p.b.n_seqs); ++b) v += seq_weight(p, b, lane, bad);
     if (lane == 0) plan[e] = v;
@@ -404,7 +412,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
 }
 
 template <int D, bool E4>
-__global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid_constant__ TileParams p) {
+__global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(const __grid_constant__ TileParams p) {
   using C = TileCfg<D, E4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -418,9 +426,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   uint64_t* s_full = q_free + 1;                                   // [2] scores complete
   uint64_t* p_full = s_full + 2;                                   // [2][2] halves of the weights written
   uint64_t* o_full = p_full + 4;                                   // [2] output complete
-  uint64_t* fix_req = o_full + 2;                                  // a value tile is to be cleaned
-  uint64_t* fix_done = fix_req + 1;
-  uint64_t* drain = fix_done + 1;                                  // after an abort: products complete
+  uint64_t* cleaned = o_full + 2;                                  // [stages] a value tile is cleaned
+  uint64_t* drain = cleaned + C::kStages;                          // after an abort: products complete
   uint64_t* piece_full = drain + 1;                                // [pieces] told
   uint64_t* piece_empty = piece_full + kPieces;                    // [pieces] read by every role
   uint64_t* group_bar = piece_empty + kPieces;                     // [2] a softmax group meets
@@ -434,12 +441,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], E4 ? 2 : 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&full[i], E4 ? 4 : 1);      // four converting warps, or the copy
+      mbar_init(&empty[i], E4 ? 1 : 2);     // the products, and the cleaning warp
+      mbar_init(&cleaned[i], 1);
     }
     for (int i = 0; i < C::kRawStages; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 2);
+      mbar_init(&raw_empty[i], 4);
     }
     mbar_init(q_full, p.q_tma ? 1 : kItemRows);
     mbar_init(q_free, 1);
@@ -449,12 +457,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       mbar_init(&p_full[2 * i + 1], kRowTile);
       mbar_init(&o_full[i], 1);
     }
-    mbar_init(fix_req, 1);
-    mbar_init(fix_done, 1);
     mbar_init(drain, 1);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&piece_full[i], 1);
-      mbar_init(&piece_empty[i], 11);   // 8 softmax warps, the products', and the last two
+      mbar_init(&piece_empty[i], E4 ? 13 : 10);   // 8 softmax warps, the products', the cleaning or converting ones
     }
     for (int i = 0; i < 2; ++i) mbar_init(&group_bar[i], kRowTile);
     mbar_init(both_bar, kItemRows);
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     }
   }
 
-  tile_plan(p, plan, warp, lane);
+  tile_plan(p, plan, warp, TileWarps<E4>::kThreads / 32, lane);
 
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
@@ -525,7 +531,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   };
 
   if (warp >= 8) {
-    setmaxnreg_dec<kRegsOther>();
+    setmaxnreg_dec<TileWarps<E4>::kOther>();
   if (warp == 8) {
     // ===== copies =====
     fence_proxy_async_global();
@@ -538,7 +544,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     uint8_t* ring = smem + (E4 ? C::kRaw : C::kRing);
     const int nb = kPosTile / p.box_rows;                // boxes per tile along the positions
     int slot = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, items = 0;
     TileWalk w;
     Piece it;
     bool more = tile_begin(p, w, plan, lane), stop = false;
@@ -567,6 +573,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       auto page_of = [&](int u) {   // page of box u of the sequence
         return p.paged && u * p.box_rows < it.see_end ? table[(u * p.box_rows) >> p.page_shift] : 0;
       };
+      bool q_due = !E4 && p.q_tma;
       int c0 = it.t0 * nb;
       int ids = page_of(c0 + lane);
       for (int j = it.t0; j < it.t1 && !stop; ++j) {
@@ -607,6 +614,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
           if (++slot == kSt) slot = 0, phase ^= 1u;
         }
+        if (!E4 && q_due && !stop) {
+          // the queries, behind the first tile (by then the last piece's products are about to have read theirs)
+          q_due = false;
+          if (!wait(q_free, (items & 1u) ^ 1u)) {
+            stop = true;
+          } else if (lane == 0) {
+            const int tiles = it.two() ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, tiles * C::kTileBytes);
+            for (int t = 0; t < tiles; ++t)
+#pragma unroll
+              for (int x = 0; x < D / 64; ++x)
+                tma_load_4d(smem + t * C::kTileBytes + x * C::kBlock, &p.tq, q_full, x * 128, it.h * p.group,
+                            it.first + (it.row0 + t * kRowTile) / p.group, 0);
+          }
+          __syncwarp();
+          ++items;
+        }
       }
       more = tile_next(p, w);
     }
@@ -614,22 +638,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       // no copy in flight at exit
       for (int i = 0; i < kSt; ++i)
         (void)mbar_wait_bounded(&bar_full[i], i < slot ? phase : phase ^ 1u, 1000000ull);
+      if (!E4 && p.q_tma && items > 0) (void)mbar_wait_bounded(q_full, (items - 1) & 1u, 1000000ull);
     }
     __syncwarp();
   } else if (warp == 9) {
     // ===== products =====
-    // One lane does it all: between two products there is no time for a
-    // warp's votes (a wait of the whole warp takes some 130 cycles even where
-    // the barrier is ready, two products' worth).
+    // A stream takes S = Q K^T of a tile, then (the weights having gone over
+    // the scores) O += P V, then the next tile's S; the streams in turn. One
+    // lane does it all, its products run in order, so no S is overwritten
+    // early. A wait takes some 100 cycles even where its barrier is ready (130
+    // for a whole warp), the products between two of them 256 or 512: a step's
+    // barriers are therefore tried together and waited for one by one only
+    // where one is not ready. (A lane per stream instead was slower, 973
+    // against 841 us for a prompt of 8192 x 64 heads: the streams then fall
+    // into step, and the products wait for the softmax of both.)
     if (elect_one()) {
       constexpr uint32_t kIdQK = idesc_f16(128, 128, !E4, false);
       constexpr uint32_t kIdPV = idesc_f16(128, D, !E4, true);
-      const uint32_t q_addr = smem_u32(smem), ring = smem_u32(smem + C::kRing);
-      uint32_t slot = 0, phase = 0;   // ring position (keys and values alternating) of the piece's first tile
-      uint32_t item = 0, fixes = 0, p_phase = 0;   // p_phase: bit s for stream s
+      const uint64_t q_desc = make_smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      const uint64_t k_desc = make_smem_desc(smem_u32(smem + C::kRing), 16, 1024, kSwizzle128B);
+      const uint64_t v_desc = make_smem_desc(smem_u32(smem + C::kRing), C::kBlock, 1024, kSwizzle128B);
+      constexpr uint32_t kTile16 = C::kTileBytes >> 4;
+      struct Ring {
+        uint32_t slot, phase;
+        __device__ __forceinline__ void skip(uint32_t n) {
+          slot += n;
+          if (slot >= C::kStages) slot -= C::kStages, phase ^= 1u;
+        }
+      };
+      Ring start{0, 0};                  // ring position (keys and values alternating) of the piece's first tile
+      uint32_t clean_phase = 0;          // a bit per stage
+      uint32_t item = 0, p_phase = 0;    // p_phase: bit s for stream s
       bool ok = true, issued = false;
       auto wait1 = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_try_wait(bar, parity)) return true;
         const uint64_t t0 = globaltimer_ns();
         for (uint32_t polls = 1;; ++polls) {
           if (mbar_try_wait(bar, parity)) return true;
@@ -653,24 +694,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         if (nt <= 0) break;
         const bool two = it.two();
         const int steps = two ? 2 * nt : nt;
-        // ring slots and parities: keys and values of the next step's tile
-        struct Ring {
-          uint32_t slot, phase;
-          __device__ __forceinline__ void skip(uint32_t n) {
-            slot += n;
-            if (slot >= C::kStages) slot -= C::kStages, phase ^= 1u;
-          }
-        };
-        Ring kr{slot, phase}, vr{slot, phase};
+        // position tile of a step: i / 2 with two row tiles, else i
+        Ring kr = start, vr = start;     // keys and values of the next step's tile
         vr.skip(1);
         // scores of step i (of stream i % 2)
-        auto wait_k = [&](int i) {
-          if (!(two && (i & 1) == 1)) ok = ok && wait1(&full[kr.slot], kr.phase);
-        };
         auto qk = [&](int i) {
           const int s = i & 1;
-          const uint64_t a = make_smem_desc(q_addr + (two ? s * C::kTileBytes : 0), 16, 1024, kSwizzle128B);
-          const uint64_t b = make_smem_desc(ring + kr.slot * C::kTileBytes, 16, 1024, kSwizzle128B);
+          const uint64_t a = q_desc + (two && s == 1 ? kTile16 : 0), b = k_desc + kr.slot * kTile16;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = ((k / 4) * C::kBlock + (k % 4) * 32) >> 4;
@@ -683,24 +713,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
           if (i + 1 == steps) tc_commit(q_free);
         };
-        // Value tiles that hold positions some row must not see are cleaned
-        // first; asked for as soon as the tile before is under way.
-        auto to_clean = [&](int j) { return !E4 && j < nt && (it.t0 + j + 1) * kPosTile > it.see_all; };
-        auto ask_clean = [&](int j) {
-          if (!to_clean(j)) return;
-          ok = ok && wait1(&full[vr.slot], vr.phase);     // (vr: the next value tile to be used)
-          mbar_arrive(fix_req);
-        };
-        ok = wait1(q_full, item & 1u);
-        wait_k(0);
+        ok = wait1(q_full, item & 1u) && wait1(&full[kr.slot], kr.phase);
         if (!ok) break;
         tc_fence_after();
         qk(0);
         issued = true;
-        ask_clean(0);
         if (steps > 1) {
-          wait_k(1);
-          if (!ok) break;
+          if (!two && !(ok = wait1(&full[kr.slot], kr.phase))) break;
           tc_fence_after();
           qk(1);
         }
@@ -710,48 +729,50 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         for (int i = 0; i < steps; ++i) {
           const int s = i & 1, j = two ? i >> 1 : i;
           const bool more = i + 2 < steps;
-          if (!(two && s == 1)) {
-            ok = wait1(&full[vr.slot], vr.phase);
-            if (ok && to_clean(j)) {
-              ok = wait1(fix_done, fixes & 1u);
-              ++fixes;
-            }
-          }
-          if (more && early) wait_k(i + 2);
-          const uint64_t b = make_smem_desc(ring + vr.slot * C::kTileBytes, C::kBlock, 1024, kSwizzle128B);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && wait1(&p_full[2 * s + half], (p_phase >> s) & 1u);
+          const bool new_v = !(two && s == 1), new_k = more && !(two && s == 1);
+          // the value tile: cleaned first where it holds positions that some row must not see
+          const bool clean = !E4 && (it.t0 + j + 1) * kPosTile > it.see_all;
+          uint64_t* v_bar = clean ? &cleaned[vr.slot] : &full[vr.slot];
+          const uint32_t v_par = clean ? (clean_phase >> vr.slot) & 1u : vr.phase, p_par = (p_phase >> s) & 1u;
+          uint32_t rv = 1, rk = 1;
+          if (new_v) rv = mbar_try_wait(v_bar, v_par);
+          if (new_k && early) rk = mbar_try_wait(&full[kr.slot], kr.phase);
+          const uint32_t rp = mbar_try_wait(&p_full[2 * s], p_par);
+          if (!(rv & rk & rp)) {
+            ok = (rv || wait1(v_bar, v_par)) && (rk || wait1(&full[kr.slot], kr.phase)) &&
+                 (rp || wait1(&p_full[2 * s], p_par));
             if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < kPosTile / 32; ++q) {
-              const int k = half * (kPosTile / 32) + q;
-              // (a stream's first product starts its sum)
-              mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, i >= 2 || k > 0);
-            }
           }
-          if (!ok) break;
+          tc_fence_after();
+          const uint64_t b = v_desc + vr.slot * kTile16;
+          // (a stream's first product starts its sum)
+#pragma unroll
+          for (int k = 0; k < kPosTile / 32; ++k)
+            mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, i >= 2 || k > 0);
+          if (!mbar_try_wait(&p_full[2 * s + 1], p_par) && !(ok = wait1(&p_full[2 * s + 1], p_par))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = kPosTile / 32; k < kPosTile / 16; ++k)
+            mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, 1u);
           p_phase ^= 1u << s;
           if (!(two && s == 0)) {
             tc_commit(&empty[vr.slot]);
+            if (clean) clean_phase ^= 1u << vr.slot;
             vr.skip(2);
           }
           if (!more) tc_commit(&o_full[s]);
           if (more) {
-            if (!early) {
-              wait_k(i + 2);
-              if (!ok) break;
+            if (new_k && !early) {
+              if (!(ok = wait1(&full[kr.slot], kr.phase))) break;
               tc_fence_after();
             }
             qk(i + 2);
           }
-          if (!two || s == 1) ask_clean(j + 1);
         }
         // 2 nt tiles further
-        const uint32_t turned = slot + 2 * static_cast<uint32_t>(nt);
-        slot = turned % C::kStages;
-        phase ^= (turned / C::kStages) & 1u;
+        const uint32_t turned = start.slot + 2 * static_cast<uint32_t>(nt);
+        start.slot = turned % C::kStages;
+        start.phase ^= (turned / C::kStages) & 1u;
         ++item;
       }
       if (!ok && issued) {
@@ -761,24 +782,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       }
     }
     __syncwarp();
-  } else if (warp >= 10) {
+  } else if (E4 ? warp >= 12 : warp == 10) {
     if (!E4) {
       // ===== cleaning of value tiles =====
       // A position that a row does not see has weight zero, but zero times a
       // NaN or an infinity is NaN: rows past the item's last position are
       // zeroed; non-finite values at positions that only some rows see are
       // zeroed too and the item noted (its epilogue adds them where they belong).
-      if (warp == 10) {
-        uint32_t pos = 0, fixes = 0;
-        int item = 0;
-        bool ok = true;
-        Piece it;
-        while (ok && next_piece(it)) {
-          for (int j = max(it.t0, it.see_all / kPosTile); j < it.t1 && ok; ++j) {
-            ok = wait(fix_req, fixes & 1u);
-            ++fixes;
-            if (!ok) break;
-            uint8_t* v = smem + C::kRing + ((pos + 2 * (j - it.t0) + 1) % C::kStages) * C::kTileBytes;
+      uint32_t slot = 0, phase = 0;
+      int item = 0;
+      bool ok = true;
+      Piece it;
+      while (ok && next_piece(it)) {
+        for (int j = it.t0; j < it.t1 && ok; ++j) {
+          // (every fill is seen in order)
+          if (!(ok = wait(&full[slot], phase))) break;
+          if (lane == 0) mbar_arrive(&empty[slot]);
+          if (++slot == C::kStages) slot = 0, phase ^= 1u;
+          if (!(ok = wait(&full[slot], phase))) break;
+          if ((j + 1) * kPosTile > it.see_all) {
+            uint8_t* v = smem + C::kRing + slot * C::kTileBytes;
             const int from = max(it.see_all - j * kPosTile, 0);
             const int to = min(max(it.see_end - j * kPosTile, from), kPosTile);
             bool nf = false;
@@ -814,37 +837,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             fence_proxy_async_smem();
             __threadfence_block();
             __syncwarp();
-            if (lane == 0) mbar_arrive(fix_done);
+            if (lane == 0) mbar_arrive(&cleaned[slot]);
           }
-          pos += 2 * (it.t1 - it.t0);
-          ++item;
+          if (lane == 0) mbar_arrive(&empty[slot]);
+          if (++slot == C::kStages) slot = 0, phase ^= 1u;
         }
-      } else {
-        // ===== copies of queries =====
-        fence_proxy_async_global();
-        uint32_t item = 0;
-        Piece it;
-        while (next_piece(it)) {
-          if (!p.q_tma) continue;
-          // the last piece's products have read its queries
-          if (!wait(q_free, (item & 1u) ^ 1u)) break;
-          if (lane == 0) {
-            const int tiles = it.two() ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, tiles * C::kTileBytes);
-            for (int t = 0; t < tiles; ++t)
-#pragma unroll
-              for (int x = 0; x < D / 64; ++x)
-                tma_load_4d(smem + t * C::kTileBytes + x * C::kBlock, &p.tq, q_full, x * 128, it.h * p.group,
-                            it.first + (it.row0 + t * kRowTile) / p.group, 0);
-          }
-          __syncwarp();
-          ++item;
-        }
-        if (*abort_flag && item > 0) (void)mbar_wait_bounded(q_full, (item - 1) & 1u, 1000000ull);   // no copy in flight at exit
+        ++item;
       }
     } else {
       // ===== E4M3 codes to fp16 tiles =====
-      const int t = (warp - 10) * 32 + lane;
+      const int t = (warp - 12) * 32 + lane;
       uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
       int item = 0;
       bool ok = true;
@@ -862,7 +864,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             const bool clean = kv == 1 && from < kPosTile;
             constexpr int kPer = D / 16;   // 16-code chunks per row
 #pragma unroll 4
-            for (int i = t; i < kPosTile * kPer; i += 64) {
+            for (int i = t; i < kPosTile * kPer; i += 128) {
               uint4 u = *reinterpret_cast<const uint4*>(src + i * 16);
               const int row = i / kPer, c = i % kPer;
               if (clean) {
@@ -910,7 +912,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   }
   } else {
     // ===== softmax =====
-    setmaxnreg_inc<kRegsSoftmax>();
+    setmaxnreg_inc<TileWarps<E4>::kSoftmax>();
     const int s = warp >> 2;                       // stream
     const int r = threadIdx.x & (kRowTile - 1);    // lane of TMEM = row of the stream
     const uint32_t quad = static_cast<uint32_t>(warp & 3) << 21;   // TMEM lane 32 (warp % 4), in bits 16..
@@ -1219,7 +1221,7 @@ int launch(const AttnArgs& a, TileParams& p) {
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(num_sms() < kTileMaxCtas ? num_sms() : kTileMaxCtas, 1, 1);
-  cfg.blockDim = dim3(kTileThreads, 1, 1);
+  cfg.blockDim = dim3(TileWarps<E4>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = a.stream;
   cudaLaunchAttribute attr{};

@@ -15,51 +15,88 @@ rows q_start[b] .. q_start[b+1] - 1 and holds kv_len[b] tokens with them.
 """
 from __future__ import annotations
 
-import contextlib
+import struct
 from typing import Optional
 
 import torch
 
 from . import _binding as E
 
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+# epilora_kv_batch as bytes: a decode step calls these helpers once or twice
+# per layer, and packing eight numbers costs a third of a ctypes struct
+_pack_batch = struct.Struct("iiiiqPPP").pack
+_lib = E.load
 
 
-def _want(ok, what):
-    if not ok:
-        raise E.EpiloraError(E.EPILORA_ERR_INVALID_ARG, what)
+def _bad(what):
+    raise E.EpiloraError(E.EPILORA_ERR_INVALID_ARG, what)
 
 
-def _strides(t, what):
-    """(token, head) strides of rows [tokens, heads, head_dim]; a dimension of
-    one element has no stride of its own."""
-    _want(t.dim() == 3 and t.dtype is _BF16, f"{what}: bf16 [tokens, heads, head_dim] wanted")
-    n, h, d = t.shape
-    s = t.stride()
-    _want(s[2] == 1, f"{what}: the elements of a head have to be contiguous")
-    hs = s[1] if h > 1 else d
-    return (s[0] if n > 1 else h * hs), hs
+def _rows(t, shape, dev, what):
+    """(address, token stride, head stride) of rows [tokens, heads, head_dim]
+    of the given shape; a dimension of one element has no stride of its own."""
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev:
+        _bad(f"{what}: bf16 [tokens, heads, head_dim] = {tuple(shape)} on device {dev} wanted")
+    n, h, d = shape
+    ts, hs, es = t.stride()
+    if es != 1 and d > 1:
+        _bad(what + ": the elements of a head have to be contiguous")
+    if h == 1:
+        hs = d
+    return t.data_ptr(), (ts if n > 1 else h * hs), hs
 
 
-def _on(device, what, *tensors):
-    for t in tensors:
-        _want(t is None or t.device == device, f"{what}: tensors on different devices")
+def _index(t, n, dev, what):
+    if t.dtype is not _I32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        _bad(f"{what}: contiguous int32 [{n}] on device {dev} wanted")
+    return t.data_ptr()
 
 
-def _index(t, shape, what):
-    _want(t.dtype is _I32 and t.shape == shape and t.is_contiguous(), f"{what}: contiguous int32 {tuple(shape)} wanted")
-    return t
-
-
-def _launch(device, stream):
-    """(context that allocates on the launching stream, its raw handle)"""
-    _want(device.type == "cuda", "a CUDA device is wanted")
-    _want(device.index == torch.cuda.current_device(), "the tensors are not on the current device")
+def _start(q, stream):
+    """(shape of q, its device, the raw handle of the launching stream, and
+    the stream itself where it is given: what a call allocates is then made
+    on it)"""
+    shape = q.shape
+    if len(shape) != 3:
+        _bad("q: [tokens, heads, head_dim] wanted")
+    dev = q.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _bad("tensors on the current CUDA device wanted")
     if stream is None:
-        return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
+        return shape, dev, torch._C._cuda_getCurrentRawStream(dev), None
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    return torch.cuda.stream(stream), stream.cuda_stream
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    return shape, dev, stream.cuda_stream, stream
+
+
+def _new(q, shape, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=_BF16, device=q.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=_BF16, device=q.device)
+
+
+def _workspace(workspace, q, dim, stream):
+    """(address, bytes); its zero fill is ordered on the launching stream."""
+    if workspace is None:
+        workspace = AttentionWorkspace(q.device)
+    elif workspace.device.index is not None and workspace.device.index != q.get_device():
+        _bad("workspace: on another device")
+    if stream is None:
+        buf = workspace.get(dim)
+    else:
+        with torch.cuda.stream(stream):
+            buf = workspace.get(dim)
+    return buf, buf.data_ptr(), buf.numel()
+
+
+def _status(status, dev):
+    if status is None:
+        return None
+    if status.dtype is not _I32 or status.numel() < 1 or status.get_device() != dev:
+        _bad("status: int32 on the tensors' device wanted")
+    return status.data_ptr()
 
 
 class PagedKVCache:
@@ -71,34 +108,39 @@ class PagedKVCache:
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
                  v_scale: Optional[torch.Tensor] = None):
-        _want(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.dtype in (_BF16, torch.uint8),
-              "cache: two bf16 or uint8 [num_pages, kv_heads, page_size, head_dim] wanted")
-        e4m3 = k.dtype is torch.uint8
-        _want((k_scale is not None and v_scale is not None) if e4m3 else (k_scale is None and v_scale is None),
-              "cache: scales go with E4M3 codes, and only with them")
+        if not (k.dim() == 4 and k.shape == v.shape and k.dtype is v.dtype and k.dtype in (_BF16, _U8)):
+            _bad("cache: two bf16 or uint8 [num_pages, kv_heads, page_size, head_dim] wanted")
+        e4m3 = k.dtype is _U8
+        if not ((k_scale is not None and v_scale is not None) if e4m3 else (k_scale is None and v_scale is None)):
+            _bad("cache: scales go with E4M3 codes, and only with them")
         for s in (k_scale, v_scale):
-            _want(s is None or (s.dtype is _F32 and s.shape == k.shape[1:2] and s.is_contiguous()),
-                  "cache: scales are contiguous fp32 [kv_heads]")
-        _on(k.device, "cache", v, k_scale, v_scale)
+            if not (s is None or (s.dtype is _F32 and s.shape == k.shape[1:2] and s.is_contiguous())):
+                _bad("cache: scales are contiguous fp32 [kv_heads]")
+        if any(t is not None and t.get_device() != k.get_device() for t in (v, k_scale, v_scale)):
+            _bad("cache: tensors on different devices")
         pages, heads, size, dim = k.shape
         c = E.KvCache(kv_fmt=E.KV_E4M3 if e4m3 else E.KV_BF16, kv_heads=heads, head_dim=dim, page_size=size,
                       num_pages=pages, reserved=0, k=k.data_ptr(), v=v.data_ptr(),
                       k_scale=k_scale.data_ptr() if e4m3 else None, v_scale=v_scale.data_ptr() if e4m3 else None)
         for n, t in (("k", k), ("v", v)):
             s = t.stride()
-            _want(s[3] == 1, "cache: the elements of a head's row have to be contiguous")
+            if s[3] != 1:
+                _bad("cache: the elements of a head's row have to be contiguous")
             for axis, name in ((0, "page"), (1, "head"), (2, "token")):
                 # a dimension of one element has no stride of its own
                 setattr(c, f"{n}_{name}_stride", s[axis] if t.shape[axis] > 1 else dim)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.dev = k.get_device()
         self.device, self.kv_heads, self.head_dim, self.page_size = k.device, heads, dim, size
         self.struct = c
+        self.address = E.ctypes.addressof(c)
 
 
 class AttentionWorkspace:
     """Caller-owned workspace of the attention calls (see
     epilora_attention_workspace_bytes), zero-filled when first used. Calls
-    that share one have to be ordered on one stream."""
+    that share one have to be ordered on one stream. After a call that
+    recorded EPILORA_ERR_TIMEOUT, take a new one."""
 
     def __init__(self, device):
         self.device = torch.device(device)
@@ -108,22 +150,24 @@ class AttentionWorkspace:
         buf = self._buf.get(head_dim)
         if buf is None:
             need = E.epilora_attention_workspace_bytes(head_dim)
-            buf = self._buf[head_dim] = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.device)
+            buf = self._buf[head_dim] = torch.zeros(max(need, 256), dtype=_U8, device=self.device)
         return buf
 
 
-def _batch(tokens, q_start, kv_len, page_table, max_new):
+def _batch(tokens, q_start, kv_len, page_table, max_new, dev):
+    """epilora_kv_batch (as bytes)."""
     n = q_start.numel() - 1
-    _want(n >= 0, "q_start: [sequences + 1] wanted")
-    _index(q_start, (n + 1,), "q_start")
-    _index(kv_len, (n,), "kv_len")
-    _want(page_table.dtype is _I32 and page_table.dim() == 2 and page_table.shape[0] == n,
-          f"page_table: int32 [{n}, pages] wanted")
-    pages = page_table.shape[1]
+    if n < 0:
+        _bad("q_start: [sequences + 1] wanted")
+    starts, lens = _index(q_start, n + 1, dev, "q_start"), _index(kv_len, n, dev, "kv_len")
+    if page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.get_device() != dev:
+        _bad(f"page_table: int32 [{n}, pages] on device {dev} wanted")
+    rows, pages = page_table.shape
     ts, cs = page_table.stride()
-    _want((cs == 1 or pages <= 1) and (ts >= pages or n <= 1), "page_table: rows have to be contiguous")
-    return E.KvBatch(n, tokens, tokens if max_new is None else max_new, pages, ts if n > 1 else pages,
-                     q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr())
+    if rows != n or (cs != 1 and pages > 1) or (ts < pages and n > 1):
+        _bad(f"page_table: [{n}, pages] with contiguous rows wanted")
+    return _pack_batch(n, tokens, tokens if max_new is None else max_new, pages, ts if n > 1 else pages, starts, lens,
+                       page_table.data_ptr())
 
 
 def kv_append(q, k, v, cache: PagedKVCache, q_start, kv_len, page_table, cos_sin=None, interleaved=False, q_out=None,
@@ -132,35 +176,38 @@ def kv_append(q, k, v, cache: PagedKVCache, q_start, kv_len, page_table, cos_sin
     and k by position with cos_sin fp32 [positions, rot_dim] (cosines, then
     sines; None: no rotation). Returns the rotated q (q_out, which may be q
     itself). epilora_kv_append has the details."""
-    T, heads, dim = q.shape
-    qs, ks, vs = _strides(q, "q"), _strides(k, "k"), _strides(v, "v")
-    _want(k.shape == v.shape == (T, cache.kv_heads, dim) and dim == cache.head_dim,
-          "kv_append: q, k, v and the cache disagree in shape")
-    _on(cache.device, "kv_append", q, k, v, q_start, kv_len, page_table, cos_sin, q_out)
+    shape, dev, raw, given = _start(q, stream)
+    T, heads, dim = shape
+    q_at, qt, qh = _rows(q, shape, dev, "q")
+    if dim != cache.head_dim or cache.dev != dev:
+        _bad("kv_append: q and the cache disagree in head_dim or device")
+    kv = (T, cache.kv_heads, dim)
+    k_at, kt, kh = _rows(k, kv, dev, "k")
+    v_at, vt, vh = _rows(v, kv, dev, "v")
     n_pos = rot = 0
+    table = None
     if cos_sin is not None:
-        _want(cos_sin.dtype is _F32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
-              "cos_sin: contiguous fp32 [positions, rot_dim] wanted")
+        if cos_sin.dtype is not _F32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
+            _bad("cos_sin: contiguous fp32 [positions, rot_dim] wanted")
         n_pos, rot = cos_sin.shape
-    ctx, raw = _launch(cache.device, stream)
-    batch = _batch(T, q_start, kv_len, page_table, None)
+        table = cos_sin.data_ptr()
+    batch = _batch(T, q_start, kv_len, page_table, None, dev)
     if q_out is None:
-        with ctx:
-            q_out = torch.empty((T, heads, dim), dtype=_BF16, device=q.device)
-    _want(q_out.shape == q.shape, "kv_append: q_out has another shape than q")
-    E.check(E.epilora_kv_append(cache.struct, batch, heads, q, qs, k, ks, v, vs, cos_sin, n_pos, rot, interleaved,
-                                q_out, _strides(q_out, "q_out"), status, raw), "kv_append")
+        q_out = _new(q, shape, given)
+    o_at, ot, oh = _rows(q_out, shape, dev, "q_out")
+    rc = _lib().epilora_kv_append(cache.address, batch, heads, q_at, qt, qh, k_at, kt, kh, v_at, vt, vh, table, n_pos,
+                                  rot, 1 if interleaved else 0, o_at, ot, oh, _status(status, dev), raw)
+    if rc:
+        E.check(rc, "kv_append")
     return q_out
 
 
-def _outputs(q, out, lse):
-    T, heads, dim = q.shape
-    if out is None:
-        out = torch.empty((T, heads, dim), dtype=_BF16, device=q.device)
-    _want(out.shape == q.shape, "out has another shape than q")
-    _want(lse is None or (lse.dtype is _F32 and lse.shape == (T, heads) and lse.is_contiguous()),
-          f"lse: contiguous fp32 {(T, heads)} wanted")
-    return out
+def _lse(lse, shape, dev):
+    if lse is None:
+        return None
+    if lse.dtype is not _F32 or lse.shape != shape[:2] or not lse.is_contiguous() or lse.get_device() != dev:
+        _bad("lse: contiguous fp32 [tokens, heads] wanted")
+    return lse.data_ptr()
 
 
 def paged_attention(q, cache: PagedKVCache, q_start, kv_len, page_table, max_new: Optional[int] = None,
@@ -171,17 +218,20 @@ def paged_attention(q, cache: PagedKVCache, q_start, kv_len, page_table, max_new
     new tokens of any sequence, known on the host (default: all of them; 1
     for a decode step). scale defaults to head_dim ** -0.5. lse (optional,
     fp32 [tokens, heads]) receives the log of the softmax sums."""
-    T, heads, dim = q.shape
-    qs = _strides(q, "q")
-    _want(dim == cache.head_dim, "paged_attention: q and the cache disagree in head_dim")
-    _on(cache.device, "paged_attention", q, q_start, kv_len, page_table, out, lse)
-    ctx, raw = _launch(cache.device, stream)
-    batch = _batch(T, q_start, kv_len, page_table, max_new)
-    with ctx:
-        out = _outputs(q, out, lse)
-        ws = (workspace or AttentionWorkspace(q.device)).get(dim)
-    E.check(E.epilora_paged_attention(cache.struct, batch, heads, q, qs, dim ** -0.5 if scale is None else scale, out,
-                                      _strides(out, "out"), lse, ws, ws.numel(), status, raw), "paged_attention")
+    shape, dev, raw, given = _start(q, stream)
+    T, heads, dim = shape
+    q_at, qt, qh = _rows(q, shape, dev, "q")
+    if dim != cache.head_dim or cache.dev != dev:
+        _bad("paged_attention: q and the cache disagree in head_dim or device")
+    batch = _batch(T, q_start, kv_len, page_table, max_new, dev)
+    if out is None:
+        out = _new(q, shape, given)
+    o_at, ot, oh = _rows(out, shape, dev, "out")
+    buf, w_at, w_bytes = _workspace(workspace, q, dim, given)
+    rc = _lib().epilora_paged_attention(cache.address, batch, heads, q_at, qt, qh, dim ** -0.5 if scale is None else scale,
+                                        o_at, ot, oh, _lse(lse, shape, dev), w_at, w_bytes, _status(status, dev), raw)
+    if rc:
+        E.check(rc, "paged_attention")
     return out
 
 
@@ -190,18 +240,26 @@ def prompt_attention(q, k, v, q_start, scale: Optional[float] = None, out=None, 
     """Causal attention of whole packed prompts: prompt b is the rows
     q_start[b] .. q_start[b+1] - 1 of q [tokens, heads, head_dim] and of k, v
     [tokens, kv_heads, head_dim]. Other arguments as paged_attention."""
-    T, heads, dim = q.shape
-    qs, ks, vs = _strides(q, "q"), _strides(k, "k"), _strides(v, "v")
-    _want(k.shape == v.shape and k.shape[0] == T and k.shape[2] == dim, "prompt_attention: q, k and v disagree in shape")
-    _on(q.device, "prompt_attention", k, v, q_start, out, lse)
+    shape, dev, raw, given = _start(q, stream)
+    T, heads, dim = shape
+    q_at, qt, qh = _rows(q, shape, dev, "q")
+    if k.dim() != 3:
+        _bad("k: [tokens, kv_heads, head_dim] wanted")
+    kv_heads = k.shape[1]
+    kv = (T, kv_heads, dim)
+    k_at, kt, kh = _rows(k, kv, dev, "k")
+    v_at, vt, vh = _rows(v, kv, dev, "v")
     n = q_start.numel() - 1
-    _want(n >= 0, "q_start: [sequences + 1] wanted")
-    _index(q_start, (n + 1,), "q_start")
-    ctx, raw = _launch(q.device, stream)
-    with ctx:
-        out = _outputs(q, out, lse)
-        ws = (workspace or AttentionWorkspace(q.device)).get(dim)
-    E.check(E.epilora_prompt_attention(n, T, q_start, heads, k.shape[1], dim, q, qs, k, ks, v, vs,
-                                       dim ** -0.5 if scale is None else scale, out, _strides(out, "out"), lse, ws,
-                                       ws.numel(), status, raw), "prompt_attention")
+    if n < 0:
+        _bad("q_start: [sequences + 1] wanted")
+    starts = _index(q_start, n + 1, dev, "q_start")
+    if out is None:
+        out = _new(q, shape, given)
+    o_at, ot, oh = _rows(out, shape, dev, "out")
+    buf, w_at, w_bytes = _workspace(workspace, q, dim, given)
+    rc = _lib().epilora_prompt_attention(n, T, starts, heads, kv_heads, dim, q_at, qt, qh, k_at, kt, kh, v_at, vt, vh,
+                                         dim ** -0.5 if scale is None else scale, o_at, ot, oh,
+                                         _lse(lse, shape, dev), w_at, w_bytes, _status(status, dev), raw)
+    if rc:
+        E.check(rc, "prompt_attention")
     return out

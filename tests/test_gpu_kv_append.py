@@ -117,7 +117,7 @@ def test_append_keys_and_values_only():
     T = 3
     k = torch.randn(T, 2, 64, device="cuda").to(torch.bfloat16)
     start, length, table = b.dev("q_start", "kv_len", "table")
-    batch = A._batch(T, start, length, table, None)
+    batch = E.KvBatch(1, T, T, table.shape[1], table.shape[1], start.data_ptr(), length.data_ptr(), table.data_ptr())
     rc = E.epilora_kv_append(b.cache.struct, batch, 4, None, (0, 0), k, (128, 64), k, (128, 64), None, 0, 0, False,
                              None, (0, 0))
     assert rc == 0

@@ -16,11 +16,12 @@
 // between blocks is joined by the block that finishes last, in the order of
 // the pieces (results do not depend on which block that is).
 // A block is one copying warp and four computing warps. The copying warp
-// brings units of 16 positions (keys and values of one page) into a ring by
-// TMA (boxes of one page's rows, so every layout with contiguous heads costs
-// the same); warp w computes unit 4 t + w of tile t with a maximum, sum and
-// output of its own, so no barrier stands in the loop; the four meet at the
-// end of a pair.
+// brings 32 positions a slot (keys and values) into a ring by TMA, in boxes of
+// up to 32 rows of a page, so every layout with contiguous heads costs the
+// same; two warps compute 16 positions each of a slot, with a maximum, sum and
+// output of their own, so no barrier stands in the loop; the four meet at the
+// end of a pair. (With 16 positions a slot the copying warp, some 700 cycles
+// a slot, was what bound it.)
 #include "attention.cuh"
 #include "ptx.cuh"
 
@@ -28,7 +29,8 @@ namespace epi {
 namespace {
 
 constexpr int kDecTile = 64;         // positions per tile
-constexpr int kDecUnit = 16;         // positions per warp and ring slot
+constexpr int kDecUnit = 16;         // positions per warp and tile
+constexpr int kDecGroup = 32;        // positions per ring slot (of two warps)
 constexpr int kDecWarps = 4;         // computing warps
 constexpr int kDecThreads = 32 * (kDecWarps + 1);
 constexpr int kDecRows = 16;
@@ -44,19 +46,20 @@ struct DecCfg {
   static constexpr int kRowBytes = D * (E4 ? 1 : 2);
   static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;   // inner extent = swizzle span
   static constexpr int kBoxes = kRowBytes / kBoxBytes;
-  static constexpr int kBox = kDecUnit * kBoxBytes;                     // bytes of one box
+  static constexpr int kUnit = kDecUnit * kBoxBytes;                    // bytes of a warp's rows of a box column
+  static constexpr int kBox = kDecGroup * kBoxBytes;                    // bytes of a box column of a slot
   static constexpr int kHalf = kBoxes * kBox;                           // keys, then values
-  static constexpr int kUnitBytes = 2 * kHalf;
-  // a multiple of the computing warps: a slot always belongs to one warp, which
-  // waits for its fills in order (a warp ahead of a slot's other readers would
-  // take the parity of the fill before last for its own)
-  static constexpr int kSlots = 64 * 1024 / kUnitBytes < 24 ? 64 * 1024 / kUnitBytes : 24;
-  static_assert(kSlots % kDecWarps == 0, "slots are dealt to the warps");
+  static constexpr int kSlotBytes = 2 * kHalf;
+  // an even number: a slot always belongs to the same two warps, which wait for
+  // its fills in order (a warp ahead of a slot's other readers would take the
+  // parity of the fill before last for its own)
+  static constexpr int kSlots = 64 * 1024 / kSlotBytes;
+  static_assert(kSlots % 2 == 0, "slots are dealt to the pairs of warps");
   static constexpr int kOld = D + 8;                                    // floats per row of the meeting buffer
   // bytes: the four warps' outputs, or the weights of a join's pieces
   static constexpr int kMeetOut = kDecWarps * kDecRows * kOld * 4, kMeetJoin = kDecMaxCtas * kDecRows * 4;
   static constexpr int kMeet = kMeetOut > kMeetJoin ? kMeetOut : kMeetJoin;
-  static constexpr int kSmem = 1024 + kSlots * kUnitBytes + kMeet + 2048;
+  static constexpr int kSmem = 1024 + kSlots * kSlotBytes + kMeet + 2048;
 };
 
 struct DecParams {
@@ -67,6 +70,7 @@ struct DecParams {
   float* lse;
   int heads, kv_heads, group;
   int page_shift, page_size, num_pages;
+  int box_rows;         // rows per TMA box
   float scale;
   const float* k_scale;
   const float* v_scale;
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   using C = DecCfg<D, E4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* meet = reinterpret_cast<float*>(smem + C::kSlots * C::kUnitBytes);
+  float* meet = reinterpret_cast<float*>(smem + C::kSlots * C::kSlotBytes);
   float* ml = meet + C::kMeet / 4;                 // [4][16][2] maximum and sum of each warp's rows
   float* row_m = ml + kDecWarps * kDecRows * 2;    // [16]
   float* row_l = row_m + kDecRows;                 // [16]
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);
     }
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -350,11 +354,12 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
     uint32_t phase = 0;
     bool stop = false;
     do {
-      const int units = (w.s.len + kDecUnit - 1) / kDecUnit;       // units that hold a token
-      const int u0 = w.t0 * (kDecTile / kDecUnit), u1 = w.t1 * (kDecTile / kDecUnit);
+      const int per = kDecGroup / p.box_rows;                       // boxes per slot
+      const int boxes = (w.s.len + p.box_rows - 1) / p.box_rows;    // boxes that hold a token
+      const int u0 = w.t0 * (kDecTile / kDecGroup) * per, u1 = w.t1 * (kDecTile / kDecGroup) * per;
       const int32_t* table = p.b.page_table + w.b * p.b.table_stride;
       auto page_of = [&](int u) {
-        return u < min(units, u1) ? table[(u * kDecUnit) >> p.page_shift] : 0;
+        return u < min(boxes, u1) ? table[(u * p.box_rows) >> p.page_shift] : 0;
       };
       int pages = page_of(u0 + lane);
       for (int c = u0; c < u1 && !stop; c += 32) {
@@ -362,29 +367,33 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
         pages = page_of(c + 32 + lane);
         if (now < 0 || now >= p.num_pages) record_status(p.status, EPILORA_ERR_INVALID_ARG);
         const int n = min(32, u1 - c);
-        for (int i = 0; i < n; ++i) {
-          const int u = c + i;
-          const int pg = __shfl_sync(0xffffffffu, now, i);
+        for (int i = 0; i < n; i += per) {
+          const int pg0 = __shfl_sync(0xffffffffu, now, i), pg1 = __shfl_sync(0xffffffffu, now, i + per - 1);
           // the whole warp waits, so that it is together again when one lane
           // issues the copies
-          const bool ok = !*abort_flag && mbar_wait_bounded(&empty[slot], phase ^ 1u, kWaitLimitNs);
-          if (!__all_sync(0xffffffffu, ok)) {
+          bool ok = mbar_try_wait(&empty[slot], phase ^ 1u);
+          if (!__all_sync(0xffffffffu, ok))
+            ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait_bounded(&empty[slot], phase ^ 1u, kWaitLimitNs));
+          if (!ok) {
             stop = true;
             break;
           }
-          if (lane == 0) {
-            if (u < units) {
-              uint8_t* dst = smem + slot * C::kUnitBytes;
-              const int row = (u * kDecUnit) & (p.page_size - 1);
-              mbar_arrive_expect_tx(&full[slot], C::kUnitBytes);
+          if (elect_one()) {
+            const int held = min(max(boxes - (c + i), 0), per);
+            uint8_t* dst = smem + slot * C::kSlotBytes;
+            if (held > 0)
+              mbar_arrive_expect_tx(&full[slot], 2 * C::kRowBytes * held * p.box_rows);
+            else
+              mbar_arrive(&full[slot]);
+            for (int k = 0; k < held; ++k) {
+              const int row = ((c + i + k) * p.box_rows) & (p.page_size - 1);
+              uint8_t* at = dst + k * p.box_rows * C::kBoxBytes;
 #pragma unroll
               for (int x = 0; x < C::kBoxes; ++x) {
                 // a page index out of range reads as zeros
-                tma_load_4d(dst + x * C::kBox, &p.tk, &full[slot], x * C::kBoxBytes, row, w.h, pg);
-                tma_load_4d(dst + C::kHalf + x * C::kBox, &p.tv, &full[slot], x * C::kBoxBytes, row, w.h, pg);
+                tma_load_4d(at + x * C::kBox, &p.tk, &full[slot], x * C::kBoxBytes, row, w.h, k ? pg1 : pg0);
+                tma_load_4d(at + C::kHalf + x * C::kBox, &p.tv, &full[slot], x * C::kBoxBytes, row, w.h, k ? pg1 : pg0);
               }
-            } else {
-              mbar_arrive(&full[slot]);
             }
           }
           __syncwarp();
@@ -413,7 +422,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   // ===== computing warps =====
   const int g = lane >> 2, q = lane & 3;
   const int tid = threadIdx.x;
-  int slot = warp;
+  int slot = warp >> 1;
   uint32_t phase = 0;
   bool dead = false;
   do {
@@ -499,14 +508,16 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
 
     for (int t = w.t0; t < w.t1; ++t) {
       const int at = t * kDecTile + warp * kDecUnit;
-      if (!dead && (*abort_flag || !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs))) {
-        *abort_flag = 1;
-        record_status(p.status, EPILORA_ERR_TIMEOUT);
-        dead = true;
+      if (!dead && !__all_sync(0xffffffffu, mbar_try_wait(&full[slot], phase))) {
+        const bool ok = !*abort_flag && mbar_wait_bounded(&full[slot], phase, kWaitLimitNs);
+        dead = !__all_sync(0xffffffffu, ok);
+        if (dead && lane == 0) {
+          *abort_flag = 1;
+          record_status(p.status, EPILORA_ERR_TIMEOUT);
+        }
       }
-      dead = __any_sync(0xffffffffu, dead);
       if (!dead && at < w.s.len) {
-        uint8_t* ks = smem + slot * C::kUnitBytes;
+        uint8_t* ks = smem + slot * C::kSlotBytes + (warp & 1) * C::kUnit;
         uint8_t* vs = ks + C::kHalf;
         // rows of the page that hold no token of this sequence
         if (at + kDecUnit > w.s.len) dec_zero_rows<D, E4>(vs, w.s.len - at, lane);
@@ -595,7 +606,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
-      slot += kDecWarps;
+      slot += 2;
       if (slot >= C::kSlots) slot -= C::kSlots, phase ^= 1u;
     }
 
@@ -734,7 +745,7 @@ int launch(const AttnArgs& a, DecParams& p, int grid) {
   const uint64_t es = E4 ? 1 : 2;
   const uint64_t dims[4] = {static_cast<uint64_t>(C::kRowBytes), static_cast<uint64_t>(c.page_size),
                             static_cast<uint64_t>(c.kv_heads), static_cast<uint64_t>(c.num_pages)};
-  const uint32_t box[4] = {static_cast<uint32_t>(C::kBoxBytes), kDecUnit, 1, 1};
+  const uint32_t box[4] = {static_cast<uint32_t>(C::kBoxBytes), static_cast<uint32_t>(p.box_rows), 1, 1};
   const uint64_t ks[3] = {c.k_token_stride * es, c.k_head_stride * es, c.k_page_stride * es};
   const uint64_t vs[3] = {c.v_token_stride * es, c.v_head_stride * es, c.v_page_stride * es};
   int rc = make_tma_4d_u8(&p.tk, c.k, dims, ks, box, C::kBoxBytes);
@@ -786,6 +797,7 @@ int launch_attn_decode(const AttnArgs& a, uint32_t* counters, float* partials) {
   p.page_shift = __builtin_ctz(a.cache.page_size);
   p.page_size = a.cache.page_size;
   p.num_pages = a.cache.num_pages;
+  p.box_rows = a.cache.page_size < kDecGroup ? a.cache.page_size : kDecGroup;
   p.scale = a.scale;
   p.k_scale = a.cache.k_scale;
   p.v_scale = a.cache.v_scale;

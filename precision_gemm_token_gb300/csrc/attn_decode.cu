@@ -10,31 +10,33 @@
 // core tile (mma.sync m16n8k16, rows = the group's heads) costs nothing even
 // where 4 or 8 of its rows are used.
 //
-// The cache's positions are cut into tiles of 64; the tiles of all (sequence,
-// head) pairs form one line that is split evenly over the thread blocks (two
-// per SM), so that any mix of lengths loads every SM alike; a pair cut
-// between blocks is joined by the block that finishes last, in the order of
-// the pieces (results do not depend on which block that is).
-// A block is one copying warp and four computing warps. The copying warp
-// brings 32 positions a slot (keys and values) into a ring by TMA, in boxes of
-// up to 32 rows of a page, so every layout with contiguous heads costs the
-// same; two warps compute 16 positions each of a slot, with a maximum, sum and
-// output of their own, so no barrier stands in the loop; the four meet at the
-// end of a pair. (With 16 positions a slot the copying warp, some 700 cycles
-// a slot, was what bound it.)
+// The cache's positions are cut into tiles; the tiles of all (sequence, head)
+// pairs form one line that is split evenly over the thread blocks (two per
+// SM), so that any mix of lengths loads every SM alike; a pair cut between
+// blocks is joined by the block that finishes last, in the order of the pieces
+// (results do not depend on which block that is).
+// A block is four computing warps, a copying and a joining one. The copying
+// warp brings 32 positions a slot (keys and values) into a ring by TMA, in
+// boxes of up to 32 rows of a page, so every layout with contiguous heads costs
+// the same (with 16 positions a slot its 700 cycles a slot were the bound). A
+// computing warp takes its positions of a tile with a maximum, sum and output
+// of its own, so no barrier stands in its loop: 16 positions of bf16, which
+// leaves it waiting for memory; 32 of E4M3, whose half as many bytes leave
+// half the time, for the chains of products of two 16s side by side. At the
+// end of a pair it hands its result to the joining warp and goes on: writing a
+// piece's result out and learning whether it was the last takes 5 us while the
+// memory is busy, and as long again to join.
 #include "attention.cuh"
 #include "ptx.cuh"
 
 namespace epi {
 namespace {
 
-constexpr int kDecTile = 64;         // positions per tile
-constexpr int kDecUnit = 16;         // positions per warp and tile
-constexpr int kDecGroup = 32;        // positions per ring slot (of two warps)
+constexpr int kDecGroup = 32;        // positions per ring slot
 constexpr int kDecWarps = 4;         // computing warps
-constexpr int kDecThreads = 32 * (kDecWarps + 1);
+constexpr int kDecThreads = 32 * (kDecWarps + 2);
 constexpr int kDecRows = 16;
-constexpr int kDecMaxCtas = 512;     // blocks of a launch (pieces of a join) at most
+constexpr int kDecMaxCtas = 512;     // blocks of a launch at most
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
 // a row's maximum is raised (and its sums rescaled) only when a score exceeds
 // it by this many powers of two: weights stay below 2^8, exact in fp32 sums
@@ -43,22 +45,24 @@ constexpr float kRaise = 8.0f;
 
 template <int D, bool E4>
 struct DecCfg {
+  static constexpr int kUnit = E4 ? 32 : 16;                            // positions per warp and tile
+  static constexpr int kTile = kUnit * kDecWarps;                       // positions per tile
+  static constexpr int kPerSlot = kDecGroup / kUnit;                    // warps that share a slot
+  static constexpr int kSlotStep = kDecWarps / kPerSlot;                // slots per tile
   static constexpr int kRowBytes = D * (E4 ? 1 : 2);
   static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;   // inner extent = swizzle span
   static constexpr int kBoxes = kRowBytes / kBoxBytes;
-  static constexpr int kUnit = kDecUnit * kBoxBytes;                    // bytes of a warp's rows of a box column
+  static constexpr int kUnitBytes = kUnit * kBoxBytes;                  // a warp's rows of a box column
   static constexpr int kBox = kDecGroup * kBoxBytes;                    // bytes of a box column of a slot
   static constexpr int kHalf = kBoxes * kBox;                           // keys, then values
   static constexpr int kSlotBytes = 2 * kHalf;
-  // an even number: a slot always belongs to the same two warps, which wait for
-  // its fills in order (a warp ahead of a slot's other readers would take the
-  // parity of the fill before last for its own)
+  // a slot always belongs to the same warps, which wait for its fills in order
+  // (a warp ahead of a slot's other readers would take the parity of the fill
+  // before last for its own)
   static constexpr int kSlots = 64 * 1024 / kSlotBytes;
-  static_assert(kSlots % 2 == 0, "slots are dealt to the pairs of warps");
+  static_assert(kSlots % kSlotStep == 0, "slots are dealt to the warps");
   static constexpr int kOld = D + 8;                                    // floats per row of the meeting buffer
-  // bytes: the four warps' outputs, or the weights of a join's pieces
-  static constexpr int kMeetOut = kDecWarps * kDecRows * kOld * 4, kMeetJoin = kDecMaxCtas * kDecRows * 4;
-  static constexpr int kMeet = kMeetOut > kMeetJoin ? kMeetOut : kMeetJoin;
+  static constexpr int kMeet = kDecWarps * kDecRows * kOld * 4;         // the four warps' outputs
   static constexpr int kSmem = 1024 + kSlots * kSlotBytes + kMeet + 2048;
 };
 
@@ -84,6 +88,7 @@ struct DecSeq {
   int first, n, len, base;   // packed rows, tokens in the cache (clamped), position of new token 0
   int tiles;                 // 0: not of this class
 };
+template <int TILE>
 __device__ __forceinline__ DecSeq dec_seq(const DecParams& p, int b, bool& bad) {
   DecSeq s;
   const SeqRows r = seq_rows(p.b.q_start, b, p.b.n_tokens, bad);
@@ -94,7 +99,7 @@ __device__ __forceinline__ DecSeq dec_seq(const DecParams& p, int b, bool& bad) 
   s.n = r.n;
   s.base = len - r.n;
   s.len = max(min(len, cap), 0);
-  s.tiles = r.n > 0 && attn_decode_takes(r.n, p.group) ? max((s.len + kDecTile - 1) / kDecTile, 1) : 0;
+  s.tiles = r.n > 0 && attn_decode_takes(r.n, p.group) ? max((s.len + TILE - 1) / TILE, 1) : 0;
   return s;
 }
 
@@ -123,10 +128,11 @@ __device__ __forceinline__ void dec_piece(const DecParams& p, DecWalk& w) {
 }
 
 // false: nothing to do. Called by whole warps.
+template <int TILE>
 __device__ __forceinline__ bool dec_begin(const DecParams& p, DecWalk& w, int lane) {
   uint64_t mine = 0;
   bool bad = false;
-  for (int b = lane; b < p.b.n_seqs; b += 32) mine += dec_seq(p, b, bad).tiles;
+  for (int b = lane; b < p.b.n_seqs; b += 32) mine += dec_seq<TILE>(p, b, bad).tiles;
   if (bad && blockIdx.x == 0 && threadIdx.x < 32) record_status(p.status, EPILORA_ERR_INVALID_ARG);
   w.total = warp_sum(mine) * p.kv_heads;
   if (w.total == 0) return false;
@@ -139,7 +145,7 @@ __device__ __forceinline__ bool dec_begin(const DecParams& p, DecWalk& w, int la
   w.b = -1;
   for (int b0 = 0; b0 < p.b.n_seqs; b0 += 32) {
     const int b = b0 + lane;
-    const uint64_t c = b < p.b.n_seqs ? static_cast<uint64_t>(dec_seq(p, b, bad).tiles) * p.kv_heads : 0;
+    const uint64_t c = b < p.b.n_seqs ? static_cast<uint64_t>(dec_seq<TILE>(p, b, bad).tiles) * p.kv_heads : 0;
     uint64_t inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -156,13 +162,14 @@ __device__ __forceinline__ bool dec_begin(const DecParams& p, DecWalk& w, int la
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
   if (w.b < 0) return false;
-  w.s = dec_seq(p, w.b, bad);
+  w.s = dec_seq<TILE>(p, w.b, bad);
   w.h = static_cast<int>((w.x - w.pair0) / w.s.tiles);
   w.pair0 += static_cast<uint64_t>(w.h) * w.s.tiles;
   dec_piece(p, w);
   return true;
 }
 
+template <int TILE>
 __device__ __forceinline__ bool dec_next(const DecParams& p, DecWalk& w) {
   w.x += w.t1 - w.t0;
   if (w.x >= w.end) return false;
@@ -172,14 +179,12 @@ __device__ __forceinline__ bool dec_next(const DecParams& p, DecWalk& w) {
     bool bad = false;
     do {   // x < end: a sequence of the class follows
       if (++w.b >= p.b.n_seqs) return false;
-      w.s = dec_seq(p, w.b, bad);
+      w.s = dec_seq<TILE>(p, w.b, bad);
     } while (w.s.tiles == 0);
   }
   dec_piece(p, w);
   return true;
 }
-
-__device__ __forceinline__ void meet_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kDecWarps * 32) : "memory"); }
 
 template <bool E4>
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -207,7 +212,7 @@ __device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t byte) {
   return a ^ (((a >> 7) & (SPAN / 16 - 1)) << 4);
 }
 
-// O += P V over one unit. SEL: only the rows of one token take the result
+// O += P V over 16 positions. SEL: only the rows of one token take the result
 // (sel0 / sel1: the thread's rows g and g + 8).
 template <int D, bool E4, bool SEL>
 __device__ __forceinline__ void dec_pv(float (&acc)[D / 8][4], const uint32_t (&pa)[4], const uint8_t* vs, int lane,
@@ -265,12 +270,12 @@ __device__ __forceinline__ void dec_pv(float (&acc)[D / 8][4], const uint32_t (&
   }
 }
 
-// zero the value rows [from, 16) of a unit (whole warp)
+// zero the value rows [from, kUnit) of a unit (whole warp)
 template <int D, bool E4>
 __device__ __forceinline__ void dec_zero_rows(uint8_t* vs, int from, int lane) {
   using C = DecCfg<D, E4>;
   constexpr int per_row = C::kRowBytes / 16;
-  const int n = (kDecUnit - from) * per_row;
+  const int n = (C::kUnit - from) * per_row;
   for (int i = lane; i < n; i += 32) {
     const int row = from + i / per_row, c = i % per_row;
     const int box = c / (C::kBoxBytes / 16), cc = c % (C::kBoxBytes / 16);
@@ -308,19 +313,21 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* meet = reinterpret_cast<float*>(smem + C::kSlots * C::kSlotBytes);
   float* ml = meet + C::kMeet / 4;                 // [4][16][2] maximum and sum of each warp's rows
-  float* row_m = ml + kDecWarps * kDecRows * 2;    // [16]
-  float* row_l = row_m + kDecRows;                 // [16]
-  uint64_t* full = reinterpret_cast<uint64_t*>(row_l + kDecRows);
+  float* fac = ml + kDecWarps * kDecRows * 2;      // [4][16] factors of the warps' outputs
+  uint64_t* full = reinterpret_cast<uint64_t*>(fac + kDecWarps * kDecRows);
   uint64_t* empty = full + C::kSlots;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kSlots);
-  volatile int* last_flag = abort_flag + 1;
+  uint64_t* meet_full = empty + C::kSlots;
+  uint64_t* meet_free = meet_full + 1;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(meet_free + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 2);
+      mbar_init(&empty[i], C::kPerSlot);
     }
+    mbar_init(meet_full, kDecWarps);
+    mbar_init(meet_free, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&p.tk);
@@ -345,7 +352,24 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   }
 
   DecWalk w;
-  if (!dec_begin(p, w, lane)) return;
+  if (!dec_begin<C::kTile>(p, w, lane)) return;
+
+  // a bounded wait of a whole warp; false once any wait of the block ran out
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    bool ok = false;
+    for (uint32_t polls = 1; !ok; ++polls) {
+      ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+      if ((polls & 63u) == 0u && (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs)) break;
+    }
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (lane == 0) {
+      *abort_flag = 1;
+      record_status(p.status, EPILORA_ERR_TIMEOUT);
+    }
+    return false;
+  };
 
   if (warp == kDecWarps) {
     // ===== copying warp =====
@@ -356,7 +380,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
     do {
       const int per = kDecGroup / p.box_rows;                       // boxes per slot
       const int boxes = (w.s.len + p.box_rows - 1) / p.box_rows;    // boxes that hold a token
-      const int u0 = w.t0 * (kDecTile / kDecGroup) * per, u1 = w.t1 * (kDecTile / kDecGroup) * per;
+      const int u0 = w.t0 * (C::kTile / kDecGroup) * per, u1 = w.t1 * (C::kTile / kDecGroup) * per;
       const int32_t* table = p.b.page_table + w.b * p.b.table_stride;
       auto page_of = [&](int u) {
         return u < min(boxes, u1) ? table[(u * p.box_rows) >> p.page_shift] : 0;
@@ -369,12 +393,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
         const int n = min(32, u1 - c);
         for (int i = 0; i < n; i += per) {
           const int pg0 = __shfl_sync(0xffffffffu, now, i), pg1 = __shfl_sync(0xffffffffu, now, i + per - 1);
-          // the whole warp waits, so that it is together again when one lane
-          // issues the copies
-          bool ok = mbar_try_wait(&empty[slot], phase ^ 1u);
-          if (!__all_sync(0xffffffffu, ok))
-            ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait_bounded(&empty[slot], phase ^ 1u, kWaitLimitNs));
-          if (!ok) {
+          if (!wait(&empty[slot], phase ^ 1u)) {
             stop = true;
             break;
           }
@@ -400,11 +419,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
           if (++slot == C::kSlots) slot = 0, phase ^= 1u;
         }
       }
-    } while (!stop && dec_next(p, w));
-    if (stop) {
-      *abort_flag = 1;
-      record_status(p.status, EPILORA_ERR_TIMEOUT);
-    }
+    } while (!stop && dec_next<C::kTile>(p, w));
     if (lane == 0) {
       // no copy in flight at exit (only after a wait that ran out is there
       // one that no computing warp has waited for): wait for the slots'
@@ -419,10 +434,115 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
     return;
   }
 
+  if (warp == kDecWarps + 1) {
+    // ===== joining warp =====
+    uint32_t piece = 0;
+    do {
+      if (!wait(meet_full, piece & 1u)) break;
+      ++piece;
+      const int rows = w.s.n * p.group;
+      // lane 2 row + i: the warps' factors of a row, its maximum and sum
+      float top = -INFINITY, sum = 0.0f;
+      {
+        const int row = lane >> 1;
+#pragma unroll
+        for (int k = 0; k < kDecWarps; ++k) top = fmaxf(top, ml[(k * kDecRows + row) * 2]);
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int k = 0; k < kDecWarps; ++k) {
+          const float f = exp2_approx(ml[(k * kDecRows + row) * 2] - base);
+          sum += ml[(k * kDecRows + row) * 2 + 1] * f;
+          if ((k & 1) == (lane & 1)) fac[k * kDecRows + row] = f;
+        }
+      }
+      __syncwarp();
+      const float vscale = E4 ? p.v_scale[w.h] : 1.0f;
+      // four outputs of a row from element d on; m, l: the row's maximum and sum
+      auto put = [&](int row, int d, float4 o, float m, float l) {
+        const int i = row / p.group, h = w.h * p.group + row % p.group;
+        const int64_t tok = w.s.first + i;
+        const float inv = vscale / l;
+        uint2 v = make_uint2(0, 0);   // (l == 0: the row sees nothing)
+        if (l != 0.0f) v = make_uint2(pack16<false>(o.x * inv, o.y * inv), pack16<false>(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2*>(p.o.p + tok * p.o.ts + h * p.o.hs + d) = v;
+        if (p.lse != nullptr && d == 0)
+          p.lse[tok * p.heads + h] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
+      };
+      const bool whole = w.t0 == 0 && w.t1 == w.s.tiles;
+      constexpr int kPart = 2 * kDecRows + kDecRows * D;   // floats of a partial result: m, l, O
+      // slot of a block's piece: 0 where it starts the block's range, else 1
+      const uint64_t range0 = blockIdx.x * w.total / w.ctas;
+      float* part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (w.x == range0 ? 0 : 1)) * kPart;
+      for (int e0 = 0; e0 < rows * (D / 4); e0 += 32) {
+        const int e = e0 + lane;
+        const int row = min(e / (D / 4), kDecRows - 1), d = 4 * (e % (D / 4));
+        const float m = __shfl_sync(0xffffffffu, top, 2 * row), l = __shfl_sync(0xffffffffu, sum, 2 * row);
+        if (e >= rows * (D / 4)) continue;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kDecWarps; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(meet + (k * kDecRows + row) * C::kOld + d);
+          const float f = fac[k * kDecRows + row];
+          o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+        }
+        if (whole)
+          put(row, d, o, m, l);
+        else
+          *reinterpret_cast<float4*>(part + 2 * kDecRows + row * D + d) = o;
+      }
+      if (!whole && (lane & 1) == 0) part[lane >> 1] = top, part[kDecRows + (lane >> 1)] = sum;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(meet_free);
+      if (whole) continue;
+      // the blocks that hold the pair's first and last tile
+      const int first = static_cast<int>(((w.pair0 + 1) * w.ctas - 1) / w.total);
+      const int last = static_cast<int>(((w.pair0 + w.s.tiles) * w.ctas - 1) / w.total);
+      const int pieces = last - first + 1;
+      uint32_t is_last = 0;
+      if (lane == 0) {
+        __threadfence();
+        is_last = atomicAdd(p.counters + first, 1u) == static_cast<uint32_t>(pieces - 1);
+        if (is_last) p.counters[first] = 0;
+      }
+      if (!__shfl_sync(0xffffffffu, is_last, 0)) continue;
+      __threadfence();
+      // the first piece starts its block's range, or follows other pairs in it
+      const bool at_start = first * w.total / w.ctas == w.pair0;
+      auto piece_at = [&](int k) {
+        const int64_t n = k == 0 ? 2 * static_cast<int64_t>(first) + (at_start ? 0 : 1) : 2 * static_cast<int64_t>(first + k);
+        return p.partials + n * kPart;
+      };
+      // a row's maximum and sum over the pieces: lane 2 row + i takes every other piece
+      top = -INFINITY, sum = 0.0f;
+      for (int k = lane & 1; k < pieces; k += 2) top = fmaxf(top, __ldcg(piece_at(k) + (lane >> 1)));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      const float base = top == -INFINITY ? 0.0f : top;
+      for (int k = lane & 1; k < pieces; k += 2)
+        sum += __ldcg(piece_at(k) + kDecRows + (lane >> 1)) * exp2_approx(__ldcg(piece_at(k) + (lane >> 1)) - base);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      for (int e0 = 0; e0 < rows * (D / 4); e0 += 32) {
+        const int e = e0 + lane;
+        const int row = min(e / (D / 4), kDecRows - 1), d = 4 * (e % (D / 4));
+        const float m = __shfl_sync(0xffffffffu, top, 2 * row), l = __shfl_sync(0xffffffffu, sum, 2 * row);
+        if (e >= rows * (D / 4)) continue;
+        const float row_base = m == -INFINITY ? 0.0f : m;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int k = 0; k < pieces; ++k) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(piece_at(k) + 2 * kDecRows + row * D + d));
+          const float f = exp2_approx(__ldcg(piece_at(k) + row) - row_base);
+          o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+        }
+        put(row, d, o, m, l);
+      }
+    } while (dec_next<C::kTile>(p, w));
+    return;
+  }
+
   // ===== computing warps =====
   const int g = lane >> 2, q = lane & 3;
-  const int tid = threadIdx.x;
-  int slot = warp >> 1;
+  int slot = warp / C::kPerSlot;
+  uint32_t piece = 0;
   uint32_t phase = 0;
   bool dead = false;
   do {
@@ -507,21 +627,17 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
     for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
 
     for (int t = w.t0; t < w.t1; ++t) {
-      const int at = t * kDecTile + warp * kDecUnit;
-      if (!dead && !__all_sync(0xffffffffu, mbar_try_wait(&full[slot], phase))) {
-        const bool ok = !*abort_flag && mbar_wait_bounded(&full[slot], phase, kWaitLimitNs);
-        dead = !__all_sync(0xffffffffu, ok);
-        if (dead && lane == 0) {
-          *abort_flag = 1;
-          record_status(p.status, EPILORA_ERR_TIMEOUT);
-        }
-      }
+      const int at = t * C::kTile + warp * C::kUnit;
+      if (!dead) dead = !wait(&full[slot], phase);
       if (!dead && at < w.s.len) {
-        uint8_t* ks = smem + slot * C::kSlotBytes + (warp & 1) * C::kUnit;
+        uint8_t* ks = smem + slot * C::kSlotBytes + (warp % C::kPerSlot) * C::kUnitBytes;
         uint8_t* vs = ks + C::kHalf;
         // rows of the page that hold no token of this sequence
-        if (at + kDecUnit > w.s.len) dec_zero_rows<D, E4>(vs, w.s.len - at, lane);
-        float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        if (at + C::kUnit > w.s.len) dec_zero_rows<D, E4>(vs, w.s.len - at, lane);
+        constexpr int NT = C::kUnit / 8;      // columns of scores, eight positions each
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
         if (!E4) {
           const uint32_t base = smem_u32(ks);
           const uint32_t tok = (lane & 7) + (lane >> 4) * 8;
@@ -534,12 +650,12 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
             mma16<E4>(s[1], qa[k], r[2], r[3]);
           }
         } else {
-          // thread (g, q): elements 64 c + 16 q .. + 15 of token g (and g + 8);
+          // thread (g, q): elements 64 c + 16 q .. + 15 of the tokens 8 nt + g;
           // step j of a c contracts elements 4 j .. 4 j + 3 of each thread
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int nt = 0; nt < NT; ++nt) {
               const uint4 v = *reinterpret_cast<const uint4*>(ks + swz<C::kBoxBytes>(nt * 8 + g, 64 * c + 16 * q));
               const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -548,14 +664,14 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
             }
         }
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
           s[nt][0] *= c0, s[nt][1] *= c0;
           s[nt][2] *= c1, s[nt][3] *= c1;
         }
-        const bool edge = at + kDecUnit > see_all;
+        const bool edge = at + C::kUnit > see_all;
         if (edge) {
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int pos = at + nt * 8 + 2 * q + e;
@@ -563,8 +679,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
               if (pos >= see1) s[nt][2 + e] = -INFINITY;
             }
         }
-        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        float x0 = fmaxf(s[0][0], s[0][1]), x1 = fmaxf(s[0][2], s[0][3]);
+#pragma unroll
+        for (int nt = 1; nt < NT; ++nt) x0 = max3(x0, s[nt][0], s[nt][1]), x1 = max3(x1, s[nt][2], s[nt][3]);
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
@@ -580,63 +697,53 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
           for (int i = 0; i < D / 8; ++i) acc[i][0] *= f0, acc[i][1] *= f0, acc[i][2] *= f1, acc[i][3] *= f1;
         }
         const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+        uint32_t pa[NT / 2][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
           s[nt][0] = exp2_approx(s[nt][0] - b0), s[nt][1] = exp2_approx(s[nt][1] - b0);
           s[nt][2] = exp2_approx(s[nt][2] - b1), s[nt][3] = exp2_approx(s[nt][3] - b1);
+          l0 += s[nt][0] + s[nt][1];
+          l1 += s[nt][2] + s[nt][3];
+          // the weights as 16-bit operands (each within 2^-8 of itself, 2^-11 in fp16)
+          pa[nt / 2][2 * (nt & 1)] = pack16<E4>(s[nt][0], s[nt][1]);
+          pa[nt / 2][2 * (nt & 1) + 1] = pack16<E4>(s[nt][2], s[nt][3]);
         }
-        l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
-        l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
-        // the weights as 16-bit operands (each within 2^-9 of itself, 2^-11 in fp16)
-        const uint32_t pa[4] = {pack16<E4>(s[0][0], s[0][1]), pack16<E4>(s[0][2], s[0][3]),
-                                pack16<E4>(s[1][0], s[1][1]), pack16<E4>(s[1][2], s[1][3])};
         // A zero weight times a NaN or an infinity is NaN: where a position
         // is hidden from some rows and holds one, each token's rows take
         // their own product, the later positions zeroed from the last token
         // to the first.
-        if (edge && n > 1 && dec_rows_nonfinite<D, E4>(vs, max(see_all - at, 0), min(kDecUnit, w.s.len - at), lane)) {
+        if (edge && n > 1 && dec_rows_nonfinite<D, E4>(vs, max(see_all - at, 0), min(C::kUnit, w.s.len - at), lane)) {
+#pragma unroll 1
           for (int i = n - 1; i >= 0; --i) {
             const int see = max(min(w.s.base + i + 1, w.s.len), 0) - at;
-            if (see < kDecUnit) dec_zero_rows<D, E4>(vs, max(see, 0), lane);
-            dec_pv<D, E4, true>(acc, pa, vs, lane, ok0 && i0 == i, ok1 && i1 == i);
+            if (see < C::kUnit) dec_zero_rows<D, E4>(vs, max(see, 0), lane);
+#pragma unroll
+            for (int u = 0; u < NT / 2; ++u)
+              dec_pv<D, E4, true>(acc, pa[u], vs + u * 16 * C::kBoxBytes, lane, ok0 && i0 == i, ok1 && i1 == i);
           }
         } else {
-          dec_pv<D, E4, false>(acc, pa, vs, lane, true, true);
+#pragma unroll
+          for (int u = 0; u < NT / 2; ++u)
+            dec_pv<D, E4, false>(acc, pa[u], vs + u * 16 * C::kBoxBytes, lane, true, true);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
-      slot += 2;
+      slot += C::kSlotStep;
       if (slot >= C::kSlots) slot -= C::kSlots, phase ^= 1u;
     }
 
-    // ===== the four warps meet =====
+    // ===== handed to the joining warp =====
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    // (after a wait that ran out nothing is waited for any more)
+    if (!dead) dead = !wait(meet_free, (piece & 1u) ^ 1u);
+    ++piece;
     if (q == 0) {
       ml[(warp * kDecRows + r0) * 2] = m0, ml[(warp * kDecRows + r0) * 2 + 1] = l0;
       ml[(warp * kDecRows + r1) * 2] = m1, ml[(warp * kDecRows + r1) * 2 + 1] = l1;
-    }
-    meet_barrier();
-    float f[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = r == 0 ? r0 : r1;
-      float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kDecWarps; ++k) top = fmaxf(top, ml[(k * kDecRows + row) * 2]);
-      const float base = top == -INFINITY ? 0.0f : top;
-      f[r] = exp2_approx((r == 0 ? m0 : m1) - base);
-      if (warp == 0 && q == 0) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kDecWarps; ++k)
-          sum += ml[(k * kDecRows + row) * 2 + 1] * exp2_approx(ml[(k * kDecRows + row) * 2] - base);
-        row_m[row] = top;
-        row_l[row] = sum;
-      }
     }
     float* mine = meet + warp * kDecRows * C::kOld;
 #pragma unroll
@@ -644,98 +751,12 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
       // columns 2q and 2q + 1 of n-tile nt
       const int d0 = E4 ? 2 * q * (D / 8) + nt : nt * 8 + 2 * q;
       const int d1 = E4 ? d0 + D / 8 : d0 + 1;
-      if (ok0) mine[r0 * C::kOld + d0] = acc[nt][0] * f[0], mine[r0 * C::kOld + d1] = acc[nt][1] * f[0];
-      if (ok1) mine[r1 * C::kOld + d0] = acc[nt][2] * f[1], mine[r1 * C::kOld + d1] = acc[nt][3] * f[1];
+      if (ok0) mine[r0 * C::kOld + d0] = acc[nt][0], mine[r0 * C::kOld + d1] = acc[nt][1];
+      if (ok1) mine[r1 * C::kOld + d0] = acc[nt][2], mine[r1 * C::kOld + d1] = acc[nt][3];
     }
-    meet_barrier();
-
-    const float vscale = E4 ? p.v_scale[w.h] : 1.0f;
-    auto put = [&](int row, int d, float o0, float o1, float m, float l) {
-      const int i = row / p.group, h = w.h * p.group + row % p.group;
-      const int64_t tok = w.s.first + i;
-      const float inv = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);
-      const uint32_t v = l == 0.0f ? 0u : pack16<false>(o0 * inv, o1 * inv);
-      *reinterpret_cast<uint32_t*>(p.o.p + tok * p.o.ts + h * p.o.hs + d) = v;
-      if (p.lse != nullptr && d == 0)
-        p.lse[tok * p.heads + h] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
-    };
-    const bool whole = w.t0 == 0 && w.t1 == w.s.tiles;
-    constexpr int kPart = 2 * kDecRows + kDecRows * D;   // floats of a partial result: m, l, O
-    // slot of a block's piece: 0 where it starts the block's range, else 1
-    const uint64_t range0 = blockIdx.x * w.total / w.ctas;
-    float* part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (w.x == range0 ? 0 : 1)) * kPart;
-    for (int e = tid; e < rows * (D / 2); e += kDecWarps * 32) {
-      const int row = e / (D / 2), d = 2 * (e % (D / 2));
-      float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int k = 0; k < kDecWarps; ++k) {
-        const float2 v = *reinterpret_cast<const float2*>(meet + (k * kDecRows + row) * C::kOld + d);
-        o.x += v.x;
-        o.y += v.y;
-      }
-      if (whole)
-        put(row, d, o.x, o.y, row_m[row], row_l[row]);
-      else
-        *reinterpret_cast<float2*>(part + 2 * kDecRows + row * D + d) = o;
-    }
-    if (!whole) {
-      if (tid < kDecRows) part[tid] = row_m[tid], part[kDecRows + tid] = row_l[tid];
-      // the blocks that hold the pair's first and last tile
-      const int first = static_cast<int>(((w.pair0 + 1) * w.ctas - 1) / w.total);
-      const int last = static_cast<int>(((w.pair0 + w.s.tiles) * w.ctas - 1) / w.total);
-      const int pieces = last - first + 1;
-      __threadfence();
-      meet_barrier();
-      if (tid == 0) {
-        const uint32_t before = atomicAdd(p.counters + first, 1u);
-        const int is_last = before == static_cast<uint32_t>(pieces - 1);
-        if (is_last) p.counters[first] = 0;
-        *last_flag = is_last;
-      }
-      meet_barrier();
-      if (*last_flag) {
-        __threadfence();
-        // the first piece starts its block's range, or follows other pairs in it
-        const bool at_start = first * w.total / w.ctas == w.pair0;
-        auto piece = [&](int k) {
-          const int64_t s = k == 0 ? 2 * static_cast<int64_t>(first) + (at_start ? 0 : 1)
-                                   : 2 * static_cast<int64_t>(first + k);
-          return p.partials + s * kPart;
-        };
-        // weights of the pieces per row: 8 threads a row
-        {
-          const int row = tid >> 3, sub = tid & 7;
-          float top = -INFINITY;
-          for (int k = sub; k < pieces; k += 8) top = fmaxf(top, __ldcg(piece(k) + row));
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float base = top == -INFINITY ? 0.0f : top;
-          for (int k = sub; k < pieces; k += 8) meet[k * kDecRows + row] = exp2_approx(__ldcg(piece(k) + row) - base);
-          if (sub == 0) row_m[row] = top;
-        }
-        meet_barrier();
-        if (tid < kDecRows) {
-          float sum = 0.0f;
-          for (int k = 0; k < pieces; ++k) sum += __ldcg(piece(k) + kDecRows + tid) * meet[k * kDecRows + tid];
-          row_l[tid] = sum;
-        }
-        meet_barrier();
-        for (int e = tid; e < rows * (D / 2); e += kDecWarps * 32) {
-          const int row = e / (D / 2), d = 2 * (e % (D / 2));
-          float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-          for (int k = 0; k < pieces; ++k) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(piece(k) + 2 * kDecRows + row * D + d));
-            const float f2 = meet[k * kDecRows + row];
-            o.x += v.x * f2;
-            o.y += v.y * f2;
-          }
-          put(row, d, o.x, o.y, row_m[row], row_l[row]);
-        }
-      }
-    }
-    meet_barrier();   // the meeting buffer is free again
-  } while (dec_next(p, w));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(meet_full);
+  } while (!dead && dec_next<C::kTile>(p, w));
 }
 
 template <int D, bool E4>
@@ -805,10 +826,11 @@ int launch_attn_decode(const AttnArgs& a, uint32_t* counters, float* partials) {
   p.partials = partials;
   p.status = a.status;
   // no more blocks than tiles there can be
-  const int64_t cap = static_cast<int64_t>(a.batch.table_pages) * a.cache.page_size;
-  const int64_t most = a.batch.n_seqs * (a.cache.kv_heads * ((cap + kDecTile - 1) / kDecTile + 1));
-  const int grid = static_cast<int>(most < 1 ? 1 : (most < dec_ctas() ? most : dec_ctas()));
   const bool e4 = a.cache.kv_fmt == EPILORA_KV_E4M3;
+  const int tile = e4 ? DecCfg<128, true>::kTile : DecCfg<128, false>::kTile;
+  const int64_t cap = static_cast<int64_t>(a.batch.table_pages) * a.cache.page_size;
+  const int64_t most = a.batch.n_seqs * (a.cache.kv_heads * ((cap + tile - 1) / tile + 1));
+  const int grid = static_cast<int>(most < 1 ? 1 : (most < dec_ctas() ? most : dec_ctas()));
   if (a.cache.head_dim == 64) return e4 ? launch<64, true>(a, p, grid) : launch<64, false>(a, p, grid);
   return e4 ? launch<128, true>(a, p, grid) : launch<128, false>(a, p, grid);
 }

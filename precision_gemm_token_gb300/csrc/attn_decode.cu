@@ -37,6 +37,8 @@ constexpr int kDecWarps = 4;         // computing warps
 constexpr int kDecThreads = 32 * (kDecWarps + 2);
 constexpr int kDecRows = 16;
 constexpr int kDecMaxCtas = 512;     // blocks of a launch at most
+constexpr int kDecPieces = 4;        // pieces of work told ahead
+constexpr int kDecPieceInts = 12;
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
 // a row's maximum is raised (and its sums rescaled) only when a score exceeds
 // it by this many powers of two: weights stay below 2^8, exact in fp32 sums
@@ -103,8 +105,7 @@ __device__ __forceinline__ DecSeq dec_seq(const DecParams& p, int b, bool& bad) 
   return s;
 }
 
-// Walks the pieces of a thread block's range of the line of tiles. Every warp
-// holds a copy and steps it alike.
+// Walks the pieces of a thread block's range of the line of tiles (one warp).
 struct DecWalk {
   uint64_t x, end;     // tiles still to do: [x, end)
   uint64_t total;
@@ -133,7 +134,7 @@ __device__ __forceinline__ bool dec_begin(const DecParams& p, DecWalk& w, int la
   uint64_t mine = 0;
   bool bad = false;
   for (int b = lane; b < p.b.n_seqs; b += 32) mine += dec_seq<TILE>(p, b, bad).tiles;
-  if (bad && blockIdx.x == 0 && threadIdx.x < 32) record_status(p.status, EPILORA_ERR_INVALID_ARG);
+  if (bad && blockIdx.x == 0) record_status(p.status, EPILORA_ERR_INVALID_ARG);
   w.total = warp_sum(mine) * p.kv_heads;
   if (w.total == 0) return false;
   w.ctas = static_cast<int>(min(static_cast<uint64_t>(gridDim.x), w.total));
@@ -184,6 +185,32 @@ __device__ __forceinline__ bool dec_next(const DecParams& p, DecWalk& w) {
   }
   dec_piece(p, w);
   return true;
+}
+
+// A piece as the walking warp tells it to the others.
+struct DecPiece {
+  int first, n, len, base;   // as in DecSeq
+  int h;
+  int t0, t1;                // tiles; t0 == t1: no more work
+  int whole;                 // the pair's only piece
+  int first_cta, pieces;     // of a pair in several pieces: the blocks first_cta, ...
+  int slot, slot0;           // where this piece's, and the first piece's, partial result goes
+};
+static_assert(sizeof(DecPiece) == 4 * kDecPieceInts, "one int per field");
+
+__device__ __forceinline__ DecPiece dec_piece_of(const DecWalk& w) {
+  DecPiece q;
+  q.first = w.s.first, q.n = w.s.n, q.len = w.s.len, q.base = w.s.base;
+  q.h = w.h;
+  q.t0 = w.t0, q.t1 = w.t1;
+  q.whole = w.t0 == 0 && w.t1 == w.s.tiles;
+  // the blocks that hold the pair's first and last tile
+  q.first_cta = static_cast<int>(((w.pair0 + 1) * w.ctas - 1) / w.total);
+  q.pieces = static_cast<int>(((w.pair0 + w.s.tiles) * w.ctas - 1) / w.total) - q.first_cta + 1;
+  // a piece that starts its block's range goes to the block's slot 0, the one that ends it to slot 1
+  q.slot = 2 * blockIdx.x + (w.x == blockIdx.x * w.total / w.ctas ? 0 : 1);
+  q.slot0 = 2 * q.first_cta + (q.first_cta * w.total / w.ctas == w.pair0 ? 0 : 1);
+  return q;
 }
 
 template <bool E4>
@@ -243,29 +270,28 @@ __device__ __forceinline__ void dec_pv(float (&acc)[D / 8][4], const uint32_t (&
   } else {
     // Thread (g, q) holds the D / 8 elements from g D / 8 on of the tokens
     // 2q, 2q+1, 2q+8, 2q+9: column g of n-tile nt is element g D / 8 + nt.
-    constexpr int W = D / 32;   // 32-bit words per thread and token
-    uint32_t w[4][W];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const uint32_t tok = 2 * q + (t & 1) + (t >> 1) * 8;
-      const uint8_t* src = vs + swz<C::kBoxBytes>(tok, g * (D / 8));
-      if (D == 128) {
-        const uint4 v = *reinterpret_cast<const uint4*>(src);
-        w[t][0] = v.x, w[t][1] = v.y, w[t][2 % W] = v.z, w[t][3 % W] = v.w;
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(src);
-        w[t][0] = v.x, w[t][1] = v.y;
+    for (int c = 0; c < D / 64; ++c) {     // eight elements at a time
+      uint2 w[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t tok = 2 * q + (t & 1) + (t >> 1) * 8;
+        w[t] = *reinterpret_cast<const uint2*>(vs + swz<C::kBoxBytes>(tok, g * (D / 8) + c * 8));
       }
-    }
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      uint32_t lo[4], hi[4];
+      for (int i = 0; i < 2; ++i) {
+        uint32_t lo[4], hi[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) lo[t] = e4m3x2_to_f16x2(w[t][i]), hi[t] = e4m3x2_to_f16x2(w[t][i] >> 16);
-      add(4 * i + 0, __byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
-      add(4 * i + 1, __byte_perm(lo[0], lo[1], 0x7632), __byte_perm(lo[2], lo[3], 0x7632));
-      add(4 * i + 2, __byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
-      add(4 * i + 3, __byte_perm(hi[0], hi[1], 0x7632), __byte_perm(hi[2], hi[3], 0x7632));
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t x = i == 0 ? w[t].x : w[t].y;
+          lo[t] = e4m3x2_to_f16x2(x), hi[t] = e4m3x2_to_f16x2(x >> 16);
+        }
+        const int nt = 8 * c + 4 * i;
+        add(nt + 0, __byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
+        add(nt + 1, __byte_perm(lo[0], lo[1], 0x7632), __byte_perm(lo[2], lo[3], 0x7632));
+        add(nt + 2, __byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
+        add(nt + 3, __byte_perm(hi[0], hi[1], 0x7632), __byte_perm(hi[2], hi[3], 0x7632));
+      }
     }
   }
 }
@@ -318,7 +344,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   uint64_t* empty = full + C::kSlots;
   uint64_t* meet_full = empty + C::kSlots;
   uint64_t* meet_free = meet_full + 1;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(meet_free + 1);
+  uint64_t* piece_full = meet_free + 1;            // [pieces] told
+  uint64_t* piece_empty = piece_full + kDecPieces; // [pieces] read by every other warp
+  volatile int* told = reinterpret_cast<volatile int*>(piece_empty + kDecPieces);
+  volatile int* abort_flag = told + kDecPieces * kDecPieceInts;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -328,6 +357,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
     }
     mbar_init(meet_full, kDecWarps);
     mbar_init(meet_free, 1);
+    for (int i = 0; i < kDecPieces; ++i) {
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], kDecWarps + 1);
+    }
     *abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&p.tk);
@@ -351,9 +384,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
     }
   }
 
-  DecWalk w;
-  if (!dec_begin<C::kTile>(p, w, lane)) return;
-
   // a bounded wait of a whole warp; false once any wait of the block ran out
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
@@ -371,13 +401,44 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
     return false;
   };
 
+  // the next piece, as the other warps get it; false: no more
+  uint32_t told_n = 0;
+  auto next_piece = [&](DecPiece& q) {
+    const int e = told_n % kDecPieces;
+    if (!wait(&piece_full[e], (told_n / kDecPieces) & 1u)) return false;
+    int* to = reinterpret_cast<int*>(&q);
+#pragma unroll
+    for (int i = 0; i < kDecPieceInts; ++i) to[i] = told[e * kDecPieceInts + i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&piece_empty[e]);
+    ++told_n;
+    return q.t1 > q.t0;
+  };
+
   if (warp == kDecWarps) {
     // ===== copying warp =====
     fence_proxy_async_global();
+    DecWalk w;
+    bool more = dec_begin<C::kTile>(p, w, lane);
     int slot = 0;
     uint32_t phase = 0;
     bool stop = false;
-    do {
+    while (!stop) {
+      {
+        const int e = told_n % kDecPieces;
+        DecPiece q{};
+        if (more) q = dec_piece_of(w);
+        if (!wait(&piece_empty[e], ((told_n / kDecPieces) & 1u) ^ 1u)) break;
+        if (lane == 0) {
+          const int* from = reinterpret_cast<const int*>(&q);
+#pragma unroll
+          for (int i = 0; i < kDecPieceInts; ++i) told[e * kDecPieceInts + i] = from[i];
+          mbar_arrive(&piece_full[e]);
+        }
+        __syncwarp();
+        ++told_n;
+        if (!more) break;
+      }
       const int per = kDecGroup / p.box_rows;                       // boxes per slot
       const int boxes = (w.s.len + p.box_rows - 1) / p.box_rows;    // boxes that hold a token
       const int u0 = w.t0 * (C::kTile / kDecGroup) * per, u1 = w.t1 * (C::kTile / kDecGroup) * per;
@@ -419,7 +480,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
           if (++slot == C::kSlots) slot = 0, phase ^= 1u;
         }
       }
-    } while (!stop && dec_next<C::kTile>(p, w));
+      more = dec_next<C::kTile>(p, w);
+    }
     if (lane == 0) {
       // no copy in flight at exit (only after a wait that ran out is there
       // one that no computing warp has waited for): wait for the slots'
@@ -437,10 +499,11 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   if (warp == kDecWarps + 1) {
     // ===== joining warp =====
     uint32_t piece = 0;
-    do {
+    DecPiece w;
+    while (next_piece(w)) {
       if (!wait(meet_full, piece & 1u)) break;
       ++piece;
-      const int rows = w.s.n * p.group;
+      const int rows = w.n * p.group;
       // lane 2 row + i: the warps' factors of a row, its maximum and sum
       float top = -INFINITY, sum = 0.0f;
       {
@@ -460,7 +523,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
       // four outputs of a row from element d on; m, l: the row's maximum and sum
       auto put = [&](int row, int d, float4 o, float m, float l) {
         const int i = row / p.group, h = w.h * p.group + row % p.group;
-        const int64_t tok = w.s.first + i;
+        const int64_t tok = w.first + i;
         const float inv = vscale / l;
         uint2 v = make_uint2(0, 0);   // (l == 0: the row sees nothing)
         if (l != 0.0f) v = make_uint2(pack16<false>(o.x * inv, o.y * inv), pack16<false>(o.z * inv, o.w * inv));
@@ -468,11 +531,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
         if (p.lse != nullptr && d == 0)
           p.lse[tok * p.heads + h] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
       };
-      const bool whole = w.t0 == 0 && w.t1 == w.s.tiles;
+      const bool whole = w.whole != 0;
       constexpr int kPart = 2 * kDecRows + kDecRows * D;   // floats of a partial result: m, l, O
-      // slot of a block's piece: 0 where it starts the block's range, else 1
-      const uint64_t range0 = blockIdx.x * w.total / w.ctas;
-      float* part = p.partials + (2 * static_cast<int64_t>(blockIdx.x) + (w.x == range0 ? 0 : 1)) * kPart;
+      float* part = p.partials + static_cast<int64_t>(w.slot) * kPart;
       for (int e0 = 0; e0 < rows * (D / 4); e0 += 32) {
         const int e = e0 + lane;
         const int row = min(e / (D / 4), kDecRows - 1), d = 4 * (e % (D / 4));
@@ -494,10 +555,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(meet_free);
       if (whole) continue;
-      // the blocks that hold the pair's first and last tile
-      const int first = static_cast<int>(((w.pair0 + 1) * w.ctas - 1) / w.total);
-      const int last = static_cast<int>(((w.pair0 + w.s.tiles) * w.ctas - 1) / w.total);
-      const int pieces = last - first + 1;
+      const int first = w.first_cta, pieces = w.pieces;
       uint32_t is_last = 0;
       if (lane == 0) {
         __threadfence();
@@ -506,11 +564,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
       }
       if (!__shfl_sync(0xffffffffu, is_last, 0)) continue;
       __threadfence();
-      // the first piece starts its block's range, or follows other pairs in it
-      const bool at_start = first * w.total / w.ctas == w.pair0;
       auto piece_at = [&](int k) {
-        const int64_t n = k == 0 ? 2 * static_cast<int64_t>(first) + (at_start ? 0 : 1) : 2 * static_cast<int64_t>(first + k);
-        return p.partials + n * kPart;
+        return p.partials + static_cast<int64_t>(k == 0 ? w.slot0 : 2 * (first + k)) * kPart;
       };
       // a row's maximum and sum over the pieces: lane 2 row + i takes every other piece
       top = -INFINITY, sum = 0.0f;
@@ -535,7 +590,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
         }
         put(row, d, o, m, l);
       }
-    } while (dec_next<C::kTile>(p, w));
+    }
     return;
   }
 
@@ -545,15 +600,16 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   uint32_t piece = 0;
   uint32_t phase = 0;
   bool dead = false;
-  do {
-    const int n = w.s.n, rows = n * p.group;
+  DecPiece w;
+  while (!dead && next_piece(w)) {
+    const int n = w.n, rows = n * p.group;
     // the thread's two rows: token i, head, positions it sees
     const int r0 = g, r1 = g + 8;
     const int i0 = r0 / p.group, i1 = r1 / p.group;
     const bool ok0 = r0 < rows, ok1 = r1 < rows;
-    const int see0 = ok0 ? max(min(w.s.base + i0 + 1, w.s.len), 0) : 0;
-    const int see1 = ok1 ? max(min(w.s.base + i1 + 1, w.s.len), 0) : 0;
-    const int see_all = max(min(w.s.base + 1, w.s.len), 0);    // positions every row sees
+    const int see0 = ok0 ? max(min(w.base + i0 + 1, w.len), 0) : 0;
+    const int see1 = ok1 ? max(min(w.base + i1 + 1, w.len), 0) : 0;
+    const int see_all = max(min(w.base + 1, w.len), 0);    // positions every row sees
     float s_eff = p.scale;
     if (E4) s_eff *= p.k_scale[w.h];
     const uint32_t flip = s_eff < 0.0f ? 0x80008000u : 0u;
@@ -562,8 +618,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
     // Q fragments
     uint32_t qa[D / 16][4];
     {
-      const __nv_bfloat16* q0 = p.q.p + (w.s.first + i0) * p.q.ts + (w.h * p.group + r0 % p.group) * p.q.hs;
-      const __nv_bfloat16* q1 = p.q.p + (w.s.first + i1) * p.q.ts + (w.h * p.group + r1 % p.group) * p.q.hs;
+      const __nv_bfloat16* q0 = p.q.p + (w.first + i0) * p.q.ts + (w.h * p.group + r0 % p.group) * p.q.hs;
+      const __nv_bfloat16* q1 = p.q.p + (w.first + i1) * p.q.ts + (w.h * p.group + r1 % p.group) * p.q.hs;
       const bool zero = s_eff == 0.0f;
       if (!E4) {
 #pragma unroll
@@ -629,11 +685,11 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
     for (int t = w.t0; t < w.t1; ++t) {
       const int at = t * C::kTile + warp * C::kUnit;
       if (!dead) dead = !wait(&full[slot], phase);
-      if (!dead && at < w.s.len) {
+      if (!dead && at < w.len) {
         uint8_t* ks = smem + slot * C::kSlotBytes + (warp % C::kPerSlot) * C::kUnitBytes;
         uint8_t* vs = ks + C::kHalf;
         // rows of the page that hold no token of this sequence
-        if (at + C::kUnit > w.s.len) dec_zero_rows<D, E4>(vs, w.s.len - at, lane);
+        if (at + C::kUnit > w.len) dec_zero_rows<D, E4>(vs, w.len - at, lane);
         constexpr int NT = C::kUnit / 8;      // columns of scores, eight positions each
         float s[NT][4];
 #pragma unroll
@@ -712,10 +768,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
         // is hidden from some rows and holds one, each token's rows take
         // their own product, the later positions zeroed from the last token
         // to the first.
-        if (edge && n > 1 && dec_rows_nonfinite<D, E4>(vs, max(see_all - at, 0), min(C::kUnit, w.s.len - at), lane)) {
+        if (edge && n > 1 && dec_rows_nonfinite<D, E4>(vs, max(see_all - at, 0), min(C::kUnit, w.len - at), lane)) {
 #pragma unroll 1
           for (int i = n - 1; i >= 0; --i) {
-            const int see = max(min(w.s.base + i + 1, w.s.len), 0) - at;
+            const int see = max(min(w.base + i + 1, w.len), 0) - at;
             if (see < C::kUnit) dec_zero_rows<D, E4>(vs, max(see, 0), lane);
 #pragma unroll
             for (int u = 0; u < NT / 2; ++u)
@@ -756,7 +812,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(meet_full);
-  } while (!dead && dec_next<C::kTile>(p, w));
+  }
 }
 
 template <int D, bool E4>

@@ -107,66 +107,76 @@ __device__ __forceinline__ DecSeq dec_seq(const DecParams& p, int b, bool& bad) 
 
 // Walks the pieces of a thread block's range of the line of tiles (one warp).
 struct DecWalk {
-  uint64_t x, end;     // tiles still to do: [x, end)
-  uint64_t total;
-  int ctas;
+  uint32_t x, end;     // tiles still to do: [x, end)
+  uint32_t each, more; // tiles per block: each + 1 for the first `more` blocks, else each
   int b, h;
   DecSeq s;
   int t0, t1;          // this piece's tiles of the pair
-  uint64_t pair0;      // line position of the pair's tile 0
+  uint32_t pair0;      // line position of the pair's tile 0
+  __device__ __forceinline__ uint32_t start_of(uint32_t cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ uint32_t owner_of(uint32_t tile) const {
+    const uint32_t low = more * (each + 1);
+    return tile < low ? tile / (each + 1) : more + (tile - low) / each;
+  }
 };
 
-__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+__device__ __forceinline__ uint32_t dec_scan(uint32_t v, int lane) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
   return v;
 }
 
-__device__ __forceinline__ void dec_piece(const DecParams& p, DecWalk& w) {
+__device__ __forceinline__ void dec_piece(DecWalk& w) {
   w.t0 = static_cast<int>(w.x - w.pair0);
-  const uint64_t left = w.end - w.x;
-  w.t1 = static_cast<int>(min(static_cast<uint64_t>(w.s.tiles - w.t0), left)) + w.t0;
+  w.t1 = static_cast<int>(min(static_cast<uint32_t>(w.s.tiles - w.t0), w.end - w.x)) + w.t0;
 }
 
-// false: nothing to do. Called by whole warps.
+// One warp; false: nothing to do.
 template <int TILE>
 __device__ __forceinline__ bool dec_begin(const DecParams& p, DecWalk& w, int lane) {
-  uint64_t mine = 0;
+  // tiles of the sequences lane, lane + 32, ...; up to 128 sequences are read once
+  constexpr int kKept = 4;
+  uint32_t kept[kKept], sum = 0;
   bool bad = false;
-  for (int b = lane; b < p.b.n_seqs; b += 32) mine += dec_seq<TILE>(p, b, bad).tiles;
-  if (bad && blockIdx.x == 0) record_status(p.status, EPILORA_ERR_INVALID_ARG);
-  w.total = warp_sum(mine) * p.kv_heads;
-  if (w.total == 0) return false;
-  w.ctas = static_cast<int>(min(static_cast<uint64_t>(gridDim.x), w.total));
-  if (static_cast<int>(blockIdx.x) >= w.ctas) return false;
-  w.x = blockIdx.x * w.total / w.ctas;
-  w.end = (blockIdx.x + 1) * w.total / w.ctas;
-  // the sequence that holds x
-  uint64_t before = 0;
-  w.b = -1;
-  for (int b0 = 0; b0 < p.b.n_seqs; b0 += 32) {
-    const int b = b0 + lane;
-    const uint64_t c = b < p.b.n_seqs ? static_cast<uint64_t>(dec_seq<TILE>(p, b, bad).tiles) * p.kv_heads : 0;
-    uint64_t inc = c;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
+  for (int i = 0; i < kKept; ++i) {
+    const int b = lane + 32 * i;
+    kept[i] = b < p.b.n_seqs ? dec_seq<TILE>(p, b, bad).tiles : 0;
+    sum += kept[i];
+  }
+  for (int b = lane + 32 * kKept; b < p.b.n_seqs; b += 32) sum += dec_seq<TILE>(p, b, bad).tiles;
+  if (bad && blockIdx.x == 0) record_status(p.status, EPILORA_ERR_INVALID_ARG);
+  const uint32_t total = __reduce_add_sync(0xffffffffu, sum) * p.kv_heads;
+  const uint32_t ctas = min(gridDim.x, total);
+  if (blockIdx.x >= ctas) return false;
+  w.each = total / ctas;
+  w.more = total - w.each * ctas;
+  w.x = w.start_of(blockIdx.x);
+  w.end = w.start_of(blockIdx.x + 1);
+  // the sequence that holds x
+  uint32_t before = 0;
+  for (int i = 0;; ++i) {
+    if (32 * i >= p.b.n_seqs) return false;   // metadata changed under the call
+    const int b = lane + 32 * i;
+    const uint32_t tiles = i < kKept ? (i == 0 ? kept[0] : i == 1 ? kept[1] : i == 2 ? kept[2] : kept[3])
+                                     : (b < p.b.n_seqs ? dec_seq<TILE>(p, b, bad).tiles : 0);
+    const uint32_t c = tiles * p.kv_heads, inc = dec_scan(c, lane);
     const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > w.x);
     if (hit != 0) {
       const int l = __ffs(hit) - 1;
-      w.b = b0 + l;
+      w.b = 32 * i + l;
       w.pair0 = before + __shfl_sync(0xffffffffu, inc - c, l);
       break;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
-  if (w.b < 0) return false;
   w.s = dec_seq<TILE>(p, w.b, bad);
   w.h = static_cast<int>((w.x - w.pair0) / w.s.tiles);
-  w.pair0 += static_cast<uint64_t>(w.h) * w.s.tiles;
-  dec_piece(p, w);
+  w.pair0 += static_cast<uint32_t>(w.h) * w.s.tiles;
+  dec_piece(w);
   return true;
 }
 
@@ -183,7 +193,7 @@ __device__ __forceinline__ bool dec_next(const DecParams& p, DecWalk& w) {
       w.s = dec_seq<TILE>(p, w.b, bad);
     } while (w.s.tiles == 0);
   }
-  dec_piece(p, w);
+  dec_piece(w);
   return true;
 }
 
@@ -205,11 +215,11 @@ __device__ __forceinline__ DecPiece dec_piece_of(const DecWalk& w) {
   q.t0 = w.t0, q.t1 = w.t1;
   q.whole = w.t0 == 0 && w.t1 == w.s.tiles;
   // the blocks that hold the pair's first and last tile
-  q.first_cta = static_cast<int>(((w.pair0 + 1) * w.ctas - 1) / w.total);
-  q.pieces = static_cast<int>(((w.pair0 + w.s.tiles) * w.ctas - 1) / w.total) - q.first_cta + 1;
+  q.first_cta = static_cast<int>(w.owner_of(w.pair0));
+  q.pieces = static_cast<int>(w.owner_of(w.pair0 + w.s.tiles - 1)) - q.first_cta + 1;
   // a piece that starts its block's range goes to the block's slot 0, the one that ends it to slot 1
-  q.slot = 2 * blockIdx.x + (w.x == blockIdx.x * w.total / w.ctas ? 0 : 1);
-  q.slot0 = 2 * q.first_cta + (q.first_cta * w.total / w.ctas == w.pair0 ? 0 : 1);
+  q.slot = 2 * blockIdx.x + (w.x == w.start_of(blockIdx.x) ? 0 : 1);
+  q.slot0 = 2 * q.first_cta + (w.start_of(q.first_cta) == w.pair0 ? 0 : 1);
   return q;
 }
 
@@ -369,21 +379,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   __syncthreads();
   pdl_wait_primary();
 
-  // packed rows of no sequence are zero
-  {
-    const int used = p.b.n_seqs > 0 ? min(max(p.b.q_start[p.b.n_seqs], 0), p.b.n_tokens) : 0;
-    const int64_t rows = static_cast<int64_t>(p.b.n_tokens - used) * p.heads;
-    constexpr int V = D / 8;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * V;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-      const int64_t r = i / V;
-      const int64_t t = used + r / p.heads;
-      const int h = static_cast<int>(r % p.heads);
-      *reinterpret_cast<uint4*>(p.o.p + t * p.o.ts + h * p.o.hs + (i % V) * 8) = make_uint4(0, 0, 0, 0);
-      if (p.lse != nullptr && i % V == 0) p.lse[t * p.heads + h] = -INFINITY;
-    }
-  }
-
   // a bounded wait of a whole warp; false once any wait of the block ran out
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
@@ -498,6 +493,20 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
 
   if (warp == kDecWarps + 1) {
     // ===== joining warp =====
+    // packed rows of no sequence are zero
+    {
+      const int used = p.b.n_seqs > 0 ? min(max(p.b.q_start[p.b.n_seqs], 0), p.b.n_tokens) : 0;
+      const int64_t rows = static_cast<int64_t>(p.b.n_tokens - used) * p.heads;
+      constexpr int V = D / 8;
+      for (int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane; i < rows * V;
+           i += static_cast<int64_t>(gridDim.x) * 32) {
+        const int64_t r = i / V;
+        const int64_t t = used + r / p.heads;
+        const int h = static_cast<int>(r % p.heads);
+        *reinterpret_cast<uint4*>(p.o.p + t * p.o.ts + h * p.o.hs + (i % V) * 8) = make_uint4(0, 0, 0, 0);
+        if (p.lse != nullptr && i % V == 0) p.lse[t * p.heads + h] = -INFINITY;
+      }
+    }
     uint32_t piece = 0;
     DecPiece w;
     while (next_piece(w)) {
@@ -567,23 +576,58 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
       auto piece_at = [&](int k) {
         return p.partials + static_cast<int64_t>(k == 0 ? w.slot0 : 2 * (first + k)) * kPart;
       };
-      // a row's maximum and sum over the pieces: lane 2 row + i takes every other piece
+      // Maximum and sum of row lane / 2 over the pieces, of which this lane
+      // takes every other one; the first 16 pieces' loads are under way at once.
+      constexpr int kAt = 8;
+      const int my_row = lane >> 1, odd = lane & 1;
+      float pm[kAt], pl[kAt];
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        const int k = 2 * i + odd;
+        pm[i] = k < pieces ? __ldcg(piece_at(k) + my_row) : -INFINITY;
+        pl[i] = k < pieces ? __ldcg(piece_at(k) + kDecRows + my_row) : 0.0f;
+      }
       top = -INFINITY, sum = 0.0f;
-      for (int k = lane & 1; k < pieces; k += 2) top = fmaxf(top, __ldcg(piece_at(k) + (lane >> 1)));
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) top = fmaxf(top, pm[i]);
+      for (int k = 2 * kAt + odd; k < pieces; k += 2) top = fmaxf(top, __ldcg(piece_at(k) + my_row));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       const float base = top == -INFINITY ? 0.0f : top;
-      for (int k = lane & 1; k < pieces; k += 2)
-        sum += __ldcg(piece_at(k) + kDecRows + (lane >> 1)) * exp2_approx(__ldcg(piece_at(k) + (lane >> 1)) - base);
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        pm[i] = exp2_approx(pm[i] - base);     // the piece's factor
+        sum += pl[i] * pm[i];
+      }
+      for (int k = 2 * kAt + odd; k < pieces; k += 2)
+        sum += __ldcg(piece_at(k) + kDecRows + my_row) * exp2_approx(__ldcg(piece_at(k) + my_row) - base);
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       for (int e0 = 0; e0 < rows * (D / 4); e0 += 32) {
         const int e = e0 + lane;
-        const int row = min(e / (D / 4), kDecRows - 1), d = 4 * (e % (D / 4));
+        const bool in = e < rows * (D / 4);
+        const int row = in ? e / (D / 4) : 0, d = 4 * (e % (D / 4));
         const float m = __shfl_sync(0xffffffffu, top, 2 * row), l = __shfl_sync(0xffffffffu, sum, 2 * row);
-        if (e >= rows * (D / 4)) continue;
         const float row_base = m == -INFINITY ? 0.0f : m;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int k = 0; k < pieces; ++k) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h * kAt >= pieces) break;
+          float4 v[kAt];
+#pragma unroll
+          for (int i = 0; i < kAt; ++i) {
+            const int k = h * kAt + i;
+            v[i] = k < pieces && in ? __ldcg(reinterpret_cast<const float4*>(piece_at(k) + 2 * kDecRows + row * D + d))
+                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          }
+#pragma unroll
+          for (int i = 0; i < kAt; ++i) {
+            const int k = h * kAt + i;
+            const float f = __shfl_sync(0xffffffffu, pm[k >> 1], 2 * row + (k & 1));
+            o.x += v[i].x * f, o.y += v[i].y * f, o.z += v[i].z * f, o.w += v[i].w * f;
+          }
+        }
+        if (!in) continue;
+#pragma unroll 4
+        for (int k = 2 * kAt; k < pieces; ++k) {
           const float4 v = __ldcg(reinterpret_cast<const float4*>(piece_at(k) + 2 * kDecRows + row * D + d));
           const float f = exp2_approx(__ldcg(piece_at(k) + row) - row_base);
           o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
@@ -886,6 +930,7 @@ int launch_attn_decode(const AttnArgs& a, uint32_t* counters, float* partials) {
   const int tile = e4 ? DecCfg<128, true>::kTile : DecCfg<128, false>::kTile;
   const int64_t cap = static_cast<int64_t>(a.batch.table_pages) * a.cache.page_size;
   const int64_t most = a.batch.n_seqs * (a.cache.kv_heads * ((cap + tile - 1) / tile + 1));
+  if (most >= (int64_t{1} << 32)) return EPILORA_ERR_UNSUPPORTED;    // the line's tiles are counted in 32 bits
   const int grid = static_cast<int>(most < 1 ? 1 : (most < dec_ctas() ? most : dec_ctas()));
   if (a.cache.head_dim == 64) return e4 ? launch<64, true>(a, p, grid) : launch<64, false>(a, p, grid);
   return e4 ? launch<128, true>(a, p, grid) : launch<128, false>(a, p, grid);

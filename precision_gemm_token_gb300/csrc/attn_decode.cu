@@ -38,6 +38,7 @@ constexpr int kDecThreads = 32 * (kDecWarps + 2);
 constexpr int kDecRows = 16;
 constexpr int kDecMaxCtas = 512;     // blocks of a launch at most
 constexpr int kDecPieces = 4;        // pieces of work told ahead
+constexpr int kDecJoin = 16;         // pieces of a join whose factors are kept
 constexpr int kDecPieceInts = 12;
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
 // a row's maximum is raised (and its sums rescaled) only when a score exceeds
@@ -65,7 +66,7 @@ struct DecCfg {
   static_assert(kSlots % kSlotStep == 0, "slots are dealt to the warps");
   static constexpr int kOld = D + 8;                                    // floats per row of the meeting buffer
   static constexpr int kMeet = kDecWarps * kDecRows * kOld * 4;         // the four warps' outputs
-  static constexpr int kSmem = 1024 + kSlots * kSlotBytes + kMeet + 2048;
+  static constexpr int kSmem = 1024 + kSlots * kSlotBytes + kMeet + 3072;
 };
 
 struct DecParams {
@@ -150,7 +151,9 @@ __device__ __forceinline__ bool dec_begin(const DecParams& p, DecWalk& w, int la
   for (int b = lane + 32 * kKept; b < p.b.n_seqs; b += 32) sum += dec_seq<TILE>(p, b, bad).tiles;
   if (bad && blockIdx.x == 0) record_status(p.status, EPILORA_ERR_INVALID_ARG);
   const uint32_t total = __reduce_add_sync(0xffffffffu, sum) * p.kv_heads;
-  const uint32_t ctas = min(gridDim.x, total);
+  // two tiles a block at least: a pair then has half as many pieces to join
+  // (1023 positions, 8 heads: 11.7 us with one)
+  const uint32_t ctas = min(gridDim.x, (total + 1) / 2);
   if (blockIdx.x >= ctas) return false;
   w.each = total / ctas;
   w.more = total - w.each * ctas;
@@ -349,8 +352,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* meet = reinterpret_cast<float*>(smem + C::kSlots * C::kSlotBytes);
   float* ml = meet + C::kMeet / 4;                 // [4][16][2] maximum and sum of each warp's rows
-  float* fac = ml + kDecWarps * kDecRows * 2;      // [4][16] factors of the warps' outputs
-  uint64_t* full = reinterpret_cast<uint64_t*>(fac + kDecWarps * kDecRows);
+  float* fac = ml + kDecWarps * kDecRows * 2;      // [16][16] factors of the warps' outputs, of a join's first pieces
+  float* row_m = fac + kDecJoin * kDecRows;        // [16] maximum and sum of the rows
+  float* row_l = row_m + kDecRows;
+  uint64_t* full = reinterpret_cast<uint64_t*>(row_l + kDecRows);
   uint64_t* empty = full + C::kSlots;
   uint64_t* meet_full = empty + C::kSlots;
   uint64_t* meet_free = meet_full + 1;
@@ -526,6 +531,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
           sum += ml[(k * kDecRows + row) * 2 + 1] * f;
           if ((k & 1) == (lane & 1)) fac[k * kDecRows + row] = f;
         }
+        if (lane & 1) row_m[row] = top, row_l[row] = sum;
       }
       __syncwarp();
       const float vscale = E4 ? p.v_scale[w.h] : 1.0f;
@@ -542,23 +548,31 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
       };
       const bool whole = w.whole != 0;
       constexpr int kPart = 2 * kDecRows + kDecRows * D;   // floats of a partial result: m, l, O
+      constexpr int kMany = 4;
       float* part = p.partials + static_cast<int64_t>(w.slot) * kPart;
-      for (int e0 = 0; e0 < rows * (D / 4); e0 += 32) {
-        const int e = e0 + lane;
-        const int row = min(e / (D / 4), kDecRows - 1), d = 4 * (e % (D / 4));
-        const float m = __shfl_sync(0xffffffffu, top, 2 * row), l = __shfl_sync(0xffffffffu, sum, 2 * row);
-        if (e >= rows * (D / 4)) continue;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      // kMany elements a lane at a time: their loads run side by side
+      for (int e0 = lane; e0 < rows * (D / 4); e0 += 32 * kMany) {
+        float4 o[kMany];
 #pragma unroll
-        for (int k = 0; k < kDecWarps; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(meet + (k * kDecRows + row) * C::kOld + d);
-          const float f = fac[k * kDecRows + row];
-          o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+        for (int y = 0; y < kMany; ++y) {
+          const int row = (e0 + 32 * y) / (D / 4) & (kDecRows - 1), d = 4 * ((e0 + 32 * y) % (D / 4));
+          o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int k = 0; k < kDecWarps; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(meet + (k * kDecRows + row) * C::kOld + d);
+            const float f = fac[k * kDecRows + row];
+            o[y].x += v.x * f, o[y].y += v.y * f, o[y].z += v.z * f, o[y].w += v.w * f;
+          }
         }
-        if (whole)
-          put(row, d, o, m, l);
-        else
-          *reinterpret_cast<float4*>(part + 2 * kDecRows + row * D + d) = o;
+#pragma unroll
+        for (int y = 0; y < kMany; ++y) {
+          const int e = e0 + 32 * y, row = e / (D / 4) & (kDecRows - 1), d = 4 * (e % (D / 4));
+          if (e >= rows * (D / 4)) continue;
+          if (whole)
+            put(row, d, o[y], row_m[row], row_l[row]);
+          else
+            *reinterpret_cast<float4*>(part + 2 * kDecRows + row * D + d) = o[y];
+        }
       }
       if (!whole && (lane & 1) == 0) part[lane >> 1] = top, part[kDecRows + (lane >> 1)] = sum;
       __syncwarp();
@@ -567,73 +581,78 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
       const int first = w.first_cta, pieces = w.pieces;
       uint32_t is_last = 0;
       if (lane == 0) {
-        __threadfence();
-        is_last = atomicAdd(p.counters + first, 1u) == static_cast<uint32_t>(pieces - 1);
+        // (the warp's stores are before it: the barrier above)
+        is_last = atom_inc_acq_rel_gpu(p.counters + first) == static_cast<uint32_t>(pieces - 1);
         if (is_last) p.counters[first] = 0;
       }
       if (!__shfl_sync(0xffffffffu, is_last, 0)) continue;
-      __threadfence();
       auto piece_at = [&](int k) {
         return p.partials + static_cast<int64_t>(k == 0 ? w.slot0 : 2 * (first + k)) * kPart;
       };
       // Maximum and sum of row lane / 2 over the pieces, of which this lane
       // takes every other one; the first 16 pieces' loads are under way at once.
-      constexpr int kAt = 8;
       const int my_row = lane >> 1, odd = lane & 1;
-      float pm[kAt], pl[kAt];
+      float pm[kDecJoin / 2], pl[kDecJoin / 2];
 #pragma unroll
-      for (int i = 0; i < kAt; ++i) {
+      for (int i = 0; i < kDecJoin / 2; ++i) {
         const int k = 2 * i + odd;
         pm[i] = k < pieces ? __ldcg(piece_at(k) + my_row) : -INFINITY;
         pl[i] = k < pieces ? __ldcg(piece_at(k) + kDecRows + my_row) : 0.0f;
       }
       top = -INFINITY, sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kAt; ++i) top = fmaxf(top, pm[i]);
-      for (int k = 2 * kAt + odd; k < pieces; k += 2) top = fmaxf(top, __ldcg(piece_at(k) + my_row));
+      for (int i = 0; i < kDecJoin / 2; ++i) top = fmaxf(top, pm[i]);
+      for (int k = kDecJoin + odd; k < pieces; k += 2) top = fmaxf(top, __ldcg(piece_at(k) + my_row));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-      for (int i = 0; i < kAt; ++i) {
-        pm[i] = exp2_approx(pm[i] - base);     // the piece's factor
+      for (int i = 0; i < kDecJoin / 2; ++i) {
+        pm[i] = exp2_approx(pm[i] - base);
         sum += pl[i] * pm[i];
+        fac[(2 * i + odd) * kDecRows + my_row] = pm[i];
       }
-      for (int k = 2 * kAt + odd; k < pieces; k += 2)
+      for (int k = kDecJoin + odd; k < pieces; k += 2)
         sum += __ldcg(piece_at(k) + kDecRows + my_row) * exp2_approx(__ldcg(piece_at(k) + my_row) - base);
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      for (int e0 = 0; e0 < rows * (D / 4); e0 += 32) {
-        const int e = e0 + lane;
-        const bool in = e < rows * (D / 4);
-        const int row = in ? e / (D / 4) : 0, d = 4 * (e % (D / 4));
-        const float m = __shfl_sync(0xffffffffu, top, 2 * row), l = __shfl_sync(0xffffffffu, sum, 2 * row);
-        const float row_base = m == -INFINITY ? 0.0f : m;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (odd) row_m[my_row] = top, row_l[my_row] = sum;
+      __syncwarp();
+      for (int e0 = lane; e0 < rows * (D / 4); e0 += 32 * kMany) {
+        float4 o[kMany];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h * kAt >= pieces) break;
-          float4 v[kAt];
+        for (int y = 0; y < kMany; ++y) o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k0 = 0; k0 < min(pieces, kDecJoin); k0 += 4) {
+          float4 v[4][kMany];
 #pragma unroll
-          for (int i = 0; i < kAt; ++i) {
-            const int k = h * kAt + i;
-            v[i] = k < pieces && in ? __ldcg(reinterpret_cast<const float4*>(piece_at(k) + 2 * kDecRows + row * D + d))
-                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          }
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int i = 0; i < kAt; ++i) {
-            const int k = h * kAt + i;
-            const float f = __shfl_sync(0xffffffffu, pm[k >> 1], 2 * row + (k & 1));
-            o.x += v[i].x * f, o.y += v[i].y * f, o.z += v[i].z * f, o.w += v[i].w * f;
-          }
+            for (int y = 0; y < kMany; ++y) {
+              const int e = e0 + 32 * y;     // (element e of the rows is float4 e of the piece's outputs)
+              v[i][y] = k0 + i < pieces && e < rows * (D / 4)
+                            ? __ldcg(reinterpret_cast<const float4*>(piece_at(k0 + i) + 2 * kDecRows) + e)
+                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int y = 0; y < kMany; ++y) {
+              const float f = fac[(k0 + i) * kDecRows + ((e0 + 32 * y) / (D / 4) & (kDecRows - 1))];
+              o[y].x += v[i][y].x * f, o[y].y += v[i][y].y * f, o[y].z += v[i][y].z * f, o[y].w += v[i][y].w * f;
+            }
         }
-        if (!in) continue;
-#pragma unroll 4
-        for (int k = 2 * kAt; k < pieces; ++k) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(piece_at(k) + 2 * kDecRows + row * D + d));
-          const float f = exp2_approx(__ldcg(piece_at(k) + row) - row_base);
-          o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+#pragma unroll
+        for (int y = 0; y < kMany; ++y) {
+          const int e = e0 + 32 * y, row = e / (D / 4), d = 4 * (e % (D / 4));
+          if (e >= rows * (D / 4)) continue;
+          const float m = row_m[row], row_base = m == -INFINITY ? 0.0f : m;
+          for (int k = kDecJoin; k < pieces; ++k) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(piece_at(k) + 2 * kDecRows) + e);
+            const float f = exp2_approx(__ldcg(piece_at(k) + row) - row_base);
+            o[y].x += v.x * f, o[y].y += v.y * f, o[y].z += v.z * f, o[y].w += v.w * f;
+          }
+          put(row, d, o[y], m, row_l[row]);
         }
-        put(row, d, o, m, l);
       }
+      __syncwarp();     // the factors are free again
     }
     return;
   }

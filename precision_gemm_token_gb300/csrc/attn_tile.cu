@@ -1113,17 +1113,15 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           pf[prow] = mc;
           pf[kItemRows + prow] = l;
           const int first = it.first_cta, pieces = it.pieces;
-          __threadfence();
           if (!meet_group()) break;
           if (r == 0) {
-            const uint32_t before = atomicAdd(p.counters + 2 * first + s, 1u);
-            const int is_last = before == static_cast<uint32_t>(pieces - 1);
+            // (the group's stores are before it: the barrier above)
+            const int is_last = atom_inc_acq_rel_gpu(p.counters + 2 * first + s) == static_cast<uint32_t>(pieces - 1);
             if (is_last) p.counters[2 * first + s] = 0;
             last_flag[s] = is_last;
           }
           if (!meet_group()) break;
           if (last_flag[s] && live) {
-            __threadfence();
             auto piece = [&](int k) {
               return p.partials + static_cast<int64_t>(k == 0 ? it.slot0 : 2 * (first + k)) * kPart;
             };

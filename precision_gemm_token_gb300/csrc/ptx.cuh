@@ -205,6 +205,15 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu_u32(const uint32_t* p) {
   return v;
 }
 
+// Adds one and returns the old value: what this thread (and, through a barrier
+// before it, its block) wrote is visible to whoever reads the counter later,
+// and what earlier adders wrote to this thread.
+__device__ __forceinline__ uint32_t atom_inc_acq_rel_gpu(uint32_t* p) {
+  uint32_t v;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // ----------------------------------------------------------------------------
 // tcgen05: tensor memory
 // ----------------------------------------------------------------------------

@@ -87,6 +87,16 @@ def test_append_pages(fmt, page, order):
     check(Batch([(70, 300), (1, page), (1, page + 1)], 4, 2, 64, fmt=fmt, page=page, order=order, seed=page))
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_many_tokens(fmt, interleaved):
+    """Enough tokens that a block takes several: sequences that begin and end
+    inside a block, a last block that is not full, padding rows."""
+    seqs = [(1, 30)] * 5 + [(301, 400), (0, 3), (2, 1), (213, 213), (1, 7), (6, 90)]
+    check(Batch(seqs, 12, 4, 64, fmt=fmt, seed=9, tail=2), interleaved=interleaved)
+    check(Batch([(600, 611)], 6, 2, 128, fmt=fmt, page=64, order="token", seed=10), 96, interleaved)
+
+
 def test_append_in_place_and_without_rotation():
     check(Batch([(9, 30), (1, 1)], 8, 2, 128, seed=1), in_place=True)
     check(Batch([(9, 30), (1, 1)], 8, 2, 128, seed=1), in_place=True, interleaved=True)

@@ -8,11 +8,11 @@
 // for a prefill chunk and by the chain of dependent loads (sequence ->
 // position -> page and rotation row -> store) for a decode step.
 //
-// A thread takes 16 elements of a head row at a time (two 16-byte loads: for
-// the half-split rotation the two halves of eight pairs). A few tokens get a
-// block each, one unit a thread; many are taken four to a block with four units
-// a thread under way. Either way the first rows are on their way while a warp
-// per token looks the token up.
+// A block takes a token. A thread takes the same 16 elements of several head
+// rows (two 16-byte loads each: for the half-split rotation the two halves of
+// eight pairs), so that its cosines and sines are loaded once; three rows are on
+// their way while every warp looks the token up for itself (a warp doing it for
+// the block, and a barrier, took longer).
 #include "attention.cuh"
 #include "ptx.cuh"
 
@@ -58,118 +58,98 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-// what the look-up of a token leaves
-struct Token {
-  int64_t k_at, v_at;   // cache offsets of its row, head 0
-  int pos;              // < 0: nothing is appended
-};
+constexpr int kThreads = 128;
+constexpr int kBatch = 3;      // rows of a thread under way; more cost blocks per SM (39, 45, 56 us with 3, 4, 5 for 8044 tokens, 48 rows)
 
-// TB tokens per block, BATCH units per thread under way
-template <int TB, int BATCH, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS) kv_append_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ Token tokens[TB];
+template <int D, bool E4>
+__global__ void __launch_bounds__(kThreads, 7) kv_append_kernel(const __grid_constant__ AppendParams p) {
   pdl_wait_primary();
-  const int t0 = blockIdx.x * TB;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_row = p.c.head_dim / 16, per_token = p.rows * per_row;
-  const int total = min(TB, p.b.n_tokens - t0) * per_token;
+  constexpr int kPerRow = D / 16, kRowStep = kThreads / kPerRow;
+  const int t = blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  const int u = threadIdx.x % kPerRow, r0 = threadIdx.x / kPerRow;
   const int half = p.rot_dim >> 1;
-  const int rot_units = p.cos_sin != nullptr ? p.rot_dim / 16 : 0;
+  const bool rotated = p.cos_sin != nullptr && u < p.rot_dim / 16;    // of a q or k row
   const bool split = p.interleaved == 0;
   const int kvh = p.c.kv_heads, nq = p.rows - 2 * kvh;
+  // element offsets of the two groups of eight; of a rotated row
+  const int e0 = u * 16, e1 = e0 + 8;
+  const int f0 = rotated && split ? u * 8 : e0, f1 = rotated && split ? half + u * 8 : e1;
 
-  // unit i of the block: token, tensor (0 q, 1 k, 2 v), head, unit of the row
-  struct Unit {
-    int tok, kind, h, u, e0, e1;
-    bool rot;
-  };
-  auto unit_of = [&](int i) {
-    Unit x;
-    x.tok = 0;
+  bool looked_up = false, live = false;
+  int64_t k_at = 0, v_at = 0;
+  float c[8], s[8];
 #pragma unroll
-    for (int k = 1; k < TB; ++k)
-      if (i >= per_token) i -= per_token, ++x.tok;
-    const int r = i / per_row;
-    x.u = i - r * per_row;
-    x.kind = r < nq ? 0 : (r < nq + kvh ? 1 : 2);
-    x.h = x.kind == 0 ? r : (x.kind == 1 ? r - nq : r - nq - kvh);
-    x.rot = x.u < rot_units && x.kind != 2;
-    // element offsets of the two groups of eight
-    x.e0 = x.rot && split ? x.u * 8 : x.u * 16;
-    x.e1 = x.rot && split ? half + x.u * 8 : x.u * 16 + 8;
-    return x;
-  };
+  for (int j = 0; j < 8; ++j) c[j] = 1.0f, s[j] = 0.0f;
 
-  bool looked_up = false;
-  for (int i0 = threadIdx.x; i0 - static_cast<int>(threadIdx.x) < total; i0 += blockDim.x * BATCH) {
-    uint4 v[BATCH][2];
+#pragma unroll 1
+  for (int rb = 0; rb < p.rows; rb += kBatch * kRowStep) {
+    uint4 v[kBatch][2];
 #pragma unroll
-    for (int y = 0; y < BATCH; ++y) {
-      const int i = i0 + y * blockDim.x;
+    for (int y = 0; y < kBatch; ++y) {
+      const int r = rb + r0 + y * kRowStep;
       v[y][0] = v[y][1] = make_uint4(0, 0, 0, 0);
-      if (i < total) {
-        const Unit x = unit_of(i);
-        const AttnRows& src = x.kind == 0 ? p.q : (x.kind == 1 ? p.k : p.v);
-        const __nv_bfloat16* row = src.p + static_cast<int64_t>(t0 + x.tok) * src.ts + x.h * src.hs;
-        v[y][0] = *reinterpret_cast<const uint4*>(row + x.e0);
-        v[y][1] = *reinterpret_cast<const uint4*>(row + x.e1);
+      if (r < p.rows) {
+        const int h = r < nq ? r : (r < nq + kvh ? r - nq : r - nq - kvh);
+        const AttnRows& src = r < nq ? p.q : (r < nq + kvh ? p.k : p.v);
+        const __nv_bfloat16* row = src.p + t * src.ts + h * src.hs;
+        v[y][0] = *reinterpret_cast<const uint4*>(row + (r < nq + kvh ? f0 : e0));
+        v[y][1] = *reinterpret_cast<const uint4*>(row + (r < nq + kvh ? f1 : e1));
       }
     }
     if (!looked_up) {
       looked_up = true;
-      for (int k = warp; k < TB; k += blockDim.x >> 5) {
-        const int t = t0 + k;
-        Token tk{0, 0, -1};
-        bool bad = false;
-        const int b = t < p.b.n_tokens ? find_seq(p.b.q_start, p.b.n_seqs, t, lane) : p.b.n_seqs;
-        if (b < p.b.n_seqs) {
-          const SeqRows s = seq_rows(p.b.q_start, b, p.b.n_tokens, bad);
-          const int pos = p.b.kv_len[b] - s.n + (t - s.first);
-          const int at = pos >> p.page_shift;
-          if (t < s.first || s.n > p.b.max_new) bad = true;
-          if (!bad && pos >= 0) {
-            if (at >= p.b.table_pages || (rot_units > 0 && pos >= p.n_pos)) {
+      bool bad = false;
+      const int b = find_seq(p.b.q_start, p.b.n_seqs, t, lane);
+      if (b < p.b.n_seqs) {
+        const SeqRows q = seq_rows(p.b.q_start, b, p.b.n_tokens, bad);
+        const int pos = p.b.kv_len[b] - q.n + (t - q.first);
+        const int at = pos >> p.page_shift;
+        if (t < q.first || q.n > p.b.max_new) bad = true;
+        if (!bad && pos >= 0) {
+          if (at >= p.b.table_pages || (p.cos_sin != nullptr && pos >= p.n_pos)) {
+            bad = true;
+          } else {
+            const int page = p.b.page_table[b * p.b.table_stride + at];
+            if (rotated) {
+              const float* row = p.cos_sin + static_cast<int64_t>(pos) * p.rot_dim + u * 8;
+#pragma unroll
+              for (int j = 0; j < 8; j += 4) {
+                const float4 cv = *reinterpret_cast<const float4*>(row + j);
+                const float4 sv = *reinterpret_cast<const float4*>(row + half + j);
+                c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
+                s[j] = sv.x, s[j + 1] = sv.y, s[j + 2] = sv.z, s[j + 3] = sv.w;
+              }
+            }
+            const int64_t row = pos & (p.c.page_size - 1);
+            if (page < 0 || page >= p.c.num_pages) {
               bad = true;
             } else {
-              const int page = p.b.page_table[b * p.b.table_stride + at];
-              const int64_t row = pos & (p.c.page_size - 1);
-              if (page < 0 || page >= p.c.num_pages) {
-                bad = true;
-              } else {
-                tk.k_at = page * p.c.k_page_stride + row * p.c.k_token_stride;
-                tk.v_at = page * p.c.v_page_stride + row * p.c.v_token_stride;
-                tk.pos = pos;
-              }
+              k_at = page * p.c.k_page_stride + row * p.c.k_token_stride;
+              v_at = page * p.c.v_page_stride + row * p.c.v_token_stride;
+              live = true;
             }
           }
         }
-        if (lane == 0) {
-          tokens[k] = tk;
-          if (bad) record_status(p.status, EPILORA_ERR_INVALID_ARG);
-        }
       }
-      __syncthreads();
+      if (bad && threadIdx.x == 0) record_status(p.status, EPILORA_ERR_INVALID_ARG);
     }
 #pragma unroll
-    for (int y = 0; y < BATCH; ++y) {
-      const int i = i0 + y * blockDim.x;
-      if (i >= total) break;
-      const Unit x = unit_of(i);
-      const Token tk = tokens[x.tok];
-      const bool live = tk.pos >= 0;
+    for (int y = 0; y < kBatch; ++y) {
+      const int r = rb + r0 + y * kRowStep;
+      if (r >= p.rows) break;
+      const int kind = r < nq ? 0 : (r < nq + kvh ? 1 : 2);
+      const int h = kind == 0 ? r : (kind == 1 ? r - nq : r - nq - kvh);
+      const int o0 = kind != 2 ? f0 : e0, o1 = kind != 2 ? f1 : e1;
+      if (kind == 0 && !live) v[y][0] = v[y][1] = make_uint4(0, 0, 0, 0);
+      if (kind != 0 && !live) continue;
       float x0[8], x1[8];
-      unpack8(v[y][0], x0);
-      unpack8(v[y][1], x1);
-      if (live && x.rot) {
-        const float* row = p.cos_sin + static_cast<int64_t>(tk.pos) * p.rot_dim + x.u * 8;
-        float c[8], s[8];
-#pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-          const float4 cv = *reinterpret_cast<const float4*>(row + j);
-          const float4 sv = *reinterpret_cast<const float4*>(row + half + j);
-          c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
-          s[j] = sv.x, s[j + 1] = sv.y, s[j + 2] = sv.z, s[j + 3] = sv.w;
-        }
+      const bool codes = E4 && kind != 0;
+      if ((rotated && kind != 2) || codes) {
+        unpack8(v[y][0], x0);
+        unpack8(v[y][1], x1);
+      }
+      if (rotated && kind != 2 && live) {
         if (split) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -188,35 +168,24 @@ __global__ void __launch_bounds__(MAX_THREADS) kv_append_kernel(const __grid_con
             x1[2 * j + 1] = __fadd_rn(__fmul_rn(b, c[j + 4]), __fmul_rn(a, s[j + 4]));
           }
         }
-        v[y][0] = pack8(x0);
-        v[y][1] = pack8(x1);
+        if (!codes) v[y][0] = pack8(x0), v[y][1] = pack8(x1);
       }
-      if (x.kind == 0) {
-        __nv_bfloat16* o = p.qo.p + static_cast<int64_t>(t0 + x.tok) * p.qo.ts + x.h * p.qo.hs;
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(o + x.e0) = live ? v[y][0] : z;
-        *reinterpret_cast<uint4*>(o + x.e1) = live ? v[y][1] : z;
-      } else if (live) {
-        const bool is_k = x.kind == 1;
-        const int64_t at = is_k ? tk.k_at + x.h * p.c.k_head_stride : tk.v_at + x.h * p.c.v_head_stride;
-        if (p.c.kv_fmt == EPILORA_KV_BF16) {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(is_k ? p.c.k : p.c.v) + at;
-          *reinterpret_cast<uint4*>(o + x.e0) = v[y][0];
-          *reinterpret_cast<uint4*>(o + x.e1) = v[y][1];
-        } else {
-          uint8_t* o = static_cast<uint8_t*>(is_k ? p.c.k : p.c.v) + at;
-          const float s = (is_k ? p.c.k_scale : p.c.v_scale)[x.h];
-          *reinterpret_cast<uint2*>(o + x.e0) = codes8(x0, s);
-          *reinterpret_cast<uint2*>(o + x.e1) = codes8(x1, s);
-        }
+      if (codes) {
+        const float scale = (kind == 1 ? p.c.k_scale : p.c.v_scale)[h];
+        uint8_t* o = kind == 1 ? static_cast<uint8_t*>(p.c.k) + k_at + h * p.c.k_head_stride
+                               : static_cast<uint8_t*>(p.c.v) + v_at + h * p.c.v_head_stride;
+        *reinterpret_cast<uint2*>(o + o0) = codes8(x0, scale);
+        *reinterpret_cast<uint2*>(o + o1) = codes8(x1, scale);
+      } else {
+        __nv_bfloat16* o = kind == 0   ? p.qo.p + t * p.qo.ts + h * p.qo.hs
+                           : kind == 1 ? static_cast<__nv_bfloat16*>(p.c.k) + k_at + h * p.c.k_head_stride
+                                       : static_cast<__nv_bfloat16*>(p.c.v) + v_at + h * p.c.v_head_stride;
+        *reinterpret_cast<uint4*>(o + o0) = v[y][0];
+        *reinterpret_cast<uint4*>(o + o1) = v[y][1];
       }
     }
   }
 }
-
-// Tokens from which on a block takes four: with fewer the blocks of one token
-// each fill the SMs at once.
-constexpr int kManyTokens = 512;
 
 }  // namespace
 
@@ -236,24 +205,19 @@ int launch_kv_append(const AppendArgs& a) {
   p.interleaved = a.interleaved;
   p.page_shift = __builtin_ctz(a.cache.page_size);
   p.status = a.status;
-  const int units = p.rows * (a.cache.head_dim / 16);
-  const bool many = a.batch.n_tokens >= kManyTokens;
-  int threads = 256;
-  if (!many) {
-    const int rounds = (units + 1023) / 1024;
-    threads = ((units + rounds - 1) / rounds + 31) / 32 * 32;
-  }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(many ? (a.batch.n_tokens + 3) / 4 : a.batch.n_tokens, 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.gridDim = dim3(a.batch.n_tokens, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = a.stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t rc = many ? cudaLaunchKernelEx(&cfg, kv_append_kernel<4, 4, 256>, p)
-                              : cudaLaunchKernelEx(&cfg, kv_append_kernel<1, 1, 1024>, p);
+  const bool e4 = a.cache.kv_fmt == EPILORA_KV_E4M3;
+  auto kern = a.cache.head_dim == 64 ? (e4 ? kv_append_kernel<64, true> : kv_append_kernel<64, false>)
+                                     : (e4 ? kv_append_kernel<128, true> : kv_append_kernel<128, false>);
+  const cudaError_t rc = cudaLaunchKernelEx(&cfg, kern, p);
   return rc == cudaSuccess ? EPILORA_OK : EPILORA_ERR_CUDA;
 }
 

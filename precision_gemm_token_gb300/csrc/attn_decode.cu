@@ -383,6 +383,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
   }
   __syncthreads();
   pdl_wait_primary();
+  // (after the wait: whoever starts now finds the kernels before this one
+  // complete. The tile kernel of the same call does not read what this one
+  // writes; any other dependent waits for its completion.)
+  pdl_allow_dependents();
 
   // a bounded wait of a whole warp; false once any wait of the block ran out
   auto wait = [&](uint64_t* bar, uint32_t parity) {

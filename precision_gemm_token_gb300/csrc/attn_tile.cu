@@ -22,6 +22,9 @@
 //             memory, by TMA
 //   9         issues the products; S and O of both streams fill the TMEM
 //   10        bf16: cleans the value rows that some row must not see
+//   11        issues every other copy of the tiles (with pages of 16 positions
+//             a bf16 tile takes 16; one warp alone: 185 us instead of 164 for a
+//             chunk of 2048 over 4096, 64 heads)
 //   12-15     E4M3: convert the copied codes to fp16 tiles
 // Where an item has at most 128 rows both streams take the same rows and
 // alternate the position tiles; they meet at the end.
@@ -441,12 +444,12 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full[i], E4 ? 4 : 1);      // four converting warps, or the copy
+      mbar_init(&full[i], E4 ? 4 : 2);      // four converting warps, or the two copying ones
       mbar_init(&empty[i], E4 ? 1 : 2);     // the products, and the cleaning warp
       mbar_init(&cleaned[i], 1);
     }
     for (int i = 0; i < C::kRawStages; ++i) {
-      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_full[i], 2);
       mbar_init(&raw_empty[i], 4);
     }
     mbar_init(q_full, p.q_tma ? 1 : kItemRows);
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
     mbar_init(drain, 1);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&piece_full[i], 1);
-      mbar_init(&piece_empty[i], E4 ? 13 : 10);   // 8 softmax warps, the products', the cleaning or converting ones
+      mbar_init(&piece_empty[i], E4 ? 14 : 11);   // 8 softmax warps, the products', the second copying, the cleaning or converting ones
     }
     for (int i = 0; i < 2; ++i) mbar_init(&group_bar[i], kRowTile);
     mbar_init(both_bar, kItemRows);
@@ -471,7 +474,10 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
     tma_prefetch_desc(&p.tv);
     if (p.q_tma) tma_prefetch_desc(&p.tq);
   }
-  pdl_wait_primary();
+  // Behind the decode kernel of a call over the cache: that kernel let this one
+  // start once the kernels before it had completed; its own results are not
+  // read here, only its completion is waited for at the end.
+  if (!p.paged) pdl_wait_primary();
 
   // packed rows of no sequence are zero (the decode kernel's part of a call over the cache)
   if (!p.paged) {
@@ -532,8 +538,8 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
 
   if (warp >= 8) {
     setmaxnreg_dec<TileWarps<E4>::kOther>();
-  if (warp == 8) {
-    // ===== copies =====
+  if (warp == 8 || warp == 11) {
+    // ===== copies (of the first of the two warps: the walk and the queries too) =====
     fence_proxy_async_global();
     constexpr int kSt = E4 ? C::kRawStages : C::kStages;
     constexpr int kBytes = E4 ? C::kRawBytes : C::kTileBytes;
@@ -543,14 +549,18 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
     uint64_t* bar_empty = E4 ? raw_empty : empty;
     uint8_t* ring = smem + (E4 ? C::kRaw : C::kRing);
     const int nb = kPosTile / p.box_rows;                // boxes per tile along the positions
+    const int part = warp == 8 ? 0 : 1;                  // copies part, part + 2, ... of a tile
+    const int mine = 2 * lane + part;
     int slot = 0;
     uint32_t phase = 0, items = 0;
     TileWalk w;
     Piece it;
-    bool more = tile_begin(p, w, plan, lane), stop = false;
+    bool more = part == 0 && tile_begin(p, w, plan, lane), stop = false;
     while (!stop) {
-      // tell the piece (one that holds no tile of its item is left out)
-      {
+      if (part == 1) {
+        if (!next_piece(it)) break;
+      } else {
+        // tell the piece (one that holds no tile of its item is left out)
         const int e = told_n % kPieces;
         it.t0 = it.t1 = 0;
         while (more) {
@@ -573,7 +583,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
       auto page_of = [&](int u) {   // page of box u of the sequence
         return p.paged && u * p.box_rows < it.see_end ? table[(u * p.box_rows) >> p.page_shift] : 0;
       };
-      bool q_due = !E4 && p.q_tma;
+      bool q_due = !E4 && p.q_tma && part == 0;
       int c0 = it.t0 * nb;
       int ids = page_of(c0 + lane);
       for (int j = it.t0; j < it.t1 && !stop; ++j) {
@@ -581,9 +591,16 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           c0 += 32;
           ids = page_of(c0 + lane);
         }
-        if (p.paged && (ids < 0 || ids >= p.c.num_pages)) record_status(p.status, EPILORA_ERR_INVALID_ARG);
+        if (p.paged && part == 0 && (ids < 0 || ids >= p.c.num_pages)) record_status(p.status, EPILORA_ERR_INVALID_ARG);
         const int held = min(max(it.see_end - j * kPosTile, 0), kPosTile);           // rows some row of the item sees
         const int boxes = p.paged ? (held + p.box_rows - 1) / p.box_rows : (held > 0 ? 1 : 0);
+        const int copies = (boxes * kBoxes + 1 - part) / 2;                           // of this warp
+        // box `mine` of the tile: rows i, columns x
+        const int i = mine / kBoxes, x = mine % kBoxes;
+        const int pg = __shfl_sync(0xffffffffu, ids, min(j * nb + i - c0, 31));
+        const int pos = j * kPosTile + i * p.box_rows;
+        // a page index out of range, and rows past the packed array, read as zeros
+        const int y = p.paged ? pos & (p.c.page_size - 1) : it.first + pos;
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           if (!wait(&bar_empty[slot], phase ^ 1u)) {
@@ -592,26 +609,16 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           }
           uint8_t* dst = ring + slot * kBytes;
           if (lane == 0) {
-            if (boxes > 0)
-              mbar_arrive_expect_tx(&bar_full[slot], boxes * p.box_rows * kBoxes * kRowBytes);
+            if (copies > 0)
+              mbar_arrive_expect_tx(&bar_full[slot], copies * p.box_rows * kRowBytes);
             else
               mbar_arrive(&bar_full[slot]);
           }
           __syncwarp();
-          const CUtensorMap* map = kv ? &p.tv : &p.tk;
-          for (int i = 0; i < boxes; ++i) {
-            const int pg = __shfl_sync(0xffffffffu, ids, j * nb + i - c0);
-            if (lane == 0) {
-              const int pos = j * kPosTile + i * p.box_rows;
-              // a page index out of range, and rows past the packed array, read as zeros
-              const int y = p.paged ? pos & (p.c.page_size - 1) : it.first + pos;
-#pragma unroll
-              for (int x = 0; x < kBoxes; ++x)
-                tma_load_4d(dst + x * C::kBlock + i * p.box_rows * kRowBytes, map, &bar_full[slot], x * kRowBytes, y,
-                            it.h, p.paged ? pg : 0);
-            }
-            __syncwarp();
-          }
+          if (lane < copies)
+            tma_load_4d(dst + x * C::kBlock + i * p.box_rows * kRowBytes, kv ? &p.tv : &p.tk, &bar_full[slot],
+                        x * kRowBytes, y, it.h, p.paged ? pg : 0);
+          __syncwarp();
           if (++slot == kSt) slot = 0, phase ^= 1u;
         }
         if (!E4 && q_due && !stop) {
@@ -624,15 +631,15 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
             mbar_arrive_expect_tx(q_full, tiles * C::kTileBytes);
             for (int t = 0; t < tiles; ++t)
 #pragma unroll
-              for (int x = 0; x < D / 64; ++x)
-                tma_load_4d(smem + t * C::kTileBytes + x * C::kBlock, &p.tq, q_full, x * 128, it.h * p.group,
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(smem + t * C::kTileBytes + c * C::kBlock, &p.tq, q_full, c * 128, it.h * p.group,
                             it.first + (it.row0 + t * kRowTile) / p.group, 0);
           }
           __syncwarp();
           ++items;
         }
       }
-      more = tile_next(p, w);
+      if (part == 0) more = tile_next(p, w);
     }
     if (*abort_flag && lane == 0) {
       // no copy in flight at exit
@@ -1166,6 +1173,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (p.paged) pdl_wait_primary();
 }
 
 // Whether a tile's 128 rows are a box [tokens][group heads] of the queries, to

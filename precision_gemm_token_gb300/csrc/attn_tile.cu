@@ -1061,8 +1061,35 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           if (p.lse != nullptr) p.lse[tok * p.heads + head] = sum == 0.0f ? -INFINITY : (mc + __log2f(sum)) * kLn2;
         };
         const float inv = vscale / l;      // (l == 0: the row sees nothing)
+        const bool plain = whole && !nf && !both && p.o_sectors;
+        if (plain) {
+          // the usual case: the next 32 columns on their way while these are stored
+          __nv_bfloat16* at = p.o.p + tok * p.o.ts + head * p.o.hs;
+          const uint64_t inv2 = f32x2(inv, inv);
+          const bool empty = l == 0.0f;
+          uint32_t o[2][32];
+          tmem_ld_32x32b_x32(to, o[0]);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t (&x)[32] = o[i & 1];
+            tmem_ld_wait();
+            loaded(x);
+            if (i + 1 < D / 32) tmem_ld_32x32b_x32(to + (i + 1) * 32, o[(i + 1) & 1]);
+            uint32_t v[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              float a, b;
+              f32x2_parts(mul_f32x2(f32x2(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1])), inv2), a, b);
+              v[q] = empty ? 0u : pack_bf16(a, b);
+            }
+            if (live) {
+              st_global_v8(at + i * 32, v);
+              st_global_v8(at + i * 32 + 16, v + 8);
+            }
+          }
+        }
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
+        for (int i = 0; i < D && !plain; i += 32) {
           uint32_t o[32];
           tmem_ld_32x32b_x32(tm_o + s * D + quad + i, o);
           tmem_ld_wait();

@@ -75,8 +75,8 @@ struct TileCfg {
   static constexpr int kRing = kQBytes, kRaw = kRing + kStages * kTileBytes;
   static constexpr int kPlan = kRaw + kRawStages * kRawBytes;
   static constexpr int kBars = kPlan + kGroups * 4;
-  // barriers: three per stage, two per raw stage, 22 more; then 12 words of flags
-  static constexpr int kBarBytes = (3 * kStages + 2 * kRawStages + 22) * 8 + 12 * 4;
+  // barriers: three per stage, two per raw stage, 24 more; then 12 words of flags
+  static constexpr int kBarBytes = (3 * kStages + 2 * kRawStages + 24) * 8 + 12 * 4;
   static constexpr int kPieceAt = kBars + (kBarBytes + 15) / 16 * 16;
   static constexpr int kBytes = kPieceAt + kPieces * kPieceInts * 4;
   static constexpr int kSmem = 1024 + kBytes;
@@ -333,13 +333,16 @@ __device__ __forceinline__ bool e4m3x4_nan(uint32_t v) {
 }
 
 // One tile of scores to weights; a thread owns a row, m is in units of S, the
-// row sees columns below lim. The scores are read from TMEM twice, 32 columns
-// at a time (a row of 128 in registers would spill): for the maximum, then for
-// the weights, which go over the scores already read. `ready` tells the
-// products' warp of each half of the weights.
-template <int D, bool E4, typename Ready>
-__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, int lim, bool started, float& m,
-                                             float& l, Ready ready) {
+// row sees columns below lim. A row's first tile is read for its maximum
+// first. After that the weights of each half (64 columns) are taken against
+// the maximum so far while the half's own is being found; only where it is
+// more than kRaise above (hardly ever) is the row of O rescaled, after the
+// products already under way, and the half taken again. The weights go over
+// scores already read; `ready` tells the products' warp of each half, `half_in`
+// waits until the first half's product is in O.
+template <int D, bool E4, typename Ready, typename HalfIn>
+__device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, float c, int lim, bool started, float& m,
+                                             float& l, Ready ready, HalfIn half_in) {
   const bool edge = __any_sync(0xffffffffu, lim < kPosTile);
   auto hide = [&](uint32_t (&v)[32], int g) {
     const int n = lim - 32 * g;
@@ -348,70 +351,84 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
     for (int i = 0; i < 32; ++i)
       if (!(seen & (1u << i))) v[i] = 0xff800000u;
   };
-  uint32_t x[2][32];
-  float top[2] = {-INFINITY, -INFINITY};
-  tmem_ld_32x32b_x32(ts, x[0]);
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    uint32_t (&v)[32] = x[g & 1];
-    tmem_ld_wait();
-    loaded(v);
-    // (the last one starts the second reading)
-    tmem_ld_32x32b_x32(ts + ((g + 1) & 3) * 32, x[(g + 1) & 1]);
-    if (edge) hide(v, g);
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      top[0] = max3(top[0], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-      top[1] = max3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-    }
-  }
-  const float mx = fmaxf(top[0], top[1]);
-  const bool up = (mx - m) * c > kRaise;      // false for -inf - -inf
-  if (__any_sync(0xffffffffu, up)) {
-    const float f = up ? exp2_approx((m - mx) * c) : 1.0f;
-    if (up) m = mx;
-    l *= f;
-    if (started) {   // (else the row's first tile: nothing in O yet)
-      // every product into O is complete: the scores' commit came after them
+  if (!started) {
+    float top = -INFINITY;
 #pragma unroll 1
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t o[16];
-        tmem_ld_32x32b_x16(to + i * 16, o);
-        tmem_ld_wait();
-        loaded(o);
+    for (int g = 0; g < 4; ++g) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(ts + g * 32, v);
+      tmem_ld_wait();
+      loaded(v);
+      if (edge) hide(v, g);
 #pragma unroll
-        for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
-        tmem_st_32x32b_x16(to + i * 16, o);
+      for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+    }
+    m = top;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+    float add;
+#pragma unroll 1
+    while (true) {
+      const float mc = m == -INFINITY ? 0.0f : m * c;
+      const uint64_t cc = f32x2(c, c), mm = f32x2(-mc, -mc);
+      float top[2] = {-INFINITY, -INFINITY};
+      uint64_t sum[2] = {0, 0};
+      uint32_t x[2][32];
+      tmem_ld_32x32b_x32(ts + h * 64, x[0]);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t (&v)[32] = x[g];
+        tmem_ld_wait();
+        loaded(v);
+        if (g == 0) tmem_ld_32x32b_x32(ts + h * 64 + 32, x[1]);
+        if (edge) hide(v, 2 * h + g);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          top[0] = max3(top[0], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          top[1] = max3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          float a, b;
+          f32x2_parts(fma_f32x2(f32x2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), cc, mm), a, b);
+          a = exp2_approx(a);
+          b = exp2_approx(b);
+          sum[q & 1] = add_f32x2(sum[q & 1], f32x2(a, b));
+          // the weights as 16-bit operands (each within 2^-8 of itself, 2^-11 in fp16)
+          pk[16 * g + q] = E4 ? pack_half(a, b) : pack_bf16(a, b);
+        }
+      }
+      float s0, s1;
+      f32x2_parts(add_f32x2(sum[0], sum[1]), s0, s1);
+      add = s0 + s1;
+      const float mx = fmaxf(top[0], top[1]);
+      const bool up = (mx - m) * c > kRaise;      // false for -inf - -inf
+      if (!__any_sync(0xffffffffu, up)) break;
+      const float f = up ? exp2_approx((m - mx) * c) : 1.0f;
+      if (up) m = mx;
+      l *= f;
+      // every earlier tile's product into O is complete: these scores' commit came after them
+      if (h == 1 && !half_in()) return false;
+      if (started || h == 1) {
+#pragma unroll 1
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t o[16];
+          tmem_ld_32x32b_x16(to + i * 16, o);
+          tmem_ld_wait();
+          loaded(o);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+          tmem_st_32x32b_x16(to + i * 16, o);
+        }
       }
     }
+    l += add;
+    tmem_st_32x32b_x32(ts + h * 32, pk);
+    ready(h);
   }
-  const float mc = m == -INFINITY ? 0.0f : m * c;
-  const uint64_t cc = f32x2(c, c), mm = f32x2(-mc, -mc);
-  uint64_t sum[2] = {0, 0};
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    uint32_t (&v)[32] = x[g & 1];
-    tmem_ld_wait();
-    loaded(v);
-    if (g < 3) tmem_ld_32x32b_x32(ts + (g + 1) * 32, x[(g + 1) & 1]);
-    if (edge) hide(v, g);
-    uint32_t pk[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      float a, b;
-      f32x2_parts(fma_f32x2(f32x2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), cc, mm), a, b);
-      a = exp2_approx(a);
-      b = exp2_approx(b);
-      sum[q & 1] = add_f32x2(sum[q & 1], f32x2(a, b));
-      // the weights as 16-bit operands (each within 2^-8 of itself, 2^-11 in fp16)
-      pk[q] = E4 ? pack_half(a, b) : pack_bf16(a, b);
-    }
-    tmem_st_32x32b_x16(ts + g * 16, pk);
-    if (g & 1) ready(g >> 1);
-  }
-  float s0, s1;
-  f32x2_parts(add_f32x2(sum[0], sum[1]), s0, s1);
-  l += s0 + s1;
+  return true;
 }
 
 template <int D, bool E4>
@@ -428,7 +445,8 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
   uint64_t* q_free = q_full + 1;                                   // and have been read
   uint64_t* s_full = q_free + 1;                                   // [2] scores complete
   uint64_t* p_full = s_full + 2;                                   // [2][2] halves of the weights written
-  uint64_t* o_full = p_full + 4;                                   // [2] output complete
+  uint64_t* h_full = p_full + 4;                                   // [2] the first half's product is in O
+  uint64_t* o_full = h_full + 2;                                   // [2] output complete
   uint64_t* cleaned = o_full + 2;                                  // [stages] a value tile is cleaned
   uint64_t* drain = cleaned + C::kStages;                          // after an abort: products complete
   uint64_t* piece_full = drain + 1;                                // [pieces] told
@@ -458,6 +476,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[2 * i], kRowTile);
       mbar_init(&p_full[2 * i + 1], kRowTile);
+      mbar_init(&h_full[i], 1);
       mbar_init(&o_full[i], 1);
     }
     mbar_init(drain, 1);
@@ -756,6 +775,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
 #pragma unroll
           for (int k = 0; k < kPosTile / 32; ++k)
             mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, i >= 2 || k > 0);
+          tc_commit(&h_full[s]);
           if (!mbar_try_wait(&p_full[2 * s + 1], p_par) && !(ok = wait1(&p_full[2 * s + 1], p_par))) break;
           tc_fence_after();
 #pragma unroll
@@ -1004,11 +1024,19 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
       for (int k = 0; k < steps; ++k) {
         if (!wait(&s_full[s], sn++ & 1u)) break;
         tc_fence_after();
-        softmax_tile<D, E4>(ts, to, c, lim, started, m, l, [&](int half) {
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&p_full[2 * s + half]);
-        });
+        const bool done = softmax_tile<D, E4>(
+            ts, to, c, lim, started, m, l,
+            [&](int half) {
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(&p_full[2 * s + half]);
+            },
+            [&]() {
+              if (!wait(&h_full[s], (sn - 1) & 1u)) return false;
+              tc_fence_after();
+              return true;
+            });
+        if (!done) break;
         started = true;
         lim -= lim_step;
       }

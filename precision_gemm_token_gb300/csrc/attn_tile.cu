@@ -343,14 +343,26 @@ __device__ __forceinline__ bool e4m3x4_nan(uint32_t v) {
 template <int D, bool E4, typename Ready, typename HalfIn>
 __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, float c, int lim, bool started, float& m,
                                              float& l, Ready ready, HalfIn half_in) {
-  const bool edge = __any_sync(0xffffffffu, lim < kPosTile);
-  auto hide = [&](uint32_t (&v)[32], int g) {
-    const int n = lim - 32 * g;
-    const uint32_t seen = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+  // (Loops are kept rolled where their body is long enough: unrolled, the
+  // kernel's paths evict one another from the instruction cache.)
+  if (__any_sync(0xffffffffu, lim < kPosTile)) {
+    // scores that the row must not see
+#pragma unroll 1
+    for (int g = 0; g < 4; ++g) {
+      const int n = lim - 32 * g;
+      if (__all_sync(0xffffffffu, n >= 32)) continue;
+      const uint32_t seen = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(ts + g * 32, v);
+      tmem_ld_wait();
+      loaded(v);
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (!(seen & (1u << i))) v[i] = 0xff800000u;
-  };
+      for (int i = 0; i < 32; ++i)
+        if (!(seen & (1u << i))) v[i] = 0xff800000u;
+      tmem_st_32x32b_x32(ts + g * 32, v);
+    }
+    tmem_st_wait();
+  }
   if (!started) {
     float top = -INFINITY;
 #pragma unroll 1
@@ -359,13 +371,12 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, float c, 
       tmem_ld_32x32b_x32(ts + g * 32, v);
       tmem_ld_wait();
       loaded(v);
-      if (edge) hide(v, g);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
     }
     m = top;
   }
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     uint32_t pk[32];
     float add;
@@ -383,7 +394,6 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, float c, 
         tmem_ld_wait();
         loaded(v);
         if (g == 0) tmem_ld_32x32b_x32(ts + h * 64 + 32, x[1]);
-        if (edge) hide(v, 2 * h + g);
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           top[0] = max3(top[0], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
@@ -1089,7 +1099,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           if (p.lse != nullptr) p.lse[tok * p.heads + head] = sum == 0.0f ? -INFINITY : (mc + __log2f(sum)) * kLn2;
         };
         const float inv = vscale / l;      // (l == 0: the row sees nothing)
-        const bool plain = whole && !nf && !both && p.o_sectors;
+        const bool plain = whole && !both && p.o_sectors;
         if (plain) {
           // the usual case: the next 32 columns on their way while these are stored
           __nv_bfloat16* at = p.o.p + tok * p.o.ts + head * p.o.hs;
@@ -1097,22 +1107,26 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           const bool empty = l == 0.0f;
           uint32_t o[2][32];
           tmem_ld_32x32b_x32(to, o[0]);
+#pragma unroll 1
+          for (int i0 = 0; i0 < D; i0 += 64) {
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t (&x)[32] = o[i & 1];
-            tmem_ld_wait();
-            loaded(x);
-            if (i + 1 < D / 32) tmem_ld_32x32b_x32(to + (i + 1) * 32, o[(i + 1) & 1]);
-            uint32_t v[16];
+            for (int y = 0; y < 2; ++y) {
+              uint32_t (&x)[32] = o[y];
+              const int i = i0 + 32 * y;
+              tmem_ld_wait();
+              loaded(x);
+              if (i + 32 < D) tmem_ld_32x32b_x32(to + i + 32, o[y ^ 1]);
+              uint32_t v[16];
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              float a, b;
-              f32x2_parts(mul_f32x2(f32x2(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1])), inv2), a, b);
-              v[q] = empty ? 0u : pack_bf16(a, b);
-            }
-            if (live) {
-              st_global_v8(at + i * 32, v);
-              st_global_v8(at + i * 32 + 16, v + 8);
+              for (int q = 0; q < 16; ++q) {
+                float a, b;
+                f32x2_parts(mul_f32x2(f32x2(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1])), inv2), a, b);
+                v[q] = empty ? 0u : pack_bf16(a, b);
+              }
+              if (live) {
+                st_global_v8(at + i, v);
+                st_global_v8(at + i + 16, v + 8);
+              }
             }
           }
         }
@@ -1132,31 +1146,6 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
 #pragma unroll
             for (int q = 0; q < 32; ++q) a[q] = a[q] * f0 + __uint_as_float(o[q]) * f1;
           }
-          if (nf) {
-            // the non-finite values that were taken out, where this row sees them
-            const int to_pos = min(see, it.t1 * kPosTile);
-            for (int pos = max(it.see_all, it.t0 * kPosTile); pos < to_pos; ++pos) {
-              if (!p.paged) {
-                const __nv_bfloat16* v = p.v.p + (it.first + pos) * p.v.ts + it.h * p.v.hs + i;
-#pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                  const float e = __bfloat162float(v[q]);
-                  if (!(fabsf(e) < INFINITY)) a[q] += e;
-                }
-              } else {
-                const int pg = p.b.page_table[it.b * p.b.table_stride + (pos >> p.page_shift)];
-                if (pg < 0 || pg >= p.c.num_pages) continue;
-                const int64_t at = pg * p.c.v_page_stride + it.h * p.c.v_head_stride +
-                                   (pos & (p.c.page_size - 1)) * p.c.v_token_stride + i;
-#pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                  const float e = E4 ? e4m3_to_f32(static_cast<const uint8_t*>(p.c.v)[at + q])
-                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(p.c.v)[at + q]);
-                  if (!(fabsf(e) < INFINITY)) a[q] += e;
-                }
-              }
-            }
-          }
           if (whole) {
             if (live) {
               put(i, a, inv, l == 0.0f);
@@ -1168,6 +1157,37 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           }
         }
         const float mc = m == -INFINITY ? -INFINITY : m * c;
+        if (nf) {
+          // the non-finite values that were taken out, where this row sees them, go into what was just written
+          const int to_pos = live ? min(see, it.t1 * kPosTile) : 0;
+#pragma unroll 1
+          for (int pos = max(it.see_all, it.t0 * kPosTile); pos < to_pos; ++pos) {
+            const __nv_bfloat16* v = nullptr;
+            const uint8_t* v4 = nullptr;
+            if (!p.paged) {
+              v = p.v.p + (it.first + pos) * p.v.ts + it.h * p.v.hs;
+            } else {
+              const int pg = p.b.page_table[it.b * p.b.table_stride + (pos >> p.page_shift)];
+              if (pg < 0 || pg >= p.c.num_pages) continue;
+              const int64_t at = pg * p.c.v_page_stride + it.h * p.c.v_head_stride +
+                                 (pos & (p.c.page_size - 1)) * p.c.v_token_stride;
+              v = static_cast<const __nv_bfloat16*>(p.c.v) + at;
+              v4 = static_cast<const uint8_t*>(p.c.v) + at;
+            }
+#pragma unroll 1
+            for (int i = 0; i < D; ++i) {
+              const float e = E4 ? e4m3_to_f32(v4[i]) : __bfloat162float(v[i]);
+              if (fabsf(e) < INFINITY) continue;
+              if (whole) {
+                __nv_bfloat16* o = p.o.p + tok * p.o.ts + head * p.o.hs + i;
+                *o = __float2bfloat16_rn(__bfloat162float(*o) + e);
+              } else {
+                float* o = reinterpret_cast<float*>(part + 2 * kItemRows / 4 + i / 4 * kItemRows + prow) + i % 4;
+                *o += e;
+              }
+            }
+          }
+        }
         if (whole) {
           if (live) put_lse(mc, l);
         } else {

@@ -93,6 +93,8 @@ struct TileParams {
   float* lse;
   int paged;
   int heads, kv_heads, group;
+  uint32_t group_mul;      // row / group = row * group_mul >> group_shift for rows below 2^30
+  int group_shift;
   int page_shift;
   int box_rows;            // rows per TMA box
   int o_sectors;           // every output row is 32-byte aligned
@@ -101,6 +103,14 @@ struct TileParams {
   float4* partials;        // [2 gridDim.x][(2 + D) * 256 / 4]
   int* status;
 };
+
+// row / group by a multiplication (the walk divides often; a division by a
+// number the compiler does not know is some thirty instructions each time):
+// group_mul = 2^(31 + s) / group rounded up, s = ceil(log2 group), is off by less
+// than one, which moves the quotient by less than 2^30 / 2^(31 + s) < 1 / group.
+__device__ __forceinline__ int token_of(const TileParams& p, int row) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(row)) * p.group_mul) >> p.group_shift);
+}
 
 struct TileSeq {
   int first, n, len, base, rts;   // packed rows, tokens held, position of new token 0, row tiles (0: not of the class)
@@ -125,7 +135,7 @@ __device__ __forceinline__ TileSeq tile_seq(const TileParams& p, int b, bool& ba
 }
 // positions that row `row` of the sequence sees
 __device__ __forceinline__ int row_sees(const TileParams& p, const TileSeq& s, int row) {
-  return max(min(s.base + row / p.group + 1, s.len), 0);
+  return max(min(s.base + token_of(p, row) + 1, s.len), 0);
 }
 __device__ __forceinline__ int item_tiles(const TileParams& p, const TileSeq& s, int rt) {
   const int e = row_sees(p, s, min((rt + 1) * kItemRows, s.n * p.group) - 1);
@@ -662,7 +672,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
                 tma_load_4d(smem + t * C::kTileBytes + c * C::kBlock, &p.tq, q_full, c * 128, it.h * p.group,
-                            it.first + (it.row0 + t * kRowTile) / p.group, 0);
+                            it.first + token_of(p, it.row0 + t * kRowTile), 0);
           }
           __syncwarp();
           ++items;
@@ -974,9 +984,10 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
       const int lrow = two ? s * kRowTile + r : r;      // row within the item
       const bool live = lrow < it.rows;
       const int grow = it.row0 + (live ? lrow : 0);
-      const int64_t tok = it.first + grow / p.group;
-      const int head = it.h * p.group + grow % p.group;
-      const int see = live ? max(min(it.base + grow / p.group + 1, it.len), 0) : 0;
+      const int new_tok = token_of(p, grow);
+      const int64_t tok = it.first + new_tok;
+      const int head = it.h * p.group + grow - new_tok * p.group;
+      const int see = live ? max(min(it.base + new_tok + 1, it.len), 0) : 0;
       float s_eff = p.scale;
       if (E4) s_eff *= p.c.k_scale[it.h];
       float c = s_eff == 0.0f ? 1.0f : fabsf(s_eff) * kLog2e;
@@ -1340,6 +1351,10 @@ int launch_attn_tile(const AttnArgs& a, uint32_t* counters, float* partials) {
   p.heads = a.heads;
   p.kv_heads = a.cache.kv_heads;
   p.group = a.heads / a.cache.kv_heads;
+  int s = 0;
+  while ((1 << s) < p.group) ++s;
+  p.group_shift = 31 + s;
+  p.group_mul = static_cast<uint32_t>(((uint64_t{1} << p.group_shift) + p.group - 1) / p.group);
   p.page_shift = a.paged ? __builtin_ctz(a.cache.page_size) : 0;
   p.box_rows = a.paged && a.cache.page_size < kPosTile ? a.cache.page_size : kPosTile;
   p.o_sectors = (reinterpret_cast<uintptr_t>(a.o.p) | static_cast<uintptr_t>(a.o.ts * 2) |

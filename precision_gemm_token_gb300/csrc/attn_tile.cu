@@ -69,9 +69,9 @@ struct TileCfg {
   static constexpr int kTileBytes = kPosTile * D * 2;            // 16-bit key or value tile
   static constexpr int kBlock = 128 * 128;                       // 128 rows of 64 elements, swizzled
   static constexpr int kQBytes = 2 * kTileBytes;
-  static constexpr int kStages = E4 ? 3 : 160 * 1024 / kTileBytes;
+  static constexpr int kStages = (E4 ? 128 : 160) * 1024 / kTileBytes;
   static constexpr int kRawBytes = kPosTile * D;                 // E4M3 codes of a tile
-  static constexpr int kRawStages = E4 ? 4 : 0;
+  static constexpr int kRawStages = E4 ? 32 * 1024 / kRawBytes : 0;
   static constexpr int kRing = kQBytes, kRaw = kRing + kStages * kTileBytes;
   static constexpr int kPlan = kRaw + kRawStages * kRawBytes;
   static constexpr int kBars = kPlan + kGroups * 4;
@@ -338,8 +338,14 @@ __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t v) {
 }
 // whether a 32-bit word of four E4M3 codes holds a NaN (they have no infinity)
 __device__ __forceinline__ bool e4m3x4_nan(uint32_t v) {
-  return ((v & 0x7Fu) == 0x7Fu) | ((v & 0x7F00u) == 0x7F00u) | ((v & 0x7F0000u) == 0x7F0000u) |
-         ((v & 0x7F000000u) == 0x7F000000u);
+  return (((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+}
+// four E4M3 codes with the NaN among them replaced by zero
+__device__ __forceinline__ uint32_t e4m3x4_strip_nan(uint32_t v) {
+#pragma unroll
+  for (int z = 0; z < 32; z += 8)
+    if (((v >> z) & 0x7Fu) == 0x7Fu) v &= ~(0xFFu << z);
+  return v;
 }
 
 // One tile of scores to weights; a thread owns a row, m is in units of S, the
@@ -769,8 +775,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           tc_fence_after();
           qk(1);
         }
-        // with three stages and one row tile the next keys arrive only once this step's values are read
-        const bool early = C::kStages >= 5 || two;
+        static_assert(C::kStages >= 4, "the next keys are waited for before this step's values are read");
 #pragma unroll 1
         for (int i = 0; i < steps; ++i) {
           const int s = i & 1, j = two ? i >> 1 : i;
@@ -782,7 +787,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           const uint32_t v_par = clean ? (clean_phase >> vr.slot) & 1u : vr.phase, p_par = (p_phase >> s) & 1u;
           uint32_t rv = 1, rk = 1;
           if (new_v) rv = mbar_try_wait(v_bar, v_par);
-          if (new_k && early) rk = mbar_try_wait(&full[kr.slot], kr.phase);
+          if (new_k) rk = mbar_try_wait(&full[kr.slot], kr.phase);
           const uint32_t rp = mbar_try_wait(&p_full[2 * s], p_par);
           if (!(rv & rk & rp)) {
             ok = (rv || wait1(v_bar, v_par)) && (rk || wait1(&full[kr.slot], kr.phase)) &&
@@ -809,10 +814,6 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           }
           if (!more) tc_commit(&o_full[s]);
           if (more) {
-            if (new_k && !early) {
-              if (!(ok = wait1(&full[kr.slot], kr.phase))) break;
-              tc_fence_after();
-            }
             qk(i + 2);
           }
         }
@@ -909,37 +910,49 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
             uint8_t* dst = smem + C::kRing + slot * C::kTileBytes;
             bool nf = false;
             const bool clean = kv == 1 && from < kPosTile;
-            constexpr int kPer = D / 16;   // 16-code chunks per row
-#pragma unroll 4
-            for (int i = t; i < kPosTile * kPer; i += 128) {
-              uint4 u = *reinterpret_cast<const uint4*>(src + i * 16);
-              const int row = i / kPer, c = i % kPer;
-              if (clean) {
-                if (row >= to) {
-                  u = make_uint4(0, 0, 0, 0);
-                } else if (row >= from && (e4m3x4_nan(u.x) | e4m3x4_nan(u.y) | e4m3x4_nan(u.z) | e4m3x4_nan(u.w))) {
-                  nf = true;
-                  uint32_t e[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int y = 0; y < 32; y += 8)
-                      if ((e[k] & (0x7Fu << y)) == (0x7Fu << y)) e[k] &= ~(0xFFu << y);
-                  u = make_uint4(e[0], e[1], e[2], e[3]);
-                }
-              }
+            // A thread takes 16-code chunk c of the rows r0, r0 + kStep, ...: chunks
+            // 2c and 2c + 1 of the 16-bit row's 16-byte chunks, swizzled alike in
+            // all of its rows (kStep is a multiple of 8). The two halves of a
+            // 128-element row store theirs in opposite order, so that they use
+            // different banks.
+            constexpr int kPer = D / 16, kStep = 128 / kPer;
+            const int r0 = t / kPer, c = t % kPer, first = (c / 4) & 1;
+            uint8_t* row_at = dst + (c / 4) * C::kBlock + r0 * 128;
+            const uint32_t at0 = (((c % 4) * 2 + first) ^ (r0 & 7)) * 16, at1 = at0 ^ 16u;
+            auto store = [&](int y, const uint4& u) {
               uint4 lo, hi;
               lo.x = e4m3x2_to_f16x2(u.x), lo.y = e4m3x2_to_f16x2(u.x >> 16);
               lo.z = e4m3x2_to_f16x2(u.y), lo.w = e4m3x2_to_f16x2(u.y >> 16);
               hi.x = e4m3x2_to_f16x2(u.z), hi.y = e4m3x2_to_f16x2(u.z >> 16);
               hi.z = e4m3x2_to_f16x2(u.w), hi.w = e4m3x2_to_f16x2(u.w >> 16);
-              // chunks 2c and 2c + 1 of the row's 16-byte chunks, swizzled; the
-              // two halves of a 128-element row store theirs in opposite order,
-              // so that they use different banks
-              uint8_t* row_at = dst + (c / 4) * C::kBlock + row * 128;
-              const int k0 = (c % 4) * 2, sw = row & 7, first = (c / 4) & 1;
-              *reinterpret_cast<uint4*>(row_at + (((k0 + first) ^ sw) * 16)) = first ? hi : lo;
-              *reinterpret_cast<uint4*>(row_at + (((k0 + 1 - first) ^ sw) * 16)) = first ? lo : hi;
+              *reinterpret_cast<uint4*>(row_at + at0 + y * kStep * 128) = first ? hi : lo;
+              *reinterpret_cast<uint4*>(row_at + at1 + y * kStep * 128) = first ? lo : hi;
+            };
+            const uint4* codes = reinterpret_cast<const uint4*>(src) + t;
+            if (!clean) {
+              // (no branch in the body: its loads and conversions overlap)
+#pragma unroll 1
+              for (int y = 0; y < kPer; y += 4) {
+                uint4 u[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) u[k] = codes[(y + k) * 128];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) store(y + k, u[k]);
+              }
+            } else {
+#pragma unroll 1
+              for (int y = 0; y < kPer; ++y) {
+                uint4 u = codes[y * 128];
+                const int row = r0 + y * kStep;
+                if (row >= to) {
+                  u = make_uint4(0, 0, 0, 0);
+                } else if (row >= from && (e4m3x4_nan(u.x) | e4m3x4_nan(u.y) | e4m3x4_nan(u.z) | e4m3x4_nan(u.w))) {
+                  nf = true;
+                  u.x = e4m3x4_strip_nan(u.x), u.y = e4m3x4_strip_nan(u.y);
+                  u.z = e4m3x4_strip_nan(u.z), u.w = e4m3x4_strip_nan(u.w);
+                }
+                store(y, u);
+              }
             }
             if (nf) nf_item[item & 7] = item + 1;
             fence_proxy_async_smem();

@@ -40,7 +40,8 @@ int cache_check(const epilora_kv_cache* c, int heads) {
                               c->v_page_stride, c->v_head_stride, c->v_token_stride};
   for (int i = 0; i < 6; ++i) {
     if (strides[i] % unit != 0 || strides[i] < c->head_dim) return EPILORA_ERR_INVALID_ARG;
-    if (strides[i] >= (int64_t{1} << 38)) return EPILORA_ERR_UNSUPPORTED;   // a tensor map's stride stays below 2^40 bytes
+    // (a tensor map's stride stays below 2^40 bytes)
+    if (strides[i] >= (int64_t{1} << 38)) return EPILORA_ERR_UNSUPPORTED;
   }
   if (c->kv_fmt == EPILORA_KV_E4M3 &&
       (c->k_scale == nullptr || c->v_scale == nullptr || !al(c->k_scale, 4) || !al(c->v_scale, 4)))

@@ -69,6 +69,8 @@ struct TileCfg {
   static constexpr int kTileBytes = kPosTile * D * 2;            // 16-bit key or value tile
   static constexpr int kBlock = 128 * 128;                       // 128 rows of 64 elements, swizzled
   static constexpr int kQBytes = 2 * kTileBytes;
+  // 160 KB of tiles: five 32 KB ones at head_dim 128. E4M3 at 128: four 16-bit tiles and two of codes (with
+  // three and four, the next keys' tile is free only when this step's values are done, and so converted late)
   static constexpr int kStages = (E4 ? 128 : 160) * 1024 / kTileBytes;
   static constexpr int kRawBytes = kPosTile * D;                 // E4M3 codes of a tile
   static constexpr int kRawStages = E4 ? 32 * 1024 / kRawBytes : 0;
@@ -291,7 +293,8 @@ struct Piece {
   int whole;           // the item's only piece
   int first_cta, pieces;   // of an item in several pieces: the blocks first_cta, ...
   int slot, slot0;     // where this piece's, and the first piece's, partial result goes
-  __device__ __forceinline__ bool two() const { return rows > kRowTile; }   // two row tiles; else both streams share one
+  // two row tiles; else both streams share one
+  __device__ __forceinline__ bool two() const { return rows > kRowTile; }
 };
 static_assert(sizeof(Piece) == kPieceInts * 4, "one int per field");
 
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(both_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* last_flag = abort_flag + 1;                        // [2]
-  volatile int* nf_item = last_flag + 2;                           // [8] pieces (by number) with non-finite hidden values
+  volatile int* nf_item = last_flag + 2;                           // [8] pieces with non-finite hidden values
   volatile int* told = reinterpret_cast<volatile int*>(smem + C::kPieceAt);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -508,7 +511,8 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
     mbar_init(drain, 1);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&piece_full[i], 1);
-      mbar_init(&piece_empty[i], E4 ? 14 : 11);   // 8 softmax warps, the products', the second copying, the cleaning or converting ones
+      // 8 softmax warps, the products', the second copying one, the cleaning or converting ones
+      mbar_init(&piece_empty[i], E4 ? 14 : 11);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&group_bar[i], kRowTile);
     mbar_init(both_bar, kItemRows);
@@ -583,393 +587,394 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
 
   if (warp >= 8) {
     setmaxnreg_dec<TileWarps<E4>::kOther>();
-  if (warp == 8 || warp == 11) {
-    // ===== copies (of the first of the two warps: the walk and the queries too) =====
-    fence_proxy_async_global();
-    constexpr int kSt = E4 ? C::kRawStages : C::kStages;
-    constexpr int kBytes = E4 ? C::kRawBytes : C::kTileBytes;
-    constexpr int kRowBytes = E4 ? D : 128;              // inner extent of a box
-    constexpr int kBoxes = E4 ? 1 : D / 64;
-    uint64_t* bar_full = E4 ? raw_full : full;
-    uint64_t* bar_empty = E4 ? raw_empty : empty;
-    uint8_t* ring = smem + (E4 ? C::kRaw : C::kRing);
-    const int nb = kPosTile / p.box_rows;                // boxes per tile along the positions
-    const int part = warp == 8 ? 0 : 1;                  // copies part, part + 2, ... of a tile
-    const int mine = 2 * lane + part;
-    int slot = 0;
-    uint32_t phase = 0, items = 0;
-    TileWalk w;
-    Piece it;
-    bool more = part == 0 && tile_begin(p, w, plan, lane), stop = false;
-    while (!stop) {
-      if (part == 1) {
-        if (!next_piece(it)) break;
-      } else {
-        // tell the piece (one that holds no tile of its item is left out)
-        const int e = told_n % kPieces;
-        it.t0 = it.t1 = 0;
-        while (more) {
-          piece_of(p, w, it);
-          if (it.t1 > it.t0) break;
-          more = tile_next(p, w);
-        }
-        if (!wait(&piece_empty[e], ((told_n / kPieces) & 1u) ^ 1u)) break;
-        if (lane == 0) {
-          const int* from = reinterpret_cast<const int*>(&it);
-#pragma unroll
-          for (int i = 0; i < kPieceInts; ++i) told[e * kPieceInts + i] = from[i];
-          mbar_arrive(&piece_full[e]);
-        }
-        __syncwarp();
-        ++told_n;
-        if (!more) break;
-      }
-      const int32_t* table = p.paged ? p.b.page_table + it.b * p.b.table_stride : nullptr;
-      auto page_of = [&](int u) {   // page of box u of the sequence
-        return p.paged && u * p.box_rows < it.see_end ? table[(u * p.box_rows) >> p.page_shift] : 0;
-      };
-      bool q_due = !E4 && p.q_tma && part == 0;
-      int c0 = it.t0 * nb;
-      int ids = page_of(c0 + lane);
-      for (int j = it.t0; j < it.t1 && !stop; ++j) {
-        if (j * nb >= c0 + 32) {
-          c0 += 32;
-          ids = page_of(c0 + lane);
-        }
-        if (p.paged && part == 0 && (ids < 0 || ids >= p.c.num_pages)) record_status(p.status, EPILORA_ERR_INVALID_ARG);
-        const int held = min(max(it.see_end - j * kPosTile, 0), kPosTile);           // rows some row of the item sees
-        const int boxes = p.paged ? (held + p.box_rows - 1) / p.box_rows : (held > 0 ? 1 : 0);
-        const int copies = (boxes * kBoxes + 1 - part) / 2;                           // of this warp
-        // box `mine` of the tile: rows i, columns x
-        const int i = mine / kBoxes, x = mine % kBoxes;
-        const int pg = __shfl_sync(0xffffffffu, ids, min(j * nb + i - c0, 31));
-        const int pos = j * kPosTile + i * p.box_rows;
-        // a page index out of range, and rows past the packed array, read as zeros
-        const int y = p.paged ? pos & (p.c.page_size - 1) : it.first + pos;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          if (!wait(&bar_empty[slot], phase ^ 1u)) {
-            stop = true;
-            break;
-          }
-          uint8_t* dst = ring + slot * kBytes;
-          if (lane == 0) {
-            if (copies > 0)
-              mbar_arrive_expect_tx(&bar_full[slot], copies * p.box_rows * kRowBytes);
-            else
-              mbar_arrive(&bar_full[slot]);
-          }
-          __syncwarp();
-          if (lane < copies)
-            tma_load_4d(dst + x * C::kBlock + i * p.box_rows * kRowBytes, kv ? &p.tv : &p.tk, &bar_full[slot],
-                        x * kRowBytes, y, it.h, p.paged ? pg : 0);
-          __syncwarp();
-          if (++slot == kSt) slot = 0, phase ^= 1u;
-        }
-        if (!E4 && q_due && !stop) {
-          // the queries, behind the first tile (by then the last piece's products are about to have read theirs)
-          q_due = false;
-          if (!wait(q_free, (items & 1u) ^ 1u)) {
-            stop = true;
-          } else if (lane == 0) {
-            const int tiles = it.two() ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, tiles * C::kTileBytes);
-            for (int t = 0; t < tiles; ++t)
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_4d(smem + t * C::kTileBytes + c * C::kBlock, &p.tq, q_full, c * 128, it.h * p.group,
-                            it.first + token_of(p, it.row0 + t * kRowTile), 0);
-          }
-          __syncwarp();
-          ++items;
-        }
-      }
-      if (part == 0) more = tile_next(p, w);
-    }
-    if (*abort_flag && lane == 0) {
-      // no copy in flight at exit
-      for (int i = 0; i < kSt; ++i)
-        (void)mbar_wait_bounded(&bar_full[i], i < slot ? phase : phase ^ 1u, 1000000ull);
-      if (!E4 && p.q_tma && items > 0) (void)mbar_wait_bounded(q_full, (items - 1) & 1u, 1000000ull);
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ===== products =====
-    // A stream takes S = Q K^T of a tile, then (the weights having gone over
-    // the scores) O += P V, then the next tile's S; the streams in turn. One
-    // lane does it all, its products run in order, so no S is overwritten
-    // early. A wait takes some 100 cycles even where its barrier is ready (130
-    // for a whole warp), the products between two of them 256 or 512: a step's
-    // barriers are therefore tried together and waited for one by one only
-    // where one is not ready. (A lane per stream instead was slower, 973
-    // against 841 us for a prompt of 8192 x 64 heads: the streams then fall
-    // into step, and the products wait for the softmax of both.)
-    if (elect_one()) {
-      constexpr uint32_t kIdQK = idesc_f16(128, 128, !E4, false);
-      constexpr uint32_t kIdPV = idesc_f16(128, D, !E4, true);
-      const uint64_t q_desc = make_smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-      const uint64_t k_desc = make_smem_desc(smem_u32(smem + C::kRing), 16, 1024, kSwizzle128B);
-      const uint64_t v_desc = make_smem_desc(smem_u32(smem + C::kRing), C::kBlock, 1024, kSwizzle128B);
-      constexpr uint32_t kTile16 = C::kTileBytes >> 4;
-      struct Ring {
-        uint32_t slot, phase;
-        __device__ __forceinline__ void skip(uint32_t n) {
-          slot += n;
-          if (slot >= C::kStages) slot -= C::kStages, phase ^= 1u;
-        }
-      };
-      Ring start{0, 0};                  // ring position (keys and values alternating) of the piece's first tile
-      uint32_t clean_phase = 0;          // a bit per stage
-      uint32_t item = 0, p_phase = 0;    // p_phase: bit s for stream s
-      bool ok = true, issued = false;
-      auto wait1 = [&](uint64_t* bar, uint32_t parity) {
-        const uint64_t t0 = globaltimer_ns();
-        for (uint32_t polls = 1;; ++polls) {
-          if (mbar_try_wait(bar, parity)) return true;
-          if ((polls & 63u) == 0u && (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs)) break;
-        }
-        *abort_flag = 1;
-        record_status(p.status, EPILORA_ERR_TIMEOUT);
-        return false;
-      };
-      while (ok) {
-        // the piece
-        const int e = told_n % kPieces;
-        if (!(ok = wait1(&piece_full[e], (told_n / kPieces) & 1u))) break;
-        Piece it;
-        int* to = reinterpret_cast<int*>(&it);
-#pragma unroll
-        for (int i = 0; i < kPieceInts; ++i) to[i] = told[e * kPieceInts + i];
-        mbar_arrive(&piece_empty[e]);
-        ++told_n;
-        const int nt = it.t1 - it.t0;
-        if (nt <= 0) break;
-        const bool two = it.two();
-        const int steps = two ? 2 * nt : nt;
-        // position tile of a step: i / 2 with two row tiles, else i
-        Ring kr = start, vr = start;     // keys and values of the next step's tile
-        vr.skip(1);
-        // scores of step i (of stream i % 2)
-        auto qk = [&](int i) {
-          const int s = i & 1;
-          const uint64_t a = q_desc + (two && s == 1 ? kTile16 : 0), b = k_desc + kr.slot * kTile16;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k / 4) * C::kBlock + (k % 4) * 32) >> 4;
-            mma_f16_ss(tm_s + s * 128, a + off, b + off, kIdQK, k > 0);
-          }
-          tc_commit(&s_full[s]);
-          if (!(two && s == 0)) {
-            tc_commit(&empty[kr.slot]);
-            kr.skip(2);
-          }
-          if (i + 1 == steps) tc_commit(q_free);
-        };
-        ok = wait1(q_full, item & 1u) && wait1(&full[kr.slot], kr.phase);
-        if (!ok) break;
-        tc_fence_after();
-        qk(0);
-        issued = true;
-        if (steps > 1) {
-          if (!two && !(ok = wait1(&full[kr.slot], kr.phase))) break;
-          tc_fence_after();
-          qk(1);
-        }
-        static_assert(C::kStages >= 4, "the next keys are waited for before this step's values are read");
-#pragma unroll 1
-        for (int i = 0; i < steps; ++i) {
-          const int s = i & 1, j = two ? i >> 1 : i;
-          const bool more = i + 2 < steps;
-          const bool new_v = !(two && s == 1), new_k = more && !(two && s == 1);
-          // the value tile: cleaned first where it holds positions that some row must not see
-          const bool clean = !E4 && (it.t0 + j + 1) * kPosTile > it.see_all;
-          uint64_t* v_bar = clean ? &cleaned[vr.slot] : &full[vr.slot];
-          const uint32_t v_par = clean ? (clean_phase >> vr.slot) & 1u : vr.phase, p_par = (p_phase >> s) & 1u;
-          uint32_t rv = 1, rk = 1;
-          if (new_v) rv = mbar_try_wait(v_bar, v_par);
-          if (new_k) rk = mbar_try_wait(&full[kr.slot], kr.phase);
-          const uint32_t rp = mbar_try_wait(&p_full[2 * s], p_par);
-          if (!(rv & rk & rp)) {
-            ok = (rv || wait1(v_bar, v_par)) && (rk || wait1(&full[kr.slot], kr.phase)) &&
-                 (rp || wait1(&p_full[2 * s], p_par));
-            if (!ok) break;
-          }
-          tc_fence_after();
-          const uint64_t b = v_desc + vr.slot * kTile16;
-          // (a stream's first product starts its sum)
-#pragma unroll
-          for (int k = 0; k < kPosTile / 32; ++k)
-            mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, i >= 2 || k > 0);
-          tc_commit(&h_full[s]);
-          if (!mbar_try_wait(&p_full[2 * s + 1], p_par) && !(ok = wait1(&p_full[2 * s + 1], p_par))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int k = kPosTile / 32; k < kPosTile / 16; ++k)
-            mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, 1u);
-          p_phase ^= 1u << s;
-          if (!(two && s == 0)) {
-            tc_commit(&empty[vr.slot]);
-            if (clean) clean_phase ^= 1u << vr.slot;
-            vr.skip(2);
-          }
-          if (!more) tc_commit(&o_full[s]);
-          if (more) {
-            qk(i + 2);
-          }
-        }
-        // 2 nt tiles further
-        const uint32_t turned = start.slot + 2 * static_cast<uint32_t>(nt);
-        start.slot = turned % C::kStages;
-        start.phase ^= (turned / C::kStages) & 1u;
-        ++item;
-      }
-      if (!ok && issued) {
-        // no product in flight at exit: a commit covers everything issued before it
-        tc_commit(drain);
-        (void)mbar_wait_bounded(drain, 0, 1000000ull);
-      }
-    }
-    __syncwarp();
-  } else if (E4 ? warp >= 12 : warp == 10) {
-    if (!E4) {
-      // ===== cleaning of value tiles =====
-      // A position that a row does not see has weight zero, but zero times a
-      // NaN or an infinity is NaN: rows past the item's last position are
-      // zeroed; non-finite values at positions that only some rows see are
-      // zeroed too and the item noted (its epilogue adds them where they belong).
-      uint32_t slot = 0, phase = 0;
-      int item = 0;
-      bool ok = true;
+    if (warp == 8 || warp == 11) {
+      // ===== copies (of the first of the two warps: the walk and the queries too) =====
+      fence_proxy_async_global();
+      constexpr int kSt = E4 ? C::kRawStages : C::kStages;
+      constexpr int kBytes = E4 ? C::kRawBytes : C::kTileBytes;
+      constexpr int kRowBytes = E4 ? D : 128;              // inner extent of a box
+      constexpr int kBoxes = E4 ? 1 : D / 64;
+      uint64_t* bar_full = E4 ? raw_full : full;
+      uint64_t* bar_empty = E4 ? raw_empty : empty;
+      uint8_t* ring = smem + (E4 ? C::kRaw : C::kRing);
+      const int nb = kPosTile / p.box_rows;                // boxes per tile along the positions
+      const int part = warp == 8 ? 0 : 1;                  // copies part, part + 2, ... of a tile
+      const int mine = 2 * lane + part;
+      int slot = 0;
+      uint32_t phase = 0, items = 0;
+      TileWalk w;
       Piece it;
-      while (ok && next_piece(it)) {
-        for (int j = it.t0; j < it.t1 && ok; ++j) {
-          // (every fill is seen in order)
-          if (!(ok = wait(&full[slot], phase))) break;
-          if (lane == 0) mbar_arrive(&empty[slot]);
-          if (++slot == C::kStages) slot = 0, phase ^= 1u;
-          if (!(ok = wait(&full[slot], phase))) break;
-          if ((j + 1) * kPosTile > it.see_all) {
-            uint8_t* v = smem + C::kRing + slot * C::kTileBytes;
-            const int from = max(it.see_all - j * kPosTile, 0);
-            const int to = min(max(it.see_end - j * kPosTile, from), kPosTile);
-            bool nf = false;
+      bool more = part == 0 && tile_begin(p, w, plan, lane), stop = false;
+      while (!stop) {
+        if (part == 1) {
+          if (!next_piece(it)) break;
+        } else {
+          // tell the piece (one that holds no tile of its item is left out)
+          const int e = told_n % kPieces;
+          it.t0 = it.t1 = 0;
+          while (more) {
+            piece_of(p, w, it);
+            if (it.t1 > it.t0) break;
+            more = tile_next(p, w);
+          }
+          if (!wait(&piece_empty[e], ((told_n / kPieces) & 1u) ^ 1u)) break;
+          if (lane == 0) {
+            const int* from = reinterpret_cast<const int*>(&it);
+#pragma unroll
+            for (int i = 0; i < kPieceInts; ++i) told[e * kPieceInts + i] = from[i];
+            mbar_arrive(&piece_full[e]);
+          }
+          __syncwarp();
+          ++told_n;
+          if (!more) break;
+        }
+        const int32_t* table = p.paged ? p.b.page_table + it.b * p.b.table_stride : nullptr;
+        auto page_of = [&](int u) {   // page of box u of the sequence
+          return p.paged && u * p.box_rows < it.see_end ? table[(u * p.box_rows) >> p.page_shift] : 0;
+        };
+        bool q_due = !E4 && p.q_tma && part == 0;
+        int c0 = it.t0 * nb;
+        int ids = page_of(c0 + lane);
+        for (int j = it.t0; j < it.t1 && !stop; ++j) {
+          if (j * nb >= c0 + 32) {
+            c0 += 32;
+            ids = page_of(c0 + lane);
+          }
+          if (p.paged && part == 0 && (ids < 0 || ids >= p.c.num_pages))
+            record_status(p.status, EPILORA_ERR_INVALID_ARG);
+          const int held = min(max(it.see_end - j * kPosTile, 0), kPosTile);           // rows some row of the item sees
+          const int boxes = p.paged ? (held + p.box_rows - 1) / p.box_rows : (held > 0 ? 1 : 0);
+          const int copies = (boxes * kBoxes + 1 - part) / 2;                           // of this warp
+          // box `mine` of the tile: rows i, columns x
+          const int i = mine / kBoxes, x = mine % kBoxes;
+          const int pg = __shfl_sync(0xffffffffu, ids, min(j * nb + i - c0, 31));
+          const int pos = j * kPosTile + i * p.box_rows;
+          // a page index out of range, and rows past the packed array, read as zeros
+          const int y = p.paged ? pos & (p.c.page_size - 1) : it.first + pos;
 #pragma unroll 1
-            for (int x = 0; x < D / 64; ++x) {
-              uint4* q = reinterpret_cast<uint4*>(v + x * C::kBlock);
-              for (int i = to * 8 + lane; i < kPosTile * 8; i += 32) q[i] = make_uint4(0, 0, 0, 0);
-              for (int i0 = from * 8 + lane; i0 < to * 8; i0 += 128) {
-                uint4 u[4];
-                bool any = false;
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!wait(&bar_empty[slot], phase ^ 1u)) {
+              stop = true;
+              break;
+            }
+            uint8_t* dst = ring + slot * kBytes;
+            if (lane == 0) {
+              if (copies > 0)
+                mbar_arrive_expect_tx(&bar_full[slot], copies * p.box_rows * kRowBytes);
+              else
+                mbar_arrive(&bar_full[slot]);
+            }
+            __syncwarp();
+            if (lane < copies)
+              tma_load_4d(dst + x * C::kBlock + i * p.box_rows * kRowBytes, kv ? &p.tv : &p.tk, &bar_full[slot],
+                          x * kRowBytes, y, it.h, p.paged ? pg : 0);
+            __syncwarp();
+            if (++slot == kSt) slot = 0, phase ^= 1u;
+          }
+          if (!E4 && q_due && !stop) {
+            // the queries, behind the first tile (by then the last piece's products are about to have read theirs)
+            q_due = false;
+            if (!wait(q_free, (items & 1u) ^ 1u)) {
+              stop = true;
+            } else if (lane == 0) {
+              const int tiles = it.two() ? 2 : 1;
+              mbar_arrive_expect_tx(q_full, tiles * C::kTileBytes);
+              for (int t = 0; t < tiles; ++t)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) u[k] = i0 + 32 * k < to * 8 ? q[i0 + 32 * k] : make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < D / 64; ++c)
+                  tma_load_4d(smem + t * C::kTileBytes + c * C::kBlock, &p.tq, q_full, c * 128, it.h * p.group,
+                              it.first + token_of(p, it.row0 + t * kRowTile), 0);
+            }
+            __syncwarp();
+            ++items;
+          }
+        }
+        if (part == 0) more = tile_next(p, w);
+      }
+      if (*abort_flag && lane == 0) {
+        // no copy in flight at exit
+        for (int i = 0; i < kSt; ++i)
+          (void)mbar_wait_bounded(&bar_full[i], i < slot ? phase : phase ^ 1u, 1000000ull);
+        if (!E4 && p.q_tma && items > 0) (void)mbar_wait_bounded(q_full, (items - 1) & 1u, 1000000ull);
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // ===== products =====
+      // A stream takes S = Q K^T of a tile, then (the weights having gone over
+      // the scores) O += P V, then the next tile's S; the streams in turn. One
+      // lane does it all, its products run in order, so no S is overwritten
+      // early. A wait takes some 100 cycles even where its barrier is ready (130
+      // for a whole warp), the products between two of them 256 or 512: a step's
+      // barriers are therefore tried together and waited for one by one only
+      // where one is not ready. (A lane per stream instead took a sixth
+      // longer for a prompt of 8192 x 64 heads: the streams then fall into
+      // step, and the products wait for the softmax of both.)
+      if (elect_one()) {
+        constexpr uint32_t kIdQK = idesc_f16(128, 128, !E4, false);
+        constexpr uint32_t kIdPV = idesc_f16(128, D, !E4, true);
+        const uint64_t q_desc = make_smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+        const uint64_t k_desc = make_smem_desc(smem_u32(smem + C::kRing), 16, 1024, kSwizzle128B);
+        const uint64_t v_desc = make_smem_desc(smem_u32(smem + C::kRing), C::kBlock, 1024, kSwizzle128B);
+        constexpr uint32_t kTile16 = C::kTileBytes >> 4;
+        struct Ring {
+          uint32_t slot, phase;
+          __device__ __forceinline__ void skip(uint32_t n) {
+            slot += n;
+            if (slot >= C::kStages) slot -= C::kStages, phase ^= 1u;
+          }
+        };
+        Ring start{0, 0};                  // ring position (keys and values alternating) of the piece's first tile
+        uint32_t clean_phase = 0;          // a bit per stage
+        uint32_t item = 0, p_phase = 0;    // p_phase: bit s for stream s
+        bool ok = true, issued = false;
+        auto wait1 = [&](uint64_t* bar, uint32_t parity) {
+          const uint64_t t0 = globaltimer_ns();
+          for (uint32_t polls = 1;; ++polls) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((polls & 63u) == 0u && (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs)) break;
+          }
+          *abort_flag = 1;
+          record_status(p.status, EPILORA_ERR_TIMEOUT);
+          return false;
+        };
+        while (ok) {
+          // the piece
+          const int e = told_n % kPieces;
+          if (!(ok = wait1(&piece_full[e], (told_n / kPieces) & 1u))) break;
+          Piece it;
+          int* to = reinterpret_cast<int*>(&it);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  any |= bf16x2_nonfinite(u[k].x) | bf16x2_nonfinite(u[k].y) | bf16x2_nonfinite(u[k].z) |
-                         bf16x2_nonfinite(u[k].w);
-                if (any) {
-                  nf = true;
+          for (int i = 0; i < kPieceInts; ++i) to[i] = told[e * kPieceInts + i];
+          mbar_arrive(&piece_empty[e]);
+          ++told_n;
+          const int nt = it.t1 - it.t0;
+          if (nt <= 0) break;
+          const bool two = it.two();
+          const int steps = two ? 2 * nt : nt;
+          // position tile of a step: i / 2 with two row tiles, else i
+          Ring kr = start, vr = start;     // keys and values of the next step's tile
+          vr.skip(1);
+          // scores of step i (of stream i % 2)
+          auto qk = [&](int i) {
+            const int s = i & 1;
+            const uint64_t a = q_desc + (two && s == 1 ? kTile16 : 0), b = k_desc + kr.slot * kTile16;
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    uint32_t e[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((k / 4) * C::kBlock + (k % 4) * 32) >> 4;
+              mma_f16_ss(tm_s + s * 128, a + off, b + off, kIdQK, k > 0);
+            }
+            tc_commit(&s_full[s]);
+            if (!(two && s == 0)) {
+              tc_commit(&empty[kr.slot]);
+              kr.skip(2);
+            }
+            if (i + 1 == steps) tc_commit(q_free);
+          };
+          ok = wait1(q_full, item & 1u) && wait1(&full[kr.slot], kr.phase);
+          if (!ok) break;
+          tc_fence_after();
+          qk(0);
+          issued = true;
+          if (steps > 1) {
+            if (!two && !(ok = wait1(&full[kr.slot], kr.phase))) break;
+            tc_fence_after();
+            qk(1);
+          }
+          static_assert(C::kStages >= 4, "the next keys are waited for before this step's values are read");
+#pragma unroll 1
+          for (int i = 0; i < steps; ++i) {
+            const int s = i & 1, j = two ? i >> 1 : i;
+            const bool more = i + 2 < steps;
+            const bool new_v = !(two && s == 1), new_k = more && !(two && s == 1);
+            // the value tile: cleaned first where it holds positions that some row must not see
+            const bool clean = !E4 && (it.t0 + j + 1) * kPosTile > it.see_all;
+            uint64_t* v_bar = clean ? &cleaned[vr.slot] : &full[vr.slot];
+            const uint32_t v_par = clean ? (clean_phase >> vr.slot) & 1u : vr.phase, p_par = (p_phase >> s) & 1u;
+            uint32_t rv = 1, rk = 1;
+            if (new_v) rv = mbar_try_wait(v_bar, v_par);
+            if (new_k) rk = mbar_try_wait(&full[kr.slot], kr.phase);
+            const uint32_t rp = mbar_try_wait(&p_full[2 * s], p_par);
+            if (!(rv & rk & rp)) {
+              ok = (rv || wait1(v_bar, v_par)) && (rk || wait1(&full[kr.slot], kr.phase)) &&
+                   (rp || wait1(&p_full[2 * s], p_par));
+              if (!ok) break;
+            }
+            tc_fence_after();
+            const uint64_t b = v_desc + vr.slot * kTile16;
+            // (a stream's first product starts its sum)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                      if ((e[y] & 0x7F80u) == 0x7F80u) e[y] &= 0xFFFF0000u;
-                      if ((e[y] & 0x7F800000u) == 0x7F800000u) e[y] &= 0xFFFFu;
+            for (int k = 0; k < kPosTile / 32; ++k)
+              mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, i >= 2 || k > 0);
+            tc_commit(&h_full[s]);
+            if (!mbar_try_wait(&p_full[2 * s + 1], p_par) && !(ok = wait1(&p_full[2 * s + 1], p_par))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = kPosTile / 32; k < kPosTile / 16; ++k)
+              mma_f16_ts(tm_o + s * D, tm_s + s * 128 + k * 8, b + (k * 2048 >> 4), kIdPV, 1u);
+            p_phase ^= 1u << s;
+            if (!(two && s == 0)) {
+              tc_commit(&empty[vr.slot]);
+              if (clean) clean_phase ^= 1u << vr.slot;
+              vr.skip(2);
+            }
+            if (!more) tc_commit(&o_full[s]);
+            if (more) {
+              qk(i + 2);
+            }
+          }
+          // 2 nt tiles further
+          const uint32_t turned = start.slot + 2 * static_cast<uint32_t>(nt);
+          start.slot = turned % C::kStages;
+          start.phase ^= (turned / C::kStages) & 1u;
+          ++item;
+        }
+        if (!ok && issued) {
+          // no product in flight at exit: a commit covers everything issued before it
+          tc_commit(drain);
+          (void)mbar_wait_bounded(drain, 0, 1000000ull);
+        }
+      }
+      __syncwarp();
+    } else if (E4 ? warp >= 12 : warp == 10) {
+      if (!E4) {
+        // ===== cleaning of value tiles =====
+        // A position that a row does not see has weight zero, but zero times a
+        // NaN or an infinity is NaN: rows past the item's last position are
+        // zeroed; non-finite values at positions that only some rows see are
+        // zeroed too and the item noted (its epilogue adds them where they belong).
+        uint32_t slot = 0, phase = 0;
+        int item = 0;
+        bool ok = true;
+        Piece it;
+        while (ok && next_piece(it)) {
+          for (int j = it.t0; j < it.t1 && ok; ++j) {
+            // (every fill is seen in order)
+            if (!(ok = wait(&full[slot], phase))) break;
+            if (lane == 0) mbar_arrive(&empty[slot]);
+            if (++slot == C::kStages) slot = 0, phase ^= 1u;
+            if (!(ok = wait(&full[slot], phase))) break;
+            if ((j + 1) * kPosTile > it.see_all) {
+              uint8_t* v = smem + C::kRing + slot * C::kTileBytes;
+              const int from = max(it.see_all - j * kPosTile, 0);
+              const int to = min(max(it.see_end - j * kPosTile, from), kPosTile);
+              bool nf = false;
+#pragma unroll 1
+              for (int x = 0; x < D / 64; ++x) {
+                uint4* q = reinterpret_cast<uint4*>(v + x * C::kBlock);
+                for (int i = to * 8 + lane; i < kPosTile * 8; i += 32) q[i] = make_uint4(0, 0, 0, 0);
+                for (int i0 = from * 8 + lane; i0 < to * 8; i0 += 128) {
+                  uint4 u[4];
+                  bool any = false;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) u[k] = i0 + 32 * k < to * 8 ? q[i0 + 32 * k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    any |= bf16x2_nonfinite(u[k].x) | bf16x2_nonfinite(u[k].y) | bf16x2_nonfinite(u[k].z) |
+                           bf16x2_nonfinite(u[k].w);
+                  if (any) {
+                    nf = true;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      uint32_t e[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                      for (int y = 0; y < 4; ++y) {
+                        if ((e[y] & 0x7F80u) == 0x7F80u) e[y] &= 0xFFFF0000u;
+                        if ((e[y] & 0x7F800000u) == 0x7F800000u) e[y] &= 0xFFFFu;
+                      }
+                      if (i0 + 32 * k < to * 8) q[i0 + 32 * k] = make_uint4(e[0], e[1], e[2], e[3]);
                     }
-                    if (i0 + 32 * k < to * 8) q[i0 + 32 * k] = make_uint4(e[0], e[1], e[2], e[3]);
                   }
                 }
               }
+              if (nf) nf_item[item & 7] = item + 1;
+              fence_proxy_async_smem();
+              __threadfence_block();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&cleaned[slot]);
             }
-            if (nf) nf_item[item & 7] = item + 1;
-            fence_proxy_async_smem();
-            __threadfence_block();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&cleaned[slot]);
-          }
-          if (lane == 0) mbar_arrive(&empty[slot]);
-          if (++slot == C::kStages) slot = 0, phase ^= 1u;
-        }
-        ++item;
-      }
-    } else {
-      // ===== E4M3 codes to fp16 tiles =====
-      const int t = (warp - 12) * 32 + lane;
-      uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
-      int item = 0;
-      bool ok = true;
-      Piece it;
-      while (ok && next_piece(it)) {
-        for (int j = it.t0; j < it.t1 && ok; ++j) {
-          const int from = max(it.see_all - j * kPosTile, 0);
-          const int to = min(max(it.see_end - j * kPosTile, 0), kPosTile);
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            ok = wait(&raw_full[rslot], rphase) && wait(&empty[slot], phase ^ 1u);
-            if (!ok) break;
-            const uint8_t* src = smem + C::kRaw + rslot * C::kRawBytes;
-            uint8_t* dst = smem + C::kRing + slot * C::kTileBytes;
-            bool nf = false;
-            const bool clean = kv == 1 && from < kPosTile;
-            // A thread takes 16-code chunk c of the rows r0, r0 + kStep, ...: chunks
-            // 2c and 2c + 1 of the 16-bit row's 16-byte chunks, swizzled alike in
-            // all of its rows (kStep is a multiple of 8). The two halves of a
-            // 128-element row store theirs in opposite order, so that they use
-            // different banks.
-            constexpr int kPer = D / 16, kStep = 128 / kPer;
-            const int r0 = t / kPer, c = t % kPer, first = (c / 4) & 1;
-            uint8_t* row_at = dst + (c / 4) * C::kBlock + r0 * 128;
-            const uint32_t at0 = (((c % 4) * 2 + first) ^ (r0 & 7)) * 16, at1 = at0 ^ 16u;
-            auto store = [&](int y, const uint4& u) {
-              uint4 lo, hi;
-              lo.x = e4m3x2_to_f16x2(u.x), lo.y = e4m3x2_to_f16x2(u.x >> 16);
-              lo.z = e4m3x2_to_f16x2(u.y), lo.w = e4m3x2_to_f16x2(u.y >> 16);
-              hi.x = e4m3x2_to_f16x2(u.z), hi.y = e4m3x2_to_f16x2(u.z >> 16);
-              hi.z = e4m3x2_to_f16x2(u.w), hi.w = e4m3x2_to_f16x2(u.w >> 16);
-              *reinterpret_cast<uint4*>(row_at + at0 + y * kStep * 128) = first ? hi : lo;
-              *reinterpret_cast<uint4*>(row_at + at1 + y * kStep * 128) = first ? lo : hi;
-            };
-            const uint4* codes = reinterpret_cast<const uint4*>(src) + t;
-            if (!clean) {
-              // (no branch in the body: its loads and conversions overlap)
-#pragma unroll 1
-              for (int y = 0; y < kPer; y += 4) {
-                uint4 u[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) u[k] = codes[(y + k) * 128];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) store(y + k, u[k]);
-              }
-            } else {
-#pragma unroll 1
-              for (int y = 0; y < kPer; ++y) {
-                uint4 u = codes[y * 128];
-                const int row = r0 + y * kStep;
-                if (row >= to) {
-                  u = make_uint4(0, 0, 0, 0);
-                } else if (row >= from && (e4m3x4_nan(u.x) | e4m3x4_nan(u.y) | e4m3x4_nan(u.z) | e4m3x4_nan(u.w))) {
-                  nf = true;
-                  u.x = e4m3x4_strip_nan(u.x), u.y = e4m3x4_strip_nan(u.y);
-                  u.z = e4m3x4_strip_nan(u.z), u.w = e4m3x4_strip_nan(u.w);
-                }
-                store(y, u);
-              }
-            }
-            if (nf) nf_item[item & 7] = item + 1;
-            fence_proxy_async_smem();
-            __threadfence_block();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&full[slot]);
-              mbar_arrive(&raw_empty[rslot]);
-            }
+            if (lane == 0) mbar_arrive(&empty[slot]);
             if (++slot == C::kStages) slot = 0, phase ^= 1u;
-            if (++rslot == C::kRawStages) rslot = 0, rphase ^= 1u;
           }
+          ++item;
         }
-        ++item;
+      } else {
+        // ===== E4M3 codes to fp16 tiles =====
+        const int t = (warp - 12) * 32 + lane;
+        uint32_t slot = 0, phase = 0, rslot = 0, rphase = 0;
+        int item = 0;
+        bool ok = true;
+        Piece it;
+        while (ok && next_piece(it)) {
+          for (int j = it.t0; j < it.t1 && ok; ++j) {
+            const int from = max(it.see_all - j * kPosTile, 0);
+            const int to = min(max(it.see_end - j * kPosTile, 0), kPosTile);
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+              ok = wait(&raw_full[rslot], rphase) && wait(&empty[slot], phase ^ 1u);
+              if (!ok) break;
+              const uint8_t* src = smem + C::kRaw + rslot * C::kRawBytes;
+              uint8_t* dst = smem + C::kRing + slot * C::kTileBytes;
+              bool nf = false;
+              const bool clean = kv == 1 && from < kPosTile;
+              // A thread takes 16-code chunk c of the rows r0, r0 + kStep, ...: chunks
+              // 2c and 2c + 1 of the 16-bit row's 16-byte chunks, swizzled alike in
+              // all of its rows (kStep is a multiple of 8). The two halves of a
+              // 128-element row store theirs in opposite order, so that they use
+              // different banks.
+              constexpr int kPer = D / 16, kStep = 128 / kPer;
+              const int r0 = t / kPer, c = t % kPer, first = (c / 4) & 1;
+              uint8_t* row_at = dst + (c / 4) * C::kBlock + r0 * 128;
+              const uint32_t at0 = (((c % 4) * 2 + first) ^ (r0 & 7)) * 16, at1 = at0 ^ 16u;
+              auto store = [&](int y, const uint4& u) {
+                uint4 lo, hi;
+                lo.x = e4m3x2_to_f16x2(u.x), lo.y = e4m3x2_to_f16x2(u.x >> 16);
+                lo.z = e4m3x2_to_f16x2(u.y), lo.w = e4m3x2_to_f16x2(u.y >> 16);
+                hi.x = e4m3x2_to_f16x2(u.z), hi.y = e4m3x2_to_f16x2(u.z >> 16);
+                hi.z = e4m3x2_to_f16x2(u.w), hi.w = e4m3x2_to_f16x2(u.w >> 16);
+                *reinterpret_cast<uint4*>(row_at + at0 + y * kStep * 128) = first ? hi : lo;
+                *reinterpret_cast<uint4*>(row_at + at1 + y * kStep * 128) = first ? lo : hi;
+              };
+              const uint4* codes = reinterpret_cast<const uint4*>(src) + t;
+              if (!clean) {
+                // (no branch in the body: its loads and conversions overlap)
+#pragma unroll 1
+                for (int y = 0; y < kPer; y += 4) {
+                  uint4 u[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) u[k] = codes[(y + k) * 128];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) store(y + k, u[k]);
+                }
+              } else {
+#pragma unroll 1
+                for (int y = 0; y < kPer; ++y) {
+                  uint4 u = codes[y * 128];
+                  const int row = r0 + y * kStep;
+                  if (row >= to) {
+                    u = make_uint4(0, 0, 0, 0);
+                  } else if (row >= from && (e4m3x4_nan(u.x) | e4m3x4_nan(u.y) | e4m3x4_nan(u.z) | e4m3x4_nan(u.w))) {
+                    nf = true;
+                    u.x = e4m3x4_strip_nan(u.x), u.y = e4m3x4_strip_nan(u.y);
+                    u.z = e4m3x4_strip_nan(u.z), u.w = e4m3x4_strip_nan(u.w);
+                  }
+                  store(y, u);
+                }
+              }
+              if (nf) nf_item[item & 7] = item + 1;
+              fence_proxy_async_smem();
+              __threadfence_block();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&full[slot]);
+                mbar_arrive(&raw_empty[rslot]);
+              }
+              if (++slot == C::kStages) slot = 0, phase ^= 1u;
+              if (++rslot == C::kRawStages) rslot = 0, rphase ^= 1u;
+            }
+          }
+          ++item;
+        }
       }
     }
-  }
   } else {
     // ===== softmax =====
     setmaxnreg_inc<TileWarps<E4>::kSoftmax>();
@@ -1012,7 +1017,8 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
         const uint32_t flip = s_eff < 0.0f ? 0x80008000u : 0u;
         uint4 u[D / 8];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) u[i] = use ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < D / 8; ++i)
+          u[i] = use ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
         if (E4) {
           // fp16 queries: bf16's 8 significant bits fit; the row is scaled by
           // the power of two that puts its largest element near 2^13
@@ -1116,7 +1122,8 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
             st_global_v8(at + 16, v + 8);
           } else {
 #pragma unroll
-            for (int q = 0; q < 16; q += 4) *reinterpret_cast<uint4*>(at + 2 * q) = make_uint4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+            for (int q = 0; q < 16; q += 4)
+              *reinterpret_cast<uint4*>(at + 2 * q) = make_uint4(v[q], v[q + 1], v[q + 2], v[q + 3]);
           }
         };
         auto put_lse = [&](float mc, float sum) {
@@ -1177,7 +1184,8 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
           } else {
 #pragma unroll
             for (int q = 0; q < 32; q += 4)
-              part[2 * kItemRows / 4 + (i + q) / 4 * kItemRows + prow] = make_float4(a[q], a[q + 1], a[q + 2], a[q + 3]);
+              part[2 * kItemRows / 4 + (i + q) / 4 * kItemRows + prow] =
+                  make_float4(a[q], a[q + 1], a[q + 2], a[q + 3]);
           }
         }
         const float mc = m == -INFINITY ? -INFINITY : m * c;

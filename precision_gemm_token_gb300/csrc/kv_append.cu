@@ -59,7 +59,8 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
 }
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 3;      // rows of a thread under way; more cost blocks per SM (39, 45, 56 us with 3, 4, 5 for 8044 tokens, 48 rows)
+// rows of a thread under way; more cost blocks per SM (39, 45, 56 us with 3, 4, 5 for 8044 tokens, 48 rows)
+constexpr int kBatch = 3;
 
 template <int D, bool E4>
 __global__ void __launch_bounds__(kThreads, 7) kv_append_kernel(const __grid_constant__ AppendParams p) {

@@ -1239,30 +1239,40 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
             auto piece = [&](int k) {
               return p.partials + static_cast<int64_t>(k == 0 ? it.slot0 : 2 * (first + k)) * kPart;
             };
-            float top = -INFINITY;
-            for (int k = 0; k < pieces; ++k) top = fmaxf(top, __ldcg(reinterpret_cast<const float*>(piece(k)) + prow));
-            const float base = top == -INFINITY ? 0.0f : top;
-            float sum = 0.0f;
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
             for (int k = 0; k < pieces; ++k) {
               const float* f = reinterpret_cast<const float*>(piece(k));
-              sum += __ldcg(f + kItemRows + prow) * exp2_approx(__ldcg(f + prow) - base);
+              const float mk = __ldcg(f + prow), lk = __ldcg(f + kItemRows + prow);
+              const float up = fmaxf(top, mk), to = up == -INFINITY ? 0.0f : up;
+              sum = sum * exp2_approx(top - to) + lk * exp2_approx(mk - to);
+              top = up;
             }
+            const float base = top == -INFINITY ? 0.0f : top;
             const float inv = vscale / sum;
+            // 64 columns of a piece at a time: the loads are what a join waits for (four prompts of 37 new tokens,
+            // cut into ten pieces each: 32.0 us with 32 columns at a time, 29.4 so)
 #pragma unroll 1
-            for (int i = 0; i < D; i += 32) {
-              float a[32];
+            for (int i = 0; i < D; i += 64) {
+              float a[64];
 #pragma unroll
-              for (int q = 0; q < 32; ++q) a[q] = 0.0f;
+              for (int q = 0; q < 64; ++q) a[q] = 0.0f;
+#pragma unroll 1
               for (int k = 0; k < pieces; ++k) {
                 const float4* f = piece(k);
-                const float wk = exp2_approx(__ldcg(reinterpret_cast<const float*>(f) + prow) - base);
+                const float mk = __ldcg(reinterpret_cast<const float*>(f) + prow);
+                float4 x[16];
 #pragma unroll
-                for (int q = 0; q < 32; q += 4) {
-                  const float4 v = __ldcg(f + 2 * kItemRows / 4 + (i + q) / 4 * kItemRows + prow);
-                  a[q] += v.x * wk, a[q + 1] += v.y * wk, a[q + 2] += v.z * wk, a[q + 3] += v.w * wk;
+                for (int q = 0; q < 16; ++q) x[q] = __ldcg(f + 2 * kItemRows / 4 + (i / 4 + q) * kItemRows + prow);
+                const float wk = exp2_approx(mk - base);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                  a[4 * q] += x[q].x * wk, a[4 * q + 1] += x[q].y * wk;
+                  a[4 * q + 2] += x[q].z * wk, a[4 * q + 3] += x[q].w * wk;
                 }
               }
               put(i, a, inv, sum == 0.0f);
+              put(i + 32, a + 32, inv, sum == 0.0f);
             }
             put_lse(top, sum);
           }

@@ -518,8 +518,9 @@ EPILORA_API int epilora_kv_append(const epilora_kv_cache* cache, const epilora_k
  * several thread blocks share). It depends on the device's number of SMs and
  * on head_dim only, so one workspace serves every layer and step of a model.
  * Zero-fill it once after allocating it; calls leave it ready for the next
- * one. Calls that share a workspace must be ordered on one stream. Returns 0
- * for a head_dim other than 64 or 128.
+ * one (after a call that recorded EPILORA_ERR_TIMEOUT, zero it again). Calls
+ * that share a workspace must be ordered on one stream. Returns 0 for a
+ * head_dim other than 64 or 128.
  */
 EPILORA_API size_t epilora_attention_workspace_bytes(int head_dim);
 
@@ -536,6 +537,12 @@ EPILORA_API size_t epilora_attention_workspace_bytes(int head_dim);
  * zero, its lse -infinity. What a masked position, a page's unused rows or
  * an unused page hold never reaches a result, NaN and infinities included.
  * scale is finite.
+ * Kernels: one for the sequences whose new tokens times G are at most 16
+ * rows; where max_new * G may exceed that, a second one for the others, which
+ * starts as the first one's blocks end. Programmatic dependents of the
+ * previous kernel on the stream, like epilora_kv_append. The results of a call
+ * are the same from run to run. n_tokens * heads has to stay below 2^30
+ * (EPILORA_ERR_UNSUPPORTED); n_tokens == 0 is a no-op.
  */
 EPILORA_API int epilora_paged_attention(const epilora_kv_cache* cache, const epilora_kv_batch* batch, int heads,
                       const void* Q, int64_t q_token_stride, int64_t q_head_stride, float scale,
@@ -547,6 +554,7 @@ EPILORA_API int epilora_paged_attention(const epilora_kv_cache* cache, const epi
  * the projection: prompt b is the packed rows q_start[b] .. q_start[b+1] - 1
  * of Q, K and V; row i of a prompt attends to its rows 0 .. i. Results and
  * conventions as epilora_paged_attention (q_start as in epilora_kv_batch).
+ * One kernel.
  */
 EPILORA_API int epilora_prompt_attention(int n_seqs, int n_tokens, const int32_t* q_start,
                       int heads, int kv_heads, int head_dim,

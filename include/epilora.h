@@ -538,8 +538,9 @@ EPILORA_API size_t epilora_attention_workspace_bytes(int head_dim);
  * an unused page hold never reaches a result, NaN and infinities included.
  * scale is finite.
  * Kernels: one for the sequences whose new tokens times G are at most 16
- * rows; where max_new * G may exceed that, a second one for the others, which
- * starts as the first one's blocks end. Programmatic dependents of the
+ * rows; where max_new * G exceeds that, a second one for the others, which
+ * starts as the first one's blocks end, or alone where n_tokens is
+ * n_seqs * max_new. Programmatic dependents of the
  * previous kernel on the stream, like epilora_kv_append. The results of a call
  * are the same from run to run. n_tokens * heads has to stay below 2^30
  * (EPILORA_ERR_UNSUPPORTED); n_tokens == 0 is a no-op.

@@ -51,9 +51,11 @@ __host__ __device__ inline bool attn_decode_takes(int n, int group) { return n <
 int launch_attn_decode(const AttnArgs& a, uint32_t* counters, float* partials);
 size_t attn_decode_counter_bytes();
 size_t attn_decode_partial_bytes(int head_dim);
-// attn_tile.cu: the other sequences of a call over the cache; all of a call
-// over packed prompts, and its packed rows of no prompt.
-int launch_attn_tile(const AttnArgs& a, uint32_t* counters, float* partials);
+// attn_tile.cu: the other sequences of a call over the cache, behind the
+// decode kernel; alone: all sequences of a call, over the cache or packed
+// prompts, and the packed rows of none.
+bool attn_tile_fits(const AttnArgs& a);   // the line's units are counted in 32 bits
+int launch_attn_tile(const AttnArgs& a, bool alone, uint32_t* counters, float* partials);
 size_t attn_tile_counter_bytes();
 size_t attn_tile_partial_bytes(int head_dim);
 

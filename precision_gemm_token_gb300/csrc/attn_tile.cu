@@ -96,6 +96,7 @@ struct TileParams {
   AttnOut o;
   float* lse;
   int paged;
+  int alone;               // no decode kernel before this one: every sequence is taken
   int heads, kv_heads, group;
   uint32_t group_mul;      // row / group = row * group_mul >> group_shift for rows below 2^30
   int group_shift;
@@ -127,9 +128,10 @@ __device__ __forceinline__ TileSeq tile_seq(const TileParams& p, int b, bool& ba
   if (p.paged) {
     const int len = p.b.kv_len[b];
     const int cap = p.b.table_pages << p.page_shift;
+    if (len > cap || len < 0 || r.n > p.b.max_new) bad = true;
     s.base = len - r.n;
     s.len = max(min(len, cap), 0);
-    s.rts = attn_decode_takes(r.n, p.group) ? 0 : (r.n * p.group + kItemRows - 1) / kItemRows;
+    s.rts = !p.alone && attn_decode_takes(r.n, p.group) ? 0 : (r.n * p.group + kItemRows - 1) / kItemRows;
   } else {
     s.base = 0;
     s.len = r.n;
@@ -528,10 +530,10 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
   // Behind the decode kernel of a call over the cache: that kernel let this one
   // start once the kernels before it had completed; its own results are not
   // read here, only its completion is waited for at the end.
-  if (!p.paged) pdl_wait_primary();
+  if (p.alone) pdl_wait_primary();
 
-  // packed rows of no sequence are zero (the decode kernel's part of a call over the cache)
-  if (!p.paged) {
+  // packed rows of no sequence are zero (the decode kernel's part where there is one)
+  if (p.alone) {
     const int used = p.b.n_seqs > 0 ? min(max(p.b.q_start[p.b.n_seqs], 0), p.b.n_tokens) : 0;
     const int64_t rows = static_cast<int64_t>(p.b.n_tokens - used) * p.heads;
     constexpr int V = D / 8;
@@ -1292,7 +1294,7 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (p.paged) pdl_wait_primary();
+  if (!p.alone) pdl_wait_primary();
 }
 
 // Whether a tile's 128 rows are a box [tokens][group heads] of the queries, to
@@ -1365,13 +1367,15 @@ size_t attn_tile_partial_bytes(int head_dim) {
   return static_cast<size_t>(2 * n) * (2 + head_dim) * kItemRows * sizeof(float);
 }
 
-int launch_attn_tile(const AttnArgs& a, uint32_t* counters, float* partials) {
-  // the line's units are counted in 32 bits
+bool attn_tile_fits(const AttnArgs& a) {
   const double longest =
       a.paged ? static_cast<double>(a.batch.table_pages) * a.cache.page_size : static_cast<double>(a.batch.n_tokens);
   const double items = static_cast<double>(a.batch.n_tokens) * a.heads / kItemRows +
                        static_cast<double>(a.batch.n_seqs) * a.cache.kv_heads;
-  if (items * (longest / kPosTile + 1 + kItemCost) >= 4e9) return EPILORA_ERR_UNSUPPORTED;
+  return items * (longest / kPosTile + 1 + kItemCost) < 4e9;
+}
+
+int launch_attn_tile(const AttnArgs& a, bool alone, uint32_t* counters, float* partials) {
   TileParams p{};
   p.b = a.batch;
   p.c = a.cache;
@@ -1381,6 +1385,7 @@ int launch_attn_tile(const AttnArgs& a, uint32_t* counters, float* partials) {
   p.o = a.o;
   p.lse = a.lse;
   p.paged = a.paged;
+  p.alone = alone;
   p.heads = a.heads;
   p.kv_heads = a.cache.kv_heads;
   p.group = a.heads / a.cache.kv_heads;

@@ -116,6 +116,22 @@ def test_max_new_selects_no_results():
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_full_batches(fmt):
+    """As many packed tokens as the bound allows, n_seqs * max_new: chunks of
+    one length, and the same sizes where rows are padding and the sequences
+    shorter, single tokens and empty ones among them."""
+    check(Batch([(37, 300), (37, 37), (37, 1000)], 8, 2, 128, fmt=fmt, seed=4))
+    for seqs, most, dim in (([(1, 100), (0, 50), (20, 300), (2, 2)], 20, 128), ([(3, 700)], 40, 64), ([(0, 9)], 40, 64),
+                            ([(1, 5), (6, 4)], 33, 128)):
+        b = Batch(seqs, 8, 2, dim, fmt=fmt, seed=7, tail=len(seqs) * most - sum(n for n, _ in seqs))
+        out, lse = torch.full_like(b.q, float("nan")).cuda(), torch.full((b.tokens, 8), float("nan"), device="cuda")
+        st = status_buf()
+        b.attend(max_new=most, out=out, lse=lse, status=st)
+        assert int(st.item()) == 0
+        assert_attention(out, lse, *b.oracle(dim ** -0.5), what=seqs, fmt=fmt)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_empty_rows(fmt):
     """More new tokens than positions (rows that see nothing), sequences of
     length zero, nothing but padding."""

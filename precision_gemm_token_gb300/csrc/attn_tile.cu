@@ -315,6 +315,8 @@ __device__ __forceinline__ void piece_of(const TileParams& p, const TileWalk& w,
   q.t0 = max(w.u0 - kItemCost, 0);
   q.t1 = max(w.u1 - kItemCost, 0);
   q.whole = q.t0 == 0 && q.t1 == w.nt;
+  q.first_cta = q.pieces = q.slot = q.slot0 = 0;
+  if (q.whole) return;
   // the blocks that hold the item's first and last tile
   const uint32_t tile0 = w.item0 + kItemCost;
   q.first_cta = static_cast<int>(w.owner_of(tile0));
@@ -532,29 +534,13 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
   // read here, only its completion is waited for at the end.
   if (p.alone) pdl_wait_primary();
 
-  // packed rows of no sequence are zero (the decode kernel's part where there is one)
-  if (p.alone) {
-    const int used = p.b.n_seqs > 0 ? min(max(p.b.q_start[p.b.n_seqs], 0), p.b.n_tokens) : 0;
-    const int64_t rows = static_cast<int64_t>(p.b.n_tokens - used) * p.heads;
-    constexpr int V = D / 8;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * V;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-      const int64_t r = i / V;
-      const int64_t t = used + r / p.heads;
-      const int h = static_cast<int>(r % p.heads);
-      *reinterpret_cast<uint4*>(p.o.p + t * p.o.ts + h * p.o.hs + (i % V) * 8) = make_uint4(0, 0, 0, 0);
-      if (p.lse != nullptr && i % V == 0) p.lse[t * p.heads + h] = -INFINITY;
-    }
-  }
-
-  tile_plan(p, plan, warp, TileWarps<E4>::kThreads / 32, lane);
-
+  // (in the shadow of the plan, whose barrier is the allocation's too)
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
+    tc_fence_before();
   }
-  tc_fence_before();
-  __syncthreads();
+  tile_plan(p, plan, warp, TileWarps<E4>::kThreads / 32, lane);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_s = tmem, tm_o = tmem + 256;   // S of stream s at tm_s + 128 s, O at tm_o + D s
@@ -982,6 +968,21 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
   } else {
     // ===== softmax =====
     setmaxnreg_inc<TileWarps<E4>::kSoftmax>();
+    if (p.alone) {
+      // packed rows of no sequence are zero (the decode kernel's part where there is one); here, before the first
+      // scores are there, it costs nothing
+      const int used = p.b.n_seqs > 0 ? min(max(p.b.q_start[p.b.n_seqs], 0), p.b.n_tokens) : 0;
+      const int64_t rows = static_cast<int64_t>(p.b.n_tokens - used) * p.heads;
+      constexpr int V = D / 8;
+      for (int64_t i = static_cast<int64_t>(blockIdx.x) * kItemRows + threadIdx.x; i < rows * V;
+           i += static_cast<int64_t>(gridDim.x) * kItemRows) {
+        const int64_t r = i / V;
+        const int64_t t = used + r / p.heads;
+        const int h = static_cast<int>(r % p.heads);
+        *reinterpret_cast<uint4*>(p.o.p + t * p.o.ts + h * p.o.hs + (i % V) * 8) = make_uint4(0, 0, 0, 0);
+        if (p.lse != nullptr && i % V == 0) p.lse[t * p.heads + h] = -INFINITY;
+      }
+    }
     const int s = warp >> 2;                       // stream
     const int r = threadIdx.x & (kRowTile - 1);    // lane of TMEM = row of the stream
     const uint32_t quad = static_cast<uint32_t>(warp & 3) << 21;   // TMEM lane 32 (warp % 4), in bits 16..

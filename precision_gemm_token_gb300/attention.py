@@ -81,8 +81,8 @@ def _workspace(workspace, q, dim, stream):
     """(address, bytes); its zero fill is ordered on the launching stream."""
     if workspace is None:
         workspace = AttentionWorkspace(q.device)
-    elif workspace.device.index is not None and workspace.device.index != q.get_device():
-        _bad("workspace: on another device")
+    elif workspace.device.index != q.get_device():
+        _bad(f"workspace: on {workspace.device}, the tensors on device {q.get_device()}")
     if stream is None:
         buf = workspace.get(dim)
     else:
@@ -138,12 +138,16 @@ class PagedKVCache:
 
 class AttentionWorkspace:
     """Caller-owned workspace of the attention calls (see
-    epilora_attention_workspace_bytes), zero-filled when first used. Calls
-    that share one have to be ordered on one stream. After a call that
-    recorded EPILORA_ERR_TIMEOUT, take a new one."""
+    epilora_attention_workspace_bytes), zero-filled when first used. `device`
+    without an index is the current one at this point. Calls that share one
+    have to be ordered on one stream. After a call that recorded
+    EPILORA_ERR_TIMEOUT, take a new one."""
 
     def __init__(self, device):
-        self.device = torch.device(device)
+        device = torch.device(device)
+        if device.type != "cuda":
+            _bad(f"workspace: a CUDA device wanted, not {device}")
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
         self._buf = {}
 
     def get(self, head_dim):

@@ -1,0 +1,37 @@
+"""Which device an attention workspace belongs to. No GPU: the current device
+and the tensors' devices are stand-ins."""
+import pytest
+import torch
+
+import precision_gemm_token_gb300 as E
+from precision_gemm_token_gb300 import attention as A
+
+
+class OnDevice:
+    """A tensor as far as the workspace looks at one."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+
+def test_device_without_an_index_is_the_current_one(monkeypatch):
+    for current in (0, 1):
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+        assert A.AttentionWorkspace("cuda").device == torch.device("cuda", current)
+        assert A.AttentionWorkspace("cuda:0").device == torch.device("cuda", 0)
+
+
+def test_workspace_of_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for made in ("cuda", "cuda:0"):
+        with pytest.raises(E.EpiloraError, match="workspace: on cuda:0"):
+            A._workspace(A.AttentionWorkspace(made), OnDevice(1), 128, None)
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+def test_other_devices_are_refused(device):
+    with pytest.raises(E.EpiloraError, match="workspace: a CUDA device"):
+        A.AttentionWorkspace(device)

@@ -516,13 +516,20 @@ EPILORA_API int epilora_kv_append(const epilora_kv_cache* cache, const epilora_k
  * Bytes of device workspace epilora_paged_attention and
  * epilora_prompt_attention need (the partial results of sequences that
  * several thread blocks share). It depends on the device's number of SMs and
- * on head_dim only, so one workspace serves every layer and step of a model.
- * Zero-fill it once after allocating it; calls leave it ready for the next
- * one (after a call that recorded EPILORA_ERR_TIMEOUT, zero it again). Calls
- * that share a workspace must be ordered on one stream. Returns 0 for a
+ * on head_dim only, so one workspace serves every layer and step of a model
+ * (head_dim 128 needs more than 64, and the larger serves both).
+ * Zero-fill its first epilora_attention_workspace_zero_bytes() bytes, or all
+ * of it, once after allocating it; calls leave it ready for the next one
+ * (after a call that recorded EPILORA_ERR_TIMEOUT, zero it again). A fill that
+ * a stream capture records is run by the graph alone: fill before the capture.
+ * Calls that share a workspace must be ordered on one stream. Returns 0 for a
  * head_dim other than 64 or 128.
  */
 EPILORA_API size_t epilora_attention_workspace_bytes(int head_dim);
+
+/* Bytes at the head of that workspace that have to be zero before a call
+ * (counters; what follows is written before it is read). */
+EPILORA_API size_t epilora_attention_workspace_zero_bytes(void);
 
 /*
  * Attention of the new tokens over the paged cache (their own keys and

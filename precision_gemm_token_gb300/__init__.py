@@ -32,6 +32,7 @@ from ._binding import (  # noqa: F401
     check,
     epilora_abi_version,
     epilora_attention_workspace_bytes,
+    epilora_attention_workspace_zero_bytes,
     epilora_gemm_lora_epilogue,
     epilora_kv_append,
     epilora_layer_forward,

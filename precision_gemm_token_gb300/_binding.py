@@ -73,6 +73,7 @@ SIGNATURES = {
     "epilora_kv_append": (_c_int, [_vp, _vp, _c_int, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _c_int,
                                    _c_int, _c_int, _vp, _i64, _i64, _vp, _vp]),
     "epilora_attention_workspace_bytes": (_sz, [_c_int]),
+    "epilora_attention_workspace_zero_bytes": (_sz, []),
     "epilora_paged_attention": (_c_int, [_vp, _vp, _c_int, _vp, _i64, _i64, _f32, _vp, _i64, _i64, _vp, _vp, _sz, _vp,
                                          _vp]),
     "epilora_prompt_attention": (_c_int, [_c_int, _c_int, _vp, _c_int, _c_int, _c_int, _vp, _i64, _i64, _vp, _i64,
@@ -244,6 +245,10 @@ def epilora_kv_append(cache: KvCache, batch: KvBatch, heads, Q, q_strides, K, k_
 
 def epilora_attention_workspace_bytes(head_dim) -> int:
     return load().epilora_attention_workspace_bytes(head_dim)
+
+
+def epilora_attention_workspace_zero_bytes() -> int:
+    return load().epilora_attention_workspace_zero_bytes()
 
 
 def epilora_paged_attention(cache: KvCache, batch: KvBatch, heads, Q, q_strides, scale, O, o_strides, lse, workspace,

@@ -77,13 +77,18 @@ def _new(q, shape, stream):
         return torch.empty(shape, dtype=_BF16, device=q.device)
 
 
-def _workspace(workspace, q, dim, stream):
-    """(address, bytes); its zero fill is ordered on the launching stream."""
+def _workspace(workspace, q, dim, raw, stream):
+    """(tensor, address, bytes), in order on the launching stream."""
     if workspace is None:
-        workspace = AttentionWorkspace(q.device)
-    elif workspace.device.index != q.get_device():
+        need = max(E.epilora_attention_workspace_bytes(dim), 256)
+        with torch.cuda.stream(stream):     # (None: the current one)
+            buf = torch.zeros(need, dtype=_U8, device=q.device)
+        return buf, buf.data_ptr(), need
+    if workspace.device.index != q.get_device():
         _bad(f"workspace: on {workspace.device}, the tensors on device {q.get_device()}")
-    if stream is None:
+    if raw not in workspace.known:
+        workspace.note(raw, stream)
+    if workspace.head is None:
         buf = workspace.get(dim)
     else:
         with torch.cuda.stream(stream):
@@ -138,24 +143,57 @@ class PagedKVCache:
 
 class AttentionWorkspace:
     """Caller-owned workspace of the attention calls (see
-    epilora_attention_workspace_bytes), zero-filled when first used. `device`
-    without an index is the current one at this point. Calls that share one
-    have to be ordered on one stream. After a call that recorded
-    EPILORA_ERR_TIMEOUT, take a new one."""
+    epilora_attention_workspace_bytes) for both head sizes, allocated and
+    zero-filled here: every stream, and every graph whether captured before or
+    after the first call, finds it ready. `device` without an index is the
+    current one at this point. Calls that share one have to be ordered on one
+    stream, and a captured graph wants it kept as long as the graph. After a
+    call that recorded EPILORA_ERR_TIMEOUT, take a new one.
+
+    One made while the current stream is being captured is zeroed by the graph
+    only, when that is replayed; each call with it therefore zeroes the part
+    that has to be zero."""
 
     def __init__(self, device):
         device = torch.device(device)
         if device.type != "cuda":
             _bad(f"workspace: a CUDA device wanted, not {device}")
         self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
-        self._buf = {}
+        self.head = None            # what every call has to zero
+        self.known = set()          # raw handles of the streams that the allocator knows the buffer's use on
+        self._buf = self._make()
+
+    def _make(self):
+        with torch.cuda.device(self.device):
+            need = max(E.epilora_attention_workspace_bytes(d) for d in (64, 128))
+            buf = torch.zeros(need, dtype=_U8, device=self.device)
+            if torch.cuda.is_current_stream_capturing():
+                self.head = buf[:E.epilora_attention_workspace_zero_bytes()]
+            else:
+                stream = torch.cuda.current_stream()
+                stream.synchronize()
+                self.known.add(stream.cuda_stream)
+        return buf
 
     def get(self, head_dim):
-        buf = self._buf.get(head_dim)
-        if buf is None:
-            need = E.epilora_attention_workspace_bytes(head_dim)
-            buf = self._buf[head_dim] = torch.zeros(max(need, 256), dtype=_U8, device=self.device)
-        return buf
+        """The buffer, ready for a call on the current stream."""
+        if self.head is not None:
+            self.head.zero_()
+        return self._buf
+
+    def note(self, raw, stream):
+        """The first call on `stream` (None: the current one; `raw` its
+        handle): the allocator will let no other tensor have the buffer before
+        that stream is done with it, should the workspace be dropped. A stream
+        that torch does not own may be gone by then: there it is the caller's
+        to keep the workspace."""
+        if isinstance(stream, torch.cuda.ExternalStream):
+            return
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        if not torch.cuda.is_current_stream_capturing():
+            self._buf.record_stream(stream)
+            self.known.add(raw)
 
 
 def _batch(tokens, q_start, kv_len, page_table, max_new, dev):
@@ -231,7 +269,7 @@ def paged_attention(q, cache: PagedKVCache, q_start, kv_len, page_table, max_new
     if out is None:
         out = _new(q, shape, given)
     o_at, ot, oh = _rows(out, shape, dev, "out")
-    buf, w_at, w_bytes = _workspace(workspace, q, dim, given)
+    buf, w_at, w_bytes = _workspace(workspace, q, dim, raw, given)
     rc = _lib().epilora_paged_attention(cache.address, batch, heads, q_at, qt, qh, dim ** -0.5 if scale is None else scale,
                                         o_at, ot, oh, _lse(lse, shape, dev), w_at, w_bytes, _status(status, dev), raw)
     if rc:
@@ -260,7 +298,7 @@ def prompt_attention(q, k, v, q_start, scale: Optional[float] = None, out=None, 
     if out is None:
         out = _new(q, shape, given)
     o_at, ot, oh = _rows(out, shape, dev, "out")
-    buf, w_at, w_bytes = _workspace(workspace, q, dim, given)
+    buf, w_at, w_bytes = _workspace(workspace, q, dim, raw, given)
     rc = _lib().epilora_prompt_attention(n, T, starts, heads, kv_heads, dim, q_at, qt, qh, k_at, kt, kh, v_at, vt, vh,
                                          dim ** -0.5 if scale is None else scale, o_at, ot, oh,
                                          _lse(lse, shape, dev), w_at, w_bytes, _status(status, dev), raw)

@@ -44,6 +44,7 @@ struct AttnArgs {
 };
 int launch_attn(const AttnArgs& a);
 size_t attn_workspace_bytes(int head_dim);
+size_t attn_workspace_zero_bytes();   // of these, at the head: the counters
 
 // attn_decode.cu: the sequences whose new tokens n satisfy
 // attn_decode_takes(n, group), and the packed rows of no sequence.

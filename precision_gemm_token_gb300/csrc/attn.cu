@@ -9,9 +9,10 @@ inline size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 // [counters of the decode kernel][of the tile kernel][partial results of the
 // decode kernel][of the tile kernel]
+size_t attn_workspace_zero_bytes() { return round256(attn_decode_counter_bytes()) + round256(attn_tile_counter_bytes()); }
 size_t attn_workspace_bytes(int head_dim) {
-  return round256(attn_decode_counter_bytes()) + round256(attn_tile_counter_bytes()) +
-         round256(attn_decode_partial_bytes(head_dim)) + round256(attn_tile_partial_bytes(head_dim));
+  return attn_workspace_zero_bytes() + round256(attn_decode_partial_bytes(head_dim)) +
+         round256(attn_tile_partial_bytes(head_dim));
 }
 
 int launch_attn(const AttnArgs& a) {

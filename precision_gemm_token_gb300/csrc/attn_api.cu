@@ -118,6 +118,8 @@ EPILORA_API size_t epilora_attention_workspace_bytes(int head_dim) {
   return head_dim == 64 || head_dim == 128 ? attn_workspace_bytes(head_dim) : 0;
 }
 
+EPILORA_API size_t epilora_attention_workspace_zero_bytes(void) { return attn_workspace_zero_bytes(); }
+
 EPILORA_API int epilora_paged_attention(const epilora_kv_cache* cache, const epilora_kv_batch* batch, int heads,
                                         const void* Q, int64_t q_token_stride, int64_t q_head_stride, float scale,
                                         void* O, int64_t o_token_stride, int64_t o_head_stride, float* lse,

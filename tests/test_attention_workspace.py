@@ -7,6 +7,11 @@ import precision_gemm_token_gb300 as E
 from precision_gemm_token_gb300 import attention as A
 
 
+@pytest.fixture(autouse=True)
+def no_allocation(monkeypatch):
+    monkeypatch.setattr(A.AttentionWorkspace, "_make", lambda self: None)
+
+
 class OnDevice:
     """A tensor as far as the workspace looks at one."""
 
@@ -28,10 +33,18 @@ def test_workspace_of_another_device_is_refused(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     for made in ("cuda", "cuda:0"):
         with pytest.raises(E.EpiloraError, match="workspace: on cuda:0"):
-            A._workspace(A.AttentionWorkspace(made), OnDevice(1), 128, None)
+            A._workspace(A.AttentionWorkspace(made), OnDevice(1), 128, 0, None)
 
 
 @pytest.mark.parametrize("device", ["cpu", "meta"])
 def test_other_devices_are_refused(device):
     with pytest.raises(E.EpiloraError, match="workspace: a CUDA device"):
         A.AttentionWorkspace(device)
+
+
+def test_bytes_to_zero():
+    """The counters: whole 256-byte units, a small part of the workspace."""
+    E.build()
+    n = E.epilora_attention_workspace_zero_bytes()
+    assert 0 < n <= 1 << 16 and n % 256 == 0
+    assert E.epilora_attention_workspace_bytes(128) > E.epilora_attention_workspace_bytes(64) > n

@@ -77,13 +77,21 @@ def _new(q, shape, stream):
         return torch.empty(shape, dtype=_BF16, device=q.device)
 
 
+def _own_workspace(q, dim):
+    """A workspace of one call: only what has to be zero is filled."""
+    need = E.epilora_attention_workspace_bytes(dim) or 256      # (0: a head size that the call will refuse)
+    buf = torch.empty(need, dtype=_U8, device=q.device)
+    buf[:E.epilora_attention_workspace_zero_bytes()].zero_()
+    return buf, buf.data_ptr(), need
+
+
 def _workspace(workspace, q, dim, raw, stream):
     """(tensor, address, bytes), in order on the launching stream."""
     if workspace is None:
-        need = max(E.epilora_attention_workspace_bytes(dim), 256)
-        with torch.cuda.stream(stream):     # (None: the current one)
-            buf = torch.zeros(need, dtype=_U8, device=q.device)
-        return buf, buf.data_ptr(), need
+        if stream is None:
+            return _own_workspace(q, dim)
+        with torch.cuda.stream(stream):
+            return _own_workspace(q, dim)
     if workspace.device.index != q.get_device():
         _bad(f"workspace: on {workspace.device}, the tensors on device {q.get_device()}")
     if raw not in workspace.known:

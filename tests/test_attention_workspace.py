@@ -15,6 +15,8 @@ def no_allocation(monkeypatch):
 class OnDevice:
     """A tensor as far as the workspace looks at one."""
 
+    device = torch.device("cpu")
+
     def __init__(self, index):
         self.index = index
 
@@ -48,3 +50,19 @@ def test_bytes_to_zero():
     n = E.epilora_attention_workspace_zero_bytes()
     assert 0 < n <= 1 << 16 and n % 256 == 0
     assert E.epilora_attention_workspace_bytes(128) > E.epilora_attention_workspace_bytes(64) > n
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_call_without_a_workspace_fills_the_counters_alone(dim, monkeypatch):
+    E.build()
+    made, empty = [], torch.empty
+
+    def ones(*a, **kw):
+        made.append(empty(*a, **kw).fill_(255))
+        return made[-1]
+
+    monkeypatch.setattr(torch, "empty", ones)
+    buf, address, size = A._workspace(None, OnDevice(0), dim, 0, None)
+    n = E.epilora_attention_workspace_zero_bytes()
+    assert buf is made[0] and address == buf.data_ptr() and size == E.epilora_attention_workspace_bytes(dim)
+    assert not buf[:n].any() and (buf[n:] == 255).all()

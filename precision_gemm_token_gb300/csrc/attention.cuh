@@ -46,6 +46,20 @@ int launch_attn(const AttnArgs& a);
 size_t attn_workspace_bytes(int head_dim);
 size_t attn_workspace_zero_bytes();   // of these, at the head: the counters
 
+// A row's running maximum is raised (and its sums rescaled) only when a score
+// exceeds it by this many powers of two, so that after a few tiles nothing is
+// rescaled any more.
+constexpr float kRaise = 8.0f;
+// The weights are powers of two of the score's distance from the maximum, plus
+// this: they stay below 2^(kRaise + lift), in range of the 16-bit operands. bf16
+// has fp32's range. fp16 (an E4M3 cache) has most of its range above 1: with
+// the maximum at 2^7 a weight is within 2^-11 of itself down to 2^-21 of the
+// maximum's, and below that off by at most 2^-32 of it (without, 2^-14 and 2^-25:
+// behind a few dominant positions a long context's many small weights
+// vanished from the outputs, though not from the sums that divide them).
+template <bool E4>
+constexpr float kWeightLift = E4 ? 7.0f : 0.0f;
+
 // attn_decode.cu: the sequences whose new tokens n satisfy
 // attn_decode_takes(n, group), and the packed rows of no sequence.
 __host__ __device__ inline bool attn_decode_takes(int n, int group) { return n <= 16 / group; }

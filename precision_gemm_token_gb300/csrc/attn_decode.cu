@@ -46,10 +46,6 @@ constexpr int kDecPieces = 4;        // pieces of work told ahead
 constexpr int kDecJoin = 16;         // pieces of a join whose factors are kept
 constexpr int kDecPieceInts = 12;
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
-// a row's maximum is raised (and its sums rescaled) only when a score exceeds
-// it by this many powers of two: weights stay below 2^8, exact in fp32 sums
-// and in range for the 16-bit operands
-constexpr float kRaise = 8.0f;
 
 template <int D, bool E4>
 struct DecCfg {
@@ -814,8 +810,11 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-        const bool up0 = x0 > m0 + kRaise, up1 = x1 > m1 + kRaise;
+        // m: the running maximum less the lift
+        constexpr float kLift = kWeightLift<E4>;
+        const bool up0 = x0 > m0 + (kRaise + kLift), up1 = x1 > m1 + (kRaise + kLift);
         if (__any_sync(0xffffffffu, up0 || up1)) {
+          x0 -= kLift, x1 -= kLift;
           const float f0 = up0 ? exp2_approx(m0 - x0) : 1.0f, f1 = up1 ? exp2_approx(m1 - x1) : 1.0f;
           if (up0) m0 = x0;
           if (up1) m1 = x1;
@@ -832,7 +831,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
           s[nt][2] = exp2_approx(s[nt][2] - b1), s[nt][3] = exp2_approx(s[nt][3] - b1);
           l0 += s[nt][0] + s[nt][1];
           l1 += s[nt][2] + s[nt][3];
-          // the weights as 16-bit operands (each within 2^-8 of itself, 2^-11 in fp16)
+          // the weights as 16-bit operands (each within 2^-8 of itself in bf16; fp16: see kWeightLift)
           pa[nt / 2][2 * (nt & 1)] = pack16<E4>(s[nt][0], s[nt][1]);
           pa[nt / 2][2 * (nt & 1) + 1] = pack16<E4>(s[nt][2], s[nt][3]);
         }

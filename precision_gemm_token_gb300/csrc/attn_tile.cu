@@ -62,10 +62,6 @@ constexpr int kGroups = 256;       // entries of the block's table of sequence w
 // at most 1024 101, 103, 105 us; four chunks of 37 over 7999 29.5, 28.4, 27.7 us)
 constexpr int kItemCost = 3;
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
-// a row's maximum is raised (and its sums rescaled) only when a score exceeds
-// it by this many powers of two: weights stay below 2^8, in range for the
-// 16-bit operands, and after a few tiles nothing is rescaled any more
-constexpr float kRaise = 8.0f;
 
 constexpr int kPieces = 4;         // pieces of work told ahead
 constexpr int kPieceInts = 16;
@@ -411,7 +407,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, float c, 
     float add;
 #pragma unroll 1
     while (true) {
-      const float mc = m == -INFINITY ? 0.0f : m * c;
+      const float mc = m == -INFINITY ? 0.0f : (E4 ? fmaf(m, c, -kWeightLift<E4>) : m * c);
       const uint64_t cc = f32x2(c, c), mm = f32x2(-mc, -mc);
       float top[2] = {-INFINITY, -INFINITY};
       uint64_t sum[2] = {0, 0};
@@ -435,7 +431,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, float c, 
           a = exp2_approx(a);
           b = exp2_approx(b);
           sum[q & 1] = add_f32x2(sum[q & 1], f32x2(a, b));
-          // the weights as 16-bit operands (each within 2^-8 of itself, 2^-11 in fp16)
+          // the weights as 16-bit operands (each within 2^-8 of itself in bf16; fp16: see kWeightLift)
           pk[16 * g + q] = E4 ? pack_half(a, b) : pack_bf16(a, b);
         }
       }
@@ -1197,7 +1193,8 @@ __global__ void __launch_bounds__(TileWarps<E4>::kThreads, 1) attn_tile_kernel(c
                   make_float4(a[q], a[q + 1], a[q + 2], a[q + 3]);
           }
         }
-        const float mc = m == -INFINITY ? -INFINITY : m * c;
+        // as in softmax_tile: the maximum less the lift
+        const float mc = m == -INFINITY ? -INFINITY : (E4 ? fmaf(m, c, -kWeightLift<E4>) : m * c);
         if (nf) {
           // the non-finite values that were taken out, where this row sees them, go into what was just written
           const int to_pos = live ? min(see, it.t1 * kPosTile) : 0;

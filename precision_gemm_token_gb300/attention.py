@@ -240,6 +240,8 @@ def kv_append(q, k, v, cache: PagedKVCache, q_start, kv_len, page_table, cos_sin
         if cos_sin.dtype is not _F32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
             _bad("cos_sin: contiguous fp32 [positions, rot_dim] wanted")
         n_pos, rot = cos_sin.shape
+        if cos_sin.numel() == 0 and T > 0:      # (without an address it would stand for no rotation)
+            _bad("cos_sin: no position or no element to rotate in it")
         table = cos_sin.data_ptr()
     batch = _batch(T, q_start, kv_len, page_table, None, dev)
     if q_out is None:

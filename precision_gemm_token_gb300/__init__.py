@@ -26,6 +26,7 @@ from ._binding import (  # noqa: F401
     FMT_NVFP4,
     KV_BF16,
     KV_E4M3,
+    WORKSPACE_SYNC_BYTES,
     EpiloraError,
     KvBatch,
     KvCache,

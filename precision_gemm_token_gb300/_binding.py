@@ -24,6 +24,8 @@ EPILORA_ERR_WORKSPACE = -5
 FMT_FP8 = 0
 FMT_NVFP4 = 1
 
+WORKSPACE_SYNC_BYTES = 2360576      # EPILORA_WORKSPACE_SYNC_BYTES
+
 KV_BF16 = 0
 KV_E4M3 = 1
 

@@ -141,10 +141,14 @@ def gemm_lora_epilogue(Xq, x_scale, w: QuantWeight, M, K, S=None, B=None, idx=No
 class LayerWorkspace:
     """Caller-owned workspace for epilora_layer_forward (grown on demand).
     Zero-filled when (re)allocated: the library wants the head of the
-    workspace zero before the first call and keeps it valid after each."""
+    workspace zero before the first call and keeps it valid after each. A
+    buffer allocated while the current stream is being captured is filled by
+    the graph only, when that is replayed: every later call with it zeroes
+    the head (a first call before the capture saves that)."""
 
     def __init__(self, device):
         self.device = torch.device(device)
+        self.head = None    # what every call has to zero
         self.buf = torch.zeros(0, dtype=torch.uint8, device=self.device)
         self._need = {}     # (fmt, M, N, K, r) -> bytes, asked of the library once per shape
 
@@ -164,6 +168,9 @@ class LayerWorkspace:
         need = self.need(fmt, M, K, r, N)
         if self.buf.numel() < need:
             self.buf = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.device)
+            self.head = self.buf[:E.WORKSPACE_SYNC_BYTES] if torch.cuda.is_current_stream_capturing() else None
+        elif self.head is not None:
+            self.head.zero_()
         return self.buf
 
 
@@ -226,12 +233,18 @@ class PreparedLayer:
         s = stream if isinstance(stream, int) else stream.cuda_stream
         self.Y = Y
         self._keep = (X, w, A, B, idx, mask, x_global_scale, buf, status, Y)
+        self._head = ws.head    # (of a workspace made under a capture, see there)
+        if self._head is not None:
+            self._stream = torch.cuda.ExternalStream(s, device=X.device)
         self._fn = E.load().epilora_layer_forward
         self._args = (w.fmt, M, N, K, p(X), X.stride(0), p(w.codes), p(w.scale), p(w.block_scale), p(w.global_scale),
                       p(x_global_scale), p(A), p(B), L, r, p(idx), p(mask), p(Y), Y.stride(0), p(buf),
                       ws.need(w.fmt, M, K, rr, N), p(status), s)
 
     def __call__(self):
+        if self._head is not None:
+            with torch.cuda.stream(self._stream):
+                self._head.zero_()
         rc = self._fn(*self._args)
         if rc != E.EPILORA_OK:
             E.check(rc, "layer_forward")

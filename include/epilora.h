@@ -464,7 +464,7 @@ typedef struct {
  * packed rows from q_start[n_seqs] up to n_tokens belong to no sequence
  * (padding of a captured graph). max_new is the caller's upper bound of the
  * new tokens of any sequence (n_tokens always is one): it selects kernels,
- * not results.
+ * whose results differ by roundings within the bounds stated at the calls.
  * Device-detected, EPILORA_ERR_INVALID_ARG in the status word: q_start that
  * descends or leaves [0, n_tokens], more new tokens than max_new, kv_len
  * beyond table_pages * page_size, a page index that is read and is outside
@@ -540,17 +540,19 @@ EPILORA_API size_t epilora_attention_workspace_zero_bytes(void);
  * with scores, statistics and sums in fp32 (the weights exp(x_j - m) are
  * rounded to the tensor cores' 16-bit operand type: bf16, or fp16 for an
  * E4M3 cache; an E4M3 cache's queries are scaled by a power of two per row
- * into fp16). A row that sees nothing (negative position, no sequence) is
- * zero, its lse -infinity. What a masked position, a page's unused rows or
- * an unused page hold never reaches a result, NaN and infinities included.
- * scale is finite.
+ * into fp16, and its weights are taken times 2^7: those below 2^-21 of the
+ * largest are off by up to 2^-32 of it). A row that sees nothing (negative
+ * position, no sequence) is zero, its lse -infinity. What a masked position,
+ * a page's unused rows or an unused page hold never reaches a result, NaN and
+ * infinities included. scale is finite. O must not overlap any input.
  * Kernels: one for the sequences whose new tokens times G are at most 16
  * rows; where max_new * G exceeds that, a second one for the others, which
  * starts as the first one's blocks end, or alone where n_tokens is
  * n_seqs * max_new. Programmatic dependents of the
- * previous kernel on the stream, like epilora_kv_append. The results of a call
- * are the same from run to run. n_tokens * heads has to stay below 2^30
- * (EPILORA_ERR_UNSUPPORTED); n_tokens == 0 is a no-op.
+ * previous kernel on the stream, like epilora_kv_append. The results of the
+ * same call (max_new included) are the same from run to run.
+ * n_tokens * heads has to stay below 2^30 (EPILORA_ERR_UNSUPPORTED);
+ * n_tokens == 0 is a no-op.
  */
 EPILORA_API int epilora_paged_attention(const epilora_kv_cache* cache, const epilora_kv_batch* batch, int heads,
                       const void* Q, int64_t q_token_stride, int64_t q_head_stride, float scale,

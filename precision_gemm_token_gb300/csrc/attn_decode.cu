@@ -28,9 +28,9 @@
 // memory is busy, and as long again to join.
 //
 // Measured (heads of 128): 64 sequences of up to 16384, 64 / 8 heads, 335 us
-// (6.9 TB/s) in bf16, 213 us (5.4 TB/s) in E4M3, where the chains of products in
+// (6.9 TB/s) in bf16, 214 us (5.4 TB/s) in E4M3, where the chains of products in
 // eight computing warps an SM are the bound; 32 of up to 4096, 32 / 8 heads,
-// 51.6 us (5.3 TB/s); one of 1023, 10.0 us.
+// 52.4 us (5.2 TB/s); one of 1023, 10.0 us.
 #include "attention.cuh"
 #include "ptx.cuh"
 

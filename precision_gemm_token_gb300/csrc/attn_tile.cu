@@ -34,9 +34,11 @@
 // between blocks is joined by the block that finishes last, in the order of
 // the pieces.
 //
-// Measured (heads of 128): a prompt of 8192, 64 / 8 heads, 686 us (1600 TFLOP/s);
-// 16 prompts of up to 1024, 32 / 8 heads, 102 us (600, an item's fixed costs);
-// 512 new tokens over 16300, E4M3, 101 us (1180, the conversion of the codes).
+// Measured (heads of 128): a prompt of 8192, 64 / 8 heads, 686 to 731 us by card
+// (1600 to 1500 TFLOP/s); 16 prompts of up to 1024, 32 / 8 heads, 102 us (605, an
+// item's fixed costs); 512 new tokens over 16300, E4M3, 101 us (1180: a step of
+// both streams takes some 3500 cycles, the products 2048 of them, the conversion
+// of its two tiles beside them 2200; the rest is not accounted for).
 #include "attention.cuh"
 #include "ptx.cuh"
 
@@ -58,8 +60,8 @@ constexpr int kRowTile = 128;      // rows per stream
 constexpr int kItemRows = 2 * kRowTile;
 constexpr int kTileMaxCtas = 512;
 constexpr int kGroups = 256;       // entries of the block's table of sequence weights
-// cost of an item besides its tiles, in tiles (2, 3, 4: a prompt of 8192, 64 heads 707, 686, 699 us; 16 prompts of
-// at most 1024 101, 103, 105 us; four chunks of 37 over 7999 29.5, 28.4, 27.7 us)
+// cost of an item besides its tiles, in tiles (2, 3, 4 on one card: a prompt of 8192, 64 heads 707, 686, 699 us; 16
+// prompts of at most 1024 101, 103, 105 us; four chunks of 37 over 7999, then behind the decode kernel, 29.5, 28.4, 27.7 us)
 constexpr int kItemCost = 3;
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
 

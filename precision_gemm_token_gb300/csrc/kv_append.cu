@@ -14,9 +14,9 @@
 // their way while every warp looks the token up for itself (a warp doing it for
 // the block, and a barrier, took longer).
 //
-// Measured: 8044 tokens of 32 + 2 x 8 heads 32.6 us (6.2 TB/s), 2112 of 64 + 2 x 8
-// into an E4M3 cache 20.6 us (4.0 TB/s, launch and first loads included), one
-// token 3.1 us.
+// Measured: 8044 tokens of 32 + 2 x 8 heads 32.3 us (6.2 TB/s), 2112 of 64 + 2 x 8
+// into an E4M3 cache 20.1 to 21.6 us (4.0 TB/s, launch and first loads included),
+// one token 3.1 us.
 #include "attention.cuh"
 #include "ptx.cuh"
 
@@ -26,7 +26,7 @@ namespace {
 struct AppendParams {
   epilora_kv_cache c;
   epilora_kv_batch b;
-  int heads, rows;   // rows = heads + 2 kv_heads (kv rows only: no Q)
+  int rows;   // heads + 2 kv_heads (kv rows only: no Q)
   AttnRows q, k, v;
   AttnOut qo;
   const float* cos_sin;
@@ -63,7 +63,9 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
 }
 
 constexpr int kThreads = 128;
-// rows of a thread under way; more cost blocks per SM (39, 45, 56 us with 3, 4, 5 for 8044 tokens, 48 rows)
+// rows of a thread under way: 34.2, 32.3, 32.7, 41.1 us with 2, 3, 4, 5 for 8044 tokens of 48 rows, 21.0, 20.1 to 21.6,
+// 21.8, 22.7 us for 2112 tokens of 80 rows into an E4M3 cache (with seven blocks per SM bf16 spills from five on, E4M3
+// 92, 164, 356 bytes with three, four, five)
 constexpr int kBatch = 3;
 
 template <int D, bool E4>
@@ -198,7 +200,6 @@ int launch_kv_append(const AppendArgs& a) {
   AppendParams p{};
   p.c = a.cache;
   p.b = a.batch;
-  p.heads = a.heads;
   p.rows = (a.qo.p != nullptr ? a.heads : 0) + 2 * a.cache.kv_heads;
   p.q = a.q;
   p.k = a.k;

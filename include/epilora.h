@@ -574,6 +574,116 @@ EPILORA_API int epilora_prompt_attention(int n_seqs, int n_tokens, const int32_t
                       void* O, int64_t o_token_stride, int64_t o_head_stride, float* lse,
                       void* workspace, size_t workspace_bytes, int* status_dev, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Projections and mixtures of experts in 8-bit blocks: E4M3 codes with one
+ * fp32 scale per 128 consecutive elements of an activation row, and one per
+ * 128 x 128 block of a weight (the last block of a row or column may be
+ * shorter). nb(n) below is ceil(n / 128).
+ *   activation codes  uint8 [M][K]          scale fp32 [nb(K)][x_scale_ld], scale[b][m]
+ *   weight codes      uint8 [N][K]          scale fp32 [nb(N)][nb(K)]
+ * Widths (K, and hidden and inner of a mixture) are multiples of 16; M and N
+ * are any. Code arrays and bf16 inputs are 16-byte aligned, bf16 rows have
+ * strides in multiples of 8 elements. All calls are forward only. Their
+ * kernels are programmatic dependents of the previous kernel on the stream
+ * and wait for it before they read anything it may have written.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Codes and scales of bf16 rows X [M][ldx], per block b of 128 elements:
+ *   s = fl32(max(amax_b, EPILORA_FP8_AMAX_FLOOR) / 448),
+ *   code = E4M3_rn_satfinite(fl32(x / s)),
+ * bit-exact functions of the inputs. A NaN element gets the code of NaN and
+ * does not count in amax; an infinity makes the block's scale infinite and
+ * its own code NaN. One kernel. M == 0 is a no-op.
+ */
+EPILORA_API int epilora_block_quant(const void* X, int M, int K, int64_t ldx, uint8_t* Xq, float* x_scale,
+                      int64_t x_scale_ld, void* stream);
+
+/* The same for a weight W [N][ldw], one scale per 128 x 128 block (load time). */
+EPILORA_API int epilora_block_quant_weight(const void* W, int N, int K, int64_t ldw, uint8_t* Wq, float* w_scale,
+                      void* stream);
+
+/*
+ * Y[m][n] = bf16( sum_b x_scale[b][m] w_scale[n / 128][b] sum_{k in b} Xq[m][k] Wq[n][k] )
+ * with fp32 sums (the products of a block on the tensor cores, then the
+ * blocks in order). Y is bf16 [M][ldy], ldy >= N, of any alignment (rows of
+ * 32-byte aligned starts are written faster), and must not overlap an input.
+ * One kernel. M == 0 is a no-op.
+ */
+EPILORA_API int epilora_block_matmul(int M, int N, int K, const uint8_t* Xq, const float* x_scale, int64_t x_scale_ld,
+                      const uint8_t* Wq, const float* w_scale, void* Y, int64_t ldy, int* status_dev, void* stream);
+
+/* epilora_block_quant of X into the workspace, then epilora_block_matmul:
+ * two kernels. The workspace (256-byte aligned) needs no initialization;
+ * calls that share one must be ordered on one stream. */
+EPILORA_API size_t epilora_block_linear_workspace_bytes(int M, int K);
+EPILORA_API int epilora_block_linear(int M, int N, int K, const void* X, int64_t ldx, const uint8_t* Wq,
+                      const float* w_scale, void* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                      int* status_dev, void* stream);
+
+#define EPILORA_MOE_MAX_EXPERTS 1024
+#define EPILORA_MOE_MAX_TOP 32
+typedef enum { EPILORA_LOGITS_F32 = 0, EPILORA_LOGITS_BF16 = 1 } epilora_logits_format;
+typedef enum { EPILORA_SCORE_SOFTMAX = 0, EPILORA_SCORE_SIGMOID = 1 } epilora_scoring;
+
+/*
+ * Chooses `top` experts for each token from its logits (row t at
+ * logits + t * ld, fp32 or bf16).
+ *   score s_e = softmax over the experts, or sigmoid, of the logits
+ *   choice c_e = s_e + bias[e]   (bias fp32 [experts] or NULL)
+ *   groups > 1: expert e belongs to group e / (experts / groups); a group's
+ *     value is the sum of its `group_best` (1 or 2) largest c, and only the
+ *     `top_groups` groups of the largest values stay (ties: lowest index)
+ *   ids[t][0 .. top): the experts of the largest c among those, descending,
+ *     ties to the lowest index, in the exact order of the real numbers c
+ *   weights[t][j] = scale * s of the j-th, divided by the sum of the chosen
+ *     s first if renormalize
+ * A logit of -infinity or NaN, or a bias of -infinity or NaN, takes the
+ * expert away for that token; +infinity counts as the largest finite number.
+ * Slots for which no expert is left have id -1 and weight 0.
+ * experts <= EPILORA_MOE_MAX_EXPERTS, a multiple of groups; groups <= 32;
+ * top <= EPILORA_MOE_MAX_TOP and <= top_groups * experts / groups. One kernel.
+ */
+EPILORA_API int epilora_moe_route(int tokens, int experts, int top, const void* logits, int logits_fmt, int64_t ld,
+                      const float* bias, int scoring, int groups, int top_groups, int group_best, int renormalize,
+                      float scale, int32_t* ids, float* weights, void* stream);
+
+/*
+ * The gated MLPs of a mixture's experts. Slot j of token t (number
+ * t * top + j) goes to expert e = ids[t][j]; a negative id is no expert, and
+ * so is one >= experts, which also records EPILORA_ERR_INVALID_ARG in the
+ * status word. A token may name an expert twice.
+ *   Wup   codes [experts][2][inner][hidden], scale [experts][2][nb(inner)][nb(hidden)]  (gate, then up)
+ *   Wdown codes [experts][hidden][inner],    scale [experts][nb(hidden)][nb(inner)]
+ * up:   x is block-quantized; h = silu(x Wup[e][0]^T) * (x Wup[e][1]^T), silu(g) = g / (1 + exp(-g)), in fp32;
+ *       Hq [tokens][top][inner] and h_scale [nb(inner)][tokens * top] are its
+ *       block quantization; slots without an expert: zero codes, zero scales
+ * down: Y[t] = bf16( sum_j weights[t][j] bf16(h[t][j] Wdown[e]^T) ), j ascending in fp32 over the slots that
+ *       have an expert (each expert's output is rounded to bf16 once, as a model that adds them up would)
+ * epilora_moe_experts is up, then down. X is bf16 [tokens][ldx], Y bf16
+ * [tokens][ldy], 16-byte aligned, ldy a multiple of 8; outputs must not
+ * overlap inputs. Kernels: up 2, down 3, both 4. The results of a token do not
+ * depend on the other tokens. tokens == 0 is a no-op.
+ * Workspace: epilora_moe_workspace_bytes(what, ...) bytes for EPILORA_MOE_UP,
+ * EPILORA_MOE_DOWN, or both or'ed together for epilora_moe_experts; 256-byte
+ * aligned, no initialization; calls that share one must be ordered on one
+ * stream. 0 for sizes that the calls refuse.
+ */
+typedef enum { EPILORA_MOE_UP = 1, EPILORA_MOE_DOWN = 2 } epilora_moe_part;
+EPILORA_API size_t epilora_moe_workspace_bytes(int what, int tokens, int top, int experts, int hidden, int inner);
+EPILORA_API int epilora_moe_experts_up(int tokens, int top, int experts, int hidden, int inner,
+                      const void* X, int64_t ldx, const int32_t* ids, const uint8_t* Wup, const float* wup_scale,
+                      uint8_t* Hq, float* h_scale, void* workspace, size_t workspace_bytes, int* status_dev,
+                      void* stream);
+EPILORA_API int epilora_moe_experts_down(int tokens, int top, int experts, int hidden, int inner,
+                      const uint8_t* Hq, const float* h_scale, const int32_t* ids, const float* weights,
+                      const uint8_t* Wdown, const float* wdown_scale, void* Y, int64_t ldy,
+                      void* workspace, size_t workspace_bytes, int* status_dev, void* stream);
+EPILORA_API int epilora_moe_experts(int tokens, int top, int experts, int hidden, int inner,
+                      const void* X, int64_t ldx, const int32_t* ids, const float* weights,
+                      const uint8_t* Wup, const float* wup_scale, const uint8_t* Wdown, const float* wdown_scale,
+                      void* Y, int64_t ldy, void* workspace, size_t workspace_bytes, int* status_dev, void* stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -7,10 +7,13 @@ NVFP4 quantizer, multi-adapter shrink, tcgen05 GEMM with the LoRA epilogue
 launched as the shrink's programmatic dependent) behind the C ABI of
 include/epilora.h. Between the qkv and o projections of a decoder layer the
 library has the attention: a paged key/value cache (append with the position
-rotation, attention of new tokens over it) and attention of packed prompts.
+rotation, attention of new tokens over it) and attention of packed prompts. For
+weights in FP8 with a scale per 128 x 128 block it has the quantizer, the
+projection and the layers of a mixture of experts (routing, the experts' MLPs).
 This package is its ctypes binding (`_binding`, same function names as the C
-ABI) plus `tensors` (the projections) and `attention`, thin helpers that
-allocate outputs with torch and call the binding. There is no CPU fallback.
+ABI) plus `tensors` (the projections), `attention`, `blocks` (projections in
+8-bit blocks) and `moe`, thin helpers that allocate outputs with torch and call
+the binding. There is no CPU fallback.
 """
 from ._binding import (  # noqa: F401
     EPILORA_ERR_CUDA,
@@ -26,6 +29,14 @@ from ._binding import (  # noqa: F401
     FMT_NVFP4,
     KV_BF16,
     KV_E4M3,
+    LOGITS_BF16,
+    LOGITS_F32,
+    MOE_DOWN,
+    MOE_MAX_EXPERTS,
+    MOE_MAX_TOP,
+    MOE_UP,
+    SCORE_SIGMOID,
+    SCORE_SOFTMAX,
     WORKSPACE_SYNC_BYTES,
     EpiloraError,
     KvBatch,
@@ -34,6 +45,11 @@ from ._binding import (  # noqa: F401
     epilora_abi_version,
     epilora_attention_workspace_bytes,
     epilora_attention_workspace_zero_bytes,
+    epilora_block_linear,
+    epilora_block_linear_workspace_bytes,
+    epilora_block_matmul,
+    epilora_block_quant,
+    epilora_block_quant_weight,
     epilora_gemm_lora_epilogue,
     epilora_kv_append,
     epilora_layer_forward,
@@ -44,6 +60,11 @@ from ._binding import (  # noqa: F401
     epilora_layer_forward_slices,
     epilora_layer_workspace_bytes,
     epilora_lora_shrink,
+    epilora_moe_experts,
+    epilora_moe_experts_down,
+    epilora_moe_experts_up,
+    epilora_moe_route,
+    epilora_moe_workspace_bytes,
     epilora_nvfp4_global_scale,
     epilora_paged_attention,
     epilora_prompt_attention,

@@ -29,6 +29,15 @@ WORKSPACE_SYNC_BYTES = 2360576      # EPILORA_WORKSPACE_SYNC_BYTES
 KV_BF16 = 0
 KV_E4M3 = 1
 
+LOGITS_F32 = 0
+LOGITS_BF16 = 1
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+MOE_UP = 1
+MOE_DOWN = 2
+MOE_MAX_EXPERTS = 1024              # EPILORA_MOE_MAX_EXPERTS
+MOE_MAX_TOP = 32                    # EPILORA_MOE_MAX_TOP
+
 _c_int, _vp, _sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
 _i64, _f32 = ctypes.c_int64, ctypes.c_float
 
@@ -80,6 +89,20 @@ SIGNATURES = {
                                          _vp]),
     "epilora_prompt_attention": (_c_int, [_c_int, _c_int, _vp, _c_int, _c_int, _c_int, _vp, _i64, _i64, _vp, _i64,
                                           _i64, _vp, _i64, _i64, _f32, _vp, _i64, _i64, _vp, _vp, _sz, _vp, _vp]),
+    "epilora_block_quant": (_c_int, [_vp, _c_int, _c_int, _i64, _vp, _vp, _i64, _vp]),
+    "epilora_block_quant_weight": (_c_int, [_vp, _c_int, _c_int, _i64, _vp, _vp, _vp]),
+    "epilora_block_matmul": (_c_int, [_c_int, _c_int, _c_int, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "epilora_block_linear_workspace_bytes": (_sz, [_c_int, _c_int]),
+    "epilora_block_linear": (_c_int, [_c_int, _c_int, _c_int, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _sz, _vp, _vp]),
+    "epilora_moe_route": (_c_int, [_c_int, _c_int, _c_int, _vp, _c_int, _i64, _vp, _c_int, _c_int, _c_int, _c_int,
+                                   _c_int, _f32, _vp, _vp, _vp]),
+    "epilora_moe_workspace_bytes": (_sz, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "epilora_moe_experts_up": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                                        _vp, _sz, _vp, _vp]),
+    "epilora_moe_experts_down": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _i64, _vp, _sz, _vp, _vp]),
+    "epilora_moe_experts": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _vp, _i64, _vp, _sz, _vp, _vp]),
 }
 
 _lib = None
@@ -266,3 +289,58 @@ def epilora_prompt_attention(n_seqs, n_tokens, q_start, heads, kv_heads, head_di
     return load().epilora_prompt_attention(n_seqs, n_tokens, _p(q_start), heads, kv_heads, head_dim, _p(Q), *q_strides,
                                            _p(K), *k_strides, _p(V), *v_strides, scale, _p(O), *o_strides, _p(lse),
                                            _p(workspace), workspace_bytes, _p(status_dev), _stream(stream))
+
+
+def epilora_block_quant(X, M, K, ldx, Xq, x_scale, x_scale_ld, stream=None) -> int:
+    return load().epilora_block_quant(_p(X), M, K, ldx, _p(Xq), _p(x_scale), x_scale_ld, _stream(stream))
+
+
+def epilora_block_quant_weight(W, N, K, ldw, Wq, w_scale, stream=None) -> int:
+    return load().epilora_block_quant_weight(_p(W), N, K, ldw, _p(Wq), _p(w_scale), _stream(stream))
+
+
+def epilora_block_matmul(M, N, K, Xq, x_scale, x_scale_ld, Wq, w_scale, Y, ldy, status_dev=None, stream=None) -> int:
+    return load().epilora_block_matmul(M, N, K, _p(Xq), _p(x_scale), x_scale_ld, _p(Wq), _p(w_scale), _p(Y), ldy,
+                                       _p(status_dev), _stream(stream))
+
+
+def epilora_block_linear_workspace_bytes(M, K) -> int:
+    return load().epilora_block_linear_workspace_bytes(M, K)
+
+
+def epilora_block_linear(M, N, K, X, ldx, Wq, w_scale, Y, ldy, workspace, workspace_bytes, status_dev=None,
+                         stream=None) -> int:
+    return load().epilora_block_linear(M, N, K, _p(X), ldx, _p(Wq), _p(w_scale), _p(Y), ldy, _p(workspace),
+                                       workspace_bytes, _p(status_dev), _stream(stream))
+
+
+def epilora_moe_route(tokens, experts, top, logits, logits_fmt, ld, bias, scoring, groups, top_groups, group_best,
+                      renormalize, scale, ids, weights, stream=None) -> int:
+    return load().epilora_moe_route(tokens, experts, top, _p(logits), logits_fmt, ld, _p(bias), scoring, groups,
+                                    top_groups, group_best, int(renormalize), scale, _p(ids), _p(weights),
+                                    _stream(stream))
+
+
+def epilora_moe_workspace_bytes(what, tokens, top, experts, hidden, inner) -> int:
+    return load().epilora_moe_workspace_bytes(what, tokens, top, experts, hidden, inner)
+
+
+def epilora_moe_experts_up(tokens, top, experts, hidden, inner, X, ldx, ids, Wup, wup_scale, Hq, h_scale, workspace,
+                           workspace_bytes, status_dev=None, stream=None) -> int:
+    return load().epilora_moe_experts_up(tokens, top, experts, hidden, inner, _p(X), ldx, _p(ids), _p(Wup),
+                                         _p(wup_scale), _p(Hq), _p(h_scale), _p(workspace), workspace_bytes,
+                                         _p(status_dev), _stream(stream))
+
+
+def epilora_moe_experts_down(tokens, top, experts, hidden, inner, Hq, h_scale, ids, weights, Wdown, wdown_scale, Y, ldy,
+                             workspace, workspace_bytes, status_dev=None, stream=None) -> int:
+    return load().epilora_moe_experts_down(tokens, top, experts, hidden, inner, _p(Hq), _p(h_scale), _p(ids),
+                                           _p(weights), _p(Wdown), _p(wdown_scale), _p(Y), ldy, _p(workspace),
+                                           workspace_bytes, _p(status_dev), _stream(stream))
+
+
+def epilora_moe_experts(tokens, top, experts, hidden, inner, X, ldx, ids, weights, Wup, wup_scale, Wdown, wdown_scale,
+                        Y, ldy, workspace, workspace_bytes, status_dev=None, stream=None) -> int:
+    return load().epilora_moe_experts(tokens, top, experts, hidden, inner, _p(X), ldx, _p(ids), _p(weights), _p(Wup),
+                                      _p(wup_scale), _p(Wdown), _p(wdown_scale), _p(Y), ldy, _p(workspace),
+                                      workspace_bytes, _p(status_dev), _stream(stream))

@@ -1,0 +1,111 @@
+// Shared definitions of the operators in 8-bit blocks: the block quantizer,
+// the block-scaled product, and the mixture-of-experts operators over it.
+#pragma once
+#include "common.cuh"
+
+namespace epi {
+
+constexpr int kBlock = 128;                      // elements of a row, and rows and columns of a weight, that share a scale
+__host__ __device__ constexpr int n_blocks(int n) { return (n + kBlock - 1) / kBlock; }
+
+// Rows of bf16 to E4M3 codes with one scale per 128 elements.
+struct BlockQuantArgs {
+  const void* X;
+  int M, K;
+  int64_t ldx;
+  uint8_t* Xq;          // [M][K]
+  float* scale;         // [n_blocks(K)][scale_ld]
+  int64_t scale_ld;
+  cudaStream_t stream;
+};
+int launch_block_quant(const BlockQuantArgs& a);
+// A weight [N][K] with one scale per 128 x 128 block: codes [N][K], scale [n_blocks(N)][n_blocks(K)].
+int launch_block_quant_weight(const void* W, int N, int K, int64_t ldw, uint8_t* Wq, float* scale, cudaStream_t stream);
+
+// The rows of a batch by expert: expert e owns rows[offsets[e]] .. rows[offsets[e + 1] - 1], each a slot
+// (token * top + place among the token's choices).
+struct MoePlan {
+  int32_t* offsets;     // [experts + 1]
+  int32_t* rows;        // [tokens * top]
+};
+struct MoePrepArgs {
+  const int32_t* ids;   // [tokens][top]; outside [0, experts): no expert there
+  int tokens, top, experts;
+  MoePlan plan;
+  int quant;            // quantize x into q as well, and zero the rows of `inner` that have no expert
+  BlockQuantArgs q;
+  uint8_t* inner;       // [tokens * top][inner_dim]
+  float* inner_scale;   // [n_blocks(inner_dim)][tokens * top]
+  int inner_dim;
+  int* status;
+  cudaStream_t stream;
+};
+int launch_moe_prep(const MoePrepArgs& a);
+
+// The block-scaled product: rows of A times rows of W.
+//   plain:   Y[m][n] = bf16( sum_b a_scale[b][m] w_scale[n / 128][b] sum_{k in b} A[m][k] W[n][k] ), m < M
+//   grouped: the rows of expert e times W[e]; A row = slot / slot_div, output row = slot
+//   gated:   W[e] is [2][N][K] (gate, up); the output is block-quantized silu(gate) * up
+struct BlockGemmArgs {
+  int M, N, K;          // grouped: M = all slots
+  const uint8_t* A;     // codes [a_rows][K]
+  int64_t a_rows;
+  const float* a_scale; // [n_blocks(K)][a_scale_ld]
+  int64_t a_scale_ld;
+  const uint8_t* W;
+  const float* w_scale;
+  void* Y;              // bf16 [M][ldy]
+  int64_t ldy;
+  int grouped, gated, experts, slot_div;
+  MoePlan plan;
+  uint8_t* inner;       // gated: codes [M][N] and scales [n_blocks(N)][M]
+  float* inner_scale;
+  int early_weights;    // the weights may be read before the preceding kernel has finished
+  int* status;
+  cudaStream_t stream;
+};
+int launch_block_gemm(const BlockGemmArgs& a);
+
+// y[t] = bf16( sum_j weights[t][j] parts[t * top + j] ), over the slots that have an expert
+struct MoeCombineArgs {
+  const int32_t* ids;
+  const float* weights;
+  int tokens, top, experts, hidden;
+  const void* parts;    // bf16 [tokens * top][hidden]
+  void* Y;
+  int64_t ldy;
+  cudaStream_t stream;
+};
+int launch_moe_combine(const MoeCombineArgs& a);
+
+struct MoeRouteArgs {
+  const void* logits;
+  int bf16;
+  int tokens, experts, top;
+  int64_t ld;
+  const float* bias;
+  int sigmoid, groups, top_groups, group_best, renormalize;
+  float scale;
+  int32_t* ids;
+  float* weights;
+  cudaStream_t stream;
+};
+int launch_moe_route(const MoeRouteArgs& a);
+
+// A launch as a programmatic dependent of the previous kernel on the stream.
+template <class P>
+int launch_dependent(void (*kern)(P), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, const P& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? EPILORA_OK : EPILORA_ERR_CUDA;
+}
+
+}  // namespace epi

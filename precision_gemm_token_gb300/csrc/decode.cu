@@ -220,34 +220,6 @@ __device__ __forceinline__ float dec_dot8(const uint4& xv, const uint4& av, floa
   return acc;
 }
 
-// x / s rounded to nearest float, from rs = 1/s rounded to nearest: P.
-// Markstein's correction of the reciprocal product ("Computation of elementary
-// functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1),
-// 1990; also Muller et al., Handbook of Floating-Point Arithmetic, the
-// theorem on division by FMA): q0 = RN(x rs) is within one ulp of x / s, the
-// residual x - q0 s is then exact in one fma, and RN(q0 + residual rs) is the
-// correctly rounded quotient, provided the residual does not underflow.
-// Callers keep |x / s| <= 448 and s >= 2^-100, so the residual is a normal
-// number or x / s is far below the smallest E4M3 subnormal.
-__device__ __forceinline__ float div_rn_by_recip(float x, float s, float rs) {
-  const float q0 = __fmul_rn(x, rs);
-  const float e = __fmaf_rn(-q0, s, x);
-  return __fmaf_rn(e, rs, q0);
-}
-
-// E4M3 codes of 8 bf16 values divided by the row scale s (rs = 1/s rounded
-// to nearest); for scales of at least 2^-100 (callers take the IEEE division
-// below that).
-__device__ __forceinline__ uint2 quant8_e4m3_rs(const uint4& v, float s, float rs) {
-  float x[8];
-  unpack8(v, x);
-  uint32_t q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q[i] = cvt_e4m3x2(div_rn_by_recip(x[2 * i], s, rs), div_rn_by_recip(x[2 * i + 1], s, rs));
-  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-}
-
 // S[v] . B[l, n] with the B row in registers (R4 float4 chunks of S from
 // shared memory; two accumulators)
 // Two E4M3 codes (the low 16 bits of c, low byte first) as floats.

@@ -1,0 +1,155 @@
+"""Tensor-level helpers over the C ABI's mixture-of-experts calls: routing,
+and the experts' gated MLPs in 8-bit blocks (see `blocks`). No arithmetic of
+the operators happens here.
+
+    w = quantize_experts(gate, up, down)               # once; or ExpertWeights of a checkpoint's codes and scales
+    ids, weights = route(logits, 8, bias=bias, scoring="sigmoid", groups=8, top_groups=4, group_best=2)
+    y = experts(x, ids, weights, w, workspace=ws)      # ws: blocks.BlockWorkspace
+    h, hs = experts_up(x, ids, w)                      # the two halves of it
+    y = experts_down(h, hs, ids, weights, w)
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import _binding as E
+from .blocks import (_BF16, _F32, _I32, _U8, BlockWorkspace, _array, _bad, _blocks, _lib, _matrix, _new, _out, _room, _start,
+                     _status, quantize_weight)
+
+_SCORING = {"softmax": E.SCORE_SOFTMAX, "sigmoid": E.SCORE_SIGMOID}
+_LOGITS = {torch.float32: E.LOGITS_F32, torch.bfloat16: E.LOGITS_BF16}
+
+
+def route(logits, top: int, bias=None, scoring: str = "softmax", groups: int = 1, top_groups: int = 1, group_best: int = 1,
+          renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """The `top` experts of each token and their weights from the router's
+    logits [tokens, experts] (fp32 or bf16, any row stride): (ids int32
+    [tokens, top], weights fp32 [tokens, top]). `bias` (fp32 [experts]) is
+    added to the scores for the choice alone; with groups > 1 the experts come
+    from the `top_groups` groups whose `group_best` largest choices sum to the
+    most. epilora_moe_route has the details."""
+    dev, raw, given = _start(logits, stream)
+    fmt, how = _LOGITS.get(logits.dtype), _SCORING.get(scoring)
+    if fmt is None or how is None:
+        _bad("route: fp32 or bf16 logits, scoring 'softmax' or 'sigmoid' wanted")
+    at, T, n, _ = _matrix(logits, logits.dtype, dev, "logits")
+    ld = logits.stride(0) if T > 1 else n
+    b_at = None if bias is None else _array(bias, _F32, (n,), dev, "bias")
+    if ids is None:
+        ids = _new(logits, (T, max(top, 0)), _I32, given)
+    if weights is None:
+        weights = _new(logits, (T, max(top, 0)), _F32, given)
+    rc = _lib().epilora_moe_route(T, n, top, at, fmt, ld, b_at, how, groups, top_groups, group_best, 1 if renormalize else 0,
+                                  scale, _array(ids, _I32, (T, max(top, 0)), dev, "ids"),
+                                  _array(weights, _F32, (T, max(top, 0)), dev, "weights"), raw)
+    if rc:
+        E.check(rc, "route")
+    return ids, weights
+
+
+class ExpertWeights:
+    """The experts' gated MLPs: E4M3 codes gate_up uint8 [experts, 2, inner,
+    hidden] (gate, then up) and down [experts, hidden, inner], with fp32 scales
+    of their 128 x 128 blocks [experts, 2, ceil(inner / 128), ceil(hidden /
+    128)] and [experts, ceil(hidden / 128), ceil(inner / 128)]. The tensors
+    stay the caller's."""
+
+    def __init__(self, gate_up, gate_up_scale, down, down_scale):
+        if gate_up.dim() != 4 or gate_up.shape[1] != 2:
+            _bad("gate_up: uint8 [experts, 2, inner, hidden] wanted")
+        n, _, inner, hidden = gate_up.shape
+        dev = gate_up.get_device()
+        self.up_at = _array(gate_up, _U8, (n, 2, inner, hidden), dev, "gate_up")
+        self.up_scale_at = _array(gate_up_scale, _F32, (n, 2, _blocks(inner), _blocks(hidden)), dev, "gate_up_scale")
+        self.down_at = _array(down, _U8, (n, hidden, inner), dev, "down")
+        self.down_scale_at = _array(down_scale, _F32, (n, _blocks(hidden), _blocks(inner)), dev, "down_scale")
+        self.gate_up, self.gate_up_scale, self.down, self.down_scale = gate_up, gate_up_scale, down, down_scale
+        self.experts, self.inner, self.hidden, self.dev = n, inner, hidden, dev
+
+
+def quantize_experts(gate, up, down) -> ExpertWeights:
+    """Load-time quantization of bf16 weights: gate and up [experts, inner,
+    hidden], down [experts, hidden, inner]."""
+    n, inner, hidden = gate.shape
+    if up.shape != gate.shape or down.shape != (n, hidden, inner):
+        _bad("quantize_experts: gate and up [experts, inner, hidden], down [experts, hidden, inner] wanted")
+    stacks = []
+    for parts in ([m for e in range(n) for m in (gate[e], up[e])], list(down)):
+        made = [quantize_weight(m) for m in parts]
+        stacks.append((torch.stack([m.codes for m in made]), torch.stack([m.scale for m in made])))
+    (gu, gus), (d, ds) = stacks
+    return ExpertWeights(gu.view(n, 2, inner, hidden), gus.view(n, 2, *gus.shape[1:]), d, ds)
+
+
+def _choices(ids, tokens, dev):
+    if ids.dim() != 2 or ids.shape[0] != tokens:
+        _bad(f"ids: int32 [{tokens}, top] wanted")
+    return _array(ids, _I32, tuple(ids.shape), dev, "ids"), ids.shape[1]
+
+
+def experts_up(x, ids, w: ExpertWeights, codes=None, scale=None, workspace: Optional[BlockWorkspace] = None, status=None,
+               stream=None):
+    """silu(x gate^T) * (x up^T) of each token's experts, block-quantized:
+    (codes uint8 [tokens, top, inner], scale fp32 [ceil(inner / 128), tokens *
+    top]). x bf16 [tokens, hidden]; ids int32 [tokens, top], negative: no
+    expert, whose rows are zero."""
+    dev, raw, given = _start(x, stream)
+    if w.dev != dev:
+        _bad("experts_up: x and the weights on different devices")
+    at, T, H, ld = _matrix(x, _BF16, dev, "x", None, w.hidden)
+    i_at, top = _choices(ids, T, dev)
+    shape, s_shape = (T, top, w.inner), (_blocks(w.inner), T * top)
+    if codes is None:
+        codes = _new(x, shape, _U8, given)
+    if scale is None:
+        scale = _new(x, s_shape, _F32, given)
+    c_at, s_at = _array(codes, _U8, shape, dev, "codes"), _array(scale, _F32, s_shape, dev, "scale")
+    need = E.epilora_moe_workspace_bytes(E.MOE_UP, T, top, w.experts, H, w.inner)
+    buf, w_at = _room(workspace, x, need, dev, raw, given)
+    rc = _lib().epilora_moe_experts_up(T, top, w.experts, H, w.inner, at, ld, i_at, w.up_at, w.up_scale_at, c_at, s_at, w_at,
+                                       need, _status(status, dev), raw)
+    if rc:
+        E.check(rc, "experts_up")
+    return codes, scale
+
+
+def experts_down(codes, scale, ids, weights, w: ExpertWeights, out=None, workspace: Optional[BlockWorkspace] = None,
+                 status=None, stream=None):
+    """The weighted sum over a token's experts of their down projections of
+    experts_up's rows: bf16 [tokens, hidden]."""
+    dev, raw, given = _start(codes, stream)
+    if w.dev != dev or codes.dim() != 3:
+        _bad("experts_down: codes [tokens, top, inner] on the weights' device wanted")
+    T, top = codes.shape[:2]
+    c_at = _array(codes, _U8, (T, top, w.inner), dev, "codes")
+    s_at = _array(scale, _F32, (_blocks(w.inner), T * top), dev, "scale")
+    i_at, f_at = _array(ids, _I32, (T, top), dev, "ids"), _array(weights, _F32, (T, top), dev, "weights")
+    out, o_at, ld = _out(out, codes, T, w.hidden, dev, given)
+    need = E.epilora_moe_workspace_bytes(E.MOE_DOWN, T, top, w.experts, w.hidden, w.inner)
+    buf, w_at = _room(workspace, codes, need, dev, raw, given)
+    rc = _lib().epilora_moe_experts_down(T, top, w.experts, w.hidden, w.inner, c_at, s_at, i_at, f_at, w.down_at,
+                                         w.down_scale_at, o_at, ld, w_at, need, _status(status, dev), raw)
+    if rc:
+        E.check(rc, "experts_down")
+    return out
+
+
+def experts(x, ids, weights, w: ExpertWeights, out=None, workspace: Optional[BlockWorkspace] = None, status=None, stream=None):
+    """experts_up, then experts_down: y[t] = sum_j weights[t, j] *
+    MLP_{ids[t, j]}(x[t]), bf16 [tokens, hidden]."""
+    dev, raw, given = _start(x, stream)
+    if w.dev != dev:
+        _bad("experts: x and the weights on different devices")
+    at, T, H, ld = _matrix(x, _BF16, dev, "x", None, w.hidden)
+    i_at, top = _choices(ids, T, dev)
+    f_at = _array(weights, _F32, (T, top), dev, "weights")
+    out, o_at, old = _out(out, x, T, w.hidden, dev, given)
+    need = E.epilora_moe_workspace_bytes(E.MOE_UP | E.MOE_DOWN, T, top, w.experts, H, w.inner)
+    buf, w_at = _room(workspace, x, need, dev, raw, given)
+    rc = _lib().epilora_moe_experts(T, top, w.experts, H, w.inner, at, ld, i_at, f_at, w.up_at, w.up_scale_at, w.down_at,
+                                    w.down_scale_at, o_at, old, w_at, need, _status(status, dev), raw)
+    if rc:
+        E.check(rc, "experts")
+    return out

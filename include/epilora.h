@@ -662,7 +662,7 @@ EPILORA_API int epilora_moe_route(int tokens, int experts, int top, const void* 
  *       have an expert (each expert's output is rounded to bf16 once, as a model that adds them up would)
  * epilora_moe_experts is up, then down. X is bf16 [tokens][ldx], Y bf16
  * [tokens][ldy], 16-byte aligned, ldy a multiple of 8; outputs must not
- * overlap inputs. Kernels: up 2, down 3, both 4. The results of a token do not
+ * overlap inputs. Kernels: up 3, down 4, both 5. The results of a token do not
  * depend on the other tokens. tokens == 0 is a no-op.
  * Workspace: epilora_moe_workspace_bytes(what, ...) bytes for EPILORA_MOE_UP,
  * EPILORA_MOE_DOWN, or both or'ed together for epilora_moe_experts; 256-byte

@@ -5,15 +5,19 @@
 //   y[m][n] = sum_b as[b][m] ws[n / 128][b] sum_{k in block b} A[m][k] W[n][k]
 //
 // A scale holds for 128 elements of K, so the tensor core's accumulator is
-// good for one block only: four MMAs (K = 32 each) fill a TMEM buffer with a
-// block's products, the accumulating warps read it and add it, times the two
-// scales, to fp32 sums in registers while the next buffer fills.
+// good for one block only: four MMAs (K = 32 each) put a block's products in
+// TMEM, the summing warps read them and add them, times the two scales, to
+// fp32 sums in registers. TMEM is two halves of 256 columns, filled and read
+// in turn; a half holds a group of 256 / BN blocks, so that a narrow tile's
+// warps wait as rarely, and have as many loads under way, as a wide one's.
 //
 // Roles (384 threads, one CTA per SM, walking its tiles of 128 rows x BN
 // columns):
-//   warp 0       copies: rows of A (one box, or four rows a gather for the
-//                rows of an expert) and of W through a ring of 128-byte stages
+//   warp 0       TMA copies of A and W, a block a stage of the ring
 //   warp 1       MMA issue
+//   warps 2, 3   the scales of the groups to come, into a ring of their own
+//                (each block needs new ones: the summing warps would wait for
+//                memory at every block)
 //   warps 4..11  sums: each warp 32 rows (its TMEM lanes) by half the columns,
 //                a thread one row; then the scales are one factor per thread
 //                and block, and a row's output needs no exchange
@@ -37,15 +41,18 @@ constexpr int kABytes = kRows * kBlock;        // a stage's rows of A
 constexpr int kSumBarrier = 1;
 // registers: 168 a thread at launch (64,512); the sums' warps take what the others give back
 constexpr int kRegsOther = 40, kRegsSum = 232;
+constexpr int kHalf = 256;                     // columns of a half of TMEM
+constexpr int kScaleBlocks = 32;               // blocks in the scales' ring
+constexpr int kScaleRow = kRows + 4;           // a block's scales: of the rows, then up to two of the weights
 
 template <int BN>
 struct Cfg {
   static constexpr int kBBytes = BN * kBlock;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kBufs = BN >= 256 ? 2 : 4;
-  static constexpr int kTmemCols = kBufs * BN;
-  static constexpr int kStagesMax = 10;
-  static constexpr int kMisc = 2048 + 2 * 2 * kRows * 4;     // barriers, amax exchange
+  static constexpr int kGroup = kHalf / BN;    // blocks of a group
+  static constexpr int kStagesMax = 16;
+  static constexpr int kSlots = kScaleBlocks / kGroup;       // groups in the scales' ring
+  static constexpr int kMisc = 1024 + 2 * 2 * kRows * 4 + kScaleBlocks * kScaleRow * 4;     // barriers, amax exchange, scales
 };
 
 struct Params {
@@ -56,10 +63,11 @@ struct Params {
   void* Y;
   uint8_t* inner;
   float* inner_scale;
-  MoePlan plan;
+  const int32_t* offsets;      // grouped: rows of expert e are [offsets[e], offsets[e + 1])
+  const int32_t* out_rows;     // the output row of each row (NULL: the same)
   int* status;
   int M, N, K, kb;
-  int n_tiles, experts, slot_div;
+  int n_tiles, experts, box_rows;
   int stages, wide_store, early_weights;
 };
 
@@ -98,22 +106,22 @@ struct Walk {
   }
 };
 
-// Four rows of a 2D tensor map (box one row high), 128 bytes each from column x (a multiple of 128).
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int4 rows) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(rows.x), "r"(rows.y),
-      "r"(rows.z), "r"(rows.w)
-      : "memory");
+// Four bytes of global memory to shared memory; complete in order of the groups committed after them.
+__device__ __forceinline__ void copy4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void sums_barrier() { asm volatile("bar.sync %0, %1;" ::"n"(kSumBarrier), "n"(kSumThreads) : "memory"); }
 
-template <int N>
-__device__ __forceinline__ void loaded(uint32_t (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
+// acc += x * f for a register of a TMEM load: volatile, so that it stays behind the wait for the load. One
+// multiply-add at a time: those of two need their operands in pairs of registers, which costs a move each.
+__device__ __forceinline__ void fma_loaded(float& acc, uint32_t x, float f) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(x)), "f"(f));
 }
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]) {
@@ -122,6 +130,10 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]) {
   else
     tmem_ld_32x32b_x32(taddr, v);
 }
+
+// g / (1 + exp(-g)) within 2^-21 of it, without a division's branches: a tile's elements are all in registers, so
+// this code stands there once for each of them, and has to stay in the instruction cache beside the loops
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + expf(-g)); }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -133,17 +145,20 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
   using C = Cfg<BN>;
   constexpr int NC = BN / 2;                    // columns of a summing thread
   constexpr int CH = NC < 32 ? NC : 32;         // of them per TMEM load
+  constexpr int LOADS = 64 / CH;                // loads under way together: a load takes some 200 cycles, whatever its size
+  constexpr int G = C::kGroup;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int stages = p.stages, kb = p.kb;
   uint8_t* misc = smem + static_cast<size_t>(stages) * C::kStage;
   uint64_t* full = reinterpret_cast<uint64_t*>(misc);
   uint64_t* empty = full + C::kStagesMax;
-  uint64_t* filled = empty + C::kStagesMax;     // [kBufs] a block's products are in the buffer
-  uint64_t* drained = filled + C::kBufs;        // [kBufs] they have been read
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + C::kBufs);
+  uint64_t* filled = empty + C::kStagesMax;     // [2] a half holds a group's products, and the ring its scales
+  uint64_t* drained = filled + 2;               // [2] they have been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* amax = reinterpret_cast<float*>(misc + 2048);                 // [2][2][kRows]
+  float* amax = reinterpret_cast<float*>(misc + 1024);                 // [2][2][kRows]
+  float* scales = amax + 4 * kRows;                                    // [kScaleBlocks][kScaleRow]
   int* offsets = reinterpret_cast<int*>(misc + C::kMisc);              // [experts + 1], grouped only
   int* starts = offsets + p.experts + 1;
 
@@ -154,8 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < C::kBufs; ++b) {
-      mbar_init(&filled[b], 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&filled[b], 3);                 // the products, and the two scale warps
       mbar_init(&drained[b], kSumThreads / 32);
     }
     *abort_flag = 0;
@@ -164,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
     tma_prefetch_desc(&p.tmB);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_alloc(tmem_slot, 2 * kHalf);
     tmem_relinquish();
   }
   if (kGrouped) {
@@ -174,8 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
       int before = 0;
       for (int e0 = 0; e0 < p.experts; e0 += 32) {
         const int e = e0 + lane;
-        const int o0 = e <= p.experts ? __ldcg(p.plan.offsets + e) : 0;
-        const int o1 = e < p.experts ? __ldcg(p.plan.offsets + e + 1) : o0;
+        const int o0 = e <= p.experts ? __ldcg(p.offsets + e) : 0;
+        const int o1 = e < p.experts ? __ldcg(p.offsets + e + 1) : o0;
         const int mt = (o1 - o0 + kRows - 1) / kRows;
         int sum = mt;
 #pragma unroll
@@ -217,197 +232,252 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
     setmaxnreg_dec<kRegsOther>();
     if (warp == 0) {
       // ===== copies =====
-      int s = 0;
-      uint32_t ph = 0, issued = 0, phases = 0;
-      bool go = true, waited = kGrouped;
-      for (int t = blockIdx.x; t < walk.total && go; t += gridDim.x) {
-        const Tile tile = walk.at(t);
-        const int n0 = tile.n * (kGated ? kBlock : BN);
-        const int wrow = kGated ? tile.expert * 2 * p.N + n0 : tile.expert * p.N + n0;
-        int4 arow = make_int4(0, 0, 0, 0);
-        if (kGrouped) {
-          // this lane's four rows; behind the last row, the last row again
-          int v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = __ldcg(p.plan.rows + tile.first + min(4 * lane + i, tile.rows - 1)) / p.slot_div;
-          arow = make_int4(v[0], v[1], v[2], v[3]);
-        }
-        const int gathers = (tile.rows + 3) / 4;
-        const uint32_t bytes = C::kBBytes + (kGrouped ? gathers * 4 * kBlock : kABytes);
-        const auto copy_b = [&](int st, int b) {
-          uint8_t* dst = smem + static_cast<size_t>(st) * C::kStage + kABytes;
-          tma_load_2d(dst, &p.tmB, &full[st], b * kBlock, wrow);
-          if (kGated) tma_load_2d(dst + kABytes, &p.tmB, &full[st], b * kBlock, wrow + p.N);
-        };
-        // the first tile of a plain product: weights of the first stages before the rows are there
-        const int early = !waited && p.early_weights ? min(stages, kb) : 0;
-        if (!kGrouped && !waited) {
-          if (lane == 0)
-            for (int b = 0; b < early; ++b) {
-              mbar_arrive_expect_tx(&full[b], bytes);
-              copy_b(b, b);
-            }
-          pdl_wait_primary();
-          fence_proxy_async_global();
-          waited = true;
-          issued |= (1u << early) - 1u;
-        }
-        if (kGrouped) fence_proxy_async_global();
-        for (int b = 0; b < kb; ++b) {
-          if (!wait(&empty[s], ph ^ 1u)) go = false;
-          go = __all_sync(0xffffffffu, go);
-          if (!go) break;
-          uint8_t* dst = smem + static_cast<size_t>(s) * C::kStage;
-          if (lane == 0 && b >= early) {
-            mbar_arrive_expect_tx(&full[s], bytes);
-            copy_b(s, b);
-          }
-          if (kGrouped) {
-            __syncwarp();
-            if (lane < gathers) tma_gather4(dst + lane * 4 * kBlock, &p.tmA, &full[s], b * kBlock, arow);
-          } else if (lane == 0) {
-            tma_load_2d(dst, &p.tmA, &full[s], b * kBlock, tile.first);
-          }
-          issued |= 1u << s;
-          phases = (phases & ~(1u << s)) | (ph << s);
-          if (++s == stages) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-      }
-      if (*abort_flag) {
-        // no copy in flight at exit
-        for (int i = 0; i < stages; ++i)
-          if (issued & (1u << i)) (void)mbar_wait_bounded(&full[i], (phases >> i) & 1u, kWaitLimitNs);
-      }
-    } else if (warp == 1) {
-      // ===== MMA issue =====
       if (elect_one()) {
-        constexpr uint32_t kIdesc = idesc_f8f6f4_e4m3(kRows, BN);
-        int s = 0, buf = 0;
-        uint32_t ph = 0, bph = 0;
-        bool go = true, any = false;
-        int last = 0;
-        uint32_t last_ph = 0;
+        int s = 0;
+        uint32_t ph = 0, issued = 0, phases = 0;
+        bool go = true, waited = kGrouped;
+        if (kGrouped) fence_proxy_async_global();
         for (int t = blockIdx.x; t < walk.total && go; t += gridDim.x) {
+          const Tile tile = walk.at(t);
+          const int n0 = tile.n * (kGated ? kBlock : BN);
+          const int wrow = tile.expert * (kGated ? 2 : 1) * p.N + n0;
+          const uint32_t bytes = C::kBBytes + (tile.rows + p.box_rows - 1) / p.box_rows * p.box_rows * kBlock;
+          const auto copy_w = [&](int st, int b) {
+            uint8_t* dst = smem + static_cast<size_t>(st) * C::kStage + kABytes;
+            mbar_arrive_expect_tx(&full[st], bytes);
+            tma_load_2d(dst, &p.tmB, &full[st], b * kBlock, wrow);
+            if (kGated) tma_load_2d(dst + kBlock * kBlock, &p.tmB, &full[st], b * kBlock, wrow + p.N);
+          };
+          // the first tile of a plain product: weights of the first stages before the rows are there
+          int early = 0;
+          if (!waited) {
+            early = p.early_weights ? min(stages, kb) : 0;
+            for (int b = 0; b < early; ++b) copy_w(b, b);
+            issued |= (1u << early) - 1u;
+            pdl_wait_primary();
+            fence_proxy_async_global();
+            waited = true;
+          }
           for (int b = 0; b < kb; ++b) {
-            if (!wait(&drained[buf], bph ^ 1u) || !wait(&full[s], ph)) {
+            if (!wait(&empty[s], ph ^ 1u)) {
               go = false;
               break;
             }
-            tc_fence_after();
-            const uint32_t a_at = smem_u32(smem + static_cast<size_t>(s) * C::kStage), b_at = a_at + kABytes;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f8f6f4(tmem_base + buf * BN, make_smem_desc(a_at + kk * 32, 16, 1024, kSwizzle128B),
-                         make_smem_desc(b_at + kk * 32, 16, 1024, kSwizzle128B), kIdesc, kk > 0);
-            tc_commit(&empty[s]);
-            tc_commit(&filled[buf]);
-            any = true;
-            last = buf;
-            last_ph = bph;
+            if (b >= early) copy_w(s, b);
+            for (int r = 0; r < tile.rows; r += p.box_rows)
+              tma_load_2d(smem + static_cast<size_t>(s) * C::kStage + r * kBlock, &p.tmA, &full[s], b * kBlock, tile.first + r);
+            issued |= 1u << s;
+            phases = (phases & ~(1u << s)) | (ph << s);
             if (++s == stages) {
               s = 0;
               ph ^= 1u;
             }
-            if (++buf == C::kBufs) {
-              buf = 0;
-              bph ^= 1u;
+          }
+        }
+        if (*abort_flag) {
+          // no copy in flight at exit
+          for (int i = 0; i < stages; ++i)
+            if (issued & (1u << i)) (void)mbar_wait_bounded(&full[i], (phases >> i) & 1u, kWaitLimitNs);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ===== MMA issue =====
+      if (elect_one()) {
+        constexpr uint32_t kIdesc = idesc_f8f6f4_e4m3(kRows, BN);
+        int s = 0, half = 0, last = 0;
+        uint32_t ph = 0, hph = 0, last_ph = 0;
+        bool go = true, any = false;
+        for (int t = blockIdx.x; t < walk.total && go; t += gridDim.x) {
+          for (int b0 = 0; b0 < kb && go; b0 += G) {
+            if (!wait(&drained[half], hph ^ 1u)) {
+              go = false;
+              break;
             }
+            const int n = min(G, kb - b0);
+            for (int u = 0; u < n; ++u) {
+              if (!wait(&full[s], ph)) {
+                go = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t a_at = smem_u32(smem + static_cast<size_t>(s) * C::kStage), b_at = a_at + kABytes;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f8f6f4(tmem_base + half * kHalf + u * BN, make_smem_desc(a_at + kk * 32, 16, 1024, kSwizzle128B),
+                           make_smem_desc(b_at + kk * 32, 16, 1024, kSwizzle128B), kIdesc, kk > 0);
+              tc_commit(&empty[s]);
+              if (++s == stages) {
+                s = 0;
+                ph ^= 1u;
+              }
+            }
+            tc_commit(&filled[half]);
+            any = true;
+            last = half;
+            last_ph = hph;
+            half ^= 1;
+            if (half == 0) hph ^= 1u;
           }
         }
         // nothing of this thread in flight at exit: the last commit covers every MMA before it
         if (any) (void)mbar_wait_bounded(&filled[last], last_ph, kWaitLimitNs);
       }
       __syncwarp();
+    } else {
+      // ===== scales =====
+      constexpr int kAhead = C::kSlots - 2;     // groups under way (the slot before the last one may be read still)
+      const int i = static_cast<int>(threadIdx.x) - 64;
+      const int nb = n_blocks(p.N);
+      constexpr int kW = BN == 256 ? 2 : 1;     // scales of the weights per block
+      pdl_wait_primary();
+      Walk<kGrouped> ahead = walk;
+      int c_t = blockIdx.x, c_b = 0, put = 0;
+      Tile tile{};
+      const float *c_a = nullptr, *c_w = nullptr;
+      const auto enter = [&] {
+        tile = ahead.at(c_t);
+        c_a = p.a_scale + tile.first;
+        const int w = i % kW;                   // (threads below kW * G)
+        const int block = kGated ? (tile.expert * 2 + w) * nb + tile.n : tile.expert * nb + min(tile.n * BN / kBlock + w, nb - 1);
+        c_w = p.w_scale + static_cast<int64_t>(block) * kb;
+      };
+      const auto fetch = [&] {
+        if (c_t < ahead.total) {
+          float* slot = scales + put * (G * kScaleRow);
+          const int n = min(G, kb - c_b);
+          for (int u = 0; u < n; ++u) {
+            const float* src = c_a + (c_b + u) * p.a_scale_ld;
+            if (i < tile.rows) copy4(slot + u * kScaleRow + i, src + i);
+            if (i + 64 < tile.rows) copy4(slot + u * kScaleRow + i + 64, src + i + 64);
+          }
+          if (i < kW * n) copy4(slot + (i / kW) * kScaleRow + kRows + i % kW, c_w + c_b + i / kW);
+          put = (put + 1) & (C::kSlots - 1);
+          c_b += G;
+          if (c_b >= kb) {
+            c_b = 0;
+            c_t += gridDim.x;
+            if (c_t < ahead.total) enter();
+          }
+        }
+        copies_commit();
+      };
+      if (c_t < ahead.total) enter();
+#pragma unroll 1
+      for (int g = 0; g < kAhead; ++g) fetch();
+      int half = 0;
+      uint32_t hph = 0;
+      bool go = true;
+      for (int t = blockIdx.x; t < walk.total && go; t += gridDim.x)
+        for (int b0 = 0; b0 < kb; b0 += G) {
+          go = __all_sync(0xffffffffu, wait(&drained[half], hph ^ 1u));
+          if (!go) break;
+          fetch();
+          copies_wait<kAhead>();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&filled[half]);
+          half ^= 1;
+          if (half == 0) hph ^= 1u;
+        }
+      copies_wait<0>();
     }
   } else {
     // ===== sums =====
     setmaxnreg_inc<kRegsSum>();
     pdl_wait_primary();
-    const int half = (warp - 4) >> 2;
+    const int side = (warp - 4) >> 2;           // of the columns
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    int buf = 0, turn = 0;
-    uint32_t bph = 0;
+    int half = 0, turn = 0, take = 0;
+    uint32_t hph = 0;
     bool dead = false;
     for (int t = blockIdx.x; t < walk.total; t += gridDim.x, turn ^= 1) {
       const Tile tile = walk.at(t);
       const bool live = r < tile.rows;
       const bool warp_live = (warp & 3) * 32 < tile.rows;
-      const int slot = !live ? 0 : kGrouped ? __ldcg(p.plan.rows + tile.first + r) : tile.first + r;
-      const float* as = p.a_scale + (kGrouped ? slot / p.slot_div : slot);
-      // this half's first column, and the rows of scales that its columns have
-      const int n0 = kGated ? tile.n * kBlock + half * NC / 2 : tile.n * BN + half * NC;
-      const int nb = n_blocks(p.N);
-      const int wb = kGated ? tile.expert * 2 * nb + tile.n : tile.expert * nb + n0 / kBlock;
+      const int row = tile.first + (live ? r : 0);
+      const int slot = p.out_rows != nullptr ? __ldcg(p.out_rows + row) : row;
+      const int n0 = kGated ? tile.n * kBlock + side * (NC / 2) : tile.n * BN + side * NC;      // this side's first column
       const bool cols = n0 < p.N;
-      const float* ws = p.w_scale + static_cast<int64_t>(cols ? wb : 0) * kb;
-      uint64_t acc[NC / 2];
+      float acc[NC];
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
-      float as_next = __ldcg(as), w0_next = __ldcg(ws), w1_next = kGated ? __ldcg(ws + static_cast<int64_t>(nb) * kb) : 0.0f;
-      for (int b = 0; b < kb; ++b) {
-        const float f0 = as_next * w0_next, f1 = as_next * w1_next;
-        if (b + 1 < kb) {
-          as_next = __ldcg(as + (b + 1) * p.a_scale_ld);
-          w0_next = __ldcg(ws + b + 1);
-          if (kGated) w1_next = __ldcg(ws + static_cast<int64_t>(nb) * kb + b + 1);
-        }
-        if (!dead && !__all_sync(0xffffffffu, wait(&filled[buf], bph))) dead = true;
+      for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
+#pragma unroll 1
+      for (int b0 = 0; b0 < kb; b0 += G) {
+        if (!dead && !__all_sync(0xffffffffu, wait(&filled[half], hph))) dead = true;
         if (!dead) {
           tc_fence_after();
+          const auto release = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&drained[half]);
+          };
           if (warp_live) {
-            // gated: the first half of the registers gate, the second up
+            const int n = min(G, kb - b0);
+            const float* sc = scales + take * (G * kScaleRow);
+            // piece c of the 128 columns that a thread has in a half: block c * CH / NC of the group, from column c * CH % NC
+            // of the thread's; gated: its first half gate, its second up
             const auto at = [&](int c) {
-              return lanes + buf * BN + (kGated ? (c >= NC / 2 ? kBlock + c - NC / 2 : c) + half * (NC / 2) : half * NC + c);
+              const int u = c * CH / NC, col = c * CH % NC;
+              return lanes + half * kHalf + u * BN +
+                     (kGated ? (col >= NC / 2 ? kBlock + col - NC / 2 : col) + side * (NC / 2) : side * NC + col);
             };
-            uint32_t v[2][CH];
-            tmem_ld(at(0), v[0]);
+            const auto block = [&](int c) { return c * CH / NC; };
+            const auto there = [&](int c) { return block(c) == 0 || block(c) < n; };
+            const auto column = [&](int c) { return c * CH % NC; };
+            const auto factor = [&](int c) {
+              const int w = kGated ? column(c) >= NC / 2 : BN == 256 ? side : 0;
+              return sc[block(c) * kScaleRow + r] * sc[block(c) * kScaleRow + kRows + w];
+            };
+            const auto add = [&](int c, uint32_t (&x)[CH], float f) {
 #pragma unroll
-            for (int c = 0; c < NC; c += CH) {
-              uint32_t (&x)[CH] = v[(c / CH) & 1];
-              tmem_ld_wait();
-              loaded(x);
-              if (c + CH < NC) tmem_ld(at(c + CH), v[(c / CH + 1) & 1]);
-              const float f = kGated && c >= NC / 2 ? f1 : f0;
-              const uint64_t ff = f32x2(f, f);
+              for (int i = 0; i < CH; ++i) fma_loaded(acc[column(c) + i], x[i], f);
+            };
+            uint32_t v[LOADS][CH];
+            float f[LOADS];
 #pragma unroll
-              for (int i = 0; i < CH / 2; ++i)
-                acc[c / 2 + i] = fma_f32x2(f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), ff, acc[c / 2 + i]);
+            for (int i = 0; i < LOADS; ++i)
+              if (there(i)) tmem_ld(at(i), v[i]);
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) f[i] = factor(i);
+            tmem_ld_wait();
+            const bool more = there(LOADS);
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+              if (there(i)) add(i, v[i], f[i]);
+              if (there(LOADS + i)) tmem_ld(at(LOADS + i), v[i]);
             }
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) f[i] = factor(LOADS + i);
+            tmem_ld_wait();
+            // the half and its scales are in registers: the next group may have both
+            release();
+            if (more) {
+#pragma unroll
+              for (int i = 0; i < LOADS; ++i)
+                if (there(LOADS + i)) add(LOADS + i, v[i], f[i]);
+            }
+          } else {
+            release();
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&drained[buf]);
         }
-        if (++buf == C::kBufs) {
-          buf = 0;
-          bph ^= 1u;
-        }
+        take = (take + 1) & (C::kSlots - 1);
+        half ^= 1;
+        if (half == 0) hph ^= 1u;
       }
       if constexpr (kGated) {
         constexpr int H = NC / 2;              // elements of the output per thread
         float h[H], m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < H; i += 2) {
-          float g[2], u[2];
-          f32x2_parts(acc[i / 2], g[0], g[1]);
-          f32x2_parts(acc[H / 2 + i / 2], u[0], u[1]);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            h[i + q] = n0 + i + q < p.N ? __fdiv_rn(g[q], 1.0f + expf(-g[q])) * u[q] : 0.0f;
-            m = fmaxf(m, fabsf(h[i + q]));
-          }
+        for (int i = 0; i < H; ++i) {
+          h[i] = n0 + i < p.N ? silu(acc[i]) * acc[H + i] : 0.0f;
+          m = fmaxf(m, fabsf(h[i]));
         }
-        float* mine = amax + (turn * 2 + half) * kRows;
-        mine[r] = m;
+        amax[(turn * 2 + side) * kRows + r] = m;
         sums_barrier();
-        m = fmaxf(m, amax[(turn * 2 + (half ^ 1)) * kRows + r]);
-        const float s = block_scale(m), rs = __fdiv_rn(1.0f, s);
-        const bool plain = block_scale_plain(s);
+        m = fmaxf(m, amax[(turn * 2 + (side ^ 1)) * kRows + r]);
+        const float s = block_scale(m);
+        const BlockDiv by = block_div(s);
         if (live && !dead) {
           uint8_t* out = p.inner + static_cast<int64_t>(slot) * p.N + n0;
 #pragma unroll
@@ -417,12 +487,12 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
             for (int i = 0; i < 4; ++i) {
               float d[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) d[e] = plain ? div_rn_by_recip(h[c + 4 * i + e], s, rs) : __fdiv_rn(h[c + 4 * i + e], s);
+              for (int e = 0; e < 4; ++e) d[e] = div_rn_by_recip(h[c + 4 * i + e], by.s, by.rs);
               q[i] = cvt_e4m3x2(d[0], d[1]) | (cvt_e4m3x2(d[2], d[3]) << 16);
             }
             if (n0 + c < p.N) *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
           }
-          if (half == 0) p.inner_scale[static_cast<int64_t>(tile.n) * p.M + slot] = s;
+          if (side == 0) p.inner_scale[static_cast<int64_t>(tile.n) * p.M + slot] = s;
         }
       } else if (live && cols && !dead) {
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.Y) + slot * p.ldy + n0;
@@ -431,9 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
           uint32_t q[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float lo, hi;
-            f32x2_parts(acc[c / 2 + i], lo, hi);
-            q[i] = pack_bf16x2(lo, hi);
+            q[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
           }
           if (p.wide_store && n0 + c + 16 <= p.N) {
             st_global_v8(out + c, q);
@@ -451,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::kTmemCols);
+    tmem_dealloc(tmem_base, 2 * kHalf);
   }
 }
 
@@ -466,14 +534,14 @@ int launch(const BlockGemmArgs& a) {
   p.ldy = a.ldy;
   p.inner = a.inner;
   p.inner_scale = a.inner_scale;
-  p.plan = a.plan;
+  p.offsets = a.offsets;
+  p.out_rows = a.out_rows;
   p.status = a.status;
   p.M = a.M;
   p.N = a.N;
   p.K = a.K;
   p.kb = n_blocks(a.K);
   p.experts = kGrouped ? a.experts : 1;
-  p.slot_div = a.slot_div;
   p.early_weights = a.early_weights;
   const int width = kGated ? kBlock : BN;
   p.n_tiles = (a.N + width - 1) / width;
@@ -482,7 +550,10 @@ int launch(const BlockGemmArgs& a) {
   // tiles, and rows of the tensor maps, are counted in 31 bits
   const int64_t tiles = (static_cast<int64_t>(a.M) / kRows + 1 + (kGrouped ? p.experts : 0)) * p.n_tiles;
   if (tiles >= (int64_t{1} << 31) || w_rows >= (int64_t{1} << 31)) return EPILORA_ERR_UNSUPPORTED;
-  int rc = make_tma_2d_u8(&p.tmA, a.A, a.a_rows, a.K, a.K, kGrouped ? 1 : kRows, kBlock, true);
+  // rows of A are copied in boxes of 32 where a tile has few of them, or the rows that follow are not its own
+  const int per_tile = kGrouped ? a.M / p.experts : a.M;
+  p.box_rows = per_tile >= 96 ? kRows : 32;
+  int rc = make_tma_2d_u8(&p.tmA, a.A, a.M, a.K, a.K, p.box_rows, kBlock, true);
   if (rc == EPILORA_OK) rc = make_tma_2d_u8(&p.tmB, a.W, w_rows, a.K, a.K, kGated ? kRows : BN, kBlock, true);
   if (rc != EPILORA_OK) return rc;
   const int extra = 1024 + C::kMisc + (kGrouped ? 2 * (p.experts + 1) * 4 : 0);
@@ -505,10 +576,30 @@ int launch(const BlockGemmArgs& a) {
 
 }  // namespace
 
+// Tiles of BN columns: as wide as pays. A block of K costs a CTA 0.50, 0.31, 0.21 or 0.20 us at 256, 128, 64 and 32
+// columns; a call takes as many of them as its fullest CTA has tiles (one token, 4096 -> 6144: 20.7, 14.4, 11.5 and
+// 17.6 us; 509 tokens, 2064 -> 1000: 46, 28, 18 and 15; 2048 tokens, 8192 -> 28672: 409, 568, 854 and 1416).
+static int tile_width(int M, int N) {
+  const int widths[4] = {256, 128, 64, 32}, costs[4] = {50, 31, 21, 20};
+  const int64_t sms = num_sms(), mt = (M + kRows - 1) / kRows;
+  int best = 256;
+  int64_t least = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t cost = (mt * ((N + widths[i] - 1) / widths[i]) + sms - 1) / sms * costs[i];
+    if (i == 0 || cost < least) best = widths[i], least = cost;
+  }
+  return best;
+}
+
 int launch_block_gemm(const BlockGemmArgs& a) {
   if (a.gated) return launch<256, true, true>(a);
-  if (a.grouped) return launch<128, true, false>(a);
-  return launch<128, false, false>(a);
+  if (a.grouped) return launch<256, true, false>(a);
+  switch (tile_width(a.M, a.N)) {
+    case 256: return launch<256, false, false>(a);
+    case 128: return launch<128, false, false>(a);
+    case 64: return launch<64, false, false>(a);
+    default: return launch<32, false, false>(a);
+  }
 }
 
 }  // namespace epi

@@ -50,12 +50,13 @@ __global__ void __launch_bounds__(kQuantThreads) block_quant_weight_kernel(const
     m = fmaxf(m, amax8(v[i]));
   }
   const float s = block_scale(block_max(m, red));
+  const BlockDiv by = block_div(s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int n = nb * kBlock + g + i * kQuantGroups;
     if (n < p.N && k < p.K)
       *reinterpret_cast<uint2*>(p.Wq + static_cast<int64_t>(n) * p.K + k) =
-          block_scale_plain(s) ? quant8_e4m3_rs(v[i], s, __fdiv_rn(1.0f, s)) : quant8_e4m3(v[i], s);
+          quant8_e4m3_rs(v[i], by.s, by.rs);
   }
   if (threadIdx.x == 0) p.scale[static_cast<int64_t>(nb) * kb + b] = s;
 }

@@ -16,20 +16,30 @@ __device__ __forceinline__ float amax8(const uint4& v) {
   return m;
 }
 __device__ __forceinline__ float block_scale(float amax) { return __fdiv_rn(fmaxf(amax, kAmaxFloor), kE4M3Max); }
-// Scales lie above 2^-49 (the floor); above 2^100 (an infinity in the block)
-// the corrected reciprocal would not do.
-__device__ __forceinline__ bool block_scale_plain(float s) { return s <= 0x1p100f; }
+// x / s rounded to nearest by the corrected reciprocal product (quant_row.cuh;
+// scales lie above 2^-49, the floor). An infinity in the block makes s
+// infinite: with rs = 0 and 0 for s the same three operations give 0, or NaN
+// for the infinity, as the division would.
+struct BlockDiv {
+  float s, rs;
+};
+__device__ __forceinline__ BlockDiv block_div(float scale) {
+  return BlockDiv{isinf(scale) ? 0.0f : scale, __fdiv_rn(1.0f, scale)};
+}
 
 // One CTA's share of a quantizer grid: kQuantGroups groups of 16 lanes, each
 // with kUnits blocks. The CTA covers 2^rt_log2 rows (so that the scales of
-// consecutive rows are written together) by as many blocks as remain.
+// consecutive rows are written together) by as many blocks as remain. With
+// `rows`, row m goes to the rows rows[m * top] .. rows[m * top + top - 1] of
+// the output (none where that is negative).
 constexpr int kQuantThreads = 256;
 constexpr int kQuantGroups = kQuantThreads / 16;
 
 template <int kUnits>
-__device__ __forceinline__ void quant_tile(const __nv_bfloat16* __restrict__ X, int M, int K, int64_t ldx,
-                                           uint8_t* __restrict__ Xq, float* __restrict__ scale, int64_t scale_ld,
-                                           int rt_log2, int tile) {
+__device__ __forceinline__ void quant_tile(const __nv_bfloat16* X, int M, int K, int64_t ldx,
+                                           uint8_t* Xq, float* scale, int64_t scale_ld,
+                                           int rt_log2, int tile, const int32_t* rows = nullptr,
+                                           int top = 1) {
   const int kb = n_blocks(K);
   const int per = kUnits * kQuantGroups >> rt_log2;      // blocks of a row in a tile
   const int across = (kb + per - 1) / per;
@@ -53,9 +63,14 @@ __device__ __forceinline__ void quant_tile(const __nv_bfloat16* __restrict__ X, 
     const int b = b0 + i * step, k = b * kBlock + lane * 8;
     const float s = block_scale(m);
     if (live && k < K) {
-      const uint2 q = block_scale_plain(s) ? quant8_e4m3_rs(v[i], s, __fdiv_rn(1.0f, s)) : quant8_e4m3(v[i], s);
-      *reinterpret_cast<uint2*>(Xq + static_cast<int64_t>(row) * K + k) = q;
-      if (lane == 0) scale[static_cast<int64_t>(b) * scale_ld + row] = s;
+      const BlockDiv by = block_div(s);
+      const uint2 q = quant8_e4m3_rs(v[i], by.s, by.rs);
+      for (int j = 0; j < top; ++j) {
+        const int to = rows == nullptr ? row : rows[static_cast<int64_t>(row) * top + j];
+        if (to < 0) continue;
+        *reinterpret_cast<uint2*>(Xq + static_cast<int64_t>(to) * K + k) = q;
+        if (lane == 0) scale[static_cast<int64_t>(b) * scale_ld + to] = s;
+      }
     }
   }
 }

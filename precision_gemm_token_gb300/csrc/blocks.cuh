@@ -22,42 +22,63 @@ int launch_block_quant(const BlockQuantArgs& a);
 // A weight [N][K] with one scale per 128 x 128 block: codes [N][K], scale [n_blocks(N)][n_blocks(K)].
 int launch_block_quant_weight(const void* W, int N, int K, int64_t ldw, uint8_t* Wq, float* scale, cudaStream_t stream);
 
-// The rows of a batch by expert: expert e owns rows[offsets[e]] .. rows[offsets[e + 1] - 1], each a slot
-// (token * top + place among the token's choices).
+// The rows of a batch by expert. Slot j of token t (number t * top + j) is
+// row `row` of the sorted batch; expert e owns the rows [offsets[e], offsets[e + 1]).
 struct MoePlan {
   int32_t* offsets;     // [experts + 1]
-  int32_t* rows;        // [tokens * top]
+  int32_t* slots;       // row -> slot
+  int32_t* rows;        // slot -> row, -1: no expert
 };
-struct MoePrepArgs {
+struct MoePlanArgs {
   const int32_t* ids;   // [tokens][top]; outside [0, experts): no expert there
   int tokens, top, experts;
   MoePlan plan;
-  int quant;            // quantize x into q as well, and zero the rows of `inner` that have no expert
-  BlockQuantArgs q;
-  uint8_t* inner;       // [tokens * top][inner_dim]
-  float* inner_scale;   // [n_blocks(inner_dim)][tokens * top]
-  int inner_dim;
   int* status;
   cudaStream_t stream;
 };
-int launch_moe_prep(const MoePrepArgs& a);
+int launch_moe_plan(const MoePlanArgs& a);
+
+// The activations of the slots, by row: token rows quantized and written to
+// the rows of their slots (scales [n_blocks(K)][slots]). `inner`, where given,
+// has zeros written for the slots without an expert.
+struct MoeScatterArgs {
+  BlockQuantArgs q;     // M = tokens; scale_ld = tokens * top
+  int top;
+  const int32_t* rows;
+  uint8_t* inner;       // [tokens * top][inner_dim]
+  float* inner_scale;   // [n_blocks(inner_dim)][tokens * top]
+  int inner_dim;
+};
+int launch_moe_scatter(const MoeScatterArgs& a);
+
+// Quantized rows by slot -> by row.
+struct MoeGatherArgs {
+  const uint8_t* src;
+  const float* src_scale;
+  uint8_t* dst;
+  float* dst_scale;
+  int slots, K;         // rows of both arrays, bytes of a row
+  const int32_t* rows;
+  cudaStream_t stream;
+};
+int launch_moe_gather(const MoeGatherArgs& a);
 
 // The block-scaled product: rows of A times rows of W.
 //   plain:   Y[m][n] = bf16( sum_b a_scale[b][m] w_scale[n / 128][b] sum_{k in b} A[m][k] W[n][k] ), m < M
-//   grouped: the rows of expert e times W[e]; A row = slot / slot_div, output row = slot
-//   gated:   W[e] is [2][N][K] (gate, up); the output is block-quantized silu(gate) * up
+//   grouped: the rows [offsets[e], offsets[e + 1]) times W[e]
+//   gated:   grouped, W[e] is [2][N][K] (gate, up); the output is block-quantized silu(gate) * up
 struct BlockGemmArgs {
-  int M, N, K;          // grouped: M = all slots
-  const uint8_t* A;     // codes [a_rows][K]
-  int64_t a_rows;
+  int M, N, K;          // grouped: M = rows that the arrays have
+  const uint8_t* A;     // codes [M][K]
   const float* a_scale; // [n_blocks(K)][a_scale_ld]
   int64_t a_scale_ld;
   const uint8_t* W;
   const float* w_scale;
   void* Y;              // bf16 [M][ldy]
   int64_t ldy;
-  int grouped, gated, experts, slot_div;
-  MoePlan plan;
+  int grouped, gated, experts;
+  const int32_t* offsets;
+  const int32_t* out_rows;   // output row of each row (NULL: the same)
   uint8_t* inner;       // gated: codes [M][N] and scales [n_blocks(N)][M]
   float* inner_scale;
   int early_weights;    // the weights may be read before the preceding kernel has finished

@@ -32,9 +32,9 @@ struct Cut {
 
 struct Parts {
   MoePlan plan;
-  uint8_t *xq, *inner;
+  uint8_t *xq, *inner;           // by row
   float *x_scale, *inner_scale;
-  void* out;
+  void* out;                     // by slot
   size_t bytes;
 };
 Parts cut_moe(void* ws, int what, int tokens, int top, int experts, int hidden, int inner) {
@@ -42,16 +42,17 @@ Parts cut_moe(void* ws, int what, int tokens, int top, int experts, int hidden, 
   Parts p{};
   const size_t slots = static_cast<size_t>(tokens) * top;
   p.plan.offsets = c.take<int32_t>(experts + 1);
+  p.plan.slots = c.take<int32_t>(slots);
   p.plan.rows = c.take<int32_t>(slots);
   if (what & EPILORA_MOE_UP) {
-    p.xq = c.take<uint8_t>(static_cast<size_t>(tokens) * hidden);
-    p.x_scale = c.take<float>(static_cast<size_t>(n_blocks(hidden)) * tokens);
+    p.xq = c.take<uint8_t>(slots * hidden);
+    p.x_scale = c.take<float>(n_blocks(hidden) * slots);
   }
-  if (what == (EPILORA_MOE_UP | EPILORA_MOE_DOWN)) {
+  if (what & EPILORA_MOE_DOWN) {
     p.inner = c.take<uint8_t>(slots * inner);
-    p.inner_scale = c.take<float>(static_cast<size_t>(n_blocks(inner)) * slots);
+    p.inner_scale = c.take<float>(n_blocks(inner) * slots);
+    p.out = c.take<uint16_t>(slots * hidden);
   }
-  if (what & EPILORA_MOE_DOWN) p.out = c.take<uint16_t>(slots * hidden);
   p.bytes = c.used;
   return p;
 }
@@ -71,39 +72,36 @@ struct MoeCall {
   cudaStream_t stream;
 };
 
-int enqueue_prep(const MoeCall& m, const Parts& p, const void* X, int64_t ldx, uint8_t* inner, float* inner_scale) {
-  MoePrepArgs a{};
-  a.ids = m.ids;
-  a.tokens = m.tokens;
-  a.top = m.top;
-  a.experts = m.experts;
-  a.plan = p.plan;
-  a.quant = X != nullptr;
-  if (a.quant) a.q = BlockQuantArgs{X, m.tokens, m.hidden, ldx, p.xq, p.x_scale, m.tokens, m.stream};
-  a.inner = inner;
-  a.inner_scale = inner_scale;
-  a.inner_dim = m.inner;
-  a.status = m.status;
-  a.stream = m.stream;
-  return launch_moe_prep(a);
+int enqueue_plan(const MoeCall& m, const Parts& p) {
+  return launch_moe_plan(MoePlanArgs{m.ids, m.tokens, m.top, m.experts, p.plan, m.status, m.stream});
 }
 
-int enqueue_up(const MoeCall& m, const Parts& p, const uint8_t* W, const float* w_scale, uint8_t* inner,
-               float* inner_scale) {
+// (by_slot: the output in the order of the slots, zeros where there is no expert)
+int enqueue_up(const MoeCall& m, const Parts& p, const void* X, int64_t ldx, const uint8_t* W, const float* w_scale,
+               uint8_t* inner, float* inner_scale, bool by_slot) {
+  const int slots = m.tokens * m.top;
+  MoeScatterArgs s{};
+  s.q = BlockQuantArgs{X, m.tokens, m.hidden, ldx, p.xq, p.x_scale, slots, m.stream};
+  s.top = m.top;
+  s.rows = p.plan.rows;
+  s.inner = by_slot ? inner : nullptr;
+  s.inner_scale = inner_scale;
+  s.inner_dim = m.inner;
+  const int rc = launch_moe_scatter(s);
+  if (rc != EPILORA_OK) return rc;
   BlockGemmArgs g{};
-  g.M = m.tokens * m.top;
+  g.M = slots;
   g.N = m.inner;
   g.K = m.hidden;
   g.A = p.xq;
-  g.a_rows = m.tokens;
   g.a_scale = p.x_scale;
-  g.a_scale_ld = m.tokens;
+  g.a_scale_ld = slots;
   g.W = W;
   g.w_scale = w_scale;
   g.grouped = g.gated = 1;
   g.experts = m.experts;
-  g.slot_div = m.top;
-  g.plan = p.plan;
+  g.offsets = p.plan.offsets;
+  g.out_rows = by_slot ? p.plan.slots : nullptr;
   g.inner = inner;
   g.inner_scale = inner_scale;
   g.status = m.status;
@@ -111,15 +109,15 @@ int enqueue_up(const MoeCall& m, const Parts& p, const uint8_t* W, const float* 
   return launch_block_gemm(g);
 }
 
-int enqueue_down(const MoeCall& m, const Parts& p, const uint8_t* inner, const float* inner_scale, const uint8_t* W,
-                 const float* w_scale, const float* weights, void* Y, int64_t ldy) {
+// from p.inner, by row
+int enqueue_down(const MoeCall& m, const Parts& p, const uint8_t* W, const float* w_scale, const float* weights, void* Y,
+                 int64_t ldy) {
   BlockGemmArgs g{};
   g.M = m.tokens * m.top;
   g.N = m.hidden;
   g.K = m.inner;
-  g.A = inner;
-  g.a_rows = g.M;
-  g.a_scale = inner_scale;
+  g.A = p.inner;
+  g.a_scale = p.inner_scale;
   g.a_scale_ld = g.M;
   g.W = W;
   g.w_scale = w_scale;
@@ -127,8 +125,8 @@ int enqueue_down(const MoeCall& m, const Parts& p, const uint8_t* inner, const f
   g.ldy = m.hidden;
   g.grouped = 1;
   g.experts = m.experts;
-  g.slot_div = 1;
-  g.plan = p.plan;
+  g.offsets = p.plan.offsets;
+  g.out_rows = p.plan.slots;
   g.status = m.status;
   g.stream = m.stream;
   const int rc = launch_block_gemm(g);
@@ -172,14 +170,12 @@ EPILORA_API int epilora_block_matmul(int M, int N, int K, const uint8_t* Xq, con
   g.N = N;
   g.K = K;
   g.A = Xq;
-  g.a_rows = M;
   g.a_scale = x_scale;
   g.a_scale_ld = x_scale_ld;
   g.W = Wq;
   g.w_scale = w_scale;
   g.Y = Y;
   g.ldy = ldy;
-  g.slot_div = 1;
   g.status = status_dev;
   g.stream = static_cast<cudaStream_t>(stream);
   return launch_block_gemm(g);
@@ -208,14 +204,12 @@ EPILORA_API int epilora_block_linear(int M, int N, int K, const void* X, int64_t
   g.N = N;
   g.K = K;
   g.A = xq;
-  g.a_rows = M;
   g.a_scale = xs;
   g.a_scale_ld = M;
   g.W = Wq;
   g.w_scale = w_scale;
   g.Y = Y;
   g.ldy = ldy;
-  g.slot_div = 1;
   g.early_weights = 1;      // (the quantizer lets this kernel start only once everything before it is done)
   g.status = status_dev;
   g.stream = s;
@@ -277,8 +271,8 @@ EPILORA_API int epilora_moe_experts_up(int tokens, int top, int experts, int hid
     return EPILORA_ERR_WORKSPACE;
   const Parts p = cut_moe(workspace, EPILORA_MOE_UP, tokens, top, experts, hidden, inner);
   const MoeCall m{tokens, top, experts, hidden, inner, ids, status_dev, static_cast<cudaStream_t>(stream)};
-  rc = enqueue_prep(m, p, X, ldx, Hq, h_scale);
-  return rc != EPILORA_OK ? rc : enqueue_up(m, p, Wup, wup_scale, Hq, h_scale);
+  rc = enqueue_plan(m, p);
+  return rc != EPILORA_OK ? rc : enqueue_up(m, p, X, ldx, Wup, wup_scale, Hq, h_scale, true);
 }
 
 EPILORA_API int epilora_moe_experts_down(int tokens, int top, int experts, int hidden, int inner, const uint8_t* Hq,
@@ -295,8 +289,11 @@ EPILORA_API int epilora_moe_experts_down(int tokens, int top, int experts, int h
     return EPILORA_ERR_WORKSPACE;
   const Parts p = cut_moe(workspace, EPILORA_MOE_DOWN, tokens, top, experts, hidden, inner);
   const MoeCall m{tokens, top, experts, hidden, inner, ids, status_dev, static_cast<cudaStream_t>(stream)};
-  rc = enqueue_prep(m, p, nullptr, 0, nullptr, nullptr);
-  return rc != EPILORA_OK ? rc : enqueue_down(m, p, Hq, h_scale, Wdown, wdown_scale, weights, Y, ldy);
+  rc = enqueue_plan(m, p);
+  if (rc == EPILORA_OK)
+    rc = launch_moe_gather(
+        MoeGatherArgs{Hq, h_scale, p.inner, p.inner_scale, tokens * top, inner, p.plan.rows, m.stream});
+  return rc != EPILORA_OK ? rc : enqueue_down(m, p, Wdown, wdown_scale, weights, Y, ldy);
 }
 
 EPILORA_API int epilora_moe_experts(int tokens, int top, int experts, int hidden, int inner, const void* X, int64_t ldx,
@@ -316,9 +313,9 @@ EPILORA_API int epilora_moe_experts(int tokens, int top, int experts, int hidden
     return EPILORA_ERR_WORKSPACE;
   const Parts p = cut_moe(workspace, kBoth, tokens, top, experts, hidden, inner);
   const MoeCall m{tokens, top, experts, hidden, inner, ids, status_dev, static_cast<cudaStream_t>(stream)};
-  rc = enqueue_prep(m, p, X, ldx, p.inner, p.inner_scale);
-  if (rc == EPILORA_OK) rc = enqueue_up(m, p, Wup, wup_scale, p.inner, p.inner_scale);
-  return rc != EPILORA_OK ? rc : enqueue_down(m, p, p.inner, p.inner_scale, Wdown, wdown_scale, weights, Y, ldy);
+  rc = enqueue_plan(m, p);
+  if (rc == EPILORA_OK) rc = enqueue_up(m, p, X, ldx, Wup, wup_scale, p.inner, p.inner_scale, false);
+  return rc != EPILORA_OK ? rc : enqueue_down(m, p, Wdown, wdown_scale, weights, Y, ldy);
 }
 
 }  // extern "C"

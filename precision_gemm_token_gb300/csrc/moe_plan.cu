@@ -1,38 +1,55 @@
-// The rows of a mixture-of-experts batch by expert, with the quantization of
-// the activations beside it, and the weighted sum of the experts' outputs.
+// The rows of a mixture-of-experts batch by expert, the activations in that
+// order, and the weighted sum of the experts' outputs.
 #include "block_quant.cuh"
 
 namespace epi {
 
 namespace {
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 512;
 constexpr int kMaxExperts = EPILORA_MOE_MAX_EXPERTS;
 
-// Offsets and rows by counting; one CTA. The order of the rows of an expert
-// is the order of the additions: no result depends on it.
-__device__ void plan_block(const MoePrepArgs& a) {
-  __shared__ int count[kMaxExperts];
+// Counting sort of the slots by expert. A cluster of CTAs, each a run of
+// slots: counts in shared memory, exchanged over the cluster; a CTA's rows of
+// an expert follow those of the CTAs before it. Within a CTA the order is that
+// of the additions: no result depends on it.
+__global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const __grid_constant__ MoePlanArgs a) {
+  __shared__ int count[kMaxExperts];     // this CTA's, read by the others
+  __shared__ int next[kMaxExperts];      // the row of the next slot
   __shared__ int sums[kPlanThreads / 32];
+  pdl_wait_primary();
+  pdl_allow_dependents();
   const int n = a.tokens * a.top;
+  const int ctas = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);
+  const int run = (n + ctas - 1) / ctas, first = min(run * rank, n), last = min(first + run, n);
   for (int e = threadIdx.x; e < a.experts; e += kPlanThreads) count[e] = 0;
   __syncthreads();
   bool bad = false;
-  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+#pragma unroll 4
+  for (int i = first + threadIdx.x; i < last; i += kPlanThreads) {
     const int e = a.ids[i];
     if (e >= 0 && e < a.experts) atomicAdd(&count[e], 1);
-    if (e >= a.experts) bad = true;
+    bad |= e >= a.experts;
   }
   if (bad) record_status(a.status, EPILORA_ERR_INVALID_ARG);
-  __syncthreads();
-  // exclusive sums: each thread kMaxExperts / kPlanThreads consecutive experts
+  cluster_arrive();
+  cluster_wait();
+  // exclusive sums over the experts of all CTAs' counts, a thread kPer consecutive experts
   constexpr int kPer = kMaxExperts / kPlanThreads;
-  int mine[kPer], total = 0;
+  int at[kPer], total = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = threadIdx.x * kPer + i;
-    mine[i] = total;
-    total += e < a.experts ? count[e] : 0;
+    at[i] = total;
+    if (e < a.experts) {
+      const uint32_t mine = smem_u32(&count[e]);
+      for (int c = 0; c < ctas; ++c) {
+        int v;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_to_cta(mine, c)) : "memory");
+        total += v;
+        if (c < rank) at[i] += v;
+      }
+    }
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int before = total;
@@ -49,43 +66,64 @@ __device__ void plan_block(const MoePrepArgs& a) {
   for (int i = 0; i < kPer; ++i) {
     const int e = threadIdx.x * kPer + i;
     if (e < a.experts) {
-      count[e] = before + mine[i];
-      a.plan.offsets[e] = before + mine[i];
-      if (e == a.experts - 1) a.plan.offsets[a.experts] = before + total;
+      next[e] = before + at[i];
+      if (rank == 0) a.plan.offsets[e] = before + at[i];
     }
   }
+  if (rank == 0 && threadIdx.x == kPlanThreads - 1) a.plan.offsets[a.experts] = before + total;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+#pragma unroll 4
+  for (int i = first + threadIdx.x; i < last; i += kPlanThreads) {
     const int e = a.ids[i];
-    if (e >= 0 && e < a.experts) a.plan.rows[atomicAdd(&count[e], 1)] = i;
+    int row = -1;
+    if (e >= 0 && e < a.experts) {
+      row = atomicAdd(&next[e], 1);
+      a.plan.slots[row] = i;
+    }
+    a.plan.rows[i] = row;
   }
+  cluster_arrive();      // (nobody leaves while another may read its counts)
+  cluster_wait();
 }
 
-struct PrepParams {
-  MoePrepArgs a;
+struct ScatterParams {
+  MoeScatterArgs a;
   int rt_log2, tiles;
 };
 
-// CTA 0 the plan, the others the quantizer's tiles and then the slots that
-// have no expert.
-__global__ void __launch_bounds__(kPlanThreads) moe_prep_kernel(const __grid_constant__ PrepParams p) {
+__global__ void __launch_bounds__(kQuantThreads) moe_scatter_kernel(const __grid_constant__ ScatterParams p) {
   pdl_wait_primary();
   pdl_allow_dependents();
-  if (blockIdx.x == 0) {
-    plan_block(p.a);
-    return;
-  }
-  const MoePrepArgs& a = p.a;
-  quant_tile<1>(static_cast<const __nv_bfloat16*>(a.q.X), a.q.M, a.q.K, a.q.ldx, a.q.Xq, a.q.scale, a.q.scale_ld,
-                p.rt_log2, static_cast<int>(blockIdx.x) - 1);
-  const int n = a.tokens * a.top, nb = n_blocks(a.inner_dim);
-  for (int i = static_cast<int>(blockIdx.x) - 1; i < n; i += p.tiles) {
-    const int e = a.ids[i];
-    if (e >= 0 && e < a.experts) continue;
+  const MoeScatterArgs& a = p.a;
+  quant_tile<1>(static_cast<const __nv_bfloat16*>(a.q.X), a.q.M, a.q.K, a.q.ldx, a.q.Xq, a.q.scale, a.q.scale_ld, p.rt_log2,
+                static_cast<int>(blockIdx.x), a.rows, a.top);
+  if (a.inner == nullptr) return;
+  const int n = a.q.M * a.top, nb = n_blocks(a.inner_dim);
+  for (int i = static_cast<int>(blockIdx.x); i < n; i += p.tiles) {
+    if (a.rows[i] >= 0) continue;
     uint4* row = reinterpret_cast<uint4*>(a.inner + static_cast<int64_t>(i) * a.inner_dim);
-    for (int c = threadIdx.x; c < a.inner_dim / 16; c += kPlanThreads) row[c] = make_uint4(0, 0, 0, 0);
-    for (int b = threadIdx.x; b < nb; b += kPlanThreads) a.inner_scale[static_cast<int64_t>(b) * n + i] = 0.0f;
+    for (int c = threadIdx.x; c < a.inner_dim / 16; c += kQuantThreads) row[c] = make_uint4(0, 0, 0, 0);
+    for (int b = threadIdx.x; b < nb; b += kQuantThreads) a.inner_scale[static_cast<int64_t>(b) * n + i] = 0.0f;
   }
+}
+
+// A warp per slot.
+constexpr int kGatherThreads = 256;
+
+__global__ void __launch_bounds__(kGatherThreads) moe_gather_kernel(const __grid_constant__ MoeGatherArgs a) {
+  pdl_wait_primary();
+  pdl_allow_dependents();
+  const int slot = static_cast<int>(blockIdx.x) * (kGatherThreads / 32) + static_cast<int>(threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (slot >= a.slots) return;
+  const int row = a.rows[slot];
+  if (row < 0) return;
+  const uint4* src = reinterpret_cast<const uint4*>(a.src + static_cast<int64_t>(slot) * a.K);
+  uint4* dst = reinterpret_cast<uint4*>(a.dst + static_cast<int64_t>(row) * a.K);
+#pragma unroll 4
+  for (int c = lane; c < a.K / 16; c += 32) dst[c] = src[c];
+  for (int b = lane; b < n_blocks(a.K); b += 32)
+    a.dst_scale[static_cast<int64_t>(b) * a.slots + row] = a.src_scale[static_cast<int64_t>(b) * a.slots + slot];
 }
 
 // A CTA sums 2048 columns of one token.
@@ -122,15 +160,36 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const __gr
 
 }  // namespace
 
-int launch_moe_prep(const MoePrepArgs& a) {
-  PrepParams p{a, 0, 0};
-  if (a.quant) {
-    p.rt_log2 = quant_rows_log2(a.q.M);
-    const int64_t tiles = quant_tiles(a.q.M, a.q.K, 1, p.rt_log2);
-    if (tiles >= 0x7fffffff) return EPILORA_ERR_UNSUPPORTED;
-    p.tiles = static_cast<int>(tiles);
-  }
-  return launch_dependent(moe_prep_kernel, static_cast<unsigned>(p.tiles + 1), kPlanThreads, 0, a.stream, p);
+int launch_moe_plan(const MoePlanArgs& a) {
+  // one CTA counts a few thousand slots as fast as a cluster does
+  const int64_t n = static_cast<int64_t>(a.tokens) * a.top;
+  const unsigned ctas = n <= 4 * kPlanThreads ? 1 : 8;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kPlanThreads, 1, 1);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, moe_plan_kernel, a) == cudaSuccess ? EPILORA_OK : EPILORA_ERR_CUDA;
+}
+
+int launch_moe_scatter(const MoeScatterArgs& a) {
+  ScatterParams p{a, quant_rows_log2(a.q.M), 0};
+  const int64_t tiles = quant_tiles(a.q.M, a.q.K, 1, p.rt_log2);
+  if (tiles > 0x7fffffff) return EPILORA_ERR_UNSUPPORTED;
+  p.tiles = static_cast<int>(tiles);
+  return launch_dependent(moe_scatter_kernel, static_cast<unsigned>(tiles), kQuantThreads, 0, a.q.stream, p);
+}
+
+int launch_moe_gather(const MoeGatherArgs& a) {
+  constexpr int per = kGatherThreads / 32;
+  return launch_dependent(moe_gather_kernel, static_cast<unsigned>((a.slots + per - 1) / per), kGatherThreads, 0, a.stream, a);
 }
 
 int launch_moe_combine(const MoeCombineArgs& a) {

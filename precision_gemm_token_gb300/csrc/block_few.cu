@@ -1,0 +1,474 @@
+// The block-scaled products of few rows (decoding): the product turned round,
+// so that the weights are the rows of the MMA.
+//
+// What such a call has to do is to read the weights once. With rows of A as
+// rows of the MMA (block_gemm.cu) a tile of few rows keeps 32 of 128 TMEM lanes
+// busy, so one warp in four, with 128 columns each per block; here 128 rows of
+// W fill the lanes, up to 32 rows of A are the columns, and all summing warps
+// share the work: 16 products a thread and block. A half of TMEM then holds
+// eight blocks, loaded together, so that a load's latency and the barriers are
+// paid once for 128 KB of weights.
+//
+// Roles (384 threads, one CTA per SM):
+//   warp 0       TMA copies through a ring of stages
+//   warp 1       MMA issue (M = 128, N = 32)
+//   warp 2       the scales of the groups to come
+//   warps 4..11  sums: each warp 32 rows of W by half of the rows of A
+// A plain product whose tiles are fewer than the SMs is split along K over the
+// CTAs of a cluster (up to 8): each leaves its sums in the leader's shared
+// memory, which adds them in the order of the CTAs.
+// Gated: a tile is 128 rows of gate and the same of up; a thread has both of
+// an element, and the largest of a token's 128 comes from the four warps that
+// hold them.
+//
+// Bound: the copies of the weights. Every wait is bounded, as in block_gemm.cu.
+#include "block_gemm.cuh"
+
+namespace epi {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTileN = 128;                    // rows of W per tile
+constexpr int kCols = kFewRows;                // rows of A per tile: columns of the MMA
+constexpr int kHalf = 256;
+constexpr int kWBytes = kTileN * kBlock, kABytes = kCols * kBlock;     // of a block
+constexpr int kStagesMax = 12;
+constexpr int kSplitMax = 8;
+// registers: 168 a thread at launch (64,512); the sums' warps take what the others give back
+constexpr int kRegsOther = 48, kRegsSum = 224;
+constexpr int kScaleRow = kCols + 4;           // a block's scales: of the rows, then of the weights (gate, up)
+constexpr int kScaleBlocks = 64;
+constexpr int kMine = kCols / 2;               // rows of A of a summing thread
+constexpr int kMisc = 1024 + 2 * 2 * 4 * kMine * 4 + kScaleBlocks * kScaleRow * 4;     // barriers, amax exchange, scales
+
+struct Params {
+  CUtensorMap tmA, tmB;
+  const float* a_scale;
+  const float* w_scale;
+  int64_t a_scale_ld, ldy;
+  void* Y;
+  uint8_t* inner;
+  float* inner_scale;
+  const int32_t* offsets;
+  const int32_t* out_rows;
+  int* status;
+  int M, N, kb, n_tiles, experts, stages, copy, whole, splits, early_weights;
+};
+
+template <bool kGrouped, bool kGated>
+__global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_constant__ Params p) {
+  constexpr int kParts = kGated ? 2 : 1;       // gate, up
+  constexpr int G = kHalf / (kCols * kParts);  // blocks of a group
+  constexpr int kSlots = kScaleBlocks / G;     // groups in the scales' ring
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int stages = p.stages, copy = kGated ? 1 : p.copy;
+  const uint32_t stage = copy * (kParts * kWBytes + kABytes);      // the blocks' weights, then their rows of A
+  uint8_t* misc = smem + static_cast<size_t>(stages) * stage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc);
+  uint64_t* empty = full + kStagesMax;
+  uint64_t* filled = empty + kStagesMax;       // [2] a half holds a group's products, and the ring its scales
+  uint64_t* drained = filled + 2;              // [2] they have been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* amax = reinterpret_cast<float*>(misc + 1024);                     // [2 turns][2 sides][4 warps][kMine]
+  float* scales = amax + 2 * 2 * 4 * kMine;                                // [kScaleBlocks][kScaleRow]
+  int* offsets = reinterpret_cast<int*>(misc + kMisc);                     // [experts + 1], grouped only
+  int* starts = offsets + p.experts + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kGrouped ? 0 : static_cast<int>(blockIdx.x) % p.splits;
+  // this CTA's blocks of K
+  const int k0 = kGrouped ? 0 : p.kb * rank / p.splits;
+  const int kb = kGrouped ? p.kb : p.kb * (rank + 1) / p.splits - k0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&filled[b], 2);                // the products, and the scales
+      mbar_init(&drained[b], 8);
+    }
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&p.tmA);
+    tma_prefetch_desc(&p.tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 2 * kHalf);
+    tmem_relinquish();
+  }
+  if (kGrouped) {
+    pdl_wait_primary();
+    if (warp == 2) fill_walk<kCols>(p.offsets, p.experts, offsets, starts, lane);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_allow_dependents();
+  const uint32_t tmem_base = *tmem_slot;
+  Walk<kGrouped, kCols> walk(p.M, p.n_tiles, p.experts, offsets, starts);
+  const int first_tile = static_cast<int>(blockIdx.x) / p.splits, step = static_cast<int>(gridDim.x) / p.splits;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag, p.status); };
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegsOther>();
+    if (warp == 0) {
+      // ===== copies =====
+      if (elect_one()) {
+        int s = 0;
+        uint32_t ph = 0, issued = 0, phases = 0;
+        bool go = true, waited = kGrouped;
+        if (kGrouped) fence_proxy_async_global();
+        for (int t = first_tile; t < walk.total && go; t += step) {
+          const Tile tile = walk.at(t);
+          const int wrow = tile.expert * kParts * p.N + tile.n * kTileN;
+          const auto load = [&](uint8_t* dst, const CUtensorMap* map, int st, int row, int b) {
+            tma_load_4d(dst, map, &full[st], p.whole ? 0 : (k0 + b) * kBlock, row, p.whole ? k0 + b : 0, 0);
+          };
+          // (a stage that reaches past this CTA's blocks copies some that nobody uses)
+          const auto copy_w = [&](int st, int b) {
+            uint8_t* dst = smem + static_cast<size_t>(st) * stage;
+            mbar_arrive_expect_tx(&full[st], stage);
+            load(dst, &p.tmB, st, wrow, b);
+            if (kGated) load(dst + kWBytes, &p.tmB, st, wrow + p.N, b);
+          };
+          int early = 0;
+          if (!waited) {
+            // weights of the first stages before the rows are there
+            early = p.early_weights ? min(stages, (kb + copy - 1) / copy) : 0;
+            for (int i = 0; i < early; ++i) copy_w(i, i * copy);
+            issued |= (1u << early) - 1u;
+            pdl_wait_primary();
+            fence_proxy_async_global();
+            waited = true;
+          }
+          for (int b = 0; b < kb; b += copy) {
+            if (!wait(&empty[s], ph ^ 1u)) {
+              go = false;
+              break;
+            }
+            if (b >= early * copy) copy_w(s, b);
+            load(smem + static_cast<size_t>(s) * stage + copy * kParts * kWBytes, &p.tmA, s, tile.first, b);
+            issued |= 1u << s;
+            phases = (phases & ~(1u << s)) | (ph << s);
+            if (++s == stages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        if (*abort_flag) {
+          // no copy in flight at exit
+          for (int i = 0; i < stages; ++i)
+            if (issued & (1u << i)) (void)mbar_wait_bounded(&full[i], (phases >> i) & 1u, kWaitLimitNs);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ===== MMA issue =====
+      if (elect_one()) {
+        constexpr uint32_t kIdesc = idesc_f8f6f4_e4m3(kTileN, kCols);
+        const uint64_t desc0 = make_smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+        int s = 0, half = 0, last = 0;
+        uint32_t ph = 0, hph = 0, last_ph = 0;
+        bool go = true, any = false;
+        for (int t = first_tile; t < walk.total && go; t += step) {
+          for (int b0 = 0; b0 < kb && go; b0 += G) {
+            if (!wait(&drained[half], hph ^ 1u)) {
+              go = false;
+              break;
+            }
+            const int n = min(G, kb - b0);
+            for (int u = 0; u < n; ++u) {
+              const int i = (b0 + u) & (copy - 1);      // of the stage's blocks
+              if (i == 0 && !wait(&full[s], ph)) {
+                go = false;
+                break;
+              }
+              tc_fence_after();
+              // (descriptors count 16 bytes: 2 more for each 32 bytes of K)
+              const uint64_t wd = desc0 + ((s * stage + i * kParts * kWBytes) >> 4);
+              const uint64_t ad = desc0 + ((s * stage + copy * kParts * kWBytes + i * kABytes) >> 4);
+              const uint32_t d = tmem_base + half * kHalf + u * kCols * kParts;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                for (int part = 0; part < kParts; ++part)
+                  mma_f8f6f4(d + part * kCols, wd + part * (kWBytes >> 4) + 2 * kk, ad + 2 * kk, kIdesc, kk > 0);
+              if (i == copy - 1 || b0 + u == kb - 1) {
+                tc_commit(&empty[s]);
+                if (++s == stages) {
+                  s = 0;
+                  ph ^= 1u;
+                }
+              }
+            }
+            tc_commit(&filled[half]);
+            any = true;
+            last = half;
+            last_ph = hph;
+            half ^= 1;
+            if (half == 0) hph ^= 1u;
+          }
+        }
+        // nothing of this thread in flight at exit: the last commit covers every MMA before it
+        if (any) (void)mbar_wait_bounded(&filled[last], last_ph, kWaitLimitNs);
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ===== scales =====
+      constexpr int kAhead = kSlots - 2;         // groups under way (the slot before the last one may be read still)
+      const int nb = n_blocks(p.N);
+      pdl_wait_primary();
+      Walk<kGrouped, kCols> ahead = walk;
+      int c_t = first_tile, c_b = 0, put = 0;
+      Tile tile{};
+      const float *c_a = nullptr, *c_w = nullptr;
+      const auto enter = [&] {
+        tile = ahead.at(c_t);
+        c_a = p.a_scale + tile.first + lane + k0 * p.a_scale_ld;
+        c_w = p.w_scale + static_cast<int64_t>((tile.expert * kParts + (lane & (kParts - 1))) * nb + tile.n) * p.kb + k0;
+      };
+      const auto fetch = [&] {
+        if (c_t < ahead.total) {
+          float* slot = scales + put * (G * kScaleRow);
+          const int n = min(G, kb - c_b);
+          for (int u = 0; u < n; ++u) {
+            if (lane < tile.rows) copy4(slot + u * kScaleRow + lane, c_a + (c_b + u) * p.a_scale_ld);
+            if (lane < kParts) copy4(slot + u * kScaleRow + kCols + lane, c_w + c_b + u);
+          }
+          put = (put + 1) & (kSlots - 1);
+          c_b += G;
+          if (c_b >= kb) {
+            c_b = 0;
+            c_t += step;
+            if (c_t < ahead.total) enter();
+          }
+        }
+        copies_commit();
+      };
+      if (c_t < ahead.total) enter();
+  #pragma unroll 1
+      for (int g = 0; g < kAhead; ++g) fetch();
+      int half = 0;
+      uint32_t hph = 0;
+      bool go = true;
+      for (int t = first_tile; t < walk.total && go; t += step)
+        for (int b0 = 0; b0 < kb; b0 += G) {
+          go = __all_sync(0xffffffffu, wait(&drained[half], hph ^ 1u));
+          if (!go) break;
+          fetch();
+          copies_wait<kAhead>();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&filled[half]);
+          half ^= 1;
+          if (half == 0) hph ^= 1u;
+        }
+      copies_wait<0>();
+    }
+    if (!kGrouped && p.splits > 1) {
+      // the cluster's barriers (below) count every thread
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+      cluster_arrive();
+      cluster_wait();
+    }
+  } else {
+    // ===== sums =====
+    setmaxnreg_inc<kRegsSum>();
+    pdl_wait_primary();
+    const int side = (warp - 4) >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;            // of the tile's rows of W
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + side * kMine;
+    int half = 0, turn = 0, take = 0;
+    uint32_t hph = 0;
+    bool dead = false;
+    for (int t = first_tile; t < walk.total; t += step, turn ^= 1) {
+      const Tile tile = walk.at(t);
+      const int mine = min(tile.rows - side * kMine, kMine);       // rows of A of this side
+      const int first = tile.first + side * kMine;
+      const int n = tile.n * kTileN + r;
+      float acc[kParts][kMine];
+#pragma unroll
+      for (int part = 0; part < kParts; ++part)
+#pragma unroll
+        for (int c = 0; c < kMine; ++c) acc[part][c] = 0.0f;
+#pragma unroll 1
+      for (int b0 = 0; b0 < kb; b0 += G) {
+        if (!dead && !__all_sync(0xffffffffu, wait(&filled[half], hph))) dead = true;
+        if (!dead) {
+          tc_fence_after();
+          const int blocks = min(G, kb - b0);
+          const float* sc = scales + take * (G * kScaleRow) + side * kMine;
+          uint32_t v[G * kParts][kMine];
+          if (mine > 0) {
+#pragma unroll
+            for (int i = 0; i < G * kParts; ++i)
+              if (i < kParts * blocks) tmem_ld_32x32b_x16(lanes + half * kHalf + i * kCols, v[i]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+              if (u < blocks) {
+                const float* row = sc + u * kScaleRow;
+                float as[kMine];
+#pragma unroll
+                for (int c = 0; c < kMine; c += 4) {
+                  const float4 q = *reinterpret_cast<const float4*>(row + c);
+                  as[c] = q.x, as[c + 1] = q.y, as[c + 2] = q.z, as[c + 3] = q.w;
+                }
+#pragma unroll
+                for (int part = 0; part < kParts; ++part) {
+                  const float ws = row[kCols - side * kMine + part];
+#pragma unroll
+                  for (int c = 0; c < kMine; ++c)
+                    asm volatile("fma.rn.f32 %0, %1, %2, %0;"      // (volatile: behind the wait for the loads)
+                                 : "+f"(acc[part][c])
+                                 : "f"(__uint_as_float(v[u * kParts + part][c])), "f"(as[c] * ws));
+                }
+              }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&drained[half]);
+        }
+        take = (take + 1) & (kSlots - 1);
+        half ^= 1;
+        if (half == 0) hph ^= 1u;
+      }
+      if constexpr (kGated) {
+        float* peak = amax + (turn * 2 + side) * 4 * kMine;
+        float h[kMine];
+#pragma unroll
+        for (int c = 0; c < kMine; ++c) {
+          h[c] = n < p.N ? silu(acc[0][c]) * acc[1][c] : 0.0f;
+          const float size = fabsf(h[c]);
+          const uint32_t most = __reduce_max_sync(0xffffffffu, size == size ? __float_as_uint(size) : 0u);
+          if (lane == 0) peak[quad * kMine + c] = __uint_as_float(most);
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + side) : "memory");
+#pragma unroll
+        for (int c = 0; c < kMine; ++c) {
+          if (c >= mine || dead) continue;
+          const float s = block_scale(fmaxf(fmaxf(peak[c], peak[kMine + c]), fmaxf(peak[2 * kMine + c], peak[3 * kMine + c])));
+          const BlockDiv by = block_div(s);
+          const int64_t to = p.out_rows != nullptr ? __ldcg(p.out_rows + first + c) : first + c;
+          if (n < p.N) p.inner[to * p.N + n] = static_cast<uint8_t>(cvt_e4m3x2(div_rn_by_recip(h[c], by.s, by.rs), 0.0f));
+          if (r == 0) p.inner_scale[static_cast<int64_t>(tile.n) * p.M + to] = s;
+        }
+      } else {
+        if (p.splits > 1) {
+          // sums of the other CTAs of the cluster, [rank - 1][row of A][row of W], in the leader's ring (done with: all
+          // of the leader's MMAs are read out)
+          float* red = reinterpret_cast<float*>(smem);
+          const int at = side * kMine * kTileN + r;
+          cluster_arrive();
+          cluster_wait();
+          if (rank != 0) {
+            const uint32_t to = map_to_cta(smem_u32(red + (rank - 1) * kCols * kTileN + at), 0);
+#pragma unroll
+            for (int c = 0; c < kMine; ++c)
+              if (c < mine) st_dsmem_f32(to + c * kTileN * 4, acc[0][c]);
+          }
+          cluster_arrive();
+          cluster_wait();
+          if (rank == 0)
+            for (int q = 1; q < p.splits; ++q)
+#pragma unroll
+              for (int c = 0; c < kMine; ++c)
+                if (c < mine) acc[0][c] += red[(q - 1) * kCols * kTileN + at + c * kTileN];
+        }
+        if (n < p.N && rank == 0 && !dead) {
+#pragma unroll
+          for (int c = 0; c < kMine; ++c) {
+            if (c >= mine) continue;
+            const int64_t to = p.out_rows != nullptr ? __ldcg(p.out_rows + first + c) : first + c;
+            static_cast<__nv_bfloat16*>(p.Y)[to * p.ldy + n] = __float2bfloat16_rn(acc[0][c]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 2 * kHalf);
+  }
+}
+
+// A tensor map of a matrix [rows][K] of bytes whose copies take `copy` blocks of K of `box_rows` rows each: 128 bytes,
+// rows, blocks. Where K ends inside a block there is no axis of blocks (the last one would run into the next row), and
+// a copy takes one, at its place in the row.
+int make_tma_blocks(CUtensorMap* map, const void* base, int64_t rows, int K, int box_rows, int copy) {
+  const bool whole = K % kBlock == 0;
+  const uint64_t row = static_cast<uint64_t>(K), n = static_cast<uint64_t>(rows);
+  const uint64_t dims[4] = {whole ? kBlock : row, n, whole ? row / kBlock : 1, 1};
+  const uint64_t strides[3] = {row, whole ? kBlock : row, row};
+  const uint32_t box[4] = {kBlock, static_cast<uint32_t>(box_rows), static_cast<uint32_t>(copy), 1};
+  return make_tma_4d_u8(map, base, dims, strides, box, 128);
+}
+
+template <bool kGrouped, bool kGated>
+int launch(const BlockGemmArgs& a) {
+  Params p{};
+  p.a_scale = a.a_scale;
+  p.w_scale = a.w_scale;
+  p.a_scale_ld = a.a_scale_ld;
+  p.Y = a.Y;
+  p.ldy = a.ldy;
+  p.inner = a.inner;
+  p.inner_scale = a.inner_scale;
+  p.offsets = a.offsets;
+  p.out_rows = a.out_rows;
+  p.status = a.status;
+  p.M = a.M;
+  p.N = a.N;
+  p.kb = n_blocks(a.K);
+  p.experts = kGrouped ? a.experts : 1;
+  p.early_weights = a.early_weights;
+  p.n_tiles = (a.N + kTileN - 1) / kTileN;
+  p.whole = a.K % kBlock == 0;
+  p.copy = kGated || !p.whole ? 1 : 2;         // 40 KB a stage, five stages
+  const int64_t w_rows = static_cast<int64_t>(p.experts) * a.N * (kGated ? 2 : 1);
+  const int64_t tiles = (static_cast<int64_t>(a.M) / kCols + 1 + (kGrouped ? p.experts : 0)) * p.n_tiles;
+  if (tiles >= (int64_t{1} << 31) || w_rows >= (int64_t{1} << 31)) return EPILORA_ERR_UNSUPPORTED;
+  int rc = make_tma_blocks(&p.tmA, a.A, a.M, a.K, kCols, p.copy);
+  if (rc == EPILORA_OK) rc = make_tma_blocks(&p.tmB, a.W, w_rows, a.K, kTileN, p.copy);
+  if (rc != EPILORA_OK) return rc;
+  const int sms = num_sms();
+  // K over a cluster: while that fills more SMs and leaves each CTA a group of blocks
+  p.splits = 1;
+  if (!kGrouped)
+    while (p.splits < kSplitMax && 2 * p.splits * p.n_tiles <= sms && p.kb >= 16 * p.splits) p.splits *= 2;
+  const int extra = 1024 + kMisc + (kGrouped ? 2 * (p.experts + 1) * 4 : 0);
+  const int stage = p.copy * ((kGated ? 2 : 1) * kWBytes + kABytes);
+  p.stages = (227 * 1024 - extra) / stage;
+  if (p.stages > kStagesMax) p.stages = kStagesMax;
+  const int smem = p.stages * stage + extra;
+  const auto kern = block_few_kernel<kGrouped, kGated>;
+  static int attr_done[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EPILORA_ERR_CUDA;
+  if (attr_done[dev] < smem) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
+      return EPILORA_ERR_CUDA;
+    attr_done[dev] = 227 * 1024;
+  }
+  // (split: a tile per cluster; few rows are one tile of them)
+  const unsigned grid = kGrouped ? sms : p.splits > 1 ? p.splits * p.n_tiles : p.n_tiles < sms ? p.n_tiles : sms;
+  return launch_dependent(kern, grid, kThreads, smem, a.stream, p, p.splits);
+}
+
+}  // namespace
+
+int launch_block_few(const BlockGemmArgs& a) {
+  if (a.gated) return launch<true, true>(a);
+  return a.grouped ? launch<true, false>(a) : launch<false, false>(a);
+}
+
+}  // namespace epi

@@ -28,7 +28,7 @@
 // Every wait is bounded: on a timeout the CTA records EPILORA_ERR_TIMEOUT,
 // stops issuing, waits (bounded) for its copies and MMAs in flight and frees
 // its TMEM.
-#include "block_quant.cuh"
+#include "block_gemm.cuh"
 
 namespace epi {
 
@@ -67,54 +67,9 @@ struct Params {
   const int32_t* out_rows;     // the output row of each row (NULL: the same)
   int* status;
   int M, N, K, kb;
-  int n_tiles, experts, box_rows;
+  int n_tiles, experts;
   int stages, wide_store, early_weights;
 };
-
-struct Tile {
-  int expert, first, rows, n;      // rows [first, first + rows) of the expert's list, columns' tile
-};
-
-// The tiles of a CTA in order: expert by expert, its row tiles fastest (CTAs
-// next to one another then share weights in L2).
-template <bool kGrouped>
-struct Walk {
-  const int* offsets;        // shared memory: [experts + 1]
-  const int* starts;         // row tiles before each expert, [experts + 1]
-  int n_tiles, M, e, total;
-  __device__ Walk(const Params& p, const int* off, const int* st) : offsets(off), starts(st), n_tiles(p.n_tiles), M(p.M), e(0) {
-    total = (kGrouped ? starts[p.experts] : (p.M + kRows - 1) / kRows) * n_tiles;
-  }
-  __device__ Tile at(int t) {
-    Tile r;
-    if (kGrouped) {
-      while (starts[e + 1] * n_tiles <= t) ++e;
-      const int mt = starts[e + 1] - starts[e], local = t - starts[e] * n_tiles;
-      const int m = local % mt;
-      r.expert = e;
-      r.n = local / mt;
-      r.first = offsets[e] + m * kRows;
-      r.rows = min(kRows, offsets[e + 1] - r.first);
-    } else {
-      const int mt = total / n_tiles, m = t % mt;
-      r.expert = 0;
-      r.n = t / mt;
-      r.first = m * kRows;
-      r.rows = min(kRows, M - r.first);
-    }
-    return r;
-  }
-};
-
-// Four bytes of global memory to shared memory; complete in order of the groups committed after them.
-__device__ __forceinline__ void copy4(float* dst, const float* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ void sums_barrier() { asm volatile("bar.sync %0, %1;" ::"n"(kSumBarrier), "n"(kSumThreads) : "memory"); }
 
@@ -130,10 +85,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]) {
   else
     tmem_ld_32x32b_x32(taddr, v);
 }
-
-// g / (1 + exp(-g)) within 2^-21 of it, without a division's branches: a tile's elements are all in registers, so
-// this code stands there once for each of them, and has to stay in the instruction cache beside the loops
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + expf(-g)); }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -185,48 +136,34 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
   if (kGrouped) {
     // row tiles before each expert: one warp, 32 experts at a time
     pdl_wait_primary();
-    if (warp == 2) {
-      int before = 0;
-      for (int e0 = 0; e0 < p.experts; e0 += 32) {
-        const int e = e0 + lane;
-        const int o0 = e <= p.experts ? __ldcg(p.offsets + e) : 0;
-        const int o1 = e < p.experts ? __ldcg(p.offsets + e + 1) : o0;
-        const int mt = (o1 - o0 + kRows - 1) / kRows;
-        int sum = mt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += v;
-        }
-        if (e < p.experts) {
-          offsets[e] = o0;
-          starts[e] = before + sum - mt;
-          if (e == p.experts - 1) {
-            offsets[e + 1] = o1;
-            starts[e + 1] = before + sum;
-          }
-        }
-        before += __shfl_sync(0xffffffffu, sum, 31);
-      }
-    }
+    if (warp == 2) fill_walk<kRows>(p.offsets, p.experts, offsets, starts, lane);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_allow_dependents();
   const uint32_t tmem_base = *tmem_slot;
-  Walk<kGrouped> walk(p, offsets, starts);
+  Walk<kGrouped, kRows> walk(p.M, p.n_tiles, p.experts, offsets, starts);
 
-  // gives up when the wait runs out or another role has
-  const auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag == 0 && mbar_wait_bounded(bar, parity, kWaitLimitNs)) return true;
-    if (*abort_flag == 0) {
-      *abort_flag = 1;
-      record_status(p.status, EPILORA_ERR_TIMEOUT);
+  // The sums' wait of a wide tile polls, with as little code as can be: a warp that the hardware suspended wakes some
+  // 100 cycles late, which is 3 % of a call with many rows (and 2 % lost on narrow tiles, whose warps mostly do wait).
+  // Gives up after 10^7 polls.
+  const auto poll = [&](uint64_t* bar, uint32_t parity) {
+    const uint32_t at = smem_u32(bar);
+    for (int i = 0; i < 10000000; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(at), "r"(parity)
+          : "memory");
+      if (ok != 0) return true;
     }
     return false;
   };
+  const auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag, p.status); };
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsOther>();
@@ -241,10 +178,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
           const Tile tile = walk.at(t);
           const int n0 = tile.n * (kGated ? kBlock : BN);
           const int wrow = tile.expert * (kGated ? 2 : 1) * p.N + n0;
-          const uint32_t bytes = C::kBBytes + (tile.rows + p.box_rows - 1) / p.box_rows * p.box_rows * kBlock;
           const auto copy_w = [&](int st, int b) {
             uint8_t* dst = smem + static_cast<size_t>(st) * C::kStage + kABytes;
-            mbar_arrive_expect_tx(&full[st], bytes);
+            mbar_arrive_expect_tx(&full[st], C::kStage);
             tma_load_2d(dst, &p.tmB, &full[st], b * kBlock, wrow);
             if (kGated) tma_load_2d(dst + kBlock * kBlock, &p.tmB, &full[st], b * kBlock, wrow + p.N);
           };
@@ -264,8 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
               break;
             }
             if (b >= early) copy_w(s, b);
-            for (int r = 0; r < tile.rows; r += p.box_rows)
-              tma_load_2d(smem + static_cast<size_t>(s) * C::kStage + r * kBlock, &p.tmA, &full[s], b * kBlock, tile.first + r);
+            tma_load_2d(smem + static_cast<size_t>(s) * C::kStage, &p.tmA, &full[s], b * kBlock, tile.first);
             issued |= 1u << s;
             phases = (phases & ~(1u << s)) | (ph << s);
             if (++s == stages) {
@@ -285,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
       // ===== MMA issue =====
       if (elect_one()) {
         constexpr uint32_t kIdesc = idesc_f8f6f4_e4m3(kRows, BN);
+        const uint64_t desc0 = make_smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
         int s = 0, half = 0, last = 0;
         uint32_t ph = 0, hph = 0, last_ph = 0;
         bool go = true, any = false;
@@ -301,11 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
                 break;
               }
               tc_fence_after();
-              const uint32_t a_at = smem_u32(smem + static_cast<size_t>(s) * C::kStage), b_at = a_at + kABytes;
+              // (descriptors count 16 bytes: 2 more for each 32 bytes of K)
+              const uint64_t ad = desc0 + s * (C::kStage >> 4), bd = ad + (kABytes >> 4);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_f8f6f4(tmem_base + half * kHalf + u * BN, make_smem_desc(a_at + kk * 32, 16, 1024, kSwizzle128B),
-                           make_smem_desc(b_at + kk * 32, 16, 1024, kSwizzle128B), kIdesc, kk > 0);
+                mma_f8f6f4(tmem_base + half * kHalf + u * BN, ad + 2 * kk, bd + 2 * kk, kIdesc, kk > 0);
               tc_commit(&empty[s]);
               if (++s == stages) {
                 s = 0;
@@ -331,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
       const int nb = n_blocks(p.N);
       constexpr int kW = BN == 256 ? 2 : 1;     // scales of the weights per block
       pdl_wait_primary();
-      Walk<kGrouped> ahead = walk;
+      Walk<kGrouped, kRows> ahead = walk;
       int c_t = blockIdx.x, c_b = 0, put = 0;
       Tile tile{};
       const float *c_a = nullptr, *c_w = nullptr;
@@ -404,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
       for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
 #pragma unroll 1
       for (int b0 = 0; b0 < kb; b0 += G) {
-        if (!dead && !__all_sync(0xffffffffu, wait(&filled[half], hph))) dead = true;
+        if (!dead && !__all_sync(0xffffffffu, BN == 256 ? poll(&filled[half], hph) : wait(&filled[half], hph))) dead = true;
         if (!dead) {
           tc_fence_after();
           const auto release = [&] {
@@ -513,6 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
         }
       }
     }
+    if (dead) {
+      *abort_flag = 1;
+      record_status(p.status, EPILORA_ERR_TIMEOUT);
+    }
   }
 
   tc_fence_before();
@@ -550,10 +490,7 @@ int launch(const BlockGemmArgs& a) {
   // tiles, and rows of the tensor maps, are counted in 31 bits
   const int64_t tiles = (static_cast<int64_t>(a.M) / kRows + 1 + (kGrouped ? p.experts : 0)) * p.n_tiles;
   if (tiles >= (int64_t{1} << 31) || w_rows >= (int64_t{1} << 31)) return EPILORA_ERR_UNSUPPORTED;
-  // rows of A are copied in boxes of 32 where a tile has few of them, or the rows that follow are not its own
-  const int per_tile = kGrouped ? a.M / p.experts : a.M;
-  p.box_rows = per_tile >= 96 ? kRows : 32;
-  int rc = make_tma_2d_u8(&p.tmA, a.A, a.M, a.K, a.K, p.box_rows, kBlock, true);
+  int rc = make_tma_2d_u8(&p.tmA, a.A, a.M, a.K, a.K, kRows, kBlock, true);
   if (rc == EPILORA_OK) rc = make_tma_2d_u8(&p.tmB, a.W, w_rows, a.K, a.K, kGated ? kRows : BN, kBlock, true);
   if (rc != EPILORA_OK) return rc;
   const int extra = 1024 + C::kMisc + (kGrouped ? 2 * (p.experts + 1) * 4 : 0);
@@ -592,6 +529,7 @@ static int tile_width(int M, int N) {
 }
 
 int launch_block_gemm(const BlockGemmArgs& a) {
+  if (a.M / (a.grouped ? a.experts : 1) <= (a.grouped ? kFewRows / 2 : kFewRows)) return launch_block_few(a);
   if (a.gated) return launch<256, true, true>(a);
   if (a.grouped) return launch<256, true, false>(a);
   switch (tile_width(a.M, a.N)) {

@@ -113,19 +113,23 @@ struct MoeRouteArgs {
 };
 int launch_moe_route(const MoeRouteArgs& a);
 
-// A launch as a programmatic dependent of the previous kernel on the stream.
+// A launch as a programmatic dependent of the previous kernel on the stream, in clusters of `cluster` CTAs.
 template <class P>
-int launch_dependent(void (*kern)(P), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, const P& p) {
+int launch_dependent(void (*kern)(P), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, const P& p,
+                     unsigned cluster = 1) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(block, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? EPILORA_OK : EPILORA_ERR_CUDA;
 }
 

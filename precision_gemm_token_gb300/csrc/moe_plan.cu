@@ -164,19 +164,7 @@ int launch_moe_plan(const MoePlanArgs& a) {
   // one CTA counts a few thousand slots as fast as a cluster does
   const int64_t n = static_cast<int64_t>(a.tokens) * a.top;
   const unsigned ctas = n <= 4 * kPlanThreads ? 1 : 8;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, 1, 1);
-  cfg.blockDim = dim3(kPlanThreads, 1, 1);
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, moe_plan_kernel, a) == cudaSuccess ? EPILORA_OK : EPILORA_ERR_CUDA;
+  return launch_dependent(moe_plan_kernel, ctas, kPlanThreads, 0, a.stream, a, ctas);
 }
 
 int launch_moe_scatter(const MoeScatterArgs& a) {

@@ -20,31 +20,54 @@ namespace {
 constexpr int kRouteThreads = 128;
 constexpr unsigned kAll = 0xffffffffu;
 
-template <class T>
-__device__ __forceinline__ T neg_inf();
-template <>
-__device__ __forceinline__ float neg_inf<float>() { return __int_as_float(0xff800000); }
-template <>
-__device__ __forceinline__ double neg_inf<double>() { return __longlong_as_double(0xfff0000000000000ll); }
-
 __device__ __forceinline__ float exp_of(float x) { return expf(x); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
+__device__ __forceinline__ float minus_inf() { return __int_as_float(0xff800000); }
 
+// Numbers as unsigned keys of the same order (the order of the bits, turned
+// round for negative numbers): maxima over the warp by redux, and 64-bit
+// comparisons without the FP64 pipe. Key 0: nobody (no number has it).
+template <class T>
+struct Keys;
+template <>
+struct Keys<float> {
+  typedef uint32_t Key;
+  static __device__ __forceinline__ Key of(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return (b & 0x80000000u) != 0 ? ~b : b | 0x80000000u;
+  }
+  static __device__ __forceinline__ float value(Key k) {
+    return __uint_as_float((k & 0x80000000u) != 0 ? k & 0x7fffffffu : ~k);
+  }
+  static __device__ __forceinline__ Key warp_max(Key k) { return __reduce_max_sync(kAll, k); }
+};
+template <>
+struct Keys<double> {
+  typedef uint64_t Key;
+  static __device__ __forceinline__ Key of(double v) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
+    return (b >> 63) != 0 ? ~b : b | (1ull << 63);
+  }
+  static __device__ __forceinline__ double value(Key k) {
+    return __longlong_as_double(static_cast<long long>((k >> 63) != 0 ? k & ~(1ull << 63) : ~k));
+  }
+  static __device__ __forceinline__ Key warp_max(Key k) {
+    const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(k >> 32));
+    const uint32_t lo = __reduce_max_sync(kAll, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+  }
+};
+
+// The warp's largest key, and the lowest index that has it.
 template <class T>
 struct Best {
-  T v;
+  typename Keys<T>::Key key;
   int i;
 };
-// largest value of the warp, the lowest index among equals
 template <class T>
-__device__ __forceinline__ Best<T> warp_best(Best<T> b) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const T v = __shfl_xor_sync(kAll, b.v, o);
-    const int i = __shfl_xor_sync(kAll, b.i, o);
-    if (v > b.v || (v == b.v && i < b.i)) b = Best<T>{v, i};
-  }
-  return b;
+__device__ __forceinline__ Best<T> warp_best(Best<T> mine) {
+  const typename Keys<T>::Key key = Keys<T>::warp_max(mine.key);
+  return Best<T>{key, static_cast<int>(__reduce_min_sync(kAll, mine.key == key ? static_cast<uint32_t>(mine.i) : 0x7fffffffu))};
 }
 template <class T>
 __device__ __forceinline__ T warp_sum(T v) {
@@ -54,117 +77,114 @@ __device__ __forceinline__ T warp_sum(T v) {
 }
 
 // A logit as the scores take it: NaN counts as -infinity (no such expert),
-// +infinity as the largest number.
+// +infinity as the largest number, -0 as 0.
 __device__ __forceinline__ float clean(float l) {
-  if (!(l > __int_as_float(0xff800000))) return __int_as_float(0xff800000);
-  return fminf(l, 3.402823466e38f);
-}
-
-template <class T>
-__device__ __forceinline__ T score_of(const MoeRouteArgs& a, float l, T top, T sum) {
-  if (!(l > neg_inf<float>())) return T(0);
-  if (a.sigmoid) return T(1) / (T(1) + exp_of(-T(l)));
-  return exp_of(T(l) - top) / sum;
+  if (!(l > minus_inf())) return minus_inf();
+  return fminf(l, 3.402823466e38f) + 0.0f;
 }
 
 // Chooses the token's experts: slot j's in lane j (-1: none left). Returns
 // whether two candidates were too close to tell (never for T = double).
 template <class T, int kPer>
 __device__ __forceinline__ bool choose(const MoeRouteArgs& a, const float (&l)[kPer], float top, int lane, int& mine) {
+  typedef typename Keys<T>::Key Key;
   constexpr bool kApprox = sizeof(T) == 4;
   const bool by_value = a.bias != nullptr || (a.groups > 1 && a.group_best > 1);
-  T c[kPer], sum = T(1), bound = T(0);
+  Key c[kPer];
+  T sum = T(1);
   if (by_value && !a.sigmoid) {
     sum = T(0);
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (l[i] > neg_inf<float>()) sum += exp_of(T(l[i]) - T(top));
+      if (l[i] > minus_inf()) sum += exp_of(T(l[i]) - T(top));
     sum = warp_sum(sum);
   }
-  T most = T(0);
+  float most = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
-    c[i] = neg_inf<T>();
-    if (e < a.experts && l[i] > neg_inf<float>()) {
-      c[i] = by_value ? score_of<T>(a, l[i], T(top), sum) : T(l[i]);
-      if (a.bias != nullptr) {
-        c[i] += T(a.bias[e]);
-        if (!(c[i] > neg_inf<T>())) c[i] = neg_inf<T>();      // (a NaN: no such expert)
-      }
-      if (kApprox && c[i] > neg_inf<T>() && c[i] < T(3e38)) most = c[i] < T(0) ? (most > -c[i] ? most : -c[i]) : (most > c[i] ? most : c[i]);
+    c[i] = 0;
+    if (e < a.experts && l[i] > minus_inf()) {
+      T v = T(l[i]);
+      if (by_value) v = a.sigmoid ? T(1) / (T(1) + exp_of(-v)) : exp_of(v - T(top)) / sum;
+      if (a.bias != nullptr) v += T(a.bias[e]);
+      if (v > T(minus_inf())) c[i] = Keys<T>::of(v);      // (a bias of -infinity or NaN: no such expert)
+      if (kApprox && fabsf(static_cast<float>(v)) < 3e38f) most = fmaxf(most, fabsf(static_cast<float>(v)));
     }
   }
-  if (kApprox && by_value) {
-    // A sigmoid is off by a few units of 2^-24; a softmax by those of its
-    // sum, at most 40 of them (additions in each lane, then five), and of
-    // the exponent's argument (x e^x < 0.37). With the rounding of c itself,
-    // 2^-24 of it; the difference of two, and of two sums of two.
-    bound = (a.sigmoid ? T(0x1p-20) : T(0x1p-16)) + T(0x1p-21) * Best<T>(warp_best(Best<T>{most, 0})).v;
-  }
+  // A sigmoid is off by a few units of 2^-24; a softmax by those of its sum,
+  // at most 40 of them (additions in each lane, then five), and of the
+  // exponent's argument (x e^x < 0.37). With the rounding of c itself, 2^-24
+  // of it; the difference of two, and of two sums of two.
+  T bound = T(0);
+  if (kApprox && by_value)
+    bound = T((a.sigmoid ? 0x1p-20f : 0x1p-16f) + 0x1p-21f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most))));
   bool close = false;
   if (a.groups > 1 && a.top_groups < a.groups) {
-    // lane g: the value of group g
     const int size = a.experts / a.groups;
-    T value = neg_inf<T>();
+    int group[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) group[i] = (lane + 32 * i) / size;
+    Key value = 0;                                        // lane g: of group g
+#pragma unroll 1
     for (int g = 0; g < a.groups; ++g) {
-      Best<T> first{neg_inf<T>(), 0x7fffffff};
+      Best<T> first{0, 0x7fffffff};
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        if (e / size == g && c[i] > first.v) first = Best<T>{c[i], e};
-      }
+      for (int i = 0; i < kPer; ++i)
+        if (group[i] == g && c[i] > first.key) first = Best<T>{c[i], lane + 32 * i};
       first = warp_best(first);
-      T v = first.v;
-      if (a.group_best > 1 && v > neg_inf<T>()) {
-        Best<T> second{neg_inf<T>(), 0x7fffffff};
+      Key v = first.key;
+      if (a.group_best > 1 && v != 0) {
+        Key second = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int e = lane + 32 * i;
-          if (e / size == g && e != first.i && c[i] > second.v) second = Best<T>{c[i], e};
-        }
-        second = warp_best(second);
-        if (second.v > neg_inf<T>()) v += second.v;
+        for (int i = 0; i < kPer; ++i)
+          if (group[i] == g && lane + 32 * i != first.i && c[i] > second) second = c[i];
+        second = Keys<T>::warp_max(second);
+        if (second != 0) v = Keys<T>::of(Keys<T>::value(v) + Keys<T>::value(second));
       }
       if (lane == g) value = v;
     }
     unsigned kept = 0;
-    T before = T(0);
+    Key before = 0;
+#pragma unroll 1
     for (int j = 0; j <= a.top_groups; ++j) {
-      const Best<T> b = warp_best(Best<T>{(kept >> lane) & 1u ? neg_inf<T>() : value, (kept >> lane) & 1u || lane >= a.groups ? 64 + lane : lane});
-      if (kApprox && by_value && j == a.top_groups && b.v > neg_inf<T>() && !(before - b.v > bound)) close = true;
-      before = b.v;
-      if (j < a.top_groups && b.i < 32) kept |= 1u << b.i;
+      // (a group that nobody is in is still there to be kept, after the others)
+      const bool there = lane < a.groups && ((kept >> lane) & 1u) == 0;
+      const Best<T> b = warp_best(Best<T>{there ? value : 0, there ? lane : 0x7fffffff});
+      if (kApprox && by_value && j == a.top_groups && b.key != 0 &&
+          !(Keys<T>::value(before) - Keys<T>::value(b.key) > bound))
+        close = true;
+      before = b.key;
+      if (j < a.top_groups) kept |= 1u << b.i;
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 32 * i;
-      if (e < a.experts && !((kept >> (e / size)) & 1u)) c[i] = neg_inf<T>();
-    }
+    for (int i = 0; i < kPer; ++i)
+      if (((kept >> (group[i] & 31)) & 1u) == 0) c[i] = 0;
   }
   // without a bias the experts themselves are told by their logits
   const bool by_logit = a.bias == nullptr;
   if (by_logit && by_value) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (c[i] > neg_inf<T>()) c[i] = T(l[i]);
+      if (c[i] != 0) c[i] = Keys<T>::of(T(l[i]));
   }
   mine = -1;
-  T before = T(0);
+  Key before = 0;
+#pragma unroll 1
   for (int j = 0; j <= a.top; ++j) {
-    Best<T> b{neg_inf<T>(), 0x7fffffff};
+    Best<T> b{0, 0x7fffffff};
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (c[i] > b.v) b = Best<T>{c[i], lane + 32 * i};
+      if (c[i] > b.key) b = Best<T>{c[i], lane + 32 * i};
     b = warp_best(b);
-    if (!(b.v > neg_inf<T>())) break;
-    if (kApprox && !by_logit && j > 0 && !(before - b.v > bound)) close = true;
-    before = b.v;
+    if (b.key == 0) break;
+    if (kApprox && !by_logit && j > 0 && !(Keys<T>::value(before) - Keys<T>::value(b.key) > bound)) close = true;
+    before = b.key;
     if (j == a.top) break;
     if (lane == j) mine = b.i;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i == b.i) c[i] = neg_inf<T>();
+      if (lane + 32 * i == b.i) c[i] = 0;
   }
   return close;
 }
@@ -176,11 +196,11 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + (threadIdx.x >> 5);
   if (t >= a.tokens) return;
-  float l[kPer], top = neg_inf<float>();
+  float l[kPer], top = minus_inf();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
-    l[i] = neg_inf<float>();
+    l[i] = minus_inf();
     if (e < a.experts)
       l[i] = clean(kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[t * a.ld + e])
                          : static_cast<const float*>(a.logits)[t * a.ld + e]);
@@ -196,10 +216,10 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
     sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (l[i] > neg_inf<float>()) sum += expf(l[i] - top);
+      if (l[i] > minus_inf()) sum += expf(l[i] - top);
     sum = warp_sum(sum);
   }
-  float lm = neg_inf<float>();
+  float lm = minus_inf();
   if (mine >= 0)
     lm = clean(kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[t * a.ld + mine])
                      : static_cast<const float*>(a.logits)[t * a.ld + mine]);

@@ -12,6 +12,7 @@ arithmetic of the operators happens here.
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -46,9 +47,9 @@ def _start(t, stream):
 
 def _new(like, shape, dtype, stream):
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _matrix(t, dtype, dev, what, rows=None, cols=None):
@@ -68,6 +69,18 @@ def _array(t, dtype, shape, dev, what):
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         _bad(f"{what}: contiguous {dtype} {list(shape)} on device {dev} wanted")
     return t.data_ptr()
+
+
+def _made(t, like, shape, dtype, dev, stream, what):
+    """(an output, its address): the caller's, or a new one."""
+    if t is None:
+        t = _new(like, shape, dtype, stream)
+        return t, t.data_ptr()
+    return t, _array(t, dtype, shape, dev, what)
+
+
+# bytes of workspace, asked of the library once per shape
+_linear_bytes = lru_cache(1024)(E.epilora_block_linear_workspace_bytes)
 
 
 def _status(status, dev):
@@ -159,12 +172,9 @@ def block_quant(x, codes=None, scale=None, stream=None):
     or into the given ones."""
     dev, raw, given = _start(x, stream)
     at, M, K, ld = _matrix(x, _BF16, dev, "x")
-    if codes is None:
-        codes = _new(x, (M, K), _U8, given)
-    if scale is None:
-        scale = _new(x, (_blocks(K), M), _F32, given)
-    rc = _lib().epilora_block_quant(at, M, K, ld, _array(codes, _U8, (M, K), dev, "codes"),
-                                    _array(scale, _F32, (_blocks(K), M), dev, "scale"), M, raw)
+    codes, c_at = _made(codes, x, (M, K), _U8, dev, given, "codes")
+    scale, s_at = _made(scale, x, (-(-K // BLOCK), M), _F32, dev, given, "scale")
+    rc = _lib().epilora_block_quant(at, M, K, ld, c_at, s_at, M, raw)
     if rc:
         E.check(rc, "block_quant")
     return codes, scale
@@ -199,7 +209,8 @@ def block_matmul(codes, scale, w: BlockWeight, out=None, status=None, stream=Non
     c_at = _array(codes, _U8, (M, w.K), dev, "codes")
     s_at = _array(scale, _F32, (_blocks(w.K), M), dev, "scale")
     out, o_at, ld = _out(out, codes, M, w.N, dev, given)
-    rc = _lib().epilora_block_matmul(M, w.N, w.K, c_at, s_at, M, w.codes_at, w.scale_at, o_at, ld, _status(status, dev), raw)
+    rc = _lib().epilora_block_matmul(M, w.N, w.K, c_at, s_at, M, w.codes_at, w.scale_at, o_at, ld, _status(status, dev),
+                                     raw)
     if rc:
         E.check(rc, "block_matmul")
     return out
@@ -212,7 +223,7 @@ def block_linear(x, w: BlockWeight, out=None, workspace: Optional[BlockWorkspace
         _bad("block_linear: x and the weight on different devices")
     at, M, K, ld = _matrix(x, _BF16, dev, "x", None, w.K)
     out, o_at, old = _out(out, x, M, w.N, dev, given)
-    need = E.epilora_block_linear_workspace_bytes(M, K)
+    need = _linear_bytes(M, K)
     buf, w_at = _room(workspace, x, need, dev, raw, given)
     rc = _lib().epilora_block_linear(M, w.N, K, at, ld, w.codes_at, w.scale_at, o_at, old, w_at, need,
                                      _status(status, dev), raw)

@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kTileN = 128;                    // rows of W per tile
-constexpr int kCols = kFewRows;                // rows of A per tile: columns of the MMA
+constexpr int kCols = 32;                      // rows of A per tile: columns of the MMA
 constexpr int kHalf = 256;
 constexpr int kWBytes = kTileN * kBlock, kABytes = kCols * kBlock;     // of a block
 constexpr int kStagesMax = 12;
@@ -56,8 +56,10 @@ struct Params {
   int M, N, kb, n_tiles, experts, stages, copy, whole, splits, early_weights;
 };
 
-template <bool kGrouped, bool kGated>
+// Gated products are of the rows by expert, others of plain matrices.
+template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_constant__ Params p) {
+  constexpr bool kGrouped = kGated;
   constexpr int kParts = kGated ? 2 : 1;       // gate, up
   constexpr int G = kHalf / (kCols * kParts);  // blocks of a group
   constexpr int kSlots = kScaleBlocks / G;     // groups in the scales' ring
@@ -386,8 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
 #pragma unroll
           for (int c = 0; c < kMine; ++c) {
             if (c >= mine) continue;
-            const int64_t to = p.out_rows != nullptr ? __ldcg(p.out_rows + first + c) : first + c;
-            static_cast<__nv_bfloat16*>(p.Y)[to * p.ldy + n] = __float2bfloat16_rn(acc[0][c]);
+            static_cast<__nv_bfloat16*>(p.Y)[(first + c) * p.ldy + n] = __float2bfloat16_rn(acc[0][c]);
           }
         }
       }
@@ -413,8 +414,17 @@ int make_tma_blocks(CUtensorMap* map, const void* base, int64_t rows, int K, int
   return make_tma_4d_u8(map, base, dims, strides, box, 128);
 }
 
-template <bool kGrouped, bool kGated>
+// CTAs that share K: as many as still find an SM each, while each keeps a group of blocks.
+int few_splits(int N, int K) {
+  const int n_tiles = (N + kTileN - 1) / kTileN, sms = num_sms();
+  int splits = 1;
+  while (splits < kSplitMax && 2 * splits * n_tiles <= sms && n_blocks(K) >= 16 * splits) splits *= 2;
+  return splits;
+}
+
+template <bool kGated>
 int launch(const BlockGemmArgs& a) {
+  constexpr bool kGrouped = kGated;
   Params p{};
   p.a_scale = a.a_scale;
   p.w_scale = a.w_scale;
@@ -441,16 +451,13 @@ int launch(const BlockGemmArgs& a) {
   if (rc == EPILORA_OK) rc = make_tma_blocks(&p.tmB, a.W, w_rows, a.K, kTileN, p.copy);
   if (rc != EPILORA_OK) return rc;
   const int sms = num_sms();
-  // K over a cluster: while that fills more SMs and leaves each CTA a group of blocks
-  p.splits = 1;
-  if (!kGrouped)
-    while (p.splits < kSplitMax && 2 * p.splits * p.n_tiles <= sms && p.kb >= 16 * p.splits) p.splits *= 2;
+  p.splits = kGrouped ? 1 : few_splits(a.N, a.K);
   const int extra = 1024 + kMisc + (kGrouped ? 2 * (p.experts + 1) * 4 : 0);
   const int stage = p.copy * ((kGated ? 2 : 1) * kWBytes + kABytes);
   p.stages = (227 * 1024 - extra) / stage;
   if (p.stages > kStagesMax) p.stages = kStagesMax;
   const int smem = p.stages * stage + extra;
-  const auto kern = block_few_kernel<kGrouped, kGated>;
+  const auto kern = block_few_kernel<kGated>;
   static int attr_done[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EPILORA_ERR_CUDA;
@@ -466,9 +473,15 @@ int launch(const BlockGemmArgs& a) {
 
 }  // namespace
 
-int launch_block_few(const BlockGemmArgs& a) {
-  if (a.gated) return launch<true, true>(a);
-  return a.grouped ? launch<true, false>(a) : launch<false, false>(a);
+// The product turned round pays where the sums are gated (one token's up projections 35.6 -> 32.1 us, of 8 tokens 99 ->
+// 85, of 64 153 -> 150: half as many blocks a group, and one warp in four left most SMs' lanes idle), and where K is
+// split (32 x 14336 -> 4096: 29.7 -> 22.1 us). Otherwise block_gemm.cu's narrower tiles spread better over the SMs
+// (32 x 4096 -> 28672: 26.4 against 30.6 us; down projections of 64 tokens 88 against 99).
+bool block_few_takes(const BlockGemmArgs& a) {
+  if (a.grouped) return a.gated && a.M / a.experts <= kCols / 2;
+  return a.M <= kCols && few_splits(a.N, a.K) > 1;
 }
+
+int launch_block_few(const BlockGemmArgs& a) { return a.gated ? launch<true>(a) : launch<false>(a); }
 
 }  // namespace epi

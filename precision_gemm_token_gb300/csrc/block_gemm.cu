@@ -529,7 +529,7 @@ static int tile_width(int M, int N) {
 }
 
 int launch_block_gemm(const BlockGemmArgs& a) {
-  if (a.M / (a.grouped ? a.experts : 1) <= (a.grouped ? kFewRows / 2 : kFewRows)) return launch_block_few(a);
+  if (block_few_takes(a)) return launch_block_few(a);
   if (a.gated) return launch<256, true, true>(a);
   if (a.grouped) return launch<256, true, false>(a);
   switch (tile_width(a.M, a.N)) {

@@ -93,8 +93,8 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
 // this code stands there once for each of them, and has to stay in the instruction cache beside the loops
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + expf(-g)); }
 
-// Calls with few rows (block_few.cu): up to so many, or experts with half as many on average.
-constexpr int kFewRows = 32;
+// Calls with few rows (block_few.cu).
+bool block_few_takes(const BlockGemmArgs& a);
 int launch_block_few(const BlockGemmArgs& a);
 
 }  // namespace epi

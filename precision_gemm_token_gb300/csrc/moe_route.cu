@@ -4,10 +4,12 @@
 //
 // The choice is by the exact order of score + bias, ties to the lowest index.
 // The kernel works it out in 32 bits with a bound on what the roundings may
-// have moved, and repeats a token in 64 bits where two candidates lie closer
-// than that (FP64 is slow on this GPU; of random scores a few tokens in a
-// thousand need it). Without a bias the order of the scores is the order of
-// the logits, which needs no arithmetic.
+// have moved. Where two candidates lie closer than that (of random scores, in
+// a few tokens of a thousand) it looks at them in 64 bits: of a sigmoid's
+// chosen experts a lane each, else the whole token again (FP64 is slow on this
+// GPU: 20 us for such a token, which then is the call's time). Without a bias
+// the order of the scores is the order of the logits, which needs no
+// arithmetic.
 //
 // Bound: instructions and the chain of the choices; the bytes are few.
 #include "blocks.cuh"
@@ -84,9 +86,12 @@ __device__ __forceinline__ float clean(float l) {
 }
 
 // Chooses the token's experts: slot j's in lane j (-1: none left). Returns
-// whether two candidates were too close to tell (never for T = double).
+// what is too close to tell (nothing for T = double): kGroups, of the groups
+// or of more experts than there are lanes; kExperts, of the chosen experts,
+// and then the lanes have all candidates for them, `top` or more.
+enum : int { kTold = 0, kExperts = 1, kGroups = 2 };
 template <class T, int kPer>
-__device__ __forceinline__ bool choose(const MoeRouteArgs& a, const float (&l)[kPer], float top, int lane, int& mine) {
+__device__ __forceinline__ int choose(const MoeRouteArgs& a, const float (&l)[kPer], float top, int lane, int& mine) {
   typedef typename Keys<T>::Key Key;
   constexpr bool kApprox = sizeof(T) == 4;
   const bool by_value = a.bias != nullptr || (a.groups > 1 && a.group_best > 1);
@@ -119,7 +124,7 @@ __device__ __forceinline__ bool choose(const MoeRouteArgs& a, const float (&l)[k
   T bound = T(0);
   if (kApprox && by_value)
     bound = T((a.sigmoid ? 0x1p-20f : 0x1p-16f) + 0x1p-21f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most))));
-  bool close = false;
+  int close = kTold;
   if (a.groups > 1 && a.top_groups < a.groups) {
     const int size = a.experts / a.groups;
     int group[kPer];
@@ -153,7 +158,7 @@ __device__ __forceinline__ bool choose(const MoeRouteArgs& a, const float (&l)[k
       const Best<T> b = warp_best(Best<T>{there ? value : 0, there ? lane : 0x7fffffff});
       if (kApprox && by_value && j == a.top_groups && b.key != 0 &&
           !(Keys<T>::value(before) - Keys<T>::value(b.key) > bound))
-        close = true;
+        close = kGroups;
       before = b.key;
       if (j < a.top_groups) kept |= 1u << b.i;
     }
@@ -171,16 +176,21 @@ __device__ __forceinline__ bool choose(const MoeRouteArgs& a, const float (&l)[k
   mine = -1;
   Key before = 0;
 #pragma unroll 1
-  for (int j = 0; j <= a.top; ++j) {
+  for (int j = 0;; ++j) {
     Best<T> b{0, 0x7fffffff};
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (c[i] > b.key) b = Best<T>{c[i], lane + 32 * i};
     b = warp_best(b);
     if (b.key == 0) break;
-    if (kApprox && !by_logit && j > 0 && !(Keys<T>::value(before) - Keys<T>::value(b.key) > bound)) close = true;
+    const bool near = kApprox && !by_logit && j > 0 && !(Keys<T>::value(before) - Keys<T>::value(b.key) > bound);
+    if (j >= a.top && !near) break;
+    if (near) close = max(close, static_cast<int>(kExperts));
+    if (j == 32) {
+      close = kGroups;
+      break;
+    }
     before = b.key;
-    if (j == a.top) break;
     if (lane == j) mine = b.i;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
@@ -196,20 +206,42 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + (threadIdx.x >> 5);
   if (t >= a.tokens) return;
+  const auto logit = [&](int e) {
+    return clean(kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[t * a.ld + e])
+                       : static_cast<const float*>(a.logits)[t * a.ld + e]);
+  };
   float l[kPer], top = minus_inf();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
     l[i] = minus_inf();
     if (e < a.experts)
-      l[i] = clean(kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[t * a.ld + e])
-                         : static_cast<const float*>(a.logits)[t * a.ld + e]);
+      l[i] = logit(e);
     top = fmaxf(top, l[i]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
   int mine;
-  if (choose<float, kPer>(a, l, top, lane, mine)) choose<double, kPer>(a, l, top, lane, mine);
+  const int close = choose<float, kPer>(a, l, top, lane, mine);
+  if (close == kExperts && a.sigmoid) {
+    // the candidates in 64 bits, a lane each, and their order
+    const Keys<double>::Key key =
+        mine < 0 ? 0 : Keys<double>::of(1.0 / (1.0 + exp(-static_cast<double>(logit(mine)))) + static_cast<double>(a.bias[mine]));
+    int before = 0, told = -1;
+    for (int o = 0; o < 32; ++o) {
+      const Keys<double>::Key k = __shfl_sync(kAll, key, o);
+      const int e = __shfl_sync(kAll, mine, o);
+      if (k > key || (k == key && e < mine)) ++before;
+    }
+    for (int j = 0; j < a.top; ++j) {
+      const unsigned who = __ballot_sync(kAll, mine >= 0 && before == j);
+      const int e = __shfl_sync(kAll, mine, who != 0 ? __ffs(who) - 1 : 0);
+      if (lane == j && who != 0) told = e;
+    }
+    mine = told;
+  } else if (close != kTold) {
+    choose<double, kPer>(a, l, top, lane, mine);
+  }
   // weights: the scores of the chosen, in 32 bits
   float sum = 1.0f;
   if (!a.sigmoid && !a.renormalize) {
@@ -220,9 +252,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
     sum = warp_sum(sum);
   }
   float lm = minus_inf();
-  if (mine >= 0)
-    lm = clean(kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[t * a.ld + mine])
-                     : static_cast<const float*>(a.logits)[t * a.ld + mine]);
+  if (mine >= 0) lm = logit(mine);
   if (a.renormalize) {
     // softmax: against the largest of the chosen, whose scores may all be too
     // small for 32 bits; a sigmoid of less than -30 is e^x within 2^-43 of it

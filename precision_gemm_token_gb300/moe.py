@@ -10,20 +10,22 @@ the operators happens here.
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional
 
 import torch
 
 from . import _binding as E
-from .blocks import (_BF16, _F32, _I32, _U8, BlockWorkspace, _array, _bad, _blocks, _lib, _matrix, _new, _out, _room, _start,
-                     _status, quantize_weight)
+from .blocks import (_BF16, _F32, _I32, _U8, BlockWorkspace, _array, _bad, _blocks, _lib, _made, _matrix, _out, _room,
+                     _start, _status, quantize_weight)
 
 _SCORING = {"softmax": E.SCORE_SOFTMAX, "sigmoid": E.SCORE_SIGMOID}
+_bytes = lru_cache(1024)(E.epilora_moe_workspace_bytes)       # asked of the library once per shape
 _LOGITS = {torch.float32: E.LOGITS_F32, torch.bfloat16: E.LOGITS_BF16}
 
 
-def route(logits, top: int, bias=None, scoring: str = "softmax", groups: int = 1, top_groups: int = 1, group_best: int = 1,
-          renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+def route(logits, top: int, bias=None, scoring: str = "softmax", groups: int = 1, top_groups: int = 1,
+          group_best: int = 1, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
     """The `top` experts of each token and their weights from the router's
     logits [tokens, experts] (fp32 or bf16, any row stride): (ids int32
     [tokens, top], weights fp32 [tokens, top]). `bias` (fp32 [experts]) is
@@ -37,13 +39,11 @@ def route(logits, top: int, bias=None, scoring: str = "softmax", groups: int = 1
     at, T, n, _ = _matrix(logits, logits.dtype, dev, "logits")
     ld = logits.stride(0) if T > 1 else n
     b_at = None if bias is None else _array(bias, _F32, (n,), dev, "bias")
-    if ids is None:
-        ids = _new(logits, (T, max(top, 0)), _I32, given)
-    if weights is None:
-        weights = _new(logits, (T, max(top, 0)), _F32, given)
-    rc = _lib().epilora_moe_route(T, n, top, at, fmt, ld, b_at, how, groups, top_groups, group_best, 1 if renormalize else 0,
-                                  scale, _array(ids, _I32, (T, max(top, 0)), dev, "ids"),
-                                  _array(weights, _F32, (T, max(top, 0)), dev, "weights"), raw)
+    shape = (T, top if top > 0 else 0)
+    ids, i_at = _made(ids, logits, shape, _I32, dev, given, "ids")
+    weights, w_at = _made(weights, logits, shape, _F32, dev, given, "weights")
+    rc = _lib().epilora_moe_route(T, n, top, at, fmt, ld, b_at, how, groups, top_groups, group_best,
+                                  1 if renormalize else 0, scale, i_at, w_at, raw)
     if rc:
         E.check(rc, "route")
     return ids, weights
@@ -89,8 +89,8 @@ def _choices(ids, tokens, dev):
     return _array(ids, _I32, tuple(ids.shape), dev, "ids"), ids.shape[1]
 
 
-def experts_up(x, ids, w: ExpertWeights, codes=None, scale=None, workspace: Optional[BlockWorkspace] = None, status=None,
-               stream=None):
+def experts_up(x, ids, w: ExpertWeights, codes=None, scale=None, workspace: Optional[BlockWorkspace] = None,
+               status=None, stream=None):
     """silu(x gate^T) * (x up^T) of each token's experts, block-quantized:
     (codes uint8 [tokens, top, inner], scale fp32 [ceil(inner / 128), tokens *
     top]). x bf16 [tokens, hidden]; ids int32 [tokens, top], negative: no
@@ -101,15 +101,12 @@ def experts_up(x, ids, w: ExpertWeights, codes=None, scale=None, workspace: Opti
     at, T, H, ld = _matrix(x, _BF16, dev, "x", None, w.hidden)
     i_at, top = _choices(ids, T, dev)
     shape, s_shape = (T, top, w.inner), (_blocks(w.inner), T * top)
-    if codes is None:
-        codes = _new(x, shape, _U8, given)
-    if scale is None:
-        scale = _new(x, s_shape, _F32, given)
-    c_at, s_at = _array(codes, _U8, shape, dev, "codes"), _array(scale, _F32, s_shape, dev, "scale")
-    need = E.epilora_moe_workspace_bytes(E.MOE_UP, T, top, w.experts, H, w.inner)
+    codes, c_at = _made(codes, x, shape, _U8, dev, given, "codes")
+    scale, s_at = _made(scale, x, s_shape, _F32, dev, given, "scale")
+    need = _bytes(E.MOE_UP, T, top, w.experts, H, w.inner)
     buf, w_at = _room(workspace, x, need, dev, raw, given)
-    rc = _lib().epilora_moe_experts_up(T, top, w.experts, H, w.inner, at, ld, i_at, w.up_at, w.up_scale_at, c_at, s_at, w_at,
-                                       need, _status(status, dev), raw)
+    rc = _lib().epilora_moe_experts_up(T, top, w.experts, H, w.inner, at, ld, i_at, w.up_at, w.up_scale_at, c_at, s_at,
+                                       w_at, need, _status(status, dev), raw)
     if rc:
         E.check(rc, "experts_up")
     return codes, scale
@@ -127,7 +124,7 @@ def experts_down(codes, scale, ids, weights, w: ExpertWeights, out=None, workspa
     s_at = _array(scale, _F32, (_blocks(w.inner), T * top), dev, "scale")
     i_at, f_at = _array(ids, _I32, (T, top), dev, "ids"), _array(weights, _F32, (T, top), dev, "weights")
     out, o_at, ld = _out(out, codes, T, w.hidden, dev, given)
-    need = E.epilora_moe_workspace_bytes(E.MOE_DOWN, T, top, w.experts, w.hidden, w.inner)
+    need = _bytes(E.MOE_DOWN, T, top, w.experts, w.hidden, w.inner)
     buf, w_at = _room(workspace, codes, need, dev, raw, given)
     rc = _lib().epilora_moe_experts_down(T, top, w.experts, w.hidden, w.inner, c_at, s_at, i_at, f_at, w.down_at,
                                          w.down_scale_at, o_at, ld, w_at, need, _status(status, dev), raw)
@@ -136,7 +133,8 @@ def experts_down(codes, scale, ids, weights, w: ExpertWeights, out=None, workspa
     return out
 
 
-def experts(x, ids, weights, w: ExpertWeights, out=None, workspace: Optional[BlockWorkspace] = None, status=None, stream=None):
+def experts(x, ids, weights, w: ExpertWeights, out=None, workspace: Optional[BlockWorkspace] = None, status=None,
+            stream=None):
     """experts_up, then experts_down: y[t] = sum_j weights[t, j] *
     MLP_{ids[t, j]}(x[t]), bf16 [tokens, hidden]."""
     dev, raw, given = _start(x, stream)
@@ -146,10 +144,10 @@ def experts(x, ids, weights, w: ExpertWeights, out=None, workspace: Optional[Blo
     i_at, top = _choices(ids, T, dev)
     f_at = _array(weights, _F32, (T, top), dev, "weights")
     out, o_at, old = _out(out, x, T, w.hidden, dev, given)
-    need = E.epilora_moe_workspace_bytes(E.MOE_UP | E.MOE_DOWN, T, top, w.experts, H, w.inner)
+    need = _bytes(E.MOE_UP | E.MOE_DOWN, T, top, w.experts, H, w.inner)
     buf, w_at = _room(workspace, x, need, dev, raw, given)
-    rc = _lib().epilora_moe_experts(T, top, w.experts, H, w.inner, at, ld, i_at, f_at, w.up_at, w.up_scale_at, w.down_at,
-                                    w.down_scale_at, o_at, old, w_at, need, _status(status, dev), raw)
+    rc = _lib().epilora_moe_experts(T, top, w.experts, H, w.inner, at, ld, i_at, f_at, w.up_at, w.up_scale_at,
+                                    w.down_at, w.down_scale_at, o_at, old, w_at, need, _status(status, dev), raw)
     if rc:
         E.check(rc, "experts")
     return out

@@ -19,7 +19,7 @@ struct QuantParams {
 };
 
 template <int kUnits>
-__global__ void __launch_bounds__(kQuantThreads) block_quant_kernel(const __grid_constant__ QuantParams p) {
+__global__ void __launch_bounds__(kQuantThreads, 6) block_quant_kernel(const __grid_constant__ QuantParams p) {
   pdl_wait_primary();
   pdl_allow_dependents();
   quant_tile<kUnits>(p.X, p.M, p.K, p.ldx, p.Xq, p.scale, p.scale_ld, p.rt_log2, static_cast<int>(blockIdx.x));

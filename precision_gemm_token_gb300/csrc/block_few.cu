@@ -23,7 +23,7 @@
 // line (the joined sums of 32 x 14336 -> 4096 took 7000 cycles to store).
 //
 // Bound: the copies of the weights, and start and end. Up projections of 64 tokens over 64 experts of 4096 x 1792 take
-// 132 us with plan and scatter (7.1 TB/s of the experts' 940 MB: some of them stay in L2), of one token 29.5 us (117 MB);
+// 132 us with plan and scatter (7.1 TB/s of the experts' 940 MB: some of them stay in L2), of one token 29.1 us (117 MB);
 // 32 x 14336 -> 4096 18.5 us with the quantizer (59 MB). Every wait is bounded, as in block_gemm.cu.
 #include "block_gemm.cuh"
 
@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
       __syncwarp();
     } else if (warp == 1) {
       // ===== MMA issue =====
+      pdl_wait_primary();      // (its first wait is for rows that the preceding kernels write, however long those take)
       if (elect_one()) {
         constexpr uint32_t kIdesc = idesc_f8f6f4_e4m3(kTileN, kCols);
         const uint64_t desc0 = make_smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
@@ -480,7 +481,7 @@ int launch(const BlockGemmArgs& a) {
 
 }  // namespace
 
-// The product turned round pays where the sums are gated (up projections of 1, 8 and 64 tokens 35.6 -> 29.5, 99 -> 78
+// The product turned round pays where the sums are gated (up projections of 1, 8 and 64 tokens 35.6 -> 29.1, 99 -> 78
 // and 153 -> 132 us), and where K is split (32 x 14336 -> 4096: 29.7 -> 18.5 us). Otherwise block_gemm.cu's narrower
 // tiles spread better over the SMs (32 x 4096 -> 28672: 26.4 against 30.6 us; down projections of 64 tokens 88 against
 // 99).

@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
       __syncwarp();
     } else if (warp == 1) {
       // ===== MMA issue =====
+      pdl_wait_primary();      // (its first wait is for rows that the preceding kernels write, however long those take)
       if (elect_one()) {
         constexpr uint32_t kIdesc = idesc_f8f6f4_e4m3(kRows, BN);
         const uint64_t desc0 = make_smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);

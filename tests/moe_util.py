@@ -67,8 +67,10 @@ def up_expected(xq, xs, ids, gu, gus):
         eg, eu = sum_bound(x.shape[1], gs), sum_bound(x.shape[1], us)
         s = O.silu(g)
         h[t, j] = s * u
-        # |silu'| < 1.1; the exponential, the quotient and the product are off by less than 2^-20 together
-        bound[t, j] = 1.1 * eg * (np.abs(u) + eu) + (np.abs(s) + 1.1 * eg) * eu + 2.0 ** -20 * np.abs(h[t, j])
+        # |silu'| < 1.1; of silu itself the exponent's argument is rounded (|g| 2^-24 of the result), and the exponential,
+        # the sum, the quotient and the product are off by less than 2^-20 together
+        own = (2.0 ** -20 + np.abs(g) * 2.0 ** -24) * np.abs(h[t, j])
+        bound[t, j] = 1.1 * eg * (np.abs(u) + eu) + (np.abs(s) + 1.1 * eg) * eu + own
     return h, bound
 
 

@@ -119,18 +119,27 @@ __global__ void __launch_bounds__(kGatherThreads) moe_gather_kernel(const __grid
   const int slot = static_cast<int>(blockIdx.x) * (kGatherThreads / 32) + static_cast<int>(threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (slot >= a.slots) return;
+  // the first 2 KB of the row on their way beside the look-up
+  const uint4* src = reinterpret_cast<const uint4*>(a.src + static_cast<int64_t>(slot) * a.K);
+  uint4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lane + 32 * i < a.K / 16) v[i] = src[lane + 32 * i];
   const int row = a.rows[slot];
   if (row < 0) return;
-  const uint4* src = reinterpret_cast<const uint4*>(a.src + static_cast<int64_t>(slot) * a.K);
   uint4* dst = reinterpret_cast<uint4*>(a.dst + static_cast<int64_t>(row) * a.K);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lane + 32 * i < a.K / 16) dst[lane + 32 * i] = v[i];
 #pragma unroll 4
-  for (int c = lane; c < a.K / 16; c += 32) dst[c] = src[c];
+  for (int c = lane + 128; c < a.K / 16; c += 32) dst[c] = src[c];
   for (int b = lane; b < n_blocks(a.K); b += 32)
     a.dst_scale[static_cast<int64_t>(b) * a.slots + row] = a.src_scale[static_cast<int64_t>(b) * a.slots + slot];
 }
 
 // A CTA sums 2048 columns of one token.
 constexpr int kCombineThreads = 256;
+constexpr int kCombineAhead = 4;         // rows that a thread has under way
 
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const __grid_constant__ MoeCombineArgs a) {
   pdl_wait_primary();
@@ -142,15 +151,26 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const __gr
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-  for (int j = 0; j < a.top; ++j) {
-    const int64_t slot = static_cast<int64_t>(t) * a.top + j;
-    const int e = a.ids[slot];
-    if (e < 0 || e >= a.experts) continue;
-    const float w = a.weights[slot];
-    float d[8];
-    unpack8(__ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.parts) + slot * a.hidden + n)), d);
+  const int64_t first = static_cast<int64_t>(t) * a.top;
+  const __nv_bfloat16* parts = static_cast<const __nv_bfloat16*>(a.parts) + first * a.hidden + n;
+  for (int j0 = 0; j0 < a.top; j0 += kCombineAhead) {
+    uint4 v[kCombineAhead];
+    bool there[kCombineAhead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(w, d[i], y[i]);
+    for (int q = 0; q < kCombineAhead; ++q) {
+      const int e = j0 + q < a.top ? a.ids[first + j0 + q] : -1;
+      there[q] = e >= 0 && e < a.experts;
+      if (there[q]) v[q] = __ldcg(reinterpret_cast<const uint4*>(parts + static_cast<int64_t>(j0 + q) * a.hidden));
+    }
+#pragma unroll
+    for (int q = 0; q < kCombineAhead; ++q) {
+      if (!there[q]) continue;
+      const float w = a.weights[first + j0 + q];
+      float d[8];
+      unpack8(v[q], d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(w, d[i], y[i]);
+    }
   }
   uint32_t o[4];
 #pragma unroll

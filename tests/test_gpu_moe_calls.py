@@ -56,7 +56,7 @@ def test_everybody_at_one_expert(t, e):
     U.close(U.f64(y), want, off)
 
 
-@pytest.mark.parametrize("t,top,e", [(1, 1, 1024), (50, 8, 1000), (3000, 6, 512)])
+@pytest.mark.parametrize("t,top,e", [(1, 1, 1024), (50, 8, 1000), (3000, 6, 512), (40, 32, 64), (7, 17, 33)])
 def test_many_experts(t, top, e):
     g = np.random.default_rng(t)
     ids = np.argsort(g.random((t, e)), 1)[:, :top].astype(np.int32)

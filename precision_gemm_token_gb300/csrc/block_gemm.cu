@@ -48,6 +48,7 @@ constexpr int kSumBarrier = 1;
 constexpr int kRegsOther = 40, kRegsSum = 232;
 constexpr int kHalf = 256;                     // columns of a half of TMEM
 constexpr int kScaleBlocks = 32;               // blocks in the scales' ring
+constexpr int kTurnedRow = 9;                  // words of a staged row of 16 outputs
 constexpr int kScaleRow = kRows + 4;           // a block's scales: of the rows, then up to two of the weights
 
 template <int BN>
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* amax = reinterpret_cast<float*>(misc + 1024);                 // [2][2][kRows]
   float* scales = amax + 4 * kRows;                                    // [kScaleBlocks][kScaleRow]
+  uint32_t* staged = reinterpret_cast<uint32_t*>(misc + C::kMisc);      // [8 warps][32][kTurnedRow], plain only
   int* offsets = reinterpret_cast<int*>(misc + C::kMisc);              // [experts + 1], grouped only
   int* starts = offsets + p.experts + 1;
 
@@ -436,21 +438,29 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
           }
           if (side == 0) p.inner_scale[static_cast<int64_t>(tile.n) * p.M + slot] = s;
         }
-      } else if (live && cols && !dead) {
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.Y) + slot * p.ldy + n0;
+      } else if (warp_live && cols && !dead) {
+        __nv_bfloat16* const Y = static_cast<__nv_bfloat16*>(p.Y);
 #pragma unroll
         for (int c = 0; c < NC; c += 16) {
           uint32_t q[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            q[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
-          }
-          if (p.wide_store && n0 + c + 16 <= p.N) {
-            st_global_v8(out + c, q);
+          for (int i = 0; i < 8; ++i) q[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
+          if (kGrouped || (p.wide_store && n0 + c + 16 <= p.N)) {
+            if (live && (!kGrouped || n0 + c < p.N)) st_global_v8(Y + slot * p.ldy + n0 + c, q);
           } else {
+            // rows that start anywhere, and the last columns: turned round in shared memory, two rows of 16 a store (a
+            // thread's own row element by element would touch 32 sectors a store)
+            uint32_t* const turned = staged + (warp - 4) * 32 * kTurnedRow;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (n0 + c + i < p.N) reinterpret_cast<uint16_t*>(out)[c + i] = static_cast<uint16_t>(q[i / 2] >> (16 * (i & 1)));
+            for (int i = 0; i < 8; ++i) turned[lane * kTurnedRow + i] = q[i];
+            __syncwarp();
+            const int n = n0 + c + (lane & 15);
+#pragma unroll 4
+            for (int i = lane >> 4; i < 32; i += 2)
+              if ((warp & 3) * 32 + i < tile.rows && n < p.N)
+                reinterpret_cast<uint16_t*>(Y)[(tile.first + (warp & 3) * 32 + i) * p.ldy + n] =
+                    reinterpret_cast<const uint16_t*>(turned + i * kTurnedRow)[lane & 15];
+            __syncwarp();
           }
         }
       }
@@ -499,7 +509,7 @@ int launch(const BlockGemmArgs& a) {
   int rc = make_tma_2d_u8(&p.tmA, a.A, a.M, a.K, a.K, kRows, kBlock, true);
   if (rc == EPILORA_OK) rc = make_tma_2d_u8(&p.tmB, a.W, w_rows, a.K, a.K, kGated ? kRows : BN, kBlock, true);
   if (rc != EPILORA_OK) return rc;
-  const int extra = 1024 + C::kMisc + (kGrouped ? 2 * (p.experts + 1) * 4 : 0);
+  const int extra = 1024 + C::kMisc + (kGrouped ? 2 * (p.experts + 1) * 4 : kSumThreads * kTurnedRow * 4);
   p.stages = (227 * 1024 - extra) / C::kStage;
   if (p.stages > C::kStagesMax) p.stages = C::kStagesMax;
   const int smem = p.stages * C::kStage + extra;
@@ -521,7 +531,7 @@ int launch(const BlockGemmArgs& a) {
 
 // Tiles of BN columns: as wide as pays. A block of K costs a CTA 0.50, 0.31, 0.21 or 0.20 us at 256, 128, 64 and 32
 // columns; a call takes as many of them as its fullest CTA has tiles (one token, 4096 -> 6144: 20.7, 14.4, 11.5 and
-// 17.6 us; 509 tokens, 2064 -> 1000: 46, 28, 18 and 15; 2048 tokens, 8192 -> 28672: 395, 568, 854 and 1416).
+// 17.6 us; 509 tokens, 2064 -> 1000, with ends 4 us longer than now: 46, 28, 18 and 15; 2048 tokens, 8192 -> 28672: 395, 568, 854 and 1416).
 static int tile_width(int M, int N) {
   const int widths[4] = {256, 128, 64, 32}, costs[4] = {50, 31, 21, 20};
   const int64_t sms = num_sms(), mt = (M + kRows - 1) / kRows;

@@ -58,7 +58,8 @@ struct Cfg {
   static constexpr int kGroup = kHalf / BN;    // blocks of a group
   static constexpr int kStagesMax = 16;
   static constexpr int kSlots = kScaleBlocks / kGroup;       // groups in the scales' ring
-  static constexpr int kMisc = 1024 + 2 * 2 * kRows * 4 + kScaleBlocks * kScaleRow * 4;     // barriers, amax exchange, scales
+  // barriers, amax exchange, scales
+  static constexpr int kMisc = 1024 + 2 * 2 * kRows * 4 + kScaleBlocks * kScaleRow * 4;
 };
 
 struct Params {
@@ -77,7 +78,9 @@ struct Params {
   int stages, wide_store, early_weights;
 };
 
-__device__ __forceinline__ void sums_barrier() { asm volatile("bar.sync %0, %1;" ::"n"(kSumBarrier), "n"(kSumThreads) : "memory"); }
+__device__ __forceinline__ void sums_barrier() {
+  asm volatile("bar.sync %0, %1;" ::"n"(kSumBarrier), "n"(kSumThreads) : "memory");
+}
 
 // acc += x * f for a register of a TMEM load: volatile, so that it stays behind the wait for the load. One
 // multiply-add at a time: those of two need their operands in pairs of registers, which costs a move each.
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
   using C = Cfg<BN>;
   constexpr int NC = BN / 2;                    // columns of a summing thread
   constexpr int CH = NC < 32 ? NC : 32;         // of them per TMEM load
-  constexpr int LOADS = 64 / CH;                // loads under way together: a load takes some 200 cycles, whatever its size
+  constexpr int LOADS = 64 / CH;                // loads under way together (some 200 cycles each, whatever the size)
   constexpr int G = C::kGroup;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -283,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
         tile = ahead.at(c_t);
         c_a = p.a_scale + tile.first;
         const int w = i % kW;                   // (threads below kW * G)
-        const int block = kGated ? (tile.expert * 2 + w) * nb + tile.n : tile.expert * nb + min(tile.n * BN / kBlock + w, nb - 1);
+        const int block = kGated ? (tile.expert * 2 + w) * nb + tile.n
+                                 : tile.expert * nb + min(tile.n * BN / kBlock + w, nb - 1);
         c_w = p.w_scale + static_cast<int64_t>(block) * kb;
       };
       const auto fetch = [&] {
@@ -341,14 +345,16 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
       const bool warp_live = (warp & 3) * 32 < tile.rows;
       const int row = tile.first + (live ? r : 0);
       const int slot = p.out_rows != nullptr ? __ldcg(p.out_rows + row) : row;
-      const int n0 = kGated ? tile.n * kBlock + side * (NC / 2) : tile.n * BN + side * NC;      // this side's first column
+      // this side's first column
+      const int n0 = kGated ? tile.n * kBlock + side * (NC / 2) : tile.n * BN + side * NC;
       const bool cols = n0 < p.N;
       float acc[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
 #pragma unroll 1
       for (int b0 = 0; b0 < kb; b0 += G) {
-        if (!dead && !__all_sync(0xffffffffu, BN == 256 ? poll(&filled[half], hph) : wait(&filled[half], hph))) dead = true;
+        if (!dead && !__all_sync(0xffffffffu, BN == 256 ? poll(&filled[half], hph) : wait(&filled[half], hph)))
+          dead = true;
         if (!dead) {
           tc_fence_after();
           const auto release = [&] {
@@ -359,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
           if (warp_live) {
             const int n = min(G, kb - b0);
             const float* sc = scales + take * (G * kScaleRow);
-            // piece c of the 128 columns that a thread has in a half: block c * CH / NC of the group, from column c * CH % NC
-            // of the thread's; gated: its first half gate, its second up
+            // piece c of the 128 columns that a thread has in a half: block c * CH / NC of the group, from column
+            // c * CH % NC of the thread's; gated: its first half gate, its second up
             const auto at = [&](int c) {
               const int u = c * CH / NC, col = c * CH % NC;
               return lanes + half * kHalf + u * BN +
@@ -531,7 +537,8 @@ int launch(const BlockGemmArgs& a) {
 
 // Tiles of BN columns: as wide as pays. A block of K costs a CTA 0.50, 0.31, 0.21 or 0.20 us at 256, 128, 64 and 32
 // columns; a call takes as many of them as its fullest CTA has tiles (one token, 4096 -> 6144: 20.7, 14.4, 11.5 and
-// 17.6 us; 509 tokens, 2064 -> 1000, with ends 4 us longer than now: 46, 28, 18 and 15; 2048 tokens, 8192 -> 28672: 395, 568, 854 and 1416).
+// 17.6 us; 509 tokens, 2064 -> 1000, with ends 4 us longer than now: 46, 28, 18 and 15; 2048 tokens, 8192 -> 28672:
+// 395, 568, 854 and 1416).
 static int tile_width(int M, int N) {
   const int widths[4] = {256, 128, 64, 32}, costs[4] = {50, 31, 21, 20};
   const int64_t sms = num_sms(), mt = (M + kRows - 1) / kRows;

@@ -38,6 +38,26 @@ def test_few_rows_over_a_cluster(m, n, k):
     U.close(U.f64(y), want, off + U.BF16 * (np.abs(want) + off))
 
 
+# tiles of every width (and the product turned round), rows of the output that start anywhere
+@pytest.mark.parametrize("m,n,k", [(2000, 4097, 256), (300, 6001, 144), (150, 2003, 1040), (64, 501, 4096), (3000, 23, 576),
+                                   (9, 1999, 4096), (257, 20001, 128)])
+def test_odd_widths(m, n, k):
+    w = block_weight(n, k, n)
+    x = U.activations(m, k, seed=m).cuda()
+    room = torch.zeros(m, -(-n // 16) * 16, dtype=torch.bfloat16, device="cuda")
+    want = B.block_linear(x, w, out=room[:, :n])
+    assert torch.equal(B.block_linear(x, w), want)
+    odd = torch.full((m, n + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.block_linear(x, w, out=odd[:, 1:n + 1])
+    assert torch.equal(odd[:, 1:n + 1], want) and (odd[:, 0] == 7).all() and (odd[:, n + 1:] == 7).all()
+    assert (room[:, n:] == 0).all()
+    rows = [0, m // 2, m - 1]
+    exact, size = O.product(O.values_rows(*O.quant_rows(x[rows].float().cpu().numpy())),
+                            O.values_weight(w.codes.cpu().numpy(), w.scale.cpu().numpy()))
+    off = U.sum_bound(k, size)
+    U.close(U.f64(want[rows]), exact, off + U.BF16 * (np.abs(exact) + off))
+
+
 @pytest.mark.parametrize("t,e", [(100, 64), (300, 64), (40, 128)])
 def test_everybody_at_one_expert(t, e):
     """Batches that are few rows an expert on average, all of them with one."""

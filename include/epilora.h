@@ -663,17 +663,20 @@ EPILORA_API int epilora_moe_route(int tokens, int experts, int top, const void* 
  *       block quantization; slots without an expert: zero codes, zero scales
  * down: Y[t] = bf16( sum_j weights[t][j] bf16(h[t][j] Wdown[e]^T) ), j ascending in fp32 over the slots that
  *       have an expert (each expert's output is rounded to bf16 once, as a model that adds them up would)
+ * epilora_moe_experts_down_f32 and epilora_moe_experts_f32 keep each expert's output in fp32 and round Y alone; they
+ * write and read 8 bytes instead of 4 per slot and column of Y on the way, in a larger workspace.
  * epilora_moe_experts is up, then down. X is bf16 [tokens][ldx], Y bf16
  * [tokens][ldy], 16-byte aligned, ldy a multiple of 8; outputs must not
  * overlap inputs. Kernels: up 3, down 4, both 5. Which kernels run depends on
  * the sizes alone, and a token's results on no other token. tokens == 0 is a
  * no-op.
  * Workspace: epilora_moe_workspace_bytes(what, ...) bytes for EPILORA_MOE_UP,
- * EPILORA_MOE_DOWN, or both or'ed together for epilora_moe_experts; 256-byte
+ * EPILORA_MOE_DOWN, or both or'ed together for epilora_moe_experts, with
+ * EPILORA_MOE_F32_PARTS or'ed to the last two for the _f32 calls; 256-byte
  * aligned, no initialization; calls that share one must be ordered on one
  * stream. 0 for sizes that the calls refuse.
  */
-typedef enum { EPILORA_MOE_UP = 1, EPILORA_MOE_DOWN = 2 } epilora_moe_part;
+typedef enum { EPILORA_MOE_UP = 1, EPILORA_MOE_DOWN = 2, EPILORA_MOE_F32_PARTS = 4 } epilora_moe_part;
 EPILORA_API size_t epilora_moe_workspace_bytes(int what, int tokens, int top, int experts, int hidden, int inner);
 EPILORA_API int epilora_moe_experts_up(int tokens, int top, int experts, int hidden, int inner,
                       const void* X, int64_t ldx, const int32_t* ids, const uint8_t* Wup, const float* wup_scale,
@@ -683,7 +686,15 @@ EPILORA_API int epilora_moe_experts_down(int tokens, int top, int experts, int h
                       const uint8_t* Hq, const float* h_scale, const int32_t* ids, const float* weights,
                       const uint8_t* Wdown, const float* wdown_scale, void* Y, int64_t ldy,
                       void* workspace, size_t workspace_bytes, int* status_dev, void* stream);
+EPILORA_API int epilora_moe_experts_down_f32(int tokens, int top, int experts, int hidden, int inner,
+                      const uint8_t* Hq, const float* h_scale, const int32_t* ids, const float* weights,
+                      const uint8_t* Wdown, const float* wdown_scale, void* Y, int64_t ldy,
+                      void* workspace, size_t workspace_bytes, int* status_dev, void* stream);
 EPILORA_API int epilora_moe_experts(int tokens, int top, int experts, int hidden, int inner,
+                      const void* X, int64_t ldx, const int32_t* ids, const float* weights,
+                      const uint8_t* Wup, const float* wup_scale, const uint8_t* Wdown, const float* wdown_scale,
+                      void* Y, int64_t ldy, void* workspace, size_t workspace_bytes, int* status_dev, void* stream);
+EPILORA_API int epilora_moe_experts_f32(int tokens, int top, int experts, int hidden, int inner,
                       const void* X, int64_t ldx, const int32_t* ids, const float* weights,
                       const uint8_t* Wup, const float* wup_scale, const uint8_t* Wdown, const float* wdown_scale,
                       void* Y, int64_t ldy, void* workspace, size_t workspace_bytes, int* status_dev, void* stream);

@@ -32,6 +32,7 @@ from ._binding import (  # noqa: F401
     LOGITS_BF16,
     LOGITS_F32,
     MOE_DOWN,
+    MOE_F32_PARTS,
     MOE_MAX_EXPERTS,
     MOE_MAX_TOP,
     MOE_UP,
@@ -62,6 +63,8 @@ from ._binding import (  # noqa: F401
     epilora_lora_shrink,
     epilora_moe_experts,
     epilora_moe_experts_down,
+    epilora_moe_experts_down_f32,
+    epilora_moe_experts_f32,
     epilora_moe_experts_up,
     epilora_moe_route,
     epilora_moe_workspace_bytes,

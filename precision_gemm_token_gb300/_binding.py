@@ -35,6 +35,7 @@ SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
 MOE_UP = 1
 MOE_DOWN = 2
+MOE_F32_PARTS = 4
 MOE_MAX_EXPERTS = 1024              # EPILORA_MOE_MAX_EXPERTS
 MOE_MAX_TOP = 32                    # EPILORA_MOE_MAX_TOP
 
@@ -103,6 +104,10 @@ SIGNATURES = {
                                           _i64, _vp, _sz, _vp, _vp]),
     "epilora_moe_experts": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
                                      _vp, _i64, _vp, _sz, _vp, _vp]),
+    "epilora_moe_experts_down_f32": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp,
+                                              _vp, _i64, _vp, _sz, _vp, _vp]),
+    "epilora_moe_experts_f32": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                                         _vp, _vp, _i64, _vp, _sz, _vp, _vp]),
 }
 
 _lib = None
@@ -339,8 +344,22 @@ def epilora_moe_experts_down(tokens, top, experts, hidden, inner, Hq, h_scale, i
                                            workspace_bytes, _p(status_dev), _stream(stream))
 
 
+def epilora_moe_experts_down_f32(tokens, top, experts, hidden, inner, Hq, h_scale, ids, weights, Wdown, wdown_scale, Y,
+                                 ldy, workspace, workspace_bytes, status_dev=None, stream=None) -> int:
+    return load().epilora_moe_experts_down_f32(tokens, top, experts, hidden, inner, _p(Hq), _p(h_scale), _p(ids),
+                                               _p(weights), _p(Wdown), _p(wdown_scale), _p(Y), ldy, _p(workspace),
+                                               workspace_bytes, _p(status_dev), _stream(stream))
+
+
 def epilora_moe_experts(tokens, top, experts, hidden, inner, X, ldx, ids, weights, Wup, wup_scale, Wdown, wdown_scale,
                         Y, ldy, workspace, workspace_bytes, status_dev=None, stream=None) -> int:
     return load().epilora_moe_experts(tokens, top, experts, hidden, inner, _p(X), ldx, _p(ids), _p(weights), _p(Wup),
                                       _p(wup_scale), _p(Wdown), _p(wdown_scale), _p(Y), ldy, _p(workspace),
                                       workspace_bytes, _p(status_dev), _stream(stream))
+
+
+def epilora_moe_experts_f32(tokens, top, experts, hidden, inner, X, ldx, ids, weights, Wup, wup_scale, Wdown,
+                            wdown_scale, Y, ldy, workspace, workspace_bytes, status_dev=None, stream=None) -> int:
+    return load().epilora_moe_experts_f32(tokens, top, experts, hidden, inner, _p(X), ldx, _p(ids), _p(weights),
+                                          _p(Wup), _p(wup_scale), _p(Wdown), _p(wdown_scale), _p(Y), ldy,
+                                          _p(workspace), workspace_bytes, _p(status_dev), _stream(stream))

@@ -100,7 +100,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int BN, bool kGrouped, bool kGated>
+// kF32: grouped products that leave in fp32, 512 bytes a thread instead of 256 (down projections of 4096 tokens, sum and
+// all, 557 us instead of 374, of 64 tokens 89.5 instead of 83.5, of one 22.3 instead of 21.2: the parts' traffic)
+template <int BN, bool kGrouped, bool kGated, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_constant__ Params p) {
   using C = Cfg<BN>;
   constexpr int NC = BN / 2;                    // columns of a summing thread
@@ -444,6 +446,17 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
           }
           if (side == 0) p.inner_scale[static_cast<int64_t>(tile.n) * p.M + slot] = s;
         }
+      } else if constexpr (kF32) {
+        if (live && !dead) {
+          float* const Y = static_cast<float*>(p.Y) + slot * p.ldy + n0;
+#pragma unroll
+          for (int c = 0; c < NC; c += 8) {
+            uint32_t q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(acc[c + i]);
+            if (n0 + c < p.N) st_global_v8(Y + c, q);
+          }
+        }
       } else if (warp_live && cols && !dead) {
         __nv_bfloat16* const Y = static_cast<__nv_bfloat16*>(p.Y);
 #pragma unroll
@@ -485,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
   }
 }
 
-template <int BN, bool kGrouped, bool kGated>
+template <int BN, bool kGrouped, bool kGated, bool kF32 = false>
 int launch(const BlockGemmArgs& a) {
   using C = Cfg<BN>;
   Params p{};
@@ -519,7 +532,7 @@ int launch(const BlockGemmArgs& a) {
   p.stages = (227 * 1024 - extra) / C::kStage;
   if (p.stages > C::kStagesMax) p.stages = C::kStagesMax;
   const int smem = p.stages * C::kStage + extra;
-  const auto kern = block_gemm_kernel<BN, kGrouped, kGated>;
+  const auto kern = block_gemm_kernel<BN, kGrouped, kGated, kF32>;
   static int attr_done[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EPILORA_ERR_CUDA;
@@ -554,7 +567,7 @@ static int tile_width(int M, int N) {
 int launch_block_gemm(const BlockGemmArgs& a) {
   if (block_few_takes(a)) return launch_block_few(a);
   if (a.gated) return launch<256, true, true>(a);
-  if (a.grouped) return launch<256, true, false>(a);
+  if (a.grouped) return a.f32 ? launch<256, true, false, true>(a) : launch<256, true, false>(a);
   switch (tile_width(a.M, a.N)) {
     case 256: return launch<256, false, false>(a);
     case 128: return launch<128, false, false>(a);

@@ -74,9 +74,9 @@ struct BlockGemmArgs {
   int64_t a_scale_ld;
   const uint8_t* W;
   const float* w_scale;
-  void* Y;              // bf16 [M][ldy]
+  void* Y;              // bf16 [M][ldy] (f32, grouped only: fp32)
   int64_t ldy;
-  int grouped, gated, experts;
+  int f32, grouped, gated, experts;
   const int32_t* offsets;
   const int32_t* out_rows;   // output row of each row (NULL: the same)
   uint8_t* inner;       // gated: codes [M][N] and scales [n_blocks(N)][M]
@@ -87,12 +87,13 @@ struct BlockGemmArgs {
 };
 int launch_block_gemm(const BlockGemmArgs& a);
 
-// y[t] = bf16( sum_j weights[t][j] parts[t * top + j] ), over the slots that have an expert
+// y[t] = bf16( sum_j weights[t][j] parts[t * top + j] ), over the slots that have an expert, in fp32
 struct MoeCombineArgs {
   const int32_t* ids;
   const float* weights;
   int tokens, top, experts, hidden;
-  const void* parts;    // bf16 [tokens * top][hidden]
+  const void* parts;    // [tokens * top][hidden], fp32 or bf16
+  int f32;
   void* Y;
   int64_t ldy;
   cudaStream_t stream;

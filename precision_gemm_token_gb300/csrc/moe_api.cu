@@ -34,7 +34,7 @@ struct Parts {
   MoePlan plan;
   uint8_t *xq, *inner;           // by row
   float *x_scale, *inner_scale;
-  void* out;                     // by slot
+  void* out;                     // by slot, fp32 with EPILORA_MOE_F32_PARTS, else bf16
   size_t bytes;
 };
 Parts cut_moe(void* ws, int what, int tokens, int top, int experts, int hidden, int inner) {
@@ -51,7 +51,7 @@ Parts cut_moe(void* ws, int what, int tokens, int top, int experts, int hidden, 
   if (what & EPILORA_MOE_DOWN) {
     p.inner = c.take<uint8_t>(slots * inner);
     p.inner_scale = c.take<float>(n_blocks(inner) * slots);
-    p.out = c.take<uint16_t>(slots * hidden);
+    p.out = c.take<uint8_t>(slots * hidden * (what & EPILORA_MOE_F32_PARTS ? sizeof(float) : sizeof(uint16_t)));
   }
   p.bytes = c.used;
   return p;
@@ -110,8 +110,8 @@ int enqueue_up(const MoeCall& m, const Parts& p, const void* X, int64_t ldx, con
 }
 
 // from p.inner, by row
-int enqueue_down(const MoeCall& m, const Parts& p, const uint8_t* W, const float* w_scale, const float* weights, void* Y,
-                 int64_t ldy) {
+int enqueue_down(const MoeCall& m, const Parts& p, int f32, const uint8_t* W, const float* w_scale,
+                 const float* weights, void* Y, int64_t ldy) {
   BlockGemmArgs g{};
   g.M = m.tokens * m.top;
   g.N = m.hidden;
@@ -122,6 +122,7 @@ int enqueue_down(const MoeCall& m, const Parts& p, const uint8_t* W, const float
   g.W = W;
   g.w_scale = w_scale;
   g.Y = p.out;
+  g.f32 = f32;
   g.ldy = m.hidden;
   g.grouped = 1;
   g.experts = m.experts;
@@ -131,11 +132,59 @@ int enqueue_down(const MoeCall& m, const Parts& p, const uint8_t* W, const float
   g.stream = m.stream;
   const int rc = launch_block_gemm(g);
   if (rc != EPILORA_OK) return rc;
-  return launch_moe_combine(MoeCombineArgs{m.ids, weights, m.tokens, m.top, m.experts, m.hidden, p.out, Y, ldy, m.stream});
+  return launch_moe_combine(
+      MoeCombineArgs{m.ids, weights, m.tokens, m.top, m.experts, m.hidden, p.out, f32, Y, ldy, m.stream});
 }
 
 bool out_ok(const void* Y, int64_t ldy, int hidden) { return there(Y, 16) && ldy >= hidden && ldy % 8 == 0; }
 bool ws_ok(const void* ws, size_t bytes, size_t need) { return there(ws, 256) && bytes >= need; }
+
+size_t moe_bytes(int what, int tokens, int top, int experts, int hidden, int inner) {
+  return cut_moe(nullptr, what, tokens, top, experts, hidden, inner).bytes;
+}
+
+// f32: the experts' outputs stay fp32 until their sum
+int experts_down(int tokens, int top, int experts, int hidden, int inner, const uint8_t* Hq, const float* h_scale,
+                 const int32_t* ids, const float* weights, const uint8_t* Wdown, const float* wdown_scale, void* Y,
+                 int64_t ldy, void* workspace, size_t workspace_bytes, int* status_dev, void* stream, int f32) {
+  const int what = EPILORA_MOE_DOWN | (f32 ? EPILORA_MOE_F32_PARTS : 0);
+  int rc = moe_sizes(tokens, top, experts, hidden, inner);
+  if (rc != EPILORA_OK) return rc;
+  if (tokens == 0) return EPILORA_OK;
+  if (!there(Hq, 16) || !there(h_scale, 4) || !there(ids, 4) || !there(weights, 4) || !there(Wdown, 16) ||
+      !there(wdown_scale, 4) || !out_ok(Y, ldy, hidden) || !al(status_dev, 4))
+    return EPILORA_ERR_INVALID_ARG;
+  if (!ws_ok(workspace, workspace_bytes, moe_bytes(what, tokens, top, experts, hidden, inner)))
+    return EPILORA_ERR_WORKSPACE;
+  const Parts p = cut_moe(workspace, what, tokens, top, experts, hidden, inner);
+  const MoeCall m{tokens, top, experts, hidden, inner, ids, status_dev, static_cast<cudaStream_t>(stream)};
+  rc = enqueue_plan(m, p);
+  if (rc == EPILORA_OK)
+    rc = launch_moe_gather(
+        MoeGatherArgs{Hq, h_scale, p.inner, p.inner_scale, tokens * top, inner, p.plan.rows, m.stream});
+  return rc != EPILORA_OK ? rc : enqueue_down(m, p, f32, Wdown, wdown_scale, weights, Y, ldy);
+}
+
+int experts_both(int tokens, int top, int experts, int hidden, int inner, const void* X, int64_t ldx,
+                 const int32_t* ids, const float* weights, const uint8_t* Wup, const float* wup_scale,
+                 const uint8_t* Wdown, const float* wdown_scale, void* Y, int64_t ldy, void* workspace,
+                 size_t workspace_bytes, int* status_dev, void* stream, int f32) {
+  const int what = EPILORA_MOE_UP | EPILORA_MOE_DOWN | (f32 ? EPILORA_MOE_F32_PARTS : 0);
+  int rc = moe_sizes(tokens, top, experts, hidden, inner);
+  if (rc != EPILORA_OK) return rc;
+  if (!quant_ok(X, tokens, hidden, ldx)) return EPILORA_ERR_INVALID_ARG;
+  if (tokens == 0) return EPILORA_OK;
+  if (!there(ids, 4) || !there(weights, 4) || !there(Wup, 16) || !there(wup_scale, 4) || !there(Wdown, 16) ||
+      !there(wdown_scale, 4) || !out_ok(Y, ldy, hidden) || !al(status_dev, 4))
+    return EPILORA_ERR_INVALID_ARG;
+  if (!ws_ok(workspace, workspace_bytes, moe_bytes(what, tokens, top, experts, hidden, inner)))
+    return EPILORA_ERR_WORKSPACE;
+  const Parts p = cut_moe(workspace, what, tokens, top, experts, hidden, inner);
+  const MoeCall m{tokens, top, experts, hidden, inner, ids, status_dev, static_cast<cudaStream_t>(stream)};
+  rc = enqueue_plan(m, p);
+  if (rc == EPILORA_OK) rc = enqueue_up(m, p, X, ldx, Wup, wup_scale, p.inner, p.inner_scale, false);
+  return rc != EPILORA_OK ? rc : enqueue_down(m, p, f32, Wdown, wdown_scale, weights, Y, ldy);
+}
 
 }  // namespace
 
@@ -250,10 +299,12 @@ EPILORA_API int epilora_moe_route(int tokens, int experts, int top, const void* 
 }
 
 EPILORA_API size_t epilora_moe_workspace_bytes(int what, int tokens, int top, int experts, int hidden, int inner) {
-  if (what < EPILORA_MOE_UP || what > (EPILORA_MOE_UP | EPILORA_MOE_DOWN) ||
+  constexpr int kAll = EPILORA_MOE_UP | EPILORA_MOE_DOWN | EPILORA_MOE_F32_PARTS;
+  // (the parts are those of down)
+  if (what < EPILORA_MOE_UP || what > kAll || ((what & EPILORA_MOE_F32_PARTS) && !(what & EPILORA_MOE_DOWN)) ||
       moe_sizes(tokens, top, experts, hidden, inner) != EPILORA_OK)
     return 0;
-  return cut_moe(nullptr, what, tokens, top, experts, hidden, inner).bytes;
+  return moe_bytes(what, tokens, top, experts, hidden, inner);
 }
 
 EPILORA_API int epilora_moe_experts_up(int tokens, int top, int experts, int hidden, int inner, const void* X,
@@ -267,7 +318,7 @@ EPILORA_API int epilora_moe_experts_up(int tokens, int top, int experts, int hid
   if (!there(ids, 4) || !there(Wup, 16) || !there(wup_scale, 4) || !there(Hq, 16) || !there(h_scale, 4) ||
       !al(status_dev, 4))
     return EPILORA_ERR_INVALID_ARG;
-  if (!ws_ok(workspace, workspace_bytes, epilora_moe_workspace_bytes(EPILORA_MOE_UP, tokens, top, experts, hidden, inner)))
+  if (!ws_ok(workspace, workspace_bytes, moe_bytes(EPILORA_MOE_UP, tokens, top, experts, hidden, inner)))
     return EPILORA_ERR_WORKSPACE;
   const Parts p = cut_moe(workspace, EPILORA_MOE_UP, tokens, top, experts, hidden, inner);
   const MoeCall m{tokens, top, experts, hidden, inner, ids, status_dev, static_cast<cudaStream_t>(stream)};
@@ -279,21 +330,16 @@ EPILORA_API int epilora_moe_experts_down(int tokens, int top, int experts, int h
                                          const float* h_scale, const int32_t* ids, const float* weights,
                                          const uint8_t* Wdown, const float* wdown_scale, void* Y, int64_t ldy,
                                          void* workspace, size_t workspace_bytes, int* status_dev, void* stream) {
-  int rc = moe_sizes(tokens, top, experts, hidden, inner);
-  if (rc != EPILORA_OK) return rc;
-  if (tokens == 0) return EPILORA_OK;
-  if (!there(Hq, 16) || !there(h_scale, 4) || !there(ids, 4) || !there(weights, 4) || !there(Wdown, 16) ||
-      !there(wdown_scale, 4) || !out_ok(Y, ldy, hidden) || !al(status_dev, 4))
-    return EPILORA_ERR_INVALID_ARG;
-  if (!ws_ok(workspace, workspace_bytes, epilora_moe_workspace_bytes(EPILORA_MOE_DOWN, tokens, top, experts, hidden, inner)))
-    return EPILORA_ERR_WORKSPACE;
-  const Parts p = cut_moe(workspace, EPILORA_MOE_DOWN, tokens, top, experts, hidden, inner);
-  const MoeCall m{tokens, top, experts, hidden, inner, ids, status_dev, static_cast<cudaStream_t>(stream)};
-  rc = enqueue_plan(m, p);
-  if (rc == EPILORA_OK)
-    rc = launch_moe_gather(
-        MoeGatherArgs{Hq, h_scale, p.inner, p.inner_scale, tokens * top, inner, p.plan.rows, m.stream});
-  return rc != EPILORA_OK ? rc : enqueue_down(m, p, Wdown, wdown_scale, weights, Y, ldy);
+  return experts_down(tokens, top, experts, hidden, inner, Hq, h_scale, ids, weights, Wdown, wdown_scale, Y, ldy,
+                      workspace, workspace_bytes, status_dev, stream, 0);
+}
+
+EPILORA_API int epilora_moe_experts_down_f32(int tokens, int top, int experts, int hidden, int inner, const uint8_t* Hq,
+                                             const float* h_scale, const int32_t* ids, const float* weights,
+                                             const uint8_t* Wdown, const float* wdown_scale, void* Y, int64_t ldy,
+                                             void* workspace, size_t workspace_bytes, int* status_dev, void* stream) {
+  return experts_down(tokens, top, experts, hidden, inner, Hq, h_scale, ids, weights, Wdown, wdown_scale, Y, ldy,
+                      workspace, workspace_bytes, status_dev, stream, 1);
 }
 
 EPILORA_API int epilora_moe_experts(int tokens, int top, int experts, int hidden, int inner, const void* X, int64_t ldx,
@@ -301,21 +347,17 @@ EPILORA_API int epilora_moe_experts(int tokens, int top, int experts, int hidden
                                     const float* wup_scale, const uint8_t* Wdown, const float* wdown_scale, void* Y,
                                     int64_t ldy, void* workspace, size_t workspace_bytes, int* status_dev,
                                     void* stream) {
-  constexpr int kBoth = EPILORA_MOE_UP | EPILORA_MOE_DOWN;
-  int rc = moe_sizes(tokens, top, experts, hidden, inner);
-  if (rc != EPILORA_OK) return rc;
-  if (!quant_ok(X, tokens, hidden, ldx)) return EPILORA_ERR_INVALID_ARG;
-  if (tokens == 0) return EPILORA_OK;
-  if (!there(ids, 4) || !there(weights, 4) || !there(Wup, 16) || !there(wup_scale, 4) || !there(Wdown, 16) ||
-      !there(wdown_scale, 4) || !out_ok(Y, ldy, hidden) || !al(status_dev, 4))
-    return EPILORA_ERR_INVALID_ARG;
-  if (!ws_ok(workspace, workspace_bytes, epilora_moe_workspace_bytes(kBoth, tokens, top, experts, hidden, inner)))
-    return EPILORA_ERR_WORKSPACE;
-  const Parts p = cut_moe(workspace, kBoth, tokens, top, experts, hidden, inner);
-  const MoeCall m{tokens, top, experts, hidden, inner, ids, status_dev, static_cast<cudaStream_t>(stream)};
-  rc = enqueue_plan(m, p);
-  if (rc == EPILORA_OK) rc = enqueue_up(m, p, X, ldx, Wup, wup_scale, p.inner, p.inner_scale, false);
-  return rc != EPILORA_OK ? rc : enqueue_down(m, p, Wdown, wdown_scale, weights, Y, ldy);
+  return experts_both(tokens, top, experts, hidden, inner, X, ldx, ids, weights, Wup, wup_scale, Wdown, wdown_scale, Y,
+                      ldy, workspace, workspace_bytes, status_dev, stream, 0);
+}
+
+EPILORA_API int epilora_moe_experts_f32(int tokens, int top, int experts, int hidden, int inner, const void* X,
+                                        int64_t ldx, const int32_t* ids, const float* weights, const uint8_t* Wup,
+                                        const float* wup_scale, const uint8_t* Wdown, const float* wdown_scale, void* Y,
+                                        int64_t ldy, void* workspace, size_t workspace_bytes, int* status_dev,
+                                        void* stream) {
+  return experts_both(tokens, top, experts, hidden, inner, X, ldx, ids, weights, Wup, wup_scale, Wdown, wdown_scale, Y,
+                      ldy, workspace, workspace_bytes, status_dev, stream, 1);
 }
 
 }  // extern "C"

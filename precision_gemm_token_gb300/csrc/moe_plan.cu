@@ -141,6 +141,13 @@ __global__ void __launch_bounds__(kGatherThreads) moe_gather_kernel(const __grid
 constexpr int kCombineThreads = 256;
 constexpr int kCombineAhead = 4;         // rows that a thread has under way
 
+// eight consecutive parts, as they are stored
+template <bool kF32>
+struct Parts8 {
+  uint4 v[kF32 ? 2 : 1];
+};
+
+template <bool kF32>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const __grid_constant__ MoeCombineArgs a) {
   pdl_wait_primary();
   pdl_allow_dependents();
@@ -152,22 +159,31 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const __gr
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.0f;
   const int64_t first = static_cast<int64_t>(t) * a.top;
-  const __nv_bfloat16* parts = static_cast<const __nv_bfloat16*>(a.parts) + first * a.hidden + n;
+  constexpr int kSize = kF32 ? 4 : 2;
+  const uint8_t* parts = static_cast<const uint8_t*>(a.parts) + (first * a.hidden + n) * kSize;
   for (int j0 = 0; j0 < a.top; j0 += kCombineAhead) {
-    uint4 v[kCombineAhead];
+    Parts8<kF32> v[kCombineAhead];
     bool there[kCombineAhead];
 #pragma unroll
     for (int q = 0; q < kCombineAhead; ++q) {
       const int e = j0 + q < a.top ? a.ids[first + j0 + q] : -1;
       there[q] = e >= 0 && e < a.experts;
-      if (there[q]) v[q] = __ldcg(reinterpret_cast<const uint4*>(parts + static_cast<int64_t>(j0 + q) * a.hidden));
+      if (there[q]) {
+        const uint4* src = reinterpret_cast<const uint4*>(parts + static_cast<int64_t>(j0 + q) * a.hidden * kSize);
+#pragma unroll
+        for (int i = 0; i < kSize / 2; ++i) v[q].v[i] = __ldcg(src + i);
+      }
     }
 #pragma unroll
     for (int q = 0; q < kCombineAhead; ++q) {
       if (!there[q]) continue;
       const float w = a.weights[first + j0 + q];
-      float d[8];
-      unpack8(v[q], d);
+      alignas(16) float d[8];
+      if constexpr (kF32) {
+        *reinterpret_cast<Parts8<true>*>(d) = v[q];
+      } else {
+        unpack8(v[q].v[0], d);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = fmaf(w, d[i], y[i]);
     }
@@ -206,7 +222,8 @@ int launch_moe_gather(const MoeGatherArgs& a) {
 int launch_moe_combine(const MoeCombineArgs& a) {
   const int64_t ctas = static_cast<int64_t>(a.tokens) * ((a.hidden + 8 * kCombineThreads - 1) / (8 * kCombineThreads));
   if (ctas > 0x7fffffff) return EPILORA_ERR_UNSUPPORTED;
-  return launch_dependent(moe_combine_kernel, static_cast<unsigned>(ctas), kCombineThreads, 0, a.stream, a);
+  return launch_dependent(a.f32 ? moe_combine_kernel<true> : moe_combine_kernel<false>, static_cast<unsigned>(ctas),
+                          kCombineThreads, 0, a.stream, a);
 }
 
 }  // namespace epi

@@ -83,6 +83,17 @@ def quantize_experts(gate, up, down) -> ExpertWeights:
     return ExpertWeights(gu.view(n, 2, inner, hidden), gus.view(n, 2, *gus.shape[1:]), d, ds)
 
 
+# what the experts' outputs are kept in until their weighted sum: (bit of the workspace's size, calls of the library)
+_PARTS = {_BF16: (0, "epilora_moe_experts_down", "epilora_moe_experts"),
+          _F32: (E.MOE_F32_PARTS, "epilora_moe_experts_down_f32", "epilora_moe_experts_f32")}
+
+
+def _parts(dtype):
+    if dtype not in _PARTS:
+        _bad("parts: torch.bfloat16 or torch.float32 wanted")
+    return _PARTS[dtype]
+
+
 def _choices(ids, tokens, dev):
     if ids.dim() != 2 or ids.shape[0] != tokens:
         _bad(f"ids: int32 [{tokens}, top] wanted")
@@ -113,10 +124,13 @@ def experts_up(x, ids, w: ExpertWeights, codes=None, scale=None, workspace: Opti
 
 
 def experts_down(codes, scale, ids, weights, w: ExpertWeights, out=None, workspace: Optional[BlockWorkspace] = None,
-                 status=None, stream=None):
+                 status=None, stream=None, parts=torch.bfloat16):
     """The weighted sum over a token's experts of their down projections of
-    experts_up's rows: bf16 [tokens, hidden]."""
+    experts_up's rows: bf16 [tokens, hidden]. With `parts` bf16 each expert's
+    output is rounded to it before the sum; with fp32 the sum alone is, for
+    twice the traffic of the outputs (which counts in prefill batches)."""
     dev, raw, given = _start(codes, stream)
+    bit, call, _ = _parts(parts)
     if w.dev != dev or codes.dim() != 3:
         _bad("experts_down: codes [tokens, top, inner] on the weights' device wanted")
     T, top = codes.shape[:2]
@@ -124,30 +138,31 @@ def experts_down(codes, scale, ids, weights, w: ExpertWeights, out=None, workspa
     s_at = _array(scale, _F32, (_blocks(w.inner), T * top), dev, "scale")
     i_at, f_at = _array(ids, _I32, (T, top), dev, "ids"), _array(weights, _F32, (T, top), dev, "weights")
     out, o_at, ld = _out(out, codes, T, w.hidden, dev, given)
-    need = _bytes(E.MOE_DOWN, T, top, w.experts, w.hidden, w.inner)
+    need = _bytes(E.MOE_DOWN | bit, T, top, w.experts, w.hidden, w.inner)
     buf, w_at = _room(workspace, codes, need, dev, raw, given)
-    rc = _lib().epilora_moe_experts_down(T, top, w.experts, w.hidden, w.inner, c_at, s_at, i_at, f_at, w.down_at,
-                                         w.down_scale_at, o_at, ld, w_at, need, _status(status, dev), raw)
+    rc = getattr(_lib(), call)(T, top, w.experts, w.hidden, w.inner, c_at, s_at, i_at, f_at, w.down_at, w.down_scale_at,
+                               o_at, ld, w_at, need, _status(status, dev), raw)
     if rc:
         E.check(rc, "experts_down")
     return out
 
 
 def experts(x, ids, weights, w: ExpertWeights, out=None, workspace: Optional[BlockWorkspace] = None, status=None,
-            stream=None):
+            stream=None, parts=torch.bfloat16):
     """experts_up, then experts_down: y[t] = sum_j weights[t, j] *
     MLP_{ids[t, j]}(x[t]), bf16 [tokens, hidden]."""
     dev, raw, given = _start(x, stream)
+    bit, _, call = _parts(parts)
     if w.dev != dev:
         _bad("experts: x and the weights on different devices")
     at, T, H, ld = _matrix(x, _BF16, dev, "x", None, w.hidden)
     i_at, top = _choices(ids, T, dev)
     f_at = _array(weights, _F32, (T, top), dev, "weights")
     out, o_at, old = _out(out, x, T, w.hidden, dev, given)
-    need = _bytes(E.MOE_UP | E.MOE_DOWN, T, top, w.experts, H, w.inner)
+    need = _bytes(E.MOE_UP | E.MOE_DOWN | bit, T, top, w.experts, H, w.inner)
     buf, w_at = _room(workspace, x, need, dev, raw, given)
-    rc = _lib().epilora_moe_experts(T, top, w.experts, H, w.inner, at, ld, i_at, f_at, w.up_at, w.up_scale_at,
-                                    w.down_at, w.down_scale_at, o_at, old, w_at, need, _status(status, dev), raw)
+    rc = getattr(_lib(), call)(T, top, w.experts, H, w.inner, at, ld, i_at, f_at, w.up_at, w.up_scale_at, w.down_at,
+                               w.down_scale_at, o_at, old, w_at, need, _status(status, dev), raw)
     if rc:
         E.check(rc, "experts")
     return out

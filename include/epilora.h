@@ -585,7 +585,10 @@ EPILORA_API int epilora_prompt_attention(int n_seqs, int n_tokens, const int32_t
  * are any. Code arrays and bf16 inputs are 16-byte aligned, bf16 rows have
  * strides in multiples of 8 elements. All calls are forward only. Their
  * kernels are programmatic dependents of the previous kernel on the stream
- * and wait for it before they read anything it may have written.
+ * and wait for it before they read anything it may have written. A wait
+ * inside a product that runs out (1 s; no call does that) records
+ * EPILORA_ERR_TIMEOUT in the status word; the results that it left unfinished
+ * are NaN, and so is what is computed from them.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -623,6 +626,14 @@ EPILORA_API size_t epilora_block_linear_workspace_bytes(int M, int K);
 EPILORA_API int epilora_block_linear(int M, int N, int K, const void* X, int64_t ldx, const uint8_t* Wq,
                       const float* w_scale, void* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
                       int* status_dev, void* stream);
+
+/*
+ * Test hook of the products in 8-bit blocks: with on != 0, later calls (in
+ * this process) expect more bytes than they copy for the last block of K of a
+ * tile, so that the waits for it run out (some seconds a call). on = 0 restores
+ * normal operation. Not for production use; returns EPILORA_OK.
+ */
+EPILORA_API int epilora_test_late_block_copies(int on);
 
 #define EPILORA_MOE_MAX_EXPERTS 1024
 #define EPILORA_MOE_MAX_TOP 32

@@ -56,6 +56,7 @@ from ._binding import (  # noqa: F401
     epilora_layer_forward,
     epilora_layer_forward_fp8_adapters,
     epilora_layer_forward_kernels,
+    epilora_test_late_block_copies,
     epilora_test_drop_shrink_results,
     epilora_layer_forward_noalloc,
     epilora_layer_forward_slices,

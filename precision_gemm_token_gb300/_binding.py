@@ -93,6 +93,7 @@ SIGNATURES = {
     "epilora_block_quant": (_c_int, [_vp, _c_int, _c_int, _i64, _vp, _vp, _i64, _vp]),
     "epilora_block_quant_weight": (_c_int, [_vp, _c_int, _c_int, _i64, _vp, _vp, _vp]),
     "epilora_block_matmul": (_c_int, [_c_int, _c_int, _c_int, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "epilora_test_late_block_copies": (_c_int, [_c_int]),
     "epilora_block_linear_workspace_bytes": (_sz, [_c_int, _c_int]),
     "epilora_block_linear": (_c_int, [_c_int, _c_int, _c_int, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _sz, _vp, _vp]),
     "epilora_moe_route": (_c_int, [_c_int, _c_int, _c_int, _vp, _c_int, _i64, _vp, _c_int, _c_int, _c_int, _c_int,
@@ -307,6 +308,12 @@ def epilora_block_quant_weight(W, N, K, ldw, Wq, w_scale, stream=None) -> int:
 def epilora_block_matmul(M, N, K, Xq, x_scale, x_scale_ld, Wq, w_scale, Y, ldy, status_dev=None, stream=None) -> int:
     return load().epilora_block_matmul(M, N, K, _p(Xq), _p(x_scale), x_scale_ld, _p(Wq), _p(w_scale), _p(Y), ldy,
                                        _p(status_dev), _stream(stream))
+
+
+def epilora_test_late_block_copies(on: bool) -> None:
+    """Test hook: the products in 8-bit blocks wait for bytes that nobody
+    copies while on (they end with EPILORA_ERR_TIMEOUT and give NaN)."""
+    load().epilora_test_late_block_copies(1 if on else 0)
 
 
 def epilora_block_linear_workspace_bytes(M, K) -> int:

@@ -60,6 +60,7 @@ struct Params {
   const int32_t* out_rows;
   int* status;
   int M, N, kb, n_tiles, experts, stages, copy, whole, splits, early_weights;
+  int late;                // the test hook: the copies of a tile's last stage never seem complete
 };
 
 // Gated products are of the rows by expert, others of plain matrices.
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
           // (a stage that reaches past this CTA's blocks copies some that nobody uses)
           const auto copy_w = [&](int st, int b) {
             uint8_t* dst = smem + static_cast<size_t>(st) * stage;
-            mbar_arrive_expect_tx(&full[st], stage);
+            mbar_arrive_expect_tx(&full[st], stage + (p.late && b + copy >= kb ? 16 : 0));
             load(dst, &p.tmB, st, wrow, b);
             if (kGated) load(dst + kWBytes, &p.tmB, st, wrow + p.N, b);
           };
@@ -183,11 +184,11 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
       if (elect_one()) {
         constexpr uint32_t kIdesc = idesc_f8f6f4_e4m3(kTileN, kCols);
         const uint64_t desc0 = make_smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-        int s = 0, half = 0, last = 0;
-        uint32_t ph = 0, hph = 0, last_ph = 0;
+        int s = 0, half = 0;
+        uint32_t ph = 0, hph = 0;
         bool go = true, any = false;
         for (int t = first_tile; t < walk.total && go; t += step) {
-          for (int b0 = 0; b0 < kb && go; b0 += G) {
+          for (int b0 = 0; b0 < kb; b0 += G) {
             if (!wait(&drained[half], hph ^ 1u)) {
               go = false;
               break;
@@ -211,22 +212,21 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
                   mma_f8f6f4(d + part * kCols, wd + part * (kWBytes >> 4) + 2 * kk, ad + 2 * kk, kIdesc, kk > 0);
               if (i == copy - 1 || b0 + u == kb - 1) {
                 tc_commit(&empty[s]);
+                any = true;
                 if (++s == stages) {
                   s = 0;
                   ph ^= 1u;
                 }
               }
             }
+            if (!go) break;        // (a group that is not whole is handed to nobody)
             tc_commit(&filled[half]);
-            any = true;
-            last = half;
-            last_ph = hph;
             half ^= 1;
             if (half == 0) hph ^= 1u;
           }
         }
-        // nothing of this thread in flight at exit: the last commit covers every MMA before it
-        if (any) (void)mbar_wait_bounded(&filled[last], last_ph, kWaitLimitNs);
+        // nothing of this thread in flight at exit: the last stage's commit covers every MMA before it
+        if (any) (void)mbar_wait_bounded(&empty[s > 0 ? s - 1 : stages - 1], s > 0 ? ph : ph ^ 1u, kWaitLimitNs);
       }
       __syncwarp();
     } else if (warp == 2) {
@@ -300,11 +300,12 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
     for (int t = first_tile; t < walk.total; t += step) {
       const Tile tile = walk.at(t);
       const int mine = min(tile.rows - side * kMine, kMine);       // rows of A of this side
+      const float start = dead ? __int_as_float(0x7fffffff) : 0.0f;
       float acc[kParts][kMine];
 #pragma unroll
       for (int part = 0; part < kParts; ++part)
 #pragma unroll
-        for (int c = 0; c < kMine; ++c) acc[part][c] = 0.0f;
+        for (int c = 0; c < kMine; ++c) acc[part][c] = start;
 #pragma unroll 1
       for (int b0 = 0; b0 < kb; b0 += G) {
         if (!dead && !__all_sync(0xffffffffu, wait(&filled[half], hph))) dead = true;
@@ -347,6 +348,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
         half ^= 1;
         if (half == 0) hph ^= 1u;
       }
+      if (dead && start == 0.0f) {     // sums that are not whole: the tile once more, as NaN (others finish them too)
+        t -= step;
+        continue;
+      }
       const int me = static_cast<int>(threadIdx.x) - 128;
       if constexpr (kGated) {
 #pragma unroll
@@ -372,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
           float d[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[i] = div_rn_by_recip(h[i], by.s, by.rs);
-          if (dead) continue;
           const int64_t to = p.out_rows != nullptr ? __ldcg(p.out_rows + tile.first + c) : tile.first + c;
           if (there)
             *reinterpret_cast<uint32_t*>(p.inner + to * p.N + n) = cvt_e4m3x2(d[0], d[1]) | (cvt_e4m3x2(d[2], d[3]) << 16);
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_few_kernel(const __grid_con
           const int row = rank * per + i / kTileN, n = tile.n * kTileN + i % kTileN;
           float y = sums[i];
           for (int q = 1; q < p.splits; ++q) y += sums[q * per * kTileN + i];
-          if (row < tile.rows && n < p.N && !dead)
+          if (row < tile.rows && n < p.N)
             static_cast<__nv_bfloat16*>(p.Y)[(tile.first + row) * p.ldy + n] = __float2bfloat16_rn(y);
         }
       }
@@ -449,6 +453,7 @@ int launch(const BlockGemmArgs& a) {
   p.kb = n_blocks(a.K);
   p.experts = kGrouped ? a.experts : 1;
   p.early_weights = a.early_weights;
+  p.late = block_test_late_copies();
   p.n_tiles = (a.N + kTileN - 1) / kTileN;
   p.whole = a.K % kBlock == 0;
   p.copy = kGated || !p.whole ? 1 : 2;         // 40 KB a stage, five stages

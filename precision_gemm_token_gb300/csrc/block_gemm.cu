@@ -31,8 +31,8 @@
 // read their 470 MB at 6.3 TB/s.
 //
 // Every wait is bounded: on a timeout the CTA records EPILORA_ERR_TIMEOUT,
-// stops issuing, waits (bounded) for its copies and MMAs in flight and frees
-// its TMEM.
+// stops issuing, waits (bounded) for its copies and MMAs in flight, writes NaN
+// for the sums that are not whole and frees its TMEM.
 #include "block_gemm.cuh"
 
 namespace epi {
@@ -76,6 +76,7 @@ struct Params {
   int M, N, K, kb;
   int n_tiles, experts;
   int stages, wide_store, early_weights;
+  int late;                    // the test hook: the block whose copies never seem complete, else -1
 };
 
 __device__ __forceinline__ void sums_barrier() {
@@ -100,8 +101,8 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// kF32: grouped products that leave in fp32, 512 bytes a thread instead of 256 (down projections of 4096 tokens, sum and
-// all, 557 us instead of 374, of 64 tokens 89.5 instead of 83.5, of one 22.3 instead of 21.2: the parts' traffic)
+// kF32: grouped products that leave in fp32, 512 bytes a thread instead of 256 (down projections of 4096 tokens, sum
+// and all, 557 us instead of 374, of 64 tokens 89.5 instead of 83.5, of one 22.3 instead of 21.2: the parts' traffic)
 template <int BN, bool kGrouped, bool kGated, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_constant__ Params p) {
   using C = Cfg<BN>;
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
           const int wrow = tile.expert * (kGated ? 2 : 1) * p.N + n0;
           const auto copy_w = [&](int st, int b) {
             uint8_t* dst = smem + static_cast<size_t>(st) * C::kStage + kABytes;
-            mbar_arrive_expect_tx(&full[st], C::kStage);
+            mbar_arrive_expect_tx(&full[st], C::kStage + (b == p.late ? 16 : 0));
             tma_load_2d(dst, &p.tmB, &full[st], b * kBlock, wrow);
             if (kGated) tma_load_2d(dst + kBlock * kBlock, &p.tmB, &full[st], b * kBlock, wrow + p.N);
           };
@@ -234,11 +235,11 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
       if (elect_one()) {
         constexpr uint32_t kIdesc = idesc_f8f6f4_e4m3(kRows, BN);
         const uint64_t desc0 = make_smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-        int s = 0, half = 0, last = 0;
-        uint32_t ph = 0, hph = 0, last_ph = 0;
+        int s = 0, half = 0;
+        uint32_t ph = 0, hph = 0;
         bool go = true, any = false;
         for (int t = blockIdx.x; t < walk.total && go; t += gridDim.x) {
-          for (int b0 = 0; b0 < kb && go; b0 += G) {
+          for (int b0 = 0; b0 < kb; b0 += G) {
             if (!wait(&drained[half], hph ^ 1u)) {
               go = false;
               break;
@@ -256,21 +257,20 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
               for (int kk = 0; kk < 4; ++kk)
                 mma_f8f6f4(tmem_base + half * kHalf + u * BN, ad + 2 * kk, bd + 2 * kk, kIdesc, kk > 0);
               tc_commit(&empty[s]);
+              any = true;
               if (++s == stages) {
                 s = 0;
                 ph ^= 1u;
               }
             }
+            if (!go) break;        // (a group that is not whole is handed to nobody)
             tc_commit(&filled[half]);
-            any = true;
-            last = half;
-            last_ph = hph;
             half ^= 1;
             if (half == 0) hph ^= 1u;
           }
         }
-        // nothing of this thread in flight at exit: the last commit covers every MMA before it
-        if (any) (void)mbar_wait_bounded(&filled[last], last_ph, kWaitLimitNs);
+        // nothing of this thread in flight at exit: the last stage's commit covers every MMA before it
+        if (any) (void)mbar_wait_bounded(&empty[s > 0 ? s - 1 : stages - 1], s > 0 ? ph : ph ^ 1u, kWaitLimitNs);
       }
       __syncwarp();
     } else {
@@ -350,9 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
       // this side's first column
       const int n0 = kGated ? tile.n * kBlock + side * (NC / 2) : tile.n * BN + side * NC;
       const bool cols = n0 < p.N;
+      const float start = dead ? __int_as_float(0x7fffffff) : 0.0f;
       float acc[NC];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
+      for (int i = 0; i < NC; ++i) acc[i] = start;
 #pragma unroll 1
       for (int b0 = 0; b0 < kb; b0 += G) {
         if (!dead && !__all_sync(0xffffffffu, BN == 256 ? poll(&filled[half], hph) : wait(&filled[half], hph)))
@@ -417,6 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
         half ^= 1;
         if (half == 0) hph ^= 1u;
       }
+      if (dead && start == 0.0f) {              // sums that are not whole: the tile once more, as NaN
+        t -= static_cast<int>(gridDim.x);
+        turn ^= 1;
+        continue;
+      }
       if constexpr (kGated) {
         constexpr int H = NC / 2;              // elements of the output per thread
         float h[H], m = 0.0f;
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
         m = fmaxf(m, amax[(turn * 2 + (side ^ 1)) * kRows + r]);
         const float s = block_scale(m);
         const BlockDiv by = block_div(s);
-        if (live && !dead) {
+        if (live) {
           uint8_t* out = p.inner + static_cast<int64_t>(slot) * p.N + n0;
 #pragma unroll
           for (int c = 0; c < H; c += 16) {
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
           if (side == 0) p.inner_scale[static_cast<int64_t>(tile.n) * p.M + slot] = s;
         }
       } else if constexpr (kF32) {
-        if (live && !dead) {
+        if (live) {
           float* const Y = static_cast<float*>(p.Y) + slot * p.ldy + n0;
 #pragma unroll
           for (int c = 0; c < NC; c += 8) {
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_co
             if (n0 + c < p.N) st_global_v8(Y + c, q);
           }
         }
-      } else if (warp_live && cols && !dead) {
+      } else if (warp_live && cols) {
         __nv_bfloat16* const Y = static_cast<__nv_bfloat16*>(p.Y);
 #pragma unroll
         for (int c = 0; c < NC; c += 16) {
@@ -518,6 +524,7 @@ int launch(const BlockGemmArgs& a) {
   p.kb = n_blocks(a.K);
   p.experts = kGrouped ? a.experts : 1;
   p.early_weights = a.early_weights;
+  p.late = block_test_late_copies() ? p.kb - 1 : -1;
   const int width = kGated ? kBlock : BN;
   p.n_tiles = (a.N + width - 1) / width;
   p.wide_store = (reinterpret_cast<uintptr_t>(a.Y) & 31) == 0 && a.ldy % 16 == 0;

@@ -86,6 +86,7 @@ struct BlockGemmArgs {
   cudaStream_t stream;
 };
 int launch_block_gemm(const BlockGemmArgs& a);
+int block_test_late_copies();      // the test hook (epilora_test_late_block_copies)
 
 // y[t] = bf16( sum_j weights[t][j] parts[t * top + j] ), over the slots that have an expert, in fp32
 struct MoeCombineArgs {

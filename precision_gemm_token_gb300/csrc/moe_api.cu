@@ -1,5 +1,6 @@
 // C ABI of the operators in 8-bit blocks and of the mixture-of-experts
 // operators: argument validation and workspace layout.
+#include <atomic>
 #include <cmath>
 
 #include "blocks.cuh"
@@ -7,6 +8,8 @@
 using namespace epi;
 
 namespace {
+
+std::atomic<int> g_late_copies{0};
 
 inline bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool there(const void* p, size_t n) { return p != nullptr && al(p, n); }
@@ -188,6 +191,8 @@ int experts_both(int tokens, int top, int experts, int hidden, int inner, const 
 
 }  // namespace
 
+int epi::block_test_late_copies() { return g_late_copies.load(); }
+
 extern "C" {
 
 EPILORA_API int epilora_block_quant(const void* X, int M, int K, int64_t ldx, uint8_t* Xq, float* x_scale,
@@ -228,6 +233,11 @@ EPILORA_API int epilora_block_matmul(int M, int N, int K, const uint8_t* Xq, con
   g.status = status_dev;
   g.stream = static_cast<cudaStream_t>(stream);
   return launch_block_gemm(g);
+}
+
+EPILORA_API int epilora_test_late_block_copies(int on) {
+  g_late_copies.store(on != 0 ? 1 : 0);
+  return EPILORA_OK;
 }
 
 EPILORA_API size_t epilora_block_linear_workspace_bytes(int M, int K) {

@@ -648,8 +648,10 @@ typedef enum { EPILORA_SCORE_SOFTMAX = 0, EPILORA_SCORE_SIGMOID = 1 } epilora_sc
  *   groups > 1: expert e belongs to group e / (experts / groups); a group's
  *     value is the sum of its `group_best` (1 or 2) largest c, and only the
  *     `top_groups` groups of the largest values stay (ties: lowest index)
- *   ids[t][0 .. top): the experts of the largest c among those, descending,
- *     ties to the lowest index, in the exact order of the real numbers c
+ *   ids[t][0 .. top): the experts of the largest c among those, descending.
+ *     c is compared in 64 bits; where those are equal (scores that a bias or a
+ *     1 swallows) the larger logit goes first, then the lowest index. With
+ *     equal biases, or none, that is the order of the real numbers c
  *   weights[t][j] = scale * s of the j-th, divided by the sum of the chosen
  *     s first if renormalize
  * A logit of -infinity or NaN, or a bias of -infinity or NaN, takes the

@@ -95,7 +95,8 @@ def route(logits, top, bias=None, scoring="softmax", groups=1, top_groups=1, gro
             out = np.ones(groups, bool)
             out[kept] = False
             order[np.repeat(out, size)] = -np.inf
-        chosen = [e for e in np.argsort(-order, kind="stable")[:top] if order[e] > -np.inf]
+        # (of choices that 64 bits cannot tell apart the larger logit first)
+        chosen = [e for e in np.lexsort((-l, -order))[:top] if order[e] > -np.inf]
         ids[t, :len(chosen)] = chosen
         if not chosen:
             continue

@@ -2,14 +2,15 @@
 // best experts of a token and their weights. A warp per token, expert e in
 // lane e % 32.
 //
-// The choice is by the exact order of score + bias, ties to the lowest index.
-// The kernel works it out in 32 bits with a bound on what the roundings may
-// have moved. Where two candidates lie closer than that (of random scores, in
-// a few tokens of a thousand) it looks at them in 64 bits: of a sigmoid's
-// chosen experts a lane each, else the whole token again (FP64 is slow on this
-// GPU: 20 us for such a token, which then is the call's time). Without a bias
-// the order of the scores is the order of the logits, which needs no
-// arithmetic.
+// The choice is by score + bias in 64 bits; where those are equal (a sigmoid
+// that is 1 there, a softmax's score below the last bit of its bias) the larger
+// logit goes first, which with equal biases is the order of the real numbers,
+// then the lowest index. The kernel works it out in 32 bits with a bound on
+// what the roundings may have moved. Where two candidates lie closer than that
+// it looks at them in 64 bits: of a sigmoid's chosen experts a lane each, else
+// the whole token again (FP64 is slow on this GPU: 20 us for such a token,
+// which then is the call's time). Without a bias the order of the scores is the
+// order of the logits, which needs no arithmetic.
 //
 // Bound: the chain of the choices (4096 x 256 with eight groups: some 30 maxima over the warp a token, 17.8 us; one
 // token of 128 experts 3 us); the bytes are few.
@@ -71,6 +72,15 @@ template <class T>
 __device__ __forceinline__ Best<T> warp_best(Best<T> mine) {
   const typename Keys<T>::Key key = Keys<T>::warp_max(mine.key);
   return Best<T>{key, static_cast<int>(__reduce_min_sync(kAll, mine.key == key ? static_cast<uint32_t>(mine.i) : 0x7fffffffu))};
+}
+// The same where equal keys go by `logit` (that of `mine`) first.
+template <class T>
+__device__ __forceinline__ Best<T> warp_best(Best<T> mine, float logit) {
+  const typename Keys<T>::Key key = Keys<T>::warp_max(mine.key);
+  const uint32_t l = mine.key == key ? Keys<float>::of(logit) : 0u;
+  const uint32_t most = __reduce_max_sync(kAll, l);        // (by all lanes, whatever their keys)
+  const bool best = mine.key == key && l == most;
+  return Best<T>{key, static_cast<int>(__reduce_min_sync(kAll, best ? static_cast<uint32_t>(mine.i) : 0x7fffffffu))};
 }
 template <class T>
 __device__ __forceinline__ T warp_sum(T v) {
@@ -179,10 +189,21 @@ __device__ __forceinline__ int choose(const MoeRouteArgs& a, const float (&l)[kP
 #pragma unroll 1
   for (int j = 0;; ++j) {
     Best<T> b{0, 0x7fffffff};
+    if constexpr (kApprox) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (c[i] > b.key) b = Best<T>{c[i], lane + 32 * i};
-    b = warp_best(b);
+      for (int i = 0; i < kPer; ++i)
+        if (c[i] > b.key) b = Best<T>{c[i], lane + 32 * i};
+      b = warp_best(b);
+    } else {
+      float logit = minus_inf();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (c[i] > b.key || (c[i] == b.key && c[i] != 0 && l[i] > logit)) {
+          b = Best<T>{c[i], lane + 32 * i};
+          logit = l[i];
+        }
+      b = warp_best(b, logit);
+    }
     if (b.key == 0) break;
     const bool near = kApprox && !by_logit && j > 0 && !(Keys<T>::value(before) - Keys<T>::value(b.key) > bound);
     if (j >= a.top && !near) break;
@@ -226,13 +247,15 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const __grid_c
   const int close = choose<float, kPer>(a, l, top, lane, mine);
   if (close == kExperts && a.sigmoid) {
     // the candidates in 64 bits, a lane each, and their order
+    const float at = mine < 0 ? minus_inf() : logit(mine);
     const Keys<double>::Key key =
-        mine < 0 ? 0 : Keys<double>::of(1.0 / (1.0 + exp(-static_cast<double>(logit(mine)))) + static_cast<double>(a.bias[mine]));
+        mine < 0 ? 0 : Keys<double>::of(1.0 / (1.0 + exp(-static_cast<double>(at))) + static_cast<double>(a.bias[mine]));
     int before = 0, told = -1;
     for (int o = 0; o < 32; ++o) {
       const Keys<double>::Key k = __shfl_sync(kAll, key, o);
+      const float le = __shfl_sync(kAll, at, o);
       const int e = __shfl_sync(kAll, mine, o);
-      if (k > key || (k == key && e < mine)) ++before;
+      if (k > key || (k == key && (le > at || (le == at && e < mine)))) ++before;
     }
     for (int j = 0; j < a.top; ++j) {
       const unsigned who = __ballot_sync(kAll, mine >= 0 && before == j);

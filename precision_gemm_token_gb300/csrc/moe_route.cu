@@ -7,13 +7,16 @@
 // logit goes first, which with equal biases is the order of the real numbers,
 // then the lowest index. The kernel works it out in 32 bits with a bound on
 // what the roundings may have moved. Where two candidates lie closer than that
-// it looks at them in 64 bits: of a sigmoid's chosen experts a lane each, else
+// (of random scores, in 1 to 20 of 1000 tokens: more, the more experts and the
+// more of them chosen) it looks at them in 64 bits: of a sigmoid's chosen experts a lane each, else
 // the whole token again (FP64 is slow on this GPU: 20 us for such a token,
 // which then is the call's time). Without a bias the order of the scores is the
 // order of the logits, which needs no arithmetic.
 //
 // Bound: the chain of the choices (4096 x 256 with eight groups: some 30 maxima over the warp a token, 17.8 us; one
-// token of 128 experts 3 us); the bytes are few.
+// token of 128 experts 3 us); the bytes are few. Softmax with a bias: of 4096
+// tokens some go through 64 bits again, 27 us of 256 experts, 65 of 512 with 16
+// chosen (without a bias 18).
 #include "blocks.cuh"
 #include "ptx.cuh"
 
@@ -82,6 +85,9 @@ __device__ __forceinline__ Best<T> warp_best(Best<T> mine, float logit) {
   const bool best = mine.key == key && l == most;
   return Best<T>{key, static_cast<int>(__reduce_min_sync(kAll, best ? static_cast<uint32_t>(mine.i) : 0x7fffffffu))};
 }
+__device__ __forceinline__ float warp_max(float v) {      // of numbers that are not negative
+  return __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(v)));
+}
 template <class T>
 __device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
@@ -108,6 +114,7 @@ __device__ __forceinline__ int choose(const MoeRouteArgs& a, const float (&l)[kP
   const bool by_value = a.bias != nullptr || (a.groups > 1 && a.group_best > 1);
   Key c[kPer];
   T sum = T(1);
+  // what roundings may do to the difference of two scores, or of two sums of two (below)
   if (by_value && !a.sigmoid) {
     sum = T(0);
 #pragma unroll
@@ -115,7 +122,7 @@ __device__ __forceinline__ int choose(const MoeRouteArgs& a, const float (&l)[kP
       if (l[i] > minus_inf()) sum += exp_of(T(l[i]) - T(top));
     sum = warp_sum(sum);
   }
-  float most = 0.0f;
+  float most = 0.0f, largest = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
@@ -123,18 +130,21 @@ __device__ __forceinline__ int choose(const MoeRouteArgs& a, const float (&l)[kP
     if (e < a.experts && l[i] > minus_inf()) {
       T v = T(l[i]);
       if (by_value) v = a.sigmoid ? T(1) / (T(1) + exp_of(-v)) : exp_of(v - T(top)) / sum;
+      if (kApprox) largest = fmaxf(largest, static_cast<float>(v));
       if (a.bias != nullptr) v += T(a.bias[e]);
       if (v > T(minus_inf())) c[i] = Keys<T>::of(v);      // (a bias of -infinity or NaN: no such expert)
       if (kApprox && fabsf(static_cast<float>(v)) < 3e38f) most = fmaxf(most, fabsf(static_cast<float>(v)));
     }
   }
-  // A sigmoid is off by a few units of 2^-24; a softmax by those of its sum,
-  // at most 40 of them (additions in each lane, then five), and of the
-  // exponent's argument (x e^x < 0.37). With the rounding of c itself, 2^-24
-  // of it; the difference of two, and of two sums of two.
+  // In units u = 2^-24: a sigmoid is off by 2.5. A softmax's score is off, in u
+  // of the largest (1 / sum), by 4.4 for the exponential (two of its own steps,
+  // and the rounded argument, |x| e^x < 0.37), 36 for the additions of the sum
+  // (31 in a lane, then five), 11 for its terms (their mean |x| is at most
+  // ln 1024) and 1 for the quotient: 53. The rounding of c itself is 1 of it;
+  // the difference of two sums of two has four times all that.
   T bound = T(0);
   if (kApprox && by_value)
-    bound = T((a.sigmoid ? 0x1p-20f : 0x1p-16f) + 0x1p-21f * __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most))));
+    bound = T((a.sigmoid ? 0x1p-20f : 0x1p-16f * warp_max(largest)) + 0x1p-21f * warp_max(most));
   int close = kTold;
   if (a.groups > 1 && a.top_groups < a.groups) {
     const int size = a.experts / a.groups;

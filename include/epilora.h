@@ -582,7 +582,8 @@ EPILORA_API int epilora_prompt_attention(int n_seqs, int n_tokens, const int32_t
  *   activation codes  uint8 [M][K]          scale fp32 [nb(K)][x_scale_ld], scale[b][m]
  *   weight codes      uint8 [N][K]          scale fp32 [nb(N)][nb(K)]
  * Widths (K, and hidden and inner of a mixture) are multiples of 16; M and N
- * are any. Code arrays and bf16 inputs are 16-byte aligned, bf16 rows have
+ * are any. No size exceeds EPILORA_BLOCK_MAX_SIZE, nor does the sum of the rows
+ * of all experts' weights (EPILORA_ERR_UNSUPPORTED). Code arrays and bf16 inputs are 16-byte aligned, bf16 rows have
  * strides in multiples of 8 elements. All calls are forward only. Their
  * kernels are programmatic dependents of the previous kernel on the stream
  * and wait for it before they read anything it may have written. A wait
@@ -590,6 +591,8 @@ EPILORA_API int epilora_prompt_attention(int n_seqs, int n_tokens, const int32_t
  * EPILORA_ERR_TIMEOUT in the status word; the results that it left unfinished
  * are NaN, and so is what is computed from them.
  * ------------------------------------------------------------------------ */
+
+#define EPILORA_BLOCK_MAX_SIZE 0x7fff0000
 
 /*
  * Codes and scales of bf16 rows X [M][ldx], per block b of 128 elements:

@@ -16,6 +16,7 @@ ABI) plus `tensors` (the projections), `attention`, `blocks` (projections in
 the binding. There is no CPU fallback.
 """
 from ._binding import (  # noqa: F401
+    BLOCK_MAX_SIZE,
     EPILORA_ERR_CUDA,
     EPILORA_ERR_INVALID_ARG,
     EPILORA_ERR_TIMEOUT,

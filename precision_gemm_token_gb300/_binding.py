@@ -36,6 +36,7 @@ SCORE_SIGMOID = 1
 MOE_UP = 1
 MOE_DOWN = 2
 MOE_F32_PARTS = 4
+BLOCK_MAX_SIZE = 0x7FFF0000         # EPILORA_BLOCK_MAX_SIZE
 MOE_MAX_EXPERTS = 1024              # EPILORA_MOE_MAX_EXPERTS
 MOE_MAX_TOP = 32                    # EPILORA_MOE_MAX_TOP
 

@@ -459,7 +459,7 @@ int launch(const BlockGemmArgs& a) {
   p.copy = kGated || !p.whole ? 1 : 2;         // 40 KB a stage, five stages
   const int64_t w_rows = static_cast<int64_t>(p.experts) * a.N * (kGated ? 2 : 1);
   const int64_t tiles = (static_cast<int64_t>(a.M) / kCols + 1 + (kGrouped ? p.experts : 0)) * p.n_tiles;
-  if (tiles >= (int64_t{1} << 31) || w_rows >= (int64_t{1} << 31)) return EPILORA_ERR_UNSUPPORTED;
+  if (tiles > EPILORA_BLOCK_MAX_SIZE || w_rows > EPILORA_BLOCK_MAX_SIZE) return EPILORA_ERR_UNSUPPORTED;
   int rc = make_tma_blocks(&p.tmA, a.A, a.M, a.K, kCols, p.copy);
   if (rc == EPILORA_OK) rc = make_tma_blocks(&p.tmB, a.W, w_rows, a.K, kTileN, p.copy);
   if (rc != EPILORA_OK) return rc;

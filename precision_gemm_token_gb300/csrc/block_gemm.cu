@@ -531,7 +531,7 @@ int launch(const BlockGemmArgs& a) {
   const int64_t w_rows = static_cast<int64_t>(p.experts) * a.N * (kGated ? 2 : 1);
   // tiles, and rows of the tensor maps, are counted in 31 bits
   const int64_t tiles = (static_cast<int64_t>(a.M) / kRows + 1 + (kGrouped ? p.experts : 0)) * p.n_tiles;
-  if (tiles >= (int64_t{1} << 31) || w_rows >= (int64_t{1} << 31)) return EPILORA_ERR_UNSUPPORTED;
+  if (tiles > EPILORA_BLOCK_MAX_SIZE || w_rows > EPILORA_BLOCK_MAX_SIZE) return EPILORA_ERR_UNSUPPORTED;
   int rc = make_tma_2d_u8(&p.tmA, a.A, a.M, a.K, a.K, kRows, kBlock, true);
   if (rc == EPILORA_OK) rc = make_tma_2d_u8(&p.tmB, a.W, w_rows, a.K, a.K, kGated ? kRows : BN, kBlock, true);
   if (rc != EPILORA_OK) return rc;

@@ -16,6 +16,11 @@ inline bool there(const void* p, size_t n) { return p != nullptr && al(p, n); }
 inline size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 inline bool width_ok(int k) { return k >= 16 && k % 16 == 0; }
 
+// beyond this, sums of a size and a tile's would not fit 32 bits
+inline bool too_large(int a, int b, int c = 0) {
+  return a > EPILORA_BLOCK_MAX_SIZE || b > EPILORA_BLOCK_MAX_SIZE || c > EPILORA_BLOCK_MAX_SIZE;
+}
+
 bool quant_ok(const void* X, int M, int K, int64_t ldx) {
   return M >= 0 && width_ok(K) && ldx >= K && ldx % 8 == 0 && (M == 0 || there(X, 16));
 }
@@ -63,7 +68,7 @@ Parts cut_moe(void* ws, int what, int tokens, int top, int experts, int hidden, 
 // sizes of a mixture: EPILORA_OK, or the refusal
 int moe_sizes(int tokens, int top, int experts, int hidden, int inner) {
   if (tokens < 0 || top < 1 || experts < 1 || !width_ok(hidden) || !width_ok(inner)) return EPILORA_ERR_INVALID_ARG;
-  if (experts > EPILORA_MOE_MAX_EXPERTS || static_cast<int64_t>(tokens) * top >= (int64_t{1} << 30))
+  if (experts > EPILORA_MOE_MAX_EXPERTS || too_large(hidden, inner) || static_cast<int64_t>(tokens) * top >= (int64_t{1} << 30))
     return EPILORA_ERR_UNSUPPORTED;
   return EPILORA_OK;
 }
@@ -198,6 +203,7 @@ extern "C" {
 EPILORA_API int epilora_block_quant(const void* X, int M, int K, int64_t ldx, uint8_t* Xq, float* x_scale,
                                     int64_t x_scale_ld, void* stream) {
   if (!quant_ok(X, M, K, ldx) || x_scale_ld < M) return EPILORA_ERR_INVALID_ARG;
+  if (too_large(M, K)) return EPILORA_ERR_UNSUPPORTED;
   if (M == 0) return EPILORA_OK;
   if (!there(Xq, 16) || !there(x_scale, 4)) return EPILORA_ERR_INVALID_ARG;
   return launch_block_quant(
@@ -207,6 +213,7 @@ EPILORA_API int epilora_block_quant(const void* X, int M, int K, int64_t ldx, ui
 EPILORA_API int epilora_block_quant_weight(const void* W, int N, int K, int64_t ldw, uint8_t* Wq, float* w_scale,
                                            void* stream) {
   if (!quant_ok(W, N, K, ldw)) return EPILORA_ERR_INVALID_ARG;
+  if (too_large(N, K)) return EPILORA_ERR_UNSUPPORTED;
   if (N == 0) return EPILORA_OK;
   if (!there(Wq, 16) || !there(w_scale, 4)) return EPILORA_ERR_INVALID_ARG;
   return launch_block_quant_weight(W, N, K, ldw, Wq, w_scale, static_cast<cudaStream_t>(stream));
@@ -216,6 +223,7 @@ EPILORA_API int epilora_block_matmul(int M, int N, int K, const uint8_t* Xq, con
                                      const uint8_t* Wq, const float* w_scale, void* Y, int64_t ldy, int* status_dev,
                                      void* stream) {
   if (M < 0 || N < 1 || !width_ok(K) || x_scale_ld < M || ldy < N) return EPILORA_ERR_INVALID_ARG;
+  if (too_large(M, N, K)) return EPILORA_ERR_UNSUPPORTED;
   if (M == 0) return EPILORA_OK;
   if (!there(Xq, 16) || !there(x_scale, 4) || !there(Wq, 16) || !there(w_scale, 4) || !there(Y, 2) || !al(status_dev, 4))
     return EPILORA_ERR_INVALID_ARG;
@@ -241,7 +249,7 @@ EPILORA_API int epilora_test_late_block_copies(int on) {
 }
 
 EPILORA_API size_t epilora_block_linear_workspace_bytes(int M, int K) {
-  if (M < 0 || !width_ok(K)) return 0;
+  if (M < 0 || !width_ok(K) || too_large(M, K)) return 0;
   return round256(static_cast<size_t>(M) * K) + round256(static_cast<size_t>(n_blocks(K)) * M * sizeof(float));
 }
 
@@ -249,6 +257,7 @@ EPILORA_API int epilora_block_linear(int M, int N, int K, const void* X, int64_t
                                      const float* w_scale, void* Y, int64_t ldy, void* workspace,
                                      size_t workspace_bytes, int* status_dev, void* stream) {
   if (N < 1 || ldy < N || !quant_ok(X, M, K, ldx)) return EPILORA_ERR_INVALID_ARG;
+  if (too_large(M, N, K)) return EPILORA_ERR_UNSUPPORTED;
   if (M == 0) return EPILORA_OK;
   if (!there(Wq, 16) || !there(w_scale, 4) || !there(Y, 2) || !al(status_dev, 4)) return EPILORA_ERR_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, epilora_block_linear_workspace_bytes(M, K))) return EPILORA_ERR_WORKSPACE;

@@ -8,10 +8,10 @@
 // then the lowest index. The kernel works it out in 32 bits with a bound on
 // what the roundings may have moved. Where two candidates lie closer than that
 // (of random scores, in 1 to 20 of 1000 tokens: more, the more experts and the
-// more of them chosen) it looks at them in 64 bits: of a sigmoid's chosen experts a lane each, else
-// the whole token again (FP64 is slow on this GPU: 20 us for such a token,
-// which then is the call's time). Without a bias the order of the scores is the
-// order of the logits, which needs no arithmetic.
+// more of them chosen) it looks at them in 64 bits: of a sigmoid's chosen
+// experts a lane each, else the whole token again (FP64 is slow on this GPU:
+// 20 us for such a token, which then is the call's time). Without a bias the
+// order of the scores is the order of the logits, which needs no arithmetic.
 //
 // Bound: the chain of the choices (4096 x 256 with eight groups: some 30 maxima over the warp a token, 17.8 us; one
 // token of 128 experts 3 us); the bytes are few. Softmax with a bias: of 4096

@@ -185,10 +185,14 @@ def quantize_weight(W, stream=None) -> BlockWeight:
     dev, raw, given = _start(W, stream)
     at, N, K, ld = _matrix(W, _BF16, dev, "W")
     codes, scale = _new(W, (N, K), _U8, given), _new(W, (_blocks(N), _blocks(K)), _F32, given)
+    _quantize_weight(at, N, K, ld, codes, scale, raw)
+    return BlockWeight(codes, scale)
+
+
+def _quantize_weight(at, N, K, ld, codes, scale, raw):
     rc = _lib().epilora_block_quant_weight(at, N, K, ld, codes.data_ptr(), scale.data_ptr(), raw)
     if rc:
         E.check(rc, "quantize_weight")
-    return BlockWeight(codes, scale)
 
 
 def _out(out, like, M, N, dev, stream):

@@ -17,7 +17,7 @@ import torch
 
 from . import _binding as E
 from .blocks import (_BF16, _F32, _I32, _U8, BlockWorkspace, _array, _bad, _blocks, _lib, _made, _matrix, _out, _room,
-                     _start, _status, quantize_weight)
+                     _new, _quantize_weight, _start, _status)
 
 _SCORING = {"softmax": E.SCORE_SOFTMAX, "sigmoid": E.SCORE_SIGMOID}
 _bytes = lru_cache(1024)(E.epilora_moe_workspace_bytes)       # asked of the library once per shape
@@ -69,18 +69,23 @@ class ExpertWeights:
         self.experts, self.inner, self.hidden, self.dev = n, inner, hidden, dev
 
 
-def quantize_experts(gate, up, down) -> ExpertWeights:
+def quantize_experts(gate, up, down, stream=None) -> ExpertWeights:
     """Load-time quantization of bf16 weights: gate and up [experts, inner,
-    hidden], down [experts, hidden, inner]."""
-    n, inner, hidden = gate.shape
-    if up.shape != gate.shape or down.shape != (n, hidden, inner):
+    hidden], down [experts, hidden, inner]. Beside them it takes the memory of
+    the codes and scales that it returns, no more."""
+    dev, raw, given = _start(gate, stream)
+    if gate.dim() != 3 or gate.shape[0] == 0 or up.shape != gate.shape or down.shape != (gate.shape[0], *gate.shape[:0:-1]):
         _bad("quantize_experts: gate and up [experts, inner, hidden], down [experts, hidden, inner] wanted")
-    stacks = []
-    for parts in ([m for e in range(n) for m in (gate[e], up[e])], list(down)):
-        made = [quantize_weight(m) for m in parts]
-        stacks.append((torch.stack([m.codes for m in made]), torch.stack([m.scale for m in made])))
-    (gu, gus), (d, ds) = stacks
-    return ExpertWeights(gu.view(n, 2, inner, hidden), gus.view(n, 2, *gus.shape[1:]), d, ds)
+    n, inner, hidden = gate.shape
+    bi, bh = _blocks(inner), _blocks(hidden)
+    parts = [(_matrix(m[e], _BF16, dev, what), e, which)
+             for e in range(n) for which, (m, what) in enumerate(((gate, "gate"), (up, "up"), (down, "down")))]
+    gu, gus = _new(gate, (n, 2, inner, hidden), _U8, given), _new(gate, (n, 2, bi, bh), _F32, given)
+    d, ds = _new(gate, (n, hidden, inner), _U8, given), _new(gate, (n, bh, bi), _F32, given)
+    for at, e, which in parts:
+        codes, scale = (gu[e, which], gus[e, which]) if which < 2 else (d[e], ds[e])
+        _quantize_weight(*at, codes, scale, raw)
+    return ExpertWeights(gu, gus, d, ds)
 
 
 # what the experts' outputs are kept in until their weighted sum: (bit of the workspace's size, calls of the library)

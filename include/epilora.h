@@ -674,7 +674,8 @@ EPILORA_API int epilora_moe_route(int tokens, int experts, int top, const void* 
  * status word. A token may name an expert twice.
  *   Wup   codes [experts][2][inner][hidden], scale [experts][2][nb(inner)][nb(hidden)]  (gate, then up)
  *   Wdown codes [experts][hidden][inner],    scale [experts][nb(hidden)][nb(inner)]
- * up:   x is block-quantized; h = silu(x Wup[e][0]^T) * (x Wup[e][1]^T), silu(g) = g / (1 + exp(-g)), in fp32;
+ * up:   x is block-quantized; h = silu(x Wup[e][0]^T) * (x Wup[e][1]^T), silu(g) = g / (1 + exp(-g)), in fp32,
+ *       silu within 2^-21 + |g| 2^-24 of its value (0 below g = -87.3, where it is less than 2^-119);
  *       Hq [tokens][top][inner] and h_scale [nb(inner)][tokens * top] are its
  *       block quantization; slots without an expert: zero codes, zero scales
  * down: Y[t] = bf16( sum_j weights[t][j] bf16(h[t][j] Wdown[e]^T) ), j ascending in fp32 over the slots that

@@ -89,9 +89,10 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
   return false;
 }
 
-// g / (1 + exp(-g)) within 2^-21 + |g| 2^-24 of it (the exponent's argument is rounded), without a division's branches:
-// a tile's elements are all in registers, so this code stands there once for each of them, and has to stay in the
-// instruction cache beside the loops.
+// g / (1 + exp(-g)) within 2^-21 + |g| 2^-24 of it (the exponent's argument is rounded) down to g = -87.3; below that 0,
+// where the value is less than 2^-119 (the quotient gives 0 from a divisor of 2^126 on; the formula in 32 bits does so
+// from g = -88.8 on, where exp(-g) overflows). Without a division's branches: a tile's elements are all in registers, so
+// this code stands there once for each of them, and has to stay in the instruction cache beside the loops.
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + exp2_approx(-1.442695041f * g)); }
 
 // Calls with few rows (block_few.cu).

@@ -73,7 +73,7 @@ struct Params {
   const int32_t* offsets;      // grouped: rows of expert e are [offsets[e], offsets[e + 1])
   const int32_t* out_rows;     // the output row of each row (NULL: the same)
   int* status;
-  int M, N, K, kb;
+  int M, N, kb;
   int n_tiles, experts;
   int stages, wide_store, early_weights;
   int late;                    // the test hook: the block whose copies never seem complete, else -1
@@ -520,7 +520,6 @@ int launch(const BlockGemmArgs& a) {
   p.status = a.status;
   p.M = a.M;
   p.N = a.N;
-  p.K = a.K;
   p.kb = n_blocks(a.K);
   p.experts = kGrouped ? a.experts : 1;
   p.early_weights = a.early_weights;

@@ -41,8 +41,9 @@ def test_memory():
     before = torch.cuda.memory_allocated()
     w = M.quantize_experts(*parts)
     made = [w.gate_up, w.gate_up_scale, w.down, w.down_scale]
-    # (the allocator rounds each tensor up to 512 bytes)
-    assert torch.cuda.max_memory_allocated() - before <= sum(t.numel() * t.element_size() + 512 for t in made)
+    # a tensor counts as the block that the allocator gives it: up to 512 bytes more, and in a cached block what is left
+    # of it where that is less than 1 MiB (it is not split off then). A second copy of the codes would be 25 MB.
+    assert torch.cuda.max_memory_allocated() - before <= sum(t.numel() * t.element_size() + 512 + (1 << 20) for t in made)
 
 
 def test_another_stream():

@@ -110,7 +110,8 @@ class BlockWorkspace:
     on demand; nothing in it has to be initialized. Calls that share one have
     to be ordered on one stream, and a captured graph wants it kept as long as
     the graph: a buffer that a capture has used is kept when a larger one
-    takes its place. `device` without an index is the current one at this
+    takes its place, and so is one used on a stream that torch does not own.
+    `device` without an index is the current one at this
     point."""
 
     def __init__(self, device):
@@ -119,6 +120,7 @@ class BlockWorkspace:
             _bad(f"workspace: a CUDA device wanted, not {device}")
         self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
         self._buf, self._captured, self._kept = None, False, []
+        self._own, self._foreign = None, False      # the stream it was allocated on; used on one the allocator knows not of
         self._known = set()         # raw handles of the streams that the allocator knows the buffer's use on
 
     def get(self, need, dev, raw, stream):
@@ -128,9 +130,10 @@ class BlockWorkspace:
         if self.device.index != dev:
             _bad(f"workspace: on {self.device}, the tensors on device {dev}")
         if self._buf is None or self._buf.numel() < need:
-            if self._captured:
+            if self._captured or self._foreign:
                 self._kept.append(self._buf)
             self._buf, self._captured, self._known = None, False, set()
+            self._own, self._foreign = raw, False
             if stream is None:
                 self._buf = torch.empty(max(need, 1 << 20), dtype=_U8, device=self.device)
             else:
@@ -144,12 +147,14 @@ class BlockWorkspace:
 
     def _note(self, raw, stream):
         """The allocator lets no other tensor have the buffer before a stream
-        that it was used on is done with it, should the workspace be dropped or
-        grow. A stream that torch does not own may be gone by then: there it is
-        the caller's to keep the workspace."""
+        was used on is done with it, should the workspace be dropped or
+        grow. A stream that torch does not own may be gone by then: there a
+        buffer that grew is kept, and the workspace is the caller's to keep."""
         if torch.cuda.is_current_stream_capturing() if stream is None else _capturing(stream):
             self._captured = True
-        elif raw not in self._known and not isinstance(stream, torch.cuda.ExternalStream):
+        elif isinstance(stream, torch.cuda.ExternalStream):
+            self._foreign |= raw != self._own
+        elif raw not in self._known:
             self._buf.record_stream(torch.cuda.current_stream() if stream is None else stream)
             self._known.add(raw)
 

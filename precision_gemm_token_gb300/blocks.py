@@ -120,7 +120,7 @@ class BlockWorkspace:
             _bad(f"workspace: a CUDA device wanted, not {device}")
         self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
         self._buf, self._captured, self._kept = None, False, []
-        self._own, self._foreign = None, False      # the stream it was allocated on; used on one the allocator knows not of
+        self._own, self._foreign = None, False      # the buffer's stream; used on one that the allocator cannot know
         self._known = set()         # raw handles of the streams that the allocator knows the buffer's use on
 
     def get(self, need, dev, raw, stream):

@@ -23,7 +23,7 @@
 // line (the joined sums of 32 x 14336 -> 4096 took 7000 cycles to store).
 //
 // Bound: the copies of the weights, and start and end. Up projections of 64 tokens over 64 experts of 4096 x 1792 take
-// 132 us with plan and scatter (7.1 TB/s of the experts' 940 MB: some of them stay in L2), of one token 29.1 us (117 MB);
+// 132 us with plan and scatter (7.1 TB/s of the experts' 940 MB: some of them stay in L2), of one token 29.5 us (117 MB);
 // 32 x 14336 -> 4096 18.5 us with the quantizer (59 MB). Every wait is bounded, as in block_gemm.cu.
 #include "block_gemm.cuh"
 
@@ -489,7 +489,8 @@ int launch(const BlockGemmArgs& a) {
 // The product turned round pays where the sums are gated (up projections of 1, 8 and 64 tokens 35.6 -> 29.1, 99 -> 78
 // and 153 -> 132 us), and where K is split (32 x 14336 -> 4096: 29.7 -> 18.5 us). Otherwise block_gemm.cu's narrower
 // tiles spread better over the SMs (32 x 4096 -> 28672: 26.4 against 30.6 us; down projections of 64 tokens 88 against
-// 99).
+// 99). The host knows the mean of an expert's rows alone: where all tokens go to the same few experts their weights are
+// read again for every 32 rows (128 tokens with the same eight experts, or with one: 52 us).
 bool block_few_takes(const BlockGemmArgs& a) {
   if (a.grouped) return a.gated && a.M / a.experts <= kCols / 2;
   return a.M <= kCols && few_splits(a.N, a.K) > 1;

@@ -25,10 +25,10 @@
 // so that a thread holds both of an element and two threads a whole block of
 // the output, which leaves quantized.
 //
-// Bound: the loop between the MMAs and the sums. 2048 x 8192 -> 28672 takes 385 us, 2.5 PFLOP/s, 64 % of twice the
-// measured bf16 rate: 980 cycles a block of 128 x 256, where the MMAs take 512 and the 96 KB that go through shared
-// memory some 820; without the sums a block takes 850. Down projections of 64 tokens over 64 experts of 4096 x 1792
-// read their 470 MB at 6.3 TB/s.
+// Bound: the loop between the MMAs and the sums. 2048 x 8192 -> 28672 takes 396 us (437 us after seconds of it, at the
+// clock that the power limit leaves), 2.4 (2.2) PFLOP/s, 62 (56) % of twice the measured bf16 rate: 980 cycles a block
+// of 128 x 256, where the MMAs take 512 and the 96 KB that go through shared memory some 820; without the sums a block
+// takes 850. Down projections of 64 tokens over 64 experts of 4096 x 1792 read their 470 MB at 6.3 TB/s.
 //
 // Every wait is bounded: on a timeout the CTA records EPILORA_ERR_TIMEOUT,
 // stops issuing, waits (bounded) for its copies and MMAs in flight, writes NaN
@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 // kF32: grouped products that leave in fp32, 512 bytes a thread instead of 256 (down projections of 4096 tokens, sum
-// and all, 557 us instead of 374, of 64 tokens 89.5 instead of 83.5, of one 22.3 instead of 21.2: the parts' traffic)
+// and all, 536 us instead of 380, of 64 tokens 89.4 instead of 83.3, of one 23.2 instead of 22.2: the parts' traffic)
 template <int BN, bool kGrouped, bool kGated, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const __grid_constant__ Params p) {
   using C = Cfg<BN>;

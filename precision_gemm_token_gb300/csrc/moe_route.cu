@@ -13,7 +13,7 @@
 // 20 us for such a token, which then is the call's time). Without a bias the
 // order of the scores is the order of the logits, which needs no arithmetic.
 //
-// Bound: the chain of the choices (4096 x 256 with eight groups: some 30 maxima over the warp a token, 17.8 us; one
+// Bound: the chain of the choices (4096 x 256 with eight groups: some 30 maxima over the warp a token, 18.4 us; one
 // token of 128 experts 3 us); the bytes are few. Softmax with a bias: of 4096
 // tokens some go through 64 bits again, 27 us of 256 experts, 65 of 512 with 16
 // chosen (without a bias 18).

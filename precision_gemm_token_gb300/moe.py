@@ -27,8 +27,8 @@ _LOGITS = {torch.float32: E.LOGITS_F32, torch.bfloat16: E.LOGITS_BF16}
 def route(logits, top: int, bias=None, scoring: str = "softmax", groups: int = 1, top_groups: int = 1,
           group_best: int = 1, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
     """The `top` experts of each token and their weights from the router's
-    logits [tokens, experts] (fp32 or bf16, any row stride): (ids int32
-    [tokens, top], weights fp32 [tokens, top]). `bias` (fp32 [experts]) is
+    logits [tokens, experts] (fp32 or bf16, rows that do not overlap): (ids
+    int32 [tokens, top], weights fp32 [tokens, top]). `bias` (fp32 [experts]) is
     added to the scores for the choice alone; with groups > 1 the experts come
     from the `top_groups` groups whose `group_best` largest choices sum to the
     most. epilora_moe_route has the details."""
@@ -74,7 +74,7 @@ def quantize_experts(gate, up, down, stream=None) -> ExpertWeights:
     hidden], down [experts, hidden, inner]. Beside them it takes the memory of
     the codes and scales that it returns, no more."""
     dev, raw, given = _start(gate, stream)
-    if gate.dim() != 3 or gate.shape[0] == 0 or up.shape != gate.shape or down.shape != (gate.shape[0], *gate.shape[:0:-1]):
+    if gate.dim() != 3 or not len(gate) or up.shape != gate.shape or down.shape != (len(gate), *gate.shape[:0:-1]):
         _bad("quantize_experts: gate and up [experts, inner, hidden], down [experts, hidden, inner] wanted")
     n, inner, hidden = gate.shape
     bi, bh = _blocks(inner), _blocks(hidden)

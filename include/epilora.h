@@ -656,7 +656,7 @@ typedef enum { EPILORA_SCORE_SOFTMAX = 0, EPILORA_SCORE_SIGMOID = 1 } epilora_sc
  *     1 swallows) the larger logit goes first, then the lowest index. With
  *     equal biases, or none, that is the order of the real numbers c
  *   weights[t][j] = scale * s of the j-th, divided by the sum of the chosen
- *     s first if renormalize
+ *     s first if renormalize, in fp32
  * A logit of -infinity or NaN, or a bias of -infinity or NaN, takes the
  * expert away for that token; +infinity counts as the largest finite number.
  * Slots for which no expert is left have id -1 and weight 0.
